@@ -84,6 +84,14 @@ _SIGS = {
     "nf4_stack_workspace_bytes": ([_LP, _i32, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
     "nf4_stack_fwd": ([_LP, _i32, _i64, _vp, _sz, _vp], ctypes.c_int),
     "nf4_stack_bwd": ([_LP, _i32, _i32, _i64, _vp, _sz, _vp], ctypes.c_int),
+    "nf4_fp8_quantize": ([_vp, _i32, _i64, _i64, _i32, _i32, _vp, _vp, _vp], ctypes.c_int),
+    "nf4_fp8_dequantize": ([_vp, _vp, _i64, _i64, _i32, _i32, _vp, _i32, _vp], ctypes.c_int),
+    "nf4_fp8_matmul": ([_vp, _i32, _vp, _i64, _vp, _vp, _i64, _i64, _i32, _vp, _vp, _i32, _vp, _vp], ctypes.c_int),
+    "nf4_fp8_matmul_grouped": ([_vp, _i32, _vp, _i64, _vp, _vp, _i32, _i64, _i64, _vp, _i32, _vp, _vp, _i32, _vp, _vp],
+                               ctypes.c_int),
+    "nf4_rmsnorm_fwd": ([_vp, _vp, _vp, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "nf4_rmsnorm_workspace_bytes": ([_i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
+    "nf4_rmsnorm_bwd": ([_vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
 }
 for _name, (_args, _res) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -485,6 +493,162 @@ def merge(base, L1: torch.Tensor, L2: torch.Tensor, s: float, bf16: bool = False
     _check(_lib.nf4lora_merge(_ptr(W), q, rows, cols, _ptr(L1), _ptr(L2), r, float(s), _ptr(out),
                               1 if bf16 else 0, _stream()), "nf4lora_merge")
     return out
+
+
+# ---------------------------------------------------------------------------
+# 8-bit storage in blocks of 128, its products and the norm
+# ---------------------------------------------------------------------------
+
+FP8_BLOCK = 128
+FP8_FORMATS = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+
+
+def _fp8_format(dtype, name: str) -> int:
+    f = FP8_FORMATS.get(dtype)
+    if f is None:
+        raise ValueError(f"{name}: expected torch.float8_e4m3fn or torch.float8_e5m2, got {dtype}")
+    return f
+
+
+def _blocks(n: int) -> int:
+    return -(-n // FP8_BLOCK)
+
+
+def fp8_quantize(X: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = torch.float8_e4m3fn,
+                 codes: torch.Tensor | None = None, scales: torch.Tensor | None = None):
+    """nf4_fp8_quantize of a cuda bf16 or fp32 [rows][cols] tensor: (codes `dtype` [rows][cols], scales fp32).
+    block_rows = 1: a scale per row and 128 columns, [rows][ceil(cols / 128)] (activations, gradients);
+    block_rows = 128: per 128 x 128 block, [ceil(rows / 128)][ceil(cols / 128)] (weights)."""
+    f = _fp8_format(dtype, "dtype")
+    if not isinstance(X, torch.Tensor) or X.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("X: expected a bf16 or fp32 tensor")
+    rows, cols = _need(X, X.dtype, (None, None), "X").shape
+    sshape = (rows if block_rows == 1 else _blocks(rows), _blocks(cols))
+    codes = _need(codes, dtype, (rows, cols), "codes") if codes is not None else \
+        torch.empty(rows, cols, dtype=dtype, device=X.device)
+    scales = _need(scales, torch.float32, sshape, "scales") if scales is not None else \
+        torch.empty(sshape, dtype=torch.float32, device=X.device)
+    _check(_lib.nf4_fp8_quantize(X.data_ptr(), X.dtype == torch.bfloat16, rows, cols, f, block_rows,
+                                 codes.data_ptr(), scales.data_ptr(), _stream()), "nf4_fp8_quantize")
+    return codes, scales
+
+
+def fp8_dequantize(codes: torch.Tensor, scales: torch.Tensor, block_rows: int = 1, bf16: bool = False,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """nf4_fp8_dequantize into fp32 (or bf16) [rows][cols], into `out` when given."""
+    f = _fp8_format(getattr(codes, "dtype", None), "codes")
+    rows, cols = _need(codes, codes.dtype, (None, None), "codes").shape
+    _need(scales, torch.float32, (rows if block_rows == 1 else _blocks(rows), _blocks(cols)), "scales")
+    odt = torch.bfloat16 if bf16 else torch.float32
+    out = _need(out, odt, (rows, cols), "out") if out is not None else \
+        torch.empty(rows, cols, dtype=odt, device=codes.device)
+    _check(_lib.nf4_fp8_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, f, block_rows, out.data_ptr(),
+                                   1 if bf16 else 0, _stream()), "nf4_fp8_dequantize")
+    return out
+
+
+def _fp8_product_args(A, a_scales, o: int, h: int, transpose: bool, A2, B2, experts: tuple, out):
+    """Checks the product's tensors against W [o][h]; returns (a_format, M, R, C)."""
+    f = _fp8_format(getattr(A, "dtype", None), "A")
+    K, N = (o, h) if transpose else (h, o)
+    M = _need(A, A.dtype, (None, K), "A").shape[0]
+    _need(a_scales, torch.float32, (M, _blocks(K)), "a_scales")
+    R = 0
+    if A2 is not None or B2 is not None:
+        if A2 is None or B2 is None:
+            raise ValueError("A2 and B2: give both or neither")
+        R = _need(A2, torch.bfloat16, (M, None), "A2").shape[1]
+        _need(B2, torch.bfloat16, (*experts, N, R), "B2")
+    C = _need(out, torch.bfloat16, (M, N), "out") if out is not None else \
+        torch.empty(M, N, dtype=torch.bfloat16, device=A.device)
+    return f, M, R, C
+
+
+def fp8_matmul(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
+               transpose: bool = False, A2: torch.Tensor | None = None, B2: torch.Tensor | None = None,
+               out: torch.Tensor | None = None) -> torch.Tensor:
+    """nf4_fp8_matmul: A * W^T (+ A2 * B2^T), or A * W (+ ...) with transpose=True, bf16 [M][N].
+    A [M][K] and a_scales as fp8_quantize(X) gives them (either format), W [o][h] (e4m3) and w_scales as
+    fp8_quantize(W, 128) does."""
+    o, h = _need(W, torch.float8_e4m3fn, (None, None), "W").shape
+    _need(w_scales, torch.float32, (_blocks(o), _blocks(h)), "w_scales")
+    f, M, R, C = _fp8_product_args(A, a_scales, o, h, transpose, A2, B2, (), out)
+    _check(_lib.nf4_fp8_matmul(A.data_ptr(), f, a_scales.data_ptr(), M, W.data_ptr(), w_scales.data_ptr(), o, h,
+                               1 if transpose else 0, A2.data_ptr() if R else None, B2.data_ptr() if R else None, R,
+                               C.data_ptr(), _stream()), "nf4_fp8_matmul")
+    return C
+
+
+def fp8_matmul_grouped(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
+                       offsets: torch.Tensor, transpose: bool = False, A2: torch.Tensor | None = None,
+                       B2: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """nf4_fp8_matmul_grouped: fp8_matmul of the rows offsets[e] .. offsets[e + 1] - 1 with expert e's W[e]
+    [experts][o][h] (w_scales [experts][..][..], B2 [experts][N][R]); offsets is a cuda int32 [experts + 1].
+    Rows outside the experts' are not written (undefined in a result that this call allocates)."""
+    E, o, h = _need(W, torch.float8_e4m3fn, (None, None, None), "W").shape
+    _need(w_scales, torch.float32, (E, _blocks(o), _blocks(h)), "w_scales")
+    _need(offsets, torch.int32, (E + 1,), "offsets")
+    f, M, R, C = _fp8_product_args(A, a_scales, o, h, transpose, A2, B2, (E,), out)
+    _check(_lib.nf4_fp8_matmul_grouped(A.data_ptr(), f, a_scales.data_ptr(), M, W.data_ptr(), w_scales.data_ptr(), E,
+                                       o, h, offsets.data_ptr(), 1 if transpose else 0,
+                                       A2.data_ptr() if R else None, B2.data_ptr() if R else None, R, C.data_ptr(),
+                                       _stream()), "nf4_fp8_matmul_grouped")
+    return C
+
+
+def rmsnorm_fwd(X: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
+                want_y: bool = True, want_fp8: bool = False, want_rstd: bool = False, outs=None):
+    """nf4_rmsnorm_fwd of bf16 X [M][H] (+ residual): (Y bf16, h bf16, codes e4m3, scales fp32, rstd fp32), None for
+    what is not asked for (h: without a residual).  `outs`: the same five, given instead of allocated."""
+    M, H = _need(X, torch.bfloat16, (None, None), "X").shape
+    _need(w, torch.bfloat16, (H,), "w")
+    if residual is not None:
+        _need(residual, torch.bfloat16, (M, H), "residual")
+    shapes = (("Y", want_y, torch.bfloat16, (M, H)), ("h", residual is not None, torch.bfloat16, (M, H)),
+              ("codes", want_fp8, torch.float8_e4m3fn, (M, H)), ("scales", want_fp8, torch.float32, (M, _blocks(H))),
+              ("rstd", want_rstd, torch.float32, (M,)))
+    if outs is None:
+        outs = tuple(torch.empty(shape, dtype=dt, device=X.device) if want else None
+                     for _, want, dt, shape in shapes)
+    else:
+        for t, (name, want, dt, shape) in zip(outs, shapes):
+            if want != (t is not None):
+                raise ValueError(f"outs.{name}: {'missing' if want else 'given, but not asked for'}")
+            if want:
+                _need(t, dt, shape, f"outs.{name}")
+    Y, h, codes, scales, rstd = outs
+    _check(_lib.nf4_rmsnorm_fwd(_ptr(X), _ptr(residual), _ptr(w), M, H, eps, _ptr(h), _ptr(Y), _ptr(codes),
+                                _ptr(scales), _ptr(rstd), _stream()), "nf4_rmsnorm_fwd")
+    return outs
+
+
+def rmsnorm_workspace_bytes(M: int, H: int) -> int:
+    b = _sz()
+    _check(_lib.nf4_rmsnorm_workspace_bytes(M, H, ctypes.byref(b)), "nf4_rmsnorm_workspace_bytes")
+    return b.value
+
+
+def rmsnorm_bwd(dY: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rstd: torch.Tensor,
+                dH: torch.Tensor | None = None, ws: torch.Tensor | None = None, outs=None):
+    """nf4_rmsnorm_bwd: (dX bf16 [M][H], the gradient of X and of the residual alike, dw fp32 [H]) from the forward's
+    h (X without a residual) and rstd; dH is the gradient that reaches h along the residual stream."""
+    M, H = _need(dY, torch.bfloat16, (None, None), "dY").shape
+    _need(h, torch.bfloat16, (M, H), "h")
+    _need(w, torch.bfloat16, (H,), "w")
+    _need(rstd, torch.float32, (M,), "rstd")
+    if dH is not None:
+        _need(dH, torch.bfloat16, (M, H), "dH")
+    if outs is None:
+        dX = torch.empty(M, H, dtype=torch.bfloat16, device=dY.device)
+        dw = torch.empty(H, dtype=torch.float32, device=dY.device)
+    else:
+        dX = _need(outs[0], torch.bfloat16, (M, H), "outs.dX")
+        dw = _need(outs[1], torch.float32, (H,), "outs.dw")
+    ws = _need_ws(ws) if ws is not None else \
+        torch.empty(rmsnorm_workspace_bytes(M, H), dtype=torch.uint8, device=dY.device)
+    _check(_lib.nf4_rmsnorm_bwd(_ptr(dY), _ptr(h), _ptr(w), _ptr(rstd), _ptr(dH), M, H, _ptr(dX), _ptr(dw), _ptr(ws),
+                                ws.numel(), _stream()), "nf4_rmsnorm_bwd")
+    return dX, dw
 
 
 # ---------------------------------------------------------------------------

@@ -37,9 +37,13 @@ DEVICE = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-p
 EXTRA = {"quant.hip": ["-ffp-contract=off"],
          # dequantized weights (and the two-stage sum) must round like nf4_dequantize: no fused multiply-add
          "gemm.hip": ["-ffp-contract=off"],
-         "merge.hip": ["-ffp-contract=off"]}
+         "merge.hip": ["-ffp-contract=off"],
+         # the 8-bit codes and scales round as the format defines; the fused multiply-adds are written out
+         "fp8_quant.hip": ["-ffp-contract=off"],
+         "norm.hip": ["-ffp-contract=off"]}
 
-HIP_SOURCES = ["quant.hip", "gemm.hip", "skinny.hip", "merge.hip", "probe.hip", "scratch.hip"]
+HIP_SOURCES = ["quant.hip", "gemm.hip", "skinny.hip", "merge.hip", "probe.hip", "scratch.hip", "fp8_quant.hip", "fp8_gemm.hip",
+               "norm.hip"]
 CPP_SOURCES = ["api.cpp", "nf4_table.cpp", "plan.cpp"]
 
 

@@ -477,6 +477,70 @@ nf4_status error_batch_shapes(const int64_t* rows, const int64_t* cols, int32_t 
   return NF4_OK;
 }
 
+// ---- 8-bit storage, its products and the norm ----
+constexpr int64_t kFp8Block = 128;
+int64_t fp8_blocks(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
+size_t fp8_scale_bytes(int64_t rows, int64_t cols, int32_t block_rows) {
+  return (size_t)(4 * (block_rows == 1 ? rows : fp8_blocks(rows)) * fp8_blocks(cols));
+}
+
+nf4_status check_fp8(int64_t rows, int64_t cols, int32_t format, int32_t block_rows) {
+  if (format != NF4_FP8_E4M3 && format != NF4_FP8_E5M2) return NF4_ERR_ARG;
+  if (block_rows != 1 && block_rows != kFp8Block) return NF4_ERR_ARG;
+  if (rows < 0 || cols < 0 || cols % 16 != 0 || cols > kMaxLayerDim) return NF4_ERR_SHAPE;
+  if (cols > 0 && rows > ((int64_t)1 << 40) / cols) return NF4_ERR_SHAPE;
+  return NF4_OK;
+}
+
+// no output may overlap an input or another output
+template <size_t NI, size_t NO>
+nf4_status check_alias(const Range (&ins)[NI], const Range (&outs)[NO]) {
+  for (size_t i = 0; i < NO; ++i) {
+    for (const Range& b : ins)
+      if (overlap(outs[i], b)) return NF4_ERR_ALIAS;
+    for (size_t j = i + 1; j < NO; ++j)
+      if (overlap(outs[i], outs[j])) return NF4_ERR_ALIAS;
+  }
+  return NF4_OK;
+}
+
+// both products; q.experts == 0 is the dense one
+nf4_status fp8_product(const Fp8Gemm& q, int32_t a_format, void* stream) {
+  if (a_format != NF4_FP8_E4M3 && a_format != NF4_FP8_E5M2) return NF4_ERR_ARG;
+  if (q.rows <= 0 || q.cols <= 0 || q.rows % 16 != 0 || q.cols % 16 != 0) return NF4_ERR_SHAPE;
+  if (q.rows > kMaxLayerDim || q.cols > kMaxLayerDim || q.rows * q.cols > kMaxLayerWeights) return NF4_ERR_SHAPE;
+  const int64_t mmax = q.experts ? (int64_t)INT32_MAX : (int64_t)1 << 31;
+  if (q.M < 0 || q.M > mmax || q.R < 0 || q.R > 256 || q.R % 16 != 0) return NF4_ERR_SHAPE;
+  if (q.M == 0) return NF4_OK;
+  if (!q.A || !q.a_scales || !q.W || !q.w_scales || !q.C || (q.R > 0 && (!q.A2 || !q.B2))) return NF4_ERR_NULL;
+  if (q.experts && !q.offsets) return NF4_ERR_NULL;
+  if (!aligned16(q.A) || !aligned16(q.a_scales) || !aligned16(q.W) || !aligned16(q.w_scales) || !aligned16(q.C) ||
+      (q.R > 0 && (!aligned16(q.A2) || !aligned16(q.B2))) || (q.experts && !aligned16(q.offsets)))
+    return NF4_ERR_ALIGN;
+  const int64_t K = q.transpose ? q.rows : q.cols, N = q.transpose ? q.cols : q.rows;
+  const int64_t E = q.experts ? q.experts : 1;
+  const Range ins[] = {rng(q.A, (size_t)(q.M * K)),
+                       rng(q.a_scales, fp8_scale_bytes(q.M, K, 1)),
+                       rng(q.W, (size_t)(E * N * K)),
+                       rng(q.w_scales, (size_t)E * fp8_scale_bytes(q.rows, q.cols, 128)),
+                       rng(q.A2, (size_t)(q.M * q.R * 2)),
+                       rng(q.B2, (size_t)(E * N * q.R * 2)),
+                       rng(q.offsets, q.experts ? (size_t)(E + 1) * 4 : 0)};
+  const Range outs[] = {rng(q.C, (size_t)(q.M * N * 2))};
+  const nf4_status st = check_alias(ins, outs);
+  if (st != NF4_OK) return st;
+  if (!launch_fp8_gemm) return NF4_ERR_HIP;
+  return hip_status(launch_fp8_gemm(q, (hipStream_t)stream));
+}
+
+nf4_status check_norm(int64_t M, int64_t H) {
+  if (M < 0 || M > ((int64_t)1 << 31)) return NF4_ERR_SHAPE;
+  if (H <= 0 || H % 16 != 0 || H > kMaxNormWidth) return NF4_ERR_SHAPE;
+  return NF4_OK;
+}
+
+size_t norm_ws(int64_t M, int64_t H) { return align256((size_t)std::max(rmsnorm_parts(M, (int)H), 1) * H * 4); }
+
 }  // namespace
 
 extern "C" {
@@ -867,6 +931,119 @@ nf4_status nf4lora_merge(const float* W, const nf4_tensor* q, int64_t rows, int6
                                  qq ? qq->dq_scale : nullptr, rr ? rr->codes : nullptr, rr ? rr->absmax : nullptr,
                                  rr ? rr->dq_scale : nullptr, L1, L2, r, s, rows, cols, out_is_bf16 != 0, W_out,
                                  codebook_consts(qq ? qq->codebook : 0), (hipStream_t)stream));
+}
+
+nf4_status nf4_fp8_quantize(const void* X, int32_t x_is_bf16, int64_t rows, int64_t cols, int32_t format,
+                            int32_t block_rows, uint8_t* codes, float* scales, void* stream) {
+  nf4_status st = check_fp8(rows, cols, format, block_rows);
+  if (st != NF4_OK) return st;
+  const int64_t n = rows * cols;
+  if (n == 0) return NF4_OK;
+  if (!X || !codes || !scales) return NF4_ERR_NULL;
+  if (!aligned16(X) || !aligned16(codes) || !aligned16(scales)) return NF4_ERR_ALIGN;
+  const Range ins[] = {rng(X, (size_t)n * (x_is_bf16 ? 2 : 4))};
+  const Range outs[] = {rng(codes, (size_t)n), rng(scales, fp8_scale_bytes(rows, cols, block_rows))};
+  st = check_alias(ins, outs);
+  if (st != NF4_OK) return st;
+  if (!launch_fp8_quantize) return NF4_ERR_HIP;
+  return hip_status(launch_fp8_quantize(X, x_is_bf16 != 0, rows, cols, format == NF4_FP8_E5M2, block_rows, codes,
+                                        scales, (hipStream_t)stream));
+}
+
+nf4_status nf4_fp8_dequantize(const uint8_t* codes, const float* scales, int64_t rows, int64_t cols, int32_t format,
+                              int32_t block_rows, void* out, int32_t out_is_bf16, void* stream) {
+  nf4_status st = check_fp8(rows, cols, format, block_rows);
+  if (st != NF4_OK) return st;
+  const int64_t n = rows * cols;
+  if (n == 0) return NF4_OK;
+  if (!codes || !scales || !out) return NF4_ERR_NULL;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(out)) return NF4_ERR_ALIGN;
+  const Range ins[] = {rng(codes, (size_t)n), rng(scales, fp8_scale_bytes(rows, cols, block_rows))};
+  const Range outs[] = {rng(out, (size_t)n * (out_is_bf16 ? 2 : 4))};
+  st = check_alias(ins, outs);
+  if (st != NF4_OK) return st;
+  if (!launch_fp8_dequantize) return NF4_ERR_HIP;
+  return hip_status(launch_fp8_dequantize(codes, scales, rows, cols, format == NF4_FP8_E5M2, block_rows,
+                                          out_is_bf16 != 0, out, (hipStream_t)stream));
+}
+
+nf4_status nf4_fp8_matmul(const uint8_t* A, int32_t a_format, const float* a_scales, int64_t M, const uint8_t* W,
+                          const float* w_scales, int64_t rows, int64_t cols, int32_t transpose, const uint16_t* A2,
+                          const uint16_t* B2, int32_t R, uint16_t* C, void* stream) {
+  if (transpose != 0 && transpose != 1) return NF4_ERR_ARG;
+  const Fp8Gemm q{A, a_format == NF4_FP8_E5M2, a_scales, M, W, w_scales, rows, cols, transpose == 1, 0, nullptr, A2, B2,
+                  R, C};
+  return fp8_product(q, a_format, stream);
+}
+
+nf4_status nf4_fp8_matmul_grouped(const uint8_t* A, int32_t a_format, const float* a_scales, int64_t M,
+                                  const uint8_t* W, const float* w_scales, int32_t experts, int64_t rows, int64_t cols,
+                                  const int32_t* offsets, int32_t transpose, const uint16_t* A2, const uint16_t* B2,
+                                  int32_t R, uint16_t* C, void* stream) {
+  if (transpose != 0 && transpose != 1) return NF4_ERR_ARG;
+  if (experts < 1 || experts > 4096) return NF4_ERR_SHAPE;
+  const Fp8Gemm q{A, a_format == NF4_FP8_E5M2, a_scales, M, W, w_scales, rows, cols, transpose == 1, experts, offsets,
+                  A2, B2, R, C};
+  return fp8_product(q, a_format, stream);
+}
+
+nf4_status nf4_rmsnorm_fwd(const uint16_t* X, const uint16_t* res, const uint16_t* w, int64_t M, int64_t H, float eps,
+                           uint16_t* H_out, uint16_t* Y, uint8_t* codes, float* scales, float* rstd, void* stream) {
+  nf4_status st = check_norm(M, H);
+  if (st != NF4_OK) return st;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return NF4_ERR_ARG;
+  if (M == 0) return NF4_OK;
+  if (!X || !w || (res && !H_out)) return NF4_ERR_NULL;
+  if ((codes == nullptr) != (scales == nullptr) || (!Y && !codes)) return NF4_ERR_NULL;
+  if (!res) H_out = nullptr;
+  if (!aligned16(X) || !aligned16(res) || !aligned16(w) || !aligned16(H_out) || !aligned16(Y) || !aligned16(codes) ||
+      !aligned16(scales) || !aligned16(rstd))
+    return NF4_ERR_ALIGN;
+  const size_t b = (size_t)(M * H * 2);
+  const Range ins[] = {rng(X, b), rng(res, res ? b : 0), rng(w, (size_t)H * 2)};
+  const Range outs[] = {rng(H_out, H_out ? b : 0), rng(Y, Y ? b : 0), rng(codes, codes ? (size_t)(M * H) : 0),
+                        rng(scales, scales ? fp8_scale_bytes(M, H, 1) : 0), rng(rstd, rstd ? (size_t)M * 4 : 0)};
+  st = check_alias(ins, outs);
+  if (st != NF4_OK) return st;
+  if (!launch_rmsnorm_fwd) return NF4_ERR_HIP;
+  return hip_status(
+      launch_rmsnorm_fwd(X, res, w, M, (int)H, eps, H_out, Y, codes, scales, rstd, (hipStream_t)stream));
+}
+
+nf4_status nf4_rmsnorm_workspace_bytes(int64_t M, int64_t H, size_t* bytes) {
+  if (!bytes) return NF4_ERR_NULL;
+  const nf4_status st = check_norm(M, H);
+  if (st != NF4_OK) return st;
+  *bytes = norm_ws(M, H);
+  return NF4_OK;
+}
+
+nf4_status nf4_rmsnorm_bwd(const uint16_t* dY, const uint16_t* h, const uint16_t* w, const float* rstd,
+                           const uint16_t* dH, int64_t M, int64_t H, uint16_t* dX, float* dw, void* ws,
+                           size_t ws_bytes, void* stream) {
+  nf4_status st = check_norm(M, H);
+  if (st != NF4_OK) return st;
+  if (!dw || (M > 0 && (!dY || !h || !w || !rstd || !dX))) return NF4_ERR_NULL;
+  const size_t need = norm_ws(M, H);
+  if (!ws || ws_bytes < need) return NF4_ERR_WORKSPACE;
+  if (!aligned16(dw) || !aligned16(ws) ||
+      (M > 0 && (!aligned16(dY) || !aligned16(h) || !aligned16(w) || !aligned16(rstd) || !aligned16(dH) ||
+                 !aligned16(dX))))
+    return NF4_ERR_ALIGN;
+  const size_t b = (size_t)(M * H * 2);
+  const Range ins[] = {rng(dY, b), rng(h, b), rng(w, M > 0 ? (size_t)H * 2 : 0), rng(rstd, (size_t)M * 4),
+                       rng(dH, dH ? b : 0)};
+  const Range outs[] = {rng(dX, b), rng(dw, (size_t)H * 4), rng(ws, need)};
+  st = check_alias(ins, outs);
+  if (st != NF4_OK) return st;
+  if (M == 0) {
+    PrepArgs pa{};
+    pa.zero[0] = ZeroJob{(uint32_t*)dw, H};
+    return hip_status(launch_prep(pa, (hipStream_t)stream));
+  }
+  if (!launch_rmsnorm_bwd) return NF4_ERR_HIP;
+  return hip_status(
+      launch_rmsnorm_bwd(dY, h, w, rstd, dH, M, (int)H, dX, dw, (float*)ws, (hipStream_t)stream));
 }
 
 }  // extern "C"

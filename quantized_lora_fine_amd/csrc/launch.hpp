@@ -154,4 +154,48 @@ int64_t nt_launch_rows(int64_t M);
 // (512 work-items per tile)
 int64_t gemm_launch_panels(int64_t tiles_n);
 
+// ---- the 8-bit operators and the norm ----
+// Weak: a host-only build of the ABI layer (argument checks without kernels)
+// links without these definitions; api.cpp then reports NF4_ERR_HIP for a call
+// that would launch one.
+#define NF4K_WEAK __attribute__((weak))
+
+// block_rows: 1 (a scale per row and 128 columns) or 128 (per 128 x 128 block)
+NF4K_WEAK hipError_t launch_fp8_quantize(const void* X, bool bf16, int64_t rows, int64_t cols, bool e5m2,
+                                         int block_rows, uint8_t* codes, float* scales, hipStream_t st);
+NF4K_WEAK hipError_t launch_fp8_dequantize(const uint8_t* codes, const float* scales, int64_t rows, int64_t cols,
+                                           bool e5m2, int block_rows, bool bf16, void* out, hipStream_t st);
+
+// threads that hold one row of width H (16, 64, 256, 512 or 1024)
+int rmsnorm_threads(int H);
+// workgroups of the norm's gradient, each with a partial dw [H]
+int rmsnorm_parts(int64_t M, int H);
+constexpr int kMaxNormWidth = 32768;  // 1024 threads, 4 chunks of 8 columns
+NF4K_WEAK hipError_t launch_rmsnorm_fwd(const uint16_t* X, const uint16_t* R, const uint16_t* w, int64_t M, int H,
+                                        float eps, uint16_t* Hout, uint16_t* Y, uint8_t* codes, float* scales,
+                                        float* rstd, hipStream_t st);
+NF4K_WEAK hipError_t launch_rmsnorm_bwd(const uint16_t* dY, const uint16_t* Hs, const uint16_t* w, const float* rstd,
+                                        const uint16_t* dH, int64_t M, int H, uint16_t* dX, float* dw, float* part,
+                                        hipStream_t st);
+
+// C [M][N] = A W^T (or A W) in 8 bits, scaled by block, plus A2 B2^T; with
+// `offsets` grouped by expert (rows offsets[e] .. offsets[e + 1] by W[e], B2[e])
+struct Fp8Gemm {
+  const uint8_t* A;
+  bool a_e5m2;
+  const float* a_scales;
+  int64_t M;
+  const uint8_t* W;
+  const float* w_scales;
+  int64_t rows, cols;
+  bool transpose;
+  int experts;  // 0: one weight, no offsets
+  const int32_t* offsets;
+  const uint16_t* A2;
+  const uint16_t* B2;
+  int R;
+  uint16_t* C;
+};
+NF4K_WEAK hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t st);
+
 }  // namespace nf4k

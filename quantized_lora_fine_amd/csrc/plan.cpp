@@ -77,6 +77,18 @@ int64_t gemm_launch_panels(int64_t tiles_n) {
   return per > 0 ? per : 1;
 }
 
+int rmsnorm_threads(int H) {
+  if (H <= 128) return 16;
+  if (H <= 2048) return 64;
+  if (H <= 8192) return 256;
+  return H <= 16384 ? 512 : 1024;
+}
+
+int rmsnorm_parts(int64_t M, int H) {
+  const int tpr = rmsnorm_threads(H), teams = tpr < 256 ? 256 / tpr : 1;
+  const int64_t groups = (M + teams - 1) / teams;
+  return (int)(groups < 512 ? groups : 512);
+}
 
 int error_batch_chunk(const int64_t* rows, const int64_t* cols, int32_t n, int32_t c0, int64_t* g0) {
   int k = 0;

@@ -1,0 +1,445 @@
+"""8-bit storage, its products and the norm against the fp64 oracle (needs an MI355X).
+
+Codes, scales, dequantized values and the norm's residual sum are bit-exact.
+Computed outputs are held to the roundings they go through: half a step of the
+output's type relative to the value, plus fp32 accumulation in proportion to the
+sum of the terms' magnitudes.  EPS32 is one fp32 step, taken per addition (the
+matrix cores' order of the 128 products of a block is theirs).
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp8
+
+pytestmark = pytest.mark.gpu
+
+try:
+    import quantized_lora_fine_amd as nf4
+except ImportError as exc:
+    if torch.cuda.is_available():
+        raise
+    pytest.skip(f"libnf4lora.so not loaded: {exc}", allow_module_level=True)
+
+DEV = "cuda"
+DTYPES = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+BF16 = 2.0 ** -8      # half a step, relative
+E4M3 = 2.0 ** -4
+EPS32 = 2.0 ** -23
+
+
+def bits(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+def f64(t):
+    return t.detach().to(torch.float64).cpu().numpy()
+
+
+def bf16_np(a):
+    return torch.from_numpy(np.ascontiguousarray(a, np.float32)).to(torch.bfloat16)
+
+
+def rows_of(rng, rows, cols):
+    """Activations: token sizes that differ, a few channels far larger."""
+    x = rng.standard_normal((rows, cols)) * np.exp(rng.standard_normal((rows, 1)))
+    x[:, rng.integers(0, cols, max(1, cols // 100))] *= 30
+    return x.astype(np.float32)
+
+
+def check_within(name, got, want, bound):
+    got = f64(got) if isinstance(got, torch.Tensor) else got
+    assert got.shape == want.shape, (name, got.shape, want.shape)
+    off = np.abs(got - want) / np.maximum(bound, 1e-300)
+    worst = np.unravel_index(np.argmax(off), off.shape) if off.size else None
+    print(f"  {name}: {off.max() if off.size else 0:.3f} of the bound", flush=True)
+    assert np.all(np.abs(got - want) <= bound), (name, worst, got[worst], want[worst], bound[worst])
+
+
+# ---------------------------------------------------------------------------------------------------------
+# quantization
+# ---------------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("rows,cols", [(1, 16), (1, 4096), (3, 272), (127, 128), (129, 1040), (260, 384)])
+def test_quantize(rows, cols, bf16, block_rows, fmt):
+    rng = np.random.default_rng(rows * 7 + cols)
+    x = rows_of(rng, rows, cols)
+    t = bf16_np(x) if bf16 else torch.from_numpy(x)
+    x = t.float().numpy()
+    codes, scales = nf4.fp8_quantize(t.to(DEV), block_rows, DTYPES[fmt])
+    want, ws = fp8.quantize(x, block_rows, fmt)
+    assert np.array_equal(scales.cpu().numpy().view(np.uint32), ws.view(np.uint32))
+    assert np.array_equal(bits(codes), want)
+    d = nf4.fp8_dequantize(codes, scales, block_rows)
+    dw = fp8.dequantize(want, ws, block_rows, fmt)
+    assert np.array_equal(d.cpu().numpy().view(np.uint32), dw.view(np.uint32))
+    db = nf4.fp8_dequantize(codes, scales, block_rows, bf16=True)
+    assert torch.equal(db.cpu().view(torch.int16), bf16_np(dw).view(torch.int16))
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_quantize_every_code_and_tie(fmt):
+    # a block whose largest value is F has scale 1: its codes are the rounding itself
+    vals = fp8.code_values(fmt)
+    grid = np.unique(np.abs(vals[np.isfinite(vals)]))
+    mid = ((grid[1:] + grid[:-1]) / 2).astype(np.float32)
+    x = np.concatenate([grid, mid, np.nextafter(mid, np.float32(0)), np.nextafter(mid, np.float32(1e9))])
+    x = np.concatenate([x, -x]).astype(np.float32)
+    x = x[np.abs(x) <= grid[-1]]
+    per = 127
+    n = -(-x.size // per)
+    X = np.zeros((n, 128), np.float32)
+    X[:, 0] = grid[-1]
+    X[:, 1:].reshape(-1)[:] = 0
+    flat = np.zeros(n * per, np.float32)
+    flat[:x.size] = x
+    X[:, 1:] = flat.reshape(n, per)
+    for block_rows in (1, 128):
+        codes, scales = nf4.fp8_quantize(torch.from_numpy(X).to(DEV), block_rows, DTYPES[fmt])
+        assert torch.all(scales == 1)
+        assert np.array_equal(bits(codes), fp8.encode(X, fmt))
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_edges(block_rows, fmt):
+    x = np.zeros((130, 272), np.float32)
+    x[0, 1] = 3e38                     # the largest magnitudes
+    x[129, 130] = 2.0 ** -120          # below the floor
+    x[129, 131] = 1e-42                # subnormal
+    x[0, 256:] = np.float32(2.0 ** -100)
+    x[1, 140] = np.nan                 # a NaN alone keeps its block's scale
+    x[1, 141] = -2.0
+    codes, scales = nf4.fp8_quantize(torch.from_numpy(x).to(DEV), block_rows, DTYPES[fmt])
+    want, ws = fp8.quantize(x, block_rows, fmt)
+    assert np.array_equal(scales.cpu().numpy().view(np.uint32), ws.view(np.uint32))
+    v, vw = f64(codes), fp8.code_values(fmt)[want]
+    assert np.array_equal(v, vw, equal_nan=True)
+    x[2, 5] = np.inf
+    codes, scales = nf4.fp8_quantize(torch.from_numpy(x).to(DEV), block_rows, DTYPES[fmt])
+    d = nf4.fp8_dequantize(codes, scales, block_rows).cpu().numpy()
+    block = d[2:3, :128] if block_rows == 1 else d[:128, :128]
+    assert np.all(np.isnan(block)) and np.all(np.isfinite(d[129, :128]))
+
+
+# ---------------------------------------------------------------------------------------------------------
+# norm
+# ---------------------------------------------------------------------------------------------------------
+
+WIDTHS = [16, 128, 144, 512, 528, 2048, 2064, 4096, 5120, 8192, 8208, 16400, 32768]
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("M,H", [(1, h) for h in WIDTHS] + [(5, h) for h in WIDTHS] + [(300, 272), (67, 4096)])
+def test_rmsnorm(M, H, residual):
+    rng = np.random.default_rng(M + H)
+    eps = 1e-6
+    X, w = bf16_np(rows_of(rng, M, H)), bf16_np(1 + 0.1 * rng.standard_normal(H))
+    R = bf16_np(rows_of(rng, M, H)) if residual else None
+    Y, h, codes, scales, rstd = nf4.rmsnorm_fwd(X.to(DEV), w.to(DEV), eps, R.to(DEV) if residual else None,
+                                                want_fp8=True, want_rstd=True)
+    hw = X if R is None else (X.float() + R.float()).to(torch.bfloat16)
+    assert (h is None) == (R is None)
+    if R is not None:
+        assert torch.equal(h.cpu().view(torch.int16), hw.view(torch.int16))
+    y, r = fp8.rmsnorm(f64(hw), f64(w), eps)
+    # the sum of squares: at most 32 terms a thread, then a tree, halved by the root
+    acc = 32 * EPS32
+    check_within("rstd", rstd, r, np.abs(r) * acc)
+    check_within("y", Y, y, np.abs(y) * (BF16 * (1 + 2.0 ** -8) + acc))
+    sw = np.maximum(np.abs(fp8._spread(fp8.block_scales(y.astype(np.float32), 1, "e4m3")[0], 1, M, H)), 0)
+    check_within("scales", scales, fp8.block_scales(y.astype(np.float32), 1, "e4m3")[0].astype(np.float64),
+                 scales.double().cpu().numpy() * 2 * acc)
+    d = nf4.fp8_dequantize(codes, scales)
+    check_within("codes", d, y, np.maximum(np.abs(y) * E4M3, sw * 2.0 ** -10) * (1 + 2.0 ** -8) + np.abs(y) * acc)
+    # each output alone is what it is beside the other
+    Y1 = nf4.rmsnorm_fwd(X.to(DEV), w.to(DEV), eps, R.to(DEV) if residual else None)[0]
+    assert torch.equal(Y1.view(torch.int16), Y.view(torch.int16))
+    _, _, c1, s1, _ = nf4.rmsnorm_fwd(X.to(DEV), w.to(DEV), eps, R.to(DEV) if residual else None, want_y=False,
+                                      want_fp8=True)
+    assert np.array_equal(bits(c1), bits(codes)) and torch.equal(s1, scales)
+
+
+def test_rmsnorm_rows_of_zeros():
+    X = torch.zeros(3, 256, dtype=torch.bfloat16, device=DEV)
+    X[1] = 2.0
+    w = torch.ones(256, dtype=torch.bfloat16, device=DEV)
+    Y, _, codes, scales, rstd = nf4.rmsnorm_fwd(X, w, 1e-6, want_fp8=True, want_rstd=True)
+    assert torch.all(Y[0] == 0) and torch.all(Y[1] == 1)
+    assert torch.all(codes[0].float() == 0)
+    assert abs(float(rstd[0]) - 1000.0) < 1e-2
+    Y, _, _, _, _ = nf4.rmsnorm_fwd(X, w, 0.0)
+    assert torch.all(torch.isnan(Y[0])) and torch.all(Y[1] == 1)
+
+
+@pytest.mark.parametrize("with_dh", [False, True])
+@pytest.mark.parametrize("M,H", [(1, h) for h in WIDTHS] + [(37, h) for h in (16, 144, 528, 2064, 5120, 8208, 16400)] +
+                         [(2500, 144), (1100, 1040), (700, 4096), (1999, 5120)])
+def test_rmsnorm_grad(M, H, with_dh):
+    rng = np.random.default_rng(M * 3 + H)
+    h, w = bf16_np(rows_of(rng, M, H)), bf16_np(1 + 0.1 * rng.standard_normal(H))
+    dy = bf16_np(1e-3 * rows_of(rng, M, H))
+    dh = bf16_np(1e-3 * rows_of(rng, M, H)) if with_dh else None
+    _, r = fp8.rmsnorm(f64(h), f64(w), 1e-6)
+    rstd = torch.from_numpy(r.astype(np.float32))
+    dX, dw = nf4.rmsnorm_bwd(dy.to(DEV), h.to(DEV), w.to(DEV), rstd.to(DEV), dh.to(DEV) if with_dh else None)
+    r = f64(rstd)
+    dx64, dw64 = fp8.rmsnorm_grad(f64(dy), f64(h), f64(w), r, f64(dh) if with_dh else None)
+    u, xhat = np.abs(f64(dy) * f64(w)), np.abs(f64(h)) * r[:, None]
+    size = r[:, None] * (u + xhat * np.mean(u * xhat, 1, keepdims=True))
+    # the dot product: at most 64 additions deep; then a handful of roundings
+    check_within("dx", dX, dx64, np.abs(dx64) * BF16 * (1 + 2.0 ** -8) + size * 40 * EPS32)
+    # dw: the rows of one workgroup in turn (at most ceil(M / 512)), 256 / 16 teams, then the parts
+    deep = -(-M // 512) + 16 + 64
+    check_within("dw", dw, dw64, np.sum(np.abs(f64(dy)) * xhat, 0) * deep * EPS32)
+    dX2, dw2 = nf4.rmsnorm_bwd(dy.to(DEV), h.to(DEV), w.to(DEV), rstd.to(DEV), dh.to(DEV) if with_dh else None)
+    assert torch.equal(dX2.view(torch.int16), dX.view(torch.int16)) and torch.equal(dw2, dw)
+
+
+# ---------------------------------------------------------------------------------------------------------
+# products
+# ---------------------------------------------------------------------------------------------------------
+
+def product_case(seed, M, o, h, transpose, R, fmt, experts=None):
+    rng = np.random.default_rng(seed)
+    K, N = (o, h) if transpose else (h, o)
+    a, s = fp8.quantize(rows_of(rng, M, K), 1, fmt) if M else (np.zeros((0, K), np.uint8),
+                                                                np.zeros((0, -(-K // 128)), np.float32))
+    many = experts or 1
+    w, ws, b2 = [], [], []
+    for _ in range(many):
+        c, t = fp8.quantize((0.02 * rows_of(rng, o, h)), 128, "e4m3")
+        w.append(c)
+        ws.append(t)
+        b2.append(bf16_np(0.05 * rng.standard_normal((N, R))))
+    A2 = bf16_np(rng.standard_normal((M, R))) if R else None
+    return a, s, w, ws, A2, (b2 if R else None)
+
+
+def t8(c, fmt="e4m3"):
+    return torch.from_numpy(np.ascontiguousarray(c)).to(DEV).view(DTYPES[fmt])
+
+
+def check_product(C, oracle, K, R):
+    """The matrix cores add the products of 8 neighbouring k aligned to the largest, p, of them and cut each off
+    below 2^-13 p; the groups of 8 are added in fp32.  So a group is off by less than 7 * 2^-13 p, p at most the sum
+    of the group's magnitudes: in all by less than 7 * 2^-13 S, and fp32 additions.  For the whole result: a product
+    of a group is cut by something between 0 and 2^-13 p, of either sign, whose square is 2^-26 p^2 / 3 on average, and
+    p^2 is at most the sum of the group's squares: a root mean square of at most 2^-13 sqrt(7 / 3) Q.  A rounding to bf16
+    is evenly spread up to 2^-8 of the value: a mean square of 2^-16 / 3 of its square."""
+    want, S, Q = oracle
+    check_within("C", C, want, np.abs(want) * BF16 * (1 + 2.0 ** -8) +
+                 S * (7 * 2.0 ** -13 + (128 + 2 * (K // 128 + 1) + R) * EPS32))
+    # each value's error over its own expectation, so that no large value stands for all
+    expected = want ** 2 * BF16 ** 2 / 3 + Q ** 2 * 2.0 ** -26 * 7 / 3
+    rms = np.sqrt(np.mean((f64(C) - want) ** 2 / np.maximum(expected, 1e-300)))
+    print(f"  rms: {rms:.3f} of its bound", flush=True)
+    assert rms <= 1 + 4 / np.sqrt(want.size)  # a mean over few values strays from its expectation
+
+
+SHAPES = [  # M, o, h
+    (1, 16, 16), (1, 272, 400), (1, 1024, 4096), (2, 144, 528), (5, 400, 272), (16, 528, 1040), (17, 512, 512),
+    (31, 272, 2064), (33, 1040, 656), (64, 256, 384), (65, 384, 256), (100, 144, 144), (128, 128, 128),
+    (129, 160, 1296), (255, 400, 272), (257, 272, 528), (513, 784, 400), (700, 2064, 1040),
+]
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("R,fmt", [(0, "e4m3"), (16, "e4m3"), (48, "e5m2"), (256, "e4m3")])
+@pytest.mark.parametrize("M,o,h", SHAPES)
+def test_matmul(M, o, h, R, fmt, transpose):
+    a, s, w, ws, A2, B2 = product_case(M * 5 + o + h, M, o, h, transpose, R, fmt)
+    want = fp8.matmul(a, s, fmt, w[0], ws[0], transpose, f64(A2) if R else None, f64(B2[0]) if R else None)
+    args = (t8(a, fmt), torch.from_numpy(s).to(DEV), t8(w[0]), torch.from_numpy(ws[0]).to(DEV), transpose,
+            A2.to(DEV) if R else None, B2[0].to(DEV) if R else None)
+    C = nf4.fp8_matmul(*args)
+    check_product(C, want, h if not transpose else o, R)
+    assert torch.equal(nf4.fp8_matmul(*args).view(torch.int16), C.view(torch.int16))
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_matmul_zero_blocks_and_nan(transpose):
+    # a zero row and zero weight blocks give exact zeros; a NaN stays in its row
+    a, s, w, ws, _, _ = product_case(3, 40, 272, 272, transpose, 0, "e4m3")
+    a[7] = 0
+    w0 = np.zeros_like(w[0])
+    z = nf4.fp8_matmul(t8(a), torch.from_numpy(s).to(DEV), t8(w0), torch.from_numpy(ws[0]).to(DEV), transpose)
+    assert torch.all(z == 0)
+    a[9, 3] = 0x7F
+    C = nf4.fp8_matmul(t8(a), torch.from_numpy(s).to(DEV), t8(w[0]), torch.from_numpy(ws[0]).to(DEV), transpose)
+    bad = torch.isnan(C).any(1).cpu()
+    assert bad[9] and int(bad.sum()) == 1 and torch.isnan(C[9]).all() and torch.all(C[7] == 0)
+
+
+GROUPED = [  # counts, rows before the first and behind the last
+    ([5], 0, 0), ([0, 7, 0, 1], 0, 3), ([130, 0, 1, 64, 17], 2, 5), ([1] * 70, 0, 0), ([0] * 66 + [3], 1, 1),
+    ([300, 5, 129, 0, 0, 40], 0, 9), ([0, 0], 0, 4),
+]
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("o,h,R,fmt", [(144, 272, 0, "e4m3"), (272, 144, 32, "e5m2"), (400, 656, 16, "e4m3")])
+@pytest.mark.parametrize("counts,before,after", GROUPED)
+def test_matmul_grouped(counts, before, after, o, h, R, fmt, transpose):
+    E, M = len(counts), before + sum(counts) + after
+    a, s, w, ws, A2, B2 = product_case(E + M, M, o, h, transpose, R, fmt, E)
+    N = h if transpose else o
+    ends = before + np.concatenate([[0], np.cumsum(counts)])
+    offsets = torch.from_numpy(ends.astype(np.int32)).to(DEV)
+    out = torch.full((M, N), 3.0, dtype=torch.bfloat16, device=DEV)
+    args = (t8(a, fmt), torch.from_numpy(s).to(DEV), t8(np.stack(w)), torch.from_numpy(np.stack(ws)).to(DEV), offsets,
+            transpose, A2.to(DEV) if R else None, torch.stack(B2).to(DEV) if R else None)
+    nf4.fp8_matmul_grouped(*args, out=out)
+    for e in range(E):
+        r = slice(ends[e], ends[e + 1])
+        if counts[e]:
+            want = fp8.matmul(a[r], s[r], fmt, w[e], ws[e], transpose, f64(A2[r]) if R else None,
+                              f64(B2[e]) if R else None)
+            check_product(out[r], want, h if not transpose else o, R)
+    rest = torch.cat([out[:ends[0]], out[ends[-1]:]])
+    assert torch.all(rest == 3.0)
+
+
+def test_matmul_grouped_offsets_outside():
+    # offsets below 0 and above M are taken as 0 and M
+    a, s, w, ws, _, _ = product_case(9, 20, 144, 272, False, 0, "e4m3", 3)
+    args = (t8(a), torch.from_numpy(s).to(DEV), t8(np.stack(w)), torch.from_numpy(np.stack(ws)).to(DEV))
+    wide = torch.tensor([-5, 8, 8, 1000], dtype=torch.int32, device=DEV)
+    good = torch.tensor([0, 8, 8, 20], dtype=torch.int32, device=DEV)
+    assert torch.equal(nf4.fp8_matmul_grouped(*args, wide), nf4.fp8_matmul_grouped(*args, good))
+
+
+def test_empty():
+    a = torch.empty(0, 272, dtype=torch.float8_e4m3fn, device=DEV)
+    s = torch.empty(0, 3, device=DEV)
+    W, ws = nf4.fp8_quantize(torch.randn(144, 272, device=DEV), 128)
+    assert nf4.fp8_matmul(a, s, W, ws).shape == (0, 144)
+    X = torch.empty(0, 272, dtype=torch.bfloat16, device=DEV)
+    c, sc = nf4.fp8_quantize(X)
+    assert c.shape == (0, 272) and sc.shape == (0, 3)
+    w = torch.ones(272, dtype=torch.bfloat16, device=DEV)
+    assert nf4.rmsnorm_fwd(X, w)[0].shape == (0, 272)
+    dX, dw = nf4.rmsnorm_bwd(X, X, w, torch.empty(0, device=DEV))
+    assert dX.shape == (0, 272) and torch.all(dw == 0)
+
+
+# ---------------------------------------------------------------------------------------------------------
+# together, captured, refused
+# ---------------------------------------------------------------------------------------------------------
+
+def layer(x, res, w, W, ws, L1, L2, s, dY, dH):
+    """Norm, frozen 8-bit linear with an adapter, and both gradients, as a training step makes them."""
+    y, h, codes, scales, rstd = nf4.rmsnorm_fwd(x, w, 1e-6, res, want_y=True, want_fp8=True, want_rstd=True)
+    T = y @ L1
+    Y = nf4.fp8_matmul(codes, scales, W, ws, A2=(s * T.float()).to(torch.bfloat16), B2=L2.t().contiguous())
+    G = (s * (dY.float() @ L2.float().t())).to(torch.bfloat16)
+    dq, ds = nf4.fp8_quantize(dY, 1, torch.float8_e5m2)
+    dy = nf4.fp8_matmul(dq, ds, W, ws, True, G, L1)
+    dX, dw = nf4.rmsnorm_bwd(dy, h, w, rstd, dH)
+    return Y, dX, dw
+
+
+def layer_case(M=200, o=400, h=272, r=16):
+    rng = np.random.default_rng(5)
+    t = lambda a: bf16_np(a).to(DEV)
+    W, ws = nf4.fp8_quantize(torch.from_numpy((0.05 * rng.standard_normal((o, h))).astype(np.float32)).to(DEV), 128)
+    return (t(rows_of(rng, M, h)), t(rows_of(rng, M, h)), t(1 + 0.1 * rng.standard_normal(h)), W, ws,
+            t(0.05 * rng.standard_normal((h, r))), t(0.05 * rng.standard_normal((r, o))), 2.0,
+            t(1e-3 * rng.standard_normal((M, o))), t(1e-3 * rng.standard_normal((M, h))))
+
+
+def test_layer_forward_and_gradient():
+    x, res, w, W, ws, L1, L2, s, dY, dH = layer_case()
+    Y, dX, dw = layer(x, res, w, W, ws, L1, L2, s, dY, dH)
+    h = f64((x.float() + res.float()).to(torch.bfloat16))
+    y, r = fp8.rmsnorm(h, f64(w), 1e-6)
+    Wd = f64(nf4.fp8_dequantize(W, ws, 128))
+    B = f64(L1) @ f64(L2) * s
+    Yw = y @ (Wd.T + B)
+    # 8-bit activations: each rounded by at most 2^-4, independent signs; relative rms of uniform rounding 2^-4 / sqrt(3)
+    rms = lambda g, v: np.sqrt(np.mean((f64(g) - v) ** 2) / np.mean(v ** 2))
+    assert rms(Y, Yw) < 2.0 ** -4
+    dyw = f64(dY) @ (Wd + B.T)
+    dxw, dww = fp8.rmsnorm_grad(dyw, h, f64(w), r, f64(dH))
+    assert rms(dX, dxw) < 2.0 ** -3 and rms(dw, dww) < 2.0 ** -3
+
+
+def test_layer_captured_and_replayed():
+    args = layer_case()
+    eager = layer(*args)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            layer(*args)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = layer(*args)
+    for k in range(4):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, eager):
+            assert torch.equal(a, b), k
+        again = layer(*args)  # eager work between the replays
+        assert all(torch.equal(a, b) for a, b in zip(again, eager))
+
+
+def test_another_stream():
+    args = layer_case(M=130)
+    want = layer(*args)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = layer(*args)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_binding_refuses():
+    x = torch.randn(8, 272, device=DEV)
+    a, s = nf4.fp8_quantize(x)
+    W, ws = nf4.fp8_quantize(torch.randn(144, 272, device=DEV), 128)
+    b = x.to(torch.bfloat16)
+    w = torch.ones(272, dtype=torch.bfloat16, device=DEV)
+    off = torch.tensor([0, 4, 8], dtype=torch.int32, device=DEV)
+    W2, ws2 = torch.stack([W.view(torch.uint8)] * 2).view(torch.float8_e4m3fn), torch.stack([ws] * 2)
+    r = torch.ones(8, device=DEV)
+    A2, B2 = torch.zeros(8, 16, dtype=torch.bfloat16, device=DEV), torch.zeros(144, 16, dtype=torch.bfloat16, device=DEV)
+    bad = [
+        lambda: nf4.fp8_quantize(x.half()), lambda: nf4.fp8_quantize(x.cpu()), lambda: nf4.fp8_quantize(x.t()),
+        lambda: nf4.fp8_quantize(x, 1, torch.float16), lambda: nf4.fp8_quantize(x, 1, scales=s[:4]),
+        lambda: nf4.fp8_quantize(x, 1, codes=a.view(torch.uint8)),
+        lambda: nf4.fp8_dequantize(x, s), lambda: nf4.fp8_dequantize(a, ws), lambda: nf4.fp8_dequantize(a, s, out=b),
+        lambda: nf4.fp8_matmul(a, ws, W, ws), lambda: nf4.fp8_matmul(a, s, W, ws, True),
+        lambda: nf4.fp8_matmul(a, s, W.view(torch.float8_e5m2), ws), lambda: nf4.fp8_matmul(x, s, W, ws),
+        lambda: nf4.fp8_matmul(a, s, W, ws, A2=A2), lambda: nf4.fp8_matmul(a, s, W, ws, A2=A2, B2=B2.t()),
+        lambda: nf4.fp8_matmul(a, s, W, ws, out=b), lambda: nf4.fp8_matmul(a[:, ::2], s, W, ws),
+        lambda: nf4.fp8_matmul_grouped(a, s, W, ws, off), lambda: nf4.fp8_matmul_grouped(a, s, W2, ws2, off.long()),
+        lambda: nf4.fp8_matmul_grouped(a, s, W2, ws2, off[:2]),
+        lambda: nf4.fp8_matmul_grouped(a, s, W2, ws2, off, A2=A2, B2=B2),
+        lambda: nf4.rmsnorm_fwd(x, w), lambda: nf4.rmsnorm_fwd(b, w.float()), lambda: nf4.rmsnorm_fwd(b, w, residual=x),
+        lambda: nf4.rmsnorm_fwd(b, w, outs=(None,) * 5), lambda: nf4.rmsnorm_bwd(b, b, w, r[:4]),
+        lambda: nf4.rmsnorm_bwd(b, b, w, r, dH=x), lambda: nf4.rmsnorm_bwd(b, b, w, r, ws=x),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"call {i} was accepted")
+    status = [
+        (lambda: nf4.fp8_quantize(x, 2), nf4.NF4_ERR_ARG), (lambda: nf4.fp8_quantize(x[:, :24].contiguous()), nf4.NF4_ERR_SHAPE),
+        (lambda: nf4.fp8_matmul(a, s, W, ws, A2=A2[:, :8].contiguous(), B2=B2[:, :8].contiguous()), nf4.NF4_ERR_SHAPE),
+        (lambda: nf4.rmsnorm_fwd(b, w, -1.0), nf4.NF4_ERR_ARG), (lambda: nf4.rmsnorm_fwd(b, w, want_y=False), nf4.NF4_ERR_NULL),
+        (lambda: nf4.rmsnorm_fwd(b[:, :24].contiguous(), w[:24].contiguous()), nf4.NF4_ERR_SHAPE),
+        (lambda: nf4.rmsnorm_fwd(b, w, outs=(b, None, None, None, None)), nf4.NF4_ERR_ALIAS),
+        (lambda: nf4.rmsnorm_bwd(b, b, w, r, ws=torch.empty(16, dtype=torch.uint8, device=DEV)), nf4.NF4_ERR_WORKSPACE),
+    ]
+    for i, (f, want) in enumerate(status):
+        with pytest.raises(nf4.NF4Error) as err:
+            f()
+        assert err.value.status == want, i
