@@ -90,28 +90,56 @@ __device__ __forceinline__ bool find_tile(const Args& p, int bm, int t, int& e, 
   return false;
 }
 
-template <int BM, int BN, int WGM, int WGN, bool TR, bool E5M2, bool GROUPED>
-__global__ __launch_bounds__(WGM* WGN * 64) void k_fp8_gemm(Args p) {
-  constexpr int NW = WGM * WGN;
-  constexpr int TM = BM / WGM, TN = BN / WGN;
-  constexpr int MI = TM / 16, NI = TN / 16;
-  constexpr int AI = BM / 8 / NW;  // 1 KB copies per wave and tile
-  constexpr int BI = BN / 8 / NW;
-  __shared__ __attribute__((aligned(1024))) uint8_t As0[BM * 128];
-  __shared__ __attribute__((aligned(1024))) uint8_t As1[BM * 128];
-  __shared__ __attribute__((aligned(1024))) uint8_t Bs0[BN * 128];
-  __shared__ __attribute__((aligned(1024))) uint8_t Bs1[BN * 128];
+constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8); }
+
+// The tile of this workgroup.  Workgroups are dealt to the 8 XCDs round-robin;
+// ids are renumbered so that an XCD's run of 32 (as many as it holds at once)
+// covers 4 row panels by 8 column tiles, which share those 12 panels in its L2.
+// A grouped product does not use the last of its tiles, so there the runs of 32
+// go to the XCDs in turn; a dense one gives each XCD one stretch.
+__device__ __forceinline__ void tile_of(bool grouped, int tiles_m, int tiles_n, int& tm, int& tn) {
+  constexpr int G = 4, U = 32;
+  const int nwg = tiles_m * tiles_n;
+  int id = blockIdx.x;
+  if (grouped) {
+    if (id < nwg / (8 * U) * (8 * U)) id = ((id >> 3) / U * 8 + (id & 7)) * U + (id >> 3) % U;
+  } else if ((nwg & 7) == 0) {
+    id = (id & 7) * (nwg >> 3) + (id >> 3);
+  }
+  const int grp = id / (G * tiles_n);
+  const int gm = min(G, tiles_m - G * grp);
+  const int gi = id - G * grp * tiles_n;
+  tm = G * grp + gi % gm;
+  tn = gi / gm;
+}
+
+template <int NI, bool TR, bool E5M2, bool GROUPED>
+__global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
+  constexpr int WGM = NI / 2, NW = 8;  // 16 / NI waves beside each other
+  constexpr int BM = 64 * WGM, BN = 256;
+  constexpr int MI = 4;
+  constexpr int WN = 16 * NI;  // columns of a wave
+  constexpr int HW = WN / 2;   // and of a half of them
+  constexpr int AI = BM / 64;  // 1 KB copies of A per wave
+  __shared__ __attribute__((aligned(1024))) uint8_t A0[BM * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t A1[BM * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t W00[BN * 64];  // W<step % 2><half>
+  __shared__ __attribute__((aligned(1024))) uint8_t W01[BN * 64];
+  __shared__ __attribute__((aligned(1024))) uint8_t W10[BN * 64];
+  __shared__ __attribute__((aligned(1024))) uint8_t W11[BN * 64];
+  __shared__ __attribute__((aligned(1024))) float S0[NW * 64];
+  __shared__ __attribute__((aligned(1024))) float S1[NW * 64];
+  constexpr int SR = BM / NW;  // A scales a wave copies
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % WGM, wn = wave / WGM;
   const int g = lane >> 4, l16 = lane & 15;
 
-  int lid = blockIdx.x;
-  const int nwg = gridDim.x;
-  if ((nwg & 7) == 0) lid = (lid & 7) * (nwg >> 3) + (lid >> 3);
-  const int tm = lid / p.tiles_n;
-  const int n0 = (lid - tm * p.tiles_n) * BN;
+  const int tiles_m = (int)gridDim.x / p.tiles_n;
+  int tm, tn;
+  tile_of(GROUPED, tiles_m, p.tiles_n, tm, tn);
+  const int n0 = tn * BN;
   const int N = p.N, K = p.K;
   const int KB = (K + 127) / 128;
   const int NB = (N + 127) / 128;
@@ -127,98 +155,103 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_fp8_gemm(Args p) {
   const uint8_t* W = p.W + (GROUPED ? (int64_t)e * N * K : 0);
   const float* ws = p.ws + (GROUPED ? (int64_t)e * NB * KB : 0);
 
-  // global -> LDS copies.  LDS rows are 128 bytes of one row's k (A, and B as
-  // stored) or BN bytes of one k (TR), in 16-byte chunks whose place is the
-  // chunk's number XOR the row's low bits, so a wave's fragment reads spread
-  // over the banks.  Rows past the tile and, in the last step, k past K read
-  // as zero through the buffer range.
   const __amdgpu_buffer_rsrc_t ar = make_rsrc(p.A + m0 * K, (uint32_t)((int64_t)mrows * K));
-  uint32_t a_off[AI], b_off[BI];
-  int a_k[AI];
-#pragma unroll
-  for (int i = 0; i < AI; ++i) {
-    const int r = (wave * AI + i) * 8 + (lane >> 3);
-    a_k[i] = ((lane & 7) ^ (r & 7)) * 16;
-    a_off[i] = (uint32_t)(r * K + a_k[i]);
-  }
-  constexpr int SL = BN / 16;  // 16-byte chunks of one k row (TR)
-#pragma unroll
-  for (int i = 0; i < BI; ++i) {
-    if constexpr (TR) {
-      const int o = (wave * BI + i) * 64 + lane;
-      const int r = o / SL;
-      const int col = n0 + ((o % SL) ^ (r & (SL - 1) & 15)) * 16;
-      b_off[i] = col < N ? (uint32_t)(r * N + col) : kOOB;
-    } else {
-      const int r = (wave * BI + i) * 8 + (lane >> 3);
-      b_off[i] = (uint32_t)(r * K + ((lane & 7) ^ (r & 7)) * 16);
-    }
-  }
-  const int nrows = min(BN, N - n0);
-  auto copy = [&](int kt, uint8_t* Ad, uint8_t* Bd) {
-    const bool last = (kt + 1) * 128 > K;
-    __amdgpu_buffer_rsrc_t br;
-    if constexpr (TR) br = make_rsrc(W + (int64_t)kt * 128 * N, (uint32_t)(min(128, K - kt * 128) * (int64_t)N));
-    else br = make_rsrc(W + (int64_t)n0 * K, (uint32_t)((int64_t)nrows * K));
-#pragma unroll
-    for (int i = 0; i < AI; ++i) {
-      const uint32_t off = last && kt * 128 + a_k[i] >= K ? kOOB : a_off[i];
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (lds_ptr_t)(Ad + (wave * AI + i) * 1024), 16, off, kt * 128, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < BI; ++i) {
-      uint32_t off = b_off[i];
-      if constexpr (!TR) {
-        const int r = (wave * BI + i) * 8 + (lane >> 3);
-        if (last && kt * 128 + ((lane & 7) ^ (r & 7)) * 16 >= K) off = kOOB;
-      }
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(br, (lds_ptr_t)(Bd + (wave * BI + i) * 1024), 16, off,
-                                               TR ? 0 : kt * 128, 0, 0);
-    }
-  };
-
-  // A scales of this lane's rows, one step ahead
   const __amdgpu_buffer_rsrc_t sr = make_rsrc(p.as + m0 * KB, (uint32_t)((int64_t)mrows * KB * 4));
-  float sa[MI];
-  auto load_scales = [&](int kt) {
+  const int nrows = min(BN, N - n0);
+  // The buffer range covers the rows that exist, and its check takes the scalar
+  // offset in, so one lane offset serves all of a wave's copies.
+  const int c_row = wave * 8 + (lane >> 3);          // of copy i: plus i * 64
+  const int c_chunk = (lane & 7) ^ (c_row & 7);      // the 16-byte chunk that goes to this lane's place
+  const uint32_t a_off = (uint32_t)(c_row * K + c_chunk * 16);
+  // half h of a W tile holds columns wn * WN + h * HW .. + HW - 1 of every wave
+  // column, 128 in all
+  uint32_t w_off;
+  int col0 = 0;
+  constexpr int CH = HW / 16;  // chunks of a wave column's half (TR)
+  if constexpr (TR) {
+    col0 = n0 + (c_chunk / CH) * WN + (c_chunk % CH) * 16;  // + h * HW
+    w_off = (uint32_t)(c_row * N + col0);
+  } else {
+    w_off = (uint32_t)(((c_row / HW) * WN + c_row % HW) * K + c_chunk * 16);  // copy 1: + 128 rows
+  }
+  const uint32_t s_off = lane < SR ? (uint32_t)((wave * SR + lane) * KB * 4) : kOOB;
+  // Steps behind the last one load its tile once more, so the loop has no
+  // branches and every wait counts the same loads.
+  auto copy_a = [&](int kt, uint8_t* Ad, float* Sd) {
+    kt = min(kt, KB - 1);
+    const uint32_t off = kt * 128 + c_chunk * 16 < K ? a_off : kOOB;
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
-      sa[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                            sr, (uint32_t)((wm * TM + i * 16 + l16) * KB * 4), kt * 4, 0));
+    for (int i = 0; i < AI; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (lds_ptr_t)(Ad + (i * NW + wave) * 1024), 16, off,
+                                               kt * 128 + i * 64 * K, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (lds_ptr_t)(Sd + wave * 64), 4, s_off, kt * 4, 0, 0);
   };
-  const int nb = (n0 + wn * TN) >> 7;  // a wave's columns lie within one block
-  auto wscale = [&](int kt) -> float {
-    if (nb >= NB) return 0.f;
-    return TR ? ws[(int64_t)kt * NB + nb] : ws[(int64_t)nb * KB + kt];
+  auto copy_w = [&](int kt, int h, uint8_t* Wd) {
+    kt = min(kt, KB - 1);
+    if constexpr (TR) {
+      const __amdgpu_buffer_rsrc_t wr =
+          make_rsrc(W + (int64_t)kt * 128 * N, (uint32_t)(min(128, K - kt * 128) * (int64_t)N));
+      const uint32_t off = col0 + h * HW < N ? w_off : kOOB;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_ptr_t)(Wd + (i * NW + wave) * 1024), 16, off,
+                                                 h * HW + i * 64 * N, 0, 0);
+    } else {
+      const __amdgpu_buffer_rsrc_t wr = make_rsrc(W + (int64_t)n0 * K, (uint32_t)((int64_t)nrows * K));
+      const uint32_t off = kt * 128 + c_chunk * 16 < K ? w_off : kOOB;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_ptr_t)(Wd + (i * NW + wave) * 1024), 16, off,
+                                                 kt * 128 + (i * 128 + h * HW) * K, 0, 0);
+    }
+  };
+  const int nb = min((n0 + wn * WN) >> 7, NB - 1);
+  auto load_ws = [&](int kt) -> float {
+    const int k = min(kt + lane, KB - 1);
+    return TR ? ws[(int64_t)k * NB + nb] : ws[(int64_t)nb * KB + k];
   };
 
-  auto frag_a = [&](const uint8_t* Ab, int i) -> i32x8 {
-    const int r = wm * TM + i * 16 + l16;
-    const u32x4 lo = *(const u32x4*)(Ab + r * 128 + ((g ^ (r & 7)) << 4));
-    const u32x4 hi = *(const u32x4*)(Ab + r * 128 + (((g + 4) ^ (r & 7)) << 4));
-    return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-  };
-  // k of a lane: 16 g .. + 15 and 64 + 16 g .. + 15, for both operands
-  auto frag_b = [&](uint8_t* Bb, int i) -> i32x8 {
+  // LDS places of this lane's fragment pieces; subtile i adds 2 KB, or (TR) flips
+  // the slot bits
+  uint32_t f_lo, f_hi;
+  if constexpr (TR) {
+    const int x = l16 >> 1;
+    f_lo = (uint32_t)((16 * g + x) * 128 + (((wn * CH) ^ x) << 4) + (l16 & 1) * 8);
+    f_hi = f_lo + 8 * 128;
+  } else {
+    f_lo = (uint32_t)((wn * HW + l16) * 128 + ((g ^ (l16 & 7)) << 4));
+    f_hi = f_lo ^ 64;
+  }
+  auto frag_w = [&](uint8_t* Wb, int i) -> i32x8 {  // i: 0 .. NI / 2 - 1 of the half
     if constexpr (TR) {
-      // ds_read_b64_tr_b8: in each group of 16 lanes, lane 2e + q points at 8 bytes
-      // of row e, columns 8q .. 8q + 7, and lane j receives column j of the 8 rows
       i32x8 f;
-      const int slot = (wn * TN + i * 16) >> 4;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int r = (q >> 1) * 64 + 16 * g + (q & 1) * 8 + (l16 >> 1);
-        uint8_t* at = Bb + r * BN + ((slot ^ (r & (SL - 1) & 15)) << 4) + (l16 & 1) * 8;
-        const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2_ptr)at);
+        const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+            (lds_i32x2_ptr)(Wb + (f_lo ^ (uint32_t)(i << 4)) + (q & 1) * 8 * 128 + (q >> 1) * 64 * 128));
         f[2 * q] = v.x;
         f[2 * q + 1] = v.y;
       }
       return f;
     } else {
-      const int r = wn * TN + i * 16 + l16;
-      const u32x4 lo = *(const u32x4*)(Bb + r * 128 + ((g ^ (r & 7)) << 4));
-      const u32x4 hi = *(const u32x4*)(Bb + r * 128 + (((g + 4) ^ (r & 7)) << 4));
+      const u32x4 lo = *(const u32x4*)(Wb + f_lo + i * 2048);
+      const u32x4 hi = *(const u32x4*)(Wb + f_hi + i * 2048);
       return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+    }
+  };
+  const uint32_t fa_lo = (uint32_t)((wm * 64 + l16) * 128 + ((g ^ (l16 & 7)) << 4));
+  const uint32_t fa_hi = fa_lo ^ 64;
+  auto frag_a = [&](const uint8_t* Ab, int i) -> i32x8 {
+    const u32x4 lo = *(const u32x4*)(Ab + fa_lo + i * 2048);
+    const u32x4 hi = *(const u32x4*)(Ab + fa_hi + i * 2048);
+    return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+  };
+  // A scale of row r of the tile: copied by wave r / SR, lane r % SR
+  auto read_s = [&](const float* Sb, float (&s)[MI]) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int r = wm * 64 + i * 16 + l16;
+      s[i] = Sb[(r / SR) * 64 + r % SR];
     }
   };
 
@@ -228,70 +261,130 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_fp8_gemm(Args p) {
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-  auto step = [&](int kt, uint8_t* Ac, uint8_t* Bc, uint8_t* An, uint8_t* Bn) {
-    __builtin_amdgcn_s_waitcnt(0);  // this wave's copies of tile kt have landed
-    __syncthreads();                // everyone's have, and nobody reads tile kt - 1 any more
-    float s[MI];
-    const float w = wscale(kt);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) s[i] = sa[i] * w;
-    if (kt + 1 < KB) {
-      copy(kt + 1, An, Bn);
-      load_scales(kt + 1);
-    }
-    i32x8 fb[NI];
-#pragma unroll
-    for (int j = 0; j < NI; ++j) fb[j] = frag_b(Bc, j);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const i32x8 fa = frag_a(Ac, i);
-#pragma unroll
-      for (int j = 0; j < NI; ++j) {
-        const floatx4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            fb[j], fa, floatx4{0.f, 0.f, 0.f, 0.f}, 0, E5M2 ? 1 : 0, 0, 0, 0, 0);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(d[v], s[i], acc[i][j][v]);
-      }
-    }
+  // A step is NI groups of 4 MFMAs, one group per 16 columns, in two halves with a
+  // barrier before each.  The group's W fragment is read during the group before
+  // it; the next step's A fragments replace this step's as the last group is done
+  // with them; the multiply-adds of a group run beside the next one's MFMAs.
+  // Copies of step kt:   before the 2nd half: A and scales (kt + 2), W (kt + 2) first half
+  //                      before the 1st half: W (kt + 1) second half
+  // each into memory whose readers the barrier has seen through, a step and more
+  // ahead of its own.
+  auto barrier = [&](auto outstanding) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(wait_vm(decltype(outstanding)::value));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   };
-  copy(0, As0, Bs0);
-  load_scales(0);
-  for (int kt = 0; kt < KB; kt += 2) {
-    step(kt, As0, Bs0, As1, Bs1);
-    if (kt + 1 < KB) step(kt + 1, As1, Bs1, As0, Bs0);
+  constexpr std::integral_constant<int, 2> kHalf0{};  // the copies issued in a 1st half
+  constexpr std::integral_constant<int, 3 + AI> kHalf1{};  // and in a 2nd half
+  i32x8 fa[MI], fw[2];
+  floatx4 d[2][MI];
+  float s[MI], sc[MI];
+  float wsr = load_ws(0);
+  auto fold = [&](int j, floatx4 (&dd)[MI]) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(dd[i][v], sc[i], acc[i][j][v]);
+  };
+  auto step = [&](int kt, uint8_t* Ac, uint8_t* An, uint8_t* Wc0, uint8_t* Wc1, uint8_t* Wn0, uint8_t* Wn1, float* Sc,
+                  const float* Sn) {
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      if (j == 0) {
+        barrier(kHalf1);
+        copy_w(kt + 1, 1, Wn1);
+      }
+      if (j == NI / 2) {
+        barrier(kHalf0);
+        copy_w(kt + 2, 0, Wc0);
+        copy_a(kt + 2, Ac, Sc);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      fw[(j + 1) & 1] = j + 1 < NI / 2 ? frag_w(Wc0, j + 1) : j + 1 < NI ? frag_w(Wc1, j + 1 - NI / 2) : frag_w(Wn0, 0);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        d[j & 1][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[j & 1], fa[i], floatx4{0.f, 0.f, 0.f, 0.f}, 0,
+                                                                       E5M2 ? 1 : 0, 0, 0, 0, 0);
+        if (j == NI - 1) fa[i] = frag_a(An, i);
+      }
+      // the group before this one (of the step before: its scales are still in sc)
+      fold((j + NI - 1) % NI, d[(j + 1) & 1]);
+      if (j == 0) {
+        const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wsr), kt & 63));
+#pragma unroll
+        for (int i = 0; i < MI; ++i) sc[i] = s[i] * w;
+      }
+      if (j == NI - 1) read_s(Sn, s);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) asm volatile("" : "+v"(acc[i][(j + NI - 1) % NI]));
+      __builtin_amdgcn_sched_group_barrier(0x100, TR ? 4 : 2, 0);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (((kt + 1) & 63) == 0) wsr = load_ws(kt + 1);
+  };
+  copy_w(0, 0, W00);
+  copy_w(0, 1, W01);
+  copy_a(0, A0, S0);
+  copy_w(1, 0, W10);
+  copy_a(1, A1, S1);
+  barrier(kHalf1);
+  fw[0] = frag_w(W00, 0);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) fa[i] = frag_a(A0, i);
+  read_s(S0, s);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    sc[i] = 0.f;
+    d[1][i] = floatx4{0.f, 0.f, 0.f, 0.f};
   }
+  int kt = 0;
+  for (; kt + 2 <= KB; kt += 2) {
+    step(kt, A0, A1, W00, W01, W10, W11, S0, S1);
+    step(kt + 1, A1, A0, W10, W11, W00, W01, S1, S0);
+  }
+  if (kt < KB) step(kt, A0, A1, W00, W01, W10, W11, S0, S1);
+  fold(NI - 1, d[(NI - 1) & 1]);
+  __builtin_amdgcn_s_waitcnt(wait_vm(0));
 
-  // the low-rank term: R columns in steps of 32, fragments straight from memory
   if (p.R) {
     const __amdgpu_buffer_rsrc_t a2 = make_rsrc(p.A2 + m0 * p.R, (uint32_t)((int64_t)mrows * p.R * 2));
     const __amdgpu_buffer_rsrc_t b2 =
         make_rsrc(p.B2 + ((GROUPED ? (int64_t)e * N : 0) + n0) * p.R, (uint32_t)((int64_t)nrows * p.R * 2));
     for (int k0 = 0; k0 < p.R; k0 += 32) {
       const int k = k0 + 8 * g;
-      bf16x8 fb[NI];
+      bf16x8 fa[MI];
 #pragma unroll
-      for (int j = 0; j < NI; ++j)
-        fb[j] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(
-            b2, k < p.R ? (uint32_t)(((wn * TN + j * 16 + l16) * p.R + k) * 2) : kOOB, 0, 0));
+      for (int i = 0; i < MI; ++i)
+        fa[i] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(
+            a2, k < p.R ? (uint32_t)(((wm * 64 + i * 16 + l16) * p.R + k) * 2) : kOOB, 0, 0));
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const bf16x8 fa = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(
-            a2, k < p.R ? (uint32_t)(((wm * TM + i * 16 + l16) * p.R + k) * 2) : kOOB, 0, 0));
+      for (int j = 0; j < NI; ++j) {
+        const bf16x8 fbb = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(
+            b2, k < p.R ? (uint32_t)(((wn * WN + j * 16 + l16) * p.R + k) * 2) : kOOB, 0, 0));
 #pragma unroll
-        for (int j = 0; j < NI; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa, acc[i][j], 0, 0, 0);
+        for (int i = 0; i < MI; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fbb, fa[i], acc[i][j], 0, 0, 0);
       }
     }
   }
 
-  // epilogue: a lane holds row i * 16 + l16 and columns j * 16 + 4 g .. + 3 of the
-  // wave's tile; through the wave's own part of LDS to rows of 16-byte pieces
   __syncthreads();
-  constexpr int WB = TM * TN * 2;
-  constexpr int PA = BM * 128 / WB, PB = BN * 128 / WB;  // wave tiles that one buffer holds
-  static_assert(2 * PA + 2 * PB >= NW, "the result tile fits the operand buffers");
-  uint8_t* st = wave < PA ? As0 + wave * WB : wave < 2 * PA ? As1 + (wave - PA) * WB
-                : wave < 2 * PA + PB ? Bs0 + (wave - 2 * PA) * WB : Bs1 + (wave - 2 * PA - PB) * WB;
-  constexpr int PC = TN / 8;  // 16-byte pieces of a row
+  // the result tile of a wave in its own part of the operand buffers
+  constexpr int WB = 64 * WN * 2, PA = BM * 128 / WB, PW = 16384 / WB;
+  static_assert(2 * PA + 4 * PW >= NW, "the result tile fits");
+  uint8_t* st;
+  if (wave < PA) st = A0 + wave * WB;
+  else if (wave < 2 * PA) st = A1 + (wave - PA) * WB;
+  else {
+    const int q = wave - 2 * PA;
+    st = (q / PW == 0 ? W00 : q / PW == 1 ? W01 : q / PW == 2 ? W10 : W11) + (q % PW) * WB;
+  }
+  constexpr int PC = WN / 8;  // 16-byte pieces of a row
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -301,24 +394,24 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_fp8_gemm(Args p) {
       uint2 o;
       o.x = pack_bf16x2(acc[i][j][0], acc[i][j][1]);
       o.y = pack_bf16x2(acc[i][j][2], acc[i][j][3]);
-      *(uint2*)(st + r * (TN * 2) + ((piece ^ (r & (PC - 1))) << 4) + (g & 1) * 8) = o;
+      *(uint2*)(st + r * (WN * 2) + ((piece ^ (r & (PC - 1))) << 4) + (g & 1) * 8) = o;
     }
   __syncthreads();
 #pragma unroll
-  for (int q = 0; q < TM * PC / 64; ++q) {
+  for (int q = 0; q < PC; ++q) {
     const int o = q * 64 + lane;
     const int r = o / PC, piece = o % PC;
-    const int row = wm * TM + r;
-    const int n = n0 + wn * TN + piece * 8;
+    const int row = wm * 64 + r;
+    const int n = n0 + wn * WN + piece * 8;
     if (row < mrows && n < N)
-      *(u32x4*)(p.C + (m0 + row) * N + n) = *(const u32x4*)(st + r * (TN * 2) + ((piece ^ (r & (PC - 1))) << 4));
+      *(u32x4*)(p.C + (m0 + row) * N + n) = *(const u32x4*)(st + r * (WN * 2) + ((piece ^ (r & (PC - 1))) << 4));
   }
 }
 
 }  // namespace
 
 hipError_t launch_fp8_gemm(const Fp8Gemm& q, hipStream_t st) {
-  constexpr int BM = 128, BN = 128, NT = 256;
+  constexpr int BN = 256, NT = 512;
   Args p{};
   p.A = q.A;
   p.as = q.a_scales;
@@ -335,23 +428,33 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& q, hipStream_t st) {
   p.experts = q.experts;
   p.tiles_n = (p.N + BN - 1) / BN;
   const int KB = (p.K + 127) / 128;
-#define NF4K_GEMM(GR)                                                                                              \
-  do {                                                                                                             \
-    if (q.transpose) {                                                                                             \
-      if (q.a_e5m2) hipLaunchKernelGGL((k_fp8_gemm<BM, BN, 2, 2, true, true, GR>), gr, dim3(NT), 0, st, p);        \
-      else hipLaunchKernelGGL((k_fp8_gemm<BM, BN, 2, 2, true, false, GR>), gr, dim3(NT), 0, st, p);                \
-    } else {                                                                                                       \
-      if (q.a_e5m2) hipLaunchKernelGGL((k_fp8_gemm<BM, BN, 2, 2, false, true, GR>), gr, dim3(NT), 0, st, p);       \
-      else hipLaunchKernelGGL((k_fp8_gemm<BM, BN, 2, 2, false, false, GR>), gr, dim3(NT), 0, st, p);               \
-    }                                                                                                              \
+#define NF4K_FP8(NI, GR)                                                                                    \
+  do {                                                                                                      \
+    if (q.transpose) {                                                                                      \
+      if (q.a_e5m2) hipLaunchKernelGGL((k_fp8_wide<NI, true, true, GR>), gr, dim3(NT), 0, st, p);           \
+      else hipLaunchKernelGGL((k_fp8_wide<NI, true, false, GR>), gr, dim3(NT), 0, st, p);                   \
+    } else {                                                                                                \
+      if (q.a_e5m2) hipLaunchKernelGGL((k_fp8_wide<NI, false, true, GR>), gr, dim3(NT), 0, st, p);          \
+      else hipLaunchKernelGGL((k_fp8_wide<NI, false, false, GR>), gr, dim3(NT), 0, st, p);                  \
+    }                                                                                                       \
+  } while (0)
+#define NF4K_FP8_NI(GR)            \
+  do {                             \
+    if (ni == 8) NF4K_FP8(8, GR);  \
+    else if (ni == 4) NF4K_FP8(4, GR); \
+    else NF4K_FP8(2, GR);          \
   } while (0)
   if (q.experts) {
+    const int ni = fp8_tile_ni(std::max<int64_t>(1, q.M / q.experts), p.N, q.experts);
     // every expert's last tile may be partly filled
-    const int64_t tiles = q.M / BM + std::min<int64_t>(q.experts, q.M);
+    const int64_t tiles = q.M / (32 * ni) + std::min<int64_t>(q.experts, q.M);
+    if (tiles * p.tiles_n > (int64_t)0xFFFFFFFF / NT) return hipErrorInvalidValue;
     const dim3 gr((unsigned)(tiles * p.tiles_n));
-    NF4K_GEMM(true);
+    NF4K_FP8_NI(true);
     return hipGetLastError();
   }
+  const int ni = fp8_tile_ni(q.M, p.N, 1);
+  const int BM = 32 * ni;
   // at most 2^32 - 1 work-items a launch: more tiles run as ranges of row panels
   const int64_t tiles_m = (q.M + BM - 1) / BM;
   const int64_t panels = std::max<int64_t>(1, (int64_t)0xFFFFFFFF / NT / p.tiles_n);
@@ -363,12 +466,13 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& q, hipStream_t st) {
     p.C = q.C + r0 * p.N;
     p.M = std::min(panels * BM, q.M - r0);
     const dim3 gr((unsigned)(std::min(panels, tiles_m - t0) * p.tiles_n));
-    NF4K_GEMM(false);
+    NF4K_FP8_NI(false);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
-#undef NF4K_GEMM
+#undef NF4K_FP8_NI
+#undef NF4K_FP8
 }
 
 }  // namespace nf4k

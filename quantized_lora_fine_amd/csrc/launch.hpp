@@ -196,6 +196,10 @@ struct Fp8Gemm {
   int R;
   uint16_t* C;
 };
+// tile of a product with M rows (of each expert, on average) and N columns: ni
+// of 8, 4 or 2 for 256, 128 or 64 rows by 256 columns, whichever fills the
+// compute units in the least time
+int fp8_tile_ni(int64_t M, int N, int experts);
 NF4K_WEAK hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t st);
 
 }  // namespace nf4k

@@ -90,6 +90,24 @@ int rmsnorm_parts(int64_t M, int H) {
   return (int)(groups < 512 ? groups : 512);
 }
 
+int fp8_tile_ni(int64_t M, int N, int experts) {
+  // microseconds per 128 of the contraction for a full set of tiles on the 256
+  // compute units: 256 x 256 tiles (ni = 8), 128 x 256 (4) and 64 x 256 (2)
+  static const double cost[3] = {2.0, 1.22, 0.8};
+  int best = 8;
+  double least = 0;
+  for (int i = 0; i < 3; ++i) {
+    const int ni = 8 >> i, bm = 32 * ni;
+    const int64_t tiles = (M + bm - 1) / bm * ((N + 255) / 256) * experts;
+    const double t = (double)((tiles + 255) / 256) * cost[i];
+    if (i == 0 || t < least) {
+      least = t;
+      best = ni;
+    }
+  }
+  return best;
+}
+
 int error_batch_chunk(const int64_t* rows, const int64_t* cols, int32_t n, int32_t c0, int64_t* g0) {
   int k = 0;
   g0[0] = 0;
