@@ -154,8 +154,14 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle straight from torch's C layer: building the Stream object around it takes longer than
+# a launch
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
 
 
 def _need(t, dtype, shape, name: str):
@@ -503,6 +509,22 @@ FP8_BLOCK = 128
 FP8_FORMATS = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
 
 
+def _held(t, dtype, shape, dev: int, name: str):
+    """_need for a whole shape and a known current device, quick where the tensor is as it should be (a decoded token's
+    calls are bound by the host); returns the address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        _need(t, dtype, shape, name)
+    return t.data_ptr()
+
+
+def _matrix(t, name: str):
+    """(rows, cols) of a tensor of two dimensions; the rest is for the caller to check."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name}: expected a tensor of two dimensions")
+    return t.shape
+
+
 def _fp8_format(dtype, name: str) -> int:
     f = FP8_FORMATS.get(dtype)
     if f is None:
@@ -518,18 +540,23 @@ def fp8_quantize(X: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = torc
                  codes: torch.Tensor | None = None, scales: torch.Tensor | None = None):
     """nf4_fp8_quantize of a cuda bf16 or fp32 [rows][cols] tensor: (codes `dtype` [rows][cols], scales fp32).
     block_rows = 1: a scale per row and 128 columns, [rows][ceil(cols / 128)] (activations, gradients);
-    block_rows = 128: per 128 x 128 block, [ceil(rows / 128)][ceil(cols / 128)] (weights)."""
+    block_rows = 128: per 128 x 128 block, [ceil(rows / 128)][ceil(cols / 128)] (weights).  codes and scales may be
+    given (an expert's part of a stack of weights, say)."""
     f = _fp8_format(dtype, "dtype")
-    if not isinstance(X, torch.Tensor) or X.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("X: expected a bf16 or fp32 tensor")
-    rows, cols = _need(X, X.dtype, (None, None), "X").shape
+    rows, cols = _matrix(X, "X")
+    bf16 = X.dtype is torch.bfloat16
+    if not bf16 and X.dtype is not torch.float32:
+        raise ValueError(f"X: expected bf16 or fp32, got {X.dtype}")
+    dev = torch.cuda.current_device()
+    x = _held(X, X.dtype, (rows, cols), dev, "X")
     sshape = (rows if block_rows == 1 else _blocks(rows), _blocks(cols))
-    codes = _need(codes, dtype, (rows, cols), "codes") if codes is not None else \
-        torch.empty(rows, cols, dtype=dtype, device=X.device)
-    scales = _need(scales, torch.float32, sshape, "scales") if scales is not None else \
-        torch.empty(sshape, dtype=torch.float32, device=X.device)
-    _check(_lib.nf4_fp8_quantize(X.data_ptr(), X.dtype == torch.bfloat16, rows, cols, f, block_rows,
-                                 codes.data_ptr(), scales.data_ptr(), _stream()), "nf4_fp8_quantize")
+    if codes is None:
+        codes = torch.empty((rows, cols), dtype=dtype, device=X.device)
+    if scales is None:
+        scales = torch.empty(sshape, dtype=torch.float32, device=X.device)
+    _check(_lib.nf4_fp8_quantize(x, bf16, rows, cols, f, block_rows, _held(codes, dtype, (rows, cols), dev, "codes"),
+                                 _held(scales, torch.float32, sshape, dev, "scales"), _raw_stream(dev)),
+           "nf4_fp8_quantize")
     return codes, scales
 
 
@@ -537,31 +564,38 @@ def fp8_dequantize(codes: torch.Tensor, scales: torch.Tensor, block_rows: int = 
                    out: torch.Tensor | None = None) -> torch.Tensor:
     """nf4_fp8_dequantize into fp32 (or bf16) [rows][cols], into `out` when given."""
     f = _fp8_format(getattr(codes, "dtype", None), "codes")
-    rows, cols = _need(codes, codes.dtype, (None, None), "codes").shape
-    _need(scales, torch.float32, (rows if block_rows == 1 else _blocks(rows), _blocks(cols)), "scales")
+    rows, cols = _matrix(codes, "codes")
+    dev = torch.cuda.current_device()
+    c = _held(codes, codes.dtype, (rows, cols), dev, "codes")
+    s = _held(scales, torch.float32, (rows if block_rows == 1 else _blocks(rows), _blocks(cols)), dev, "scales")
     odt = torch.bfloat16 if bf16 else torch.float32
-    out = _need(out, odt, (rows, cols), "out") if out is not None else \
-        torch.empty(rows, cols, dtype=odt, device=codes.device)
-    _check(_lib.nf4_fp8_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, f, block_rows, out.data_ptr(),
-                                   1 if bf16 else 0, _stream()), "nf4_fp8_dequantize")
+    if out is None:
+        out = torch.empty((rows, cols), dtype=odt, device=codes.device)
+    _check(_lib.nf4_fp8_dequantize(c, s, rows, cols, f, block_rows, _held(out, odt, (rows, cols), dev, "out"),
+                                   1 if bf16 else 0, _raw_stream(dev)), "nf4_fp8_dequantize")
     return out
 
 
-def _fp8_product_args(A, a_scales, o: int, h: int, transpose: bool, A2, B2, experts: tuple, out):
-    """Checks the product's tensors against W [o][h]; returns (a_format, M, R, C)."""
+def _fp8_product(A, a_scales, o: int, h: int, transpose, A2, B2, experts: tuple, out, dev: int):
+    """Checks the product's tensors against W [o][h]; returns (A, a_format, a_scales, M, transpose, A2, B2, R, C tensor)
+    as the C calls take them."""
     f = _fp8_format(getattr(A, "dtype", None), "A")
     K, N = (o, h) if transpose else (h, o)
-    M = _need(A, A.dtype, (None, K), "A").shape[0]
-    _need(a_scales, torch.float32, (M, _blocks(K)), "a_scales")
-    R = 0
+    M = _matrix(A, "A")[0]
+    a = _held(A, A.dtype, (M, K), dev, "A")
+    s = _held(a_scales, torch.float32, (M, _blocks(K)), dev, "a_scales")
+    R, a2, b2 = 0, None, None
     if A2 is not None or B2 is not None:
         if A2 is None or B2 is None:
             raise ValueError("A2 and B2: give both or neither")
-        R = _need(A2, torch.bfloat16, (M, None), "A2").shape[1]
-        _need(B2, torch.bfloat16, (*experts, N, R), "B2")
-    C = _need(out, torch.bfloat16, (M, N), "out") if out is not None else \
-        torch.empty(M, N, dtype=torch.bfloat16, device=A.device)
-    return f, M, R, C
+        R = _matrix(A2, "A2")[1]
+        a2 = _held(A2, torch.bfloat16, (M, R), dev, "A2")
+        b2 = _held(B2, torch.bfloat16, (*experts, N, R), dev, "B2")
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+    else:
+        _held(out, torch.bfloat16, (M, N), dev, "out")
+    return a, f, s, M, 1 if transpose else 0, a2, b2, R, out
 
 
 def fp8_matmul(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
@@ -570,12 +604,13 @@ def fp8_matmul(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scale
     """nf4_fp8_matmul: A * W^T (+ A2 * B2^T), or A * W (+ ...) with transpose=True, bf16 [M][N].
     A [M][K] and a_scales as fp8_quantize(X) gives them (either format), W [o][h] (e4m3) and w_scales as
     fp8_quantize(W, 128) does."""
-    o, h = _need(W, torch.float8_e4m3fn, (None, None), "W").shape
-    _need(w_scales, torch.float32, (_blocks(o), _blocks(h)), "w_scales")
-    f, M, R, C = _fp8_product_args(A, a_scales, o, h, transpose, A2, B2, (), out)
-    _check(_lib.nf4_fp8_matmul(A.data_ptr(), f, a_scales.data_ptr(), M, W.data_ptr(), w_scales.data_ptr(), o, h,
-                               1 if transpose else 0, A2.data_ptr() if R else None, B2.data_ptr() if R else None, R,
-                               C.data_ptr(), _stream()), "nf4_fp8_matmul")
+    o, h = _matrix(W, "W")
+    dev = torch.cuda.current_device()
+    w = _held(W, torch.float8_e4m3fn, (o, h), dev, "W")
+    ws = _held(w_scales, torch.float32, (_blocks(o), _blocks(h)), dev, "w_scales")
+    a, f, s, M, tr, a2, b2, R, C = _fp8_product(A, a_scales, o, h, transpose, A2, B2, (), out, dev)
+    _check(_lib.nf4_fp8_matmul(a, f, s, M, w, ws, o, h, tr, a2, b2, R, C.data_ptr(), _raw_stream(dev)),
+           "nf4_fp8_matmul")
     return C
 
 
@@ -585,14 +620,16 @@ def fp8_matmul_grouped(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor,
     """nf4_fp8_matmul_grouped: fp8_matmul of the rows offsets[e] .. offsets[e + 1] - 1 with expert e's W[e]
     [experts][o][h] (w_scales [experts][..][..], B2 [experts][N][R]); offsets is a cuda int32 [experts + 1].
     Rows outside the experts' are not written (undefined in a result that this call allocates)."""
-    E, o, h = _need(W, torch.float8_e4m3fn, (None, None, None), "W").shape
-    _need(w_scales, torch.float32, (E, _blocks(o), _blocks(h)), "w_scales")
-    _need(offsets, torch.int32, (E + 1,), "offsets")
-    f, M, R, C = _fp8_product_args(A, a_scales, o, h, transpose, A2, B2, (E,), out)
-    _check(_lib.nf4_fp8_matmul_grouped(A.data_ptr(), f, a_scales.data_ptr(), M, W.data_ptr(), w_scales.data_ptr(), E,
-                                       o, h, offsets.data_ptr(), 1 if transpose else 0,
-                                       A2.data_ptr() if R else None, B2.data_ptr() if R else None, R, C.data_ptr(),
-                                       _stream()), "nf4_fp8_matmul_grouped")
+    if not isinstance(W, torch.Tensor) or W.dim() != 3:
+        raise ValueError("W: expected a tensor of three dimensions, [experts][o][h]")
+    E, o, h = W.shape
+    dev = torch.cuda.current_device()
+    w = _held(W, torch.float8_e4m3fn, (E, o, h), dev, "W")
+    ws = _held(w_scales, torch.float32, (E, _blocks(o), _blocks(h)), dev, "w_scales")
+    off = _held(offsets, torch.int32, (E + 1,), dev, "offsets")
+    a, f, s, M, tr, a2, b2, R, C = _fp8_product(A, a_scales, o, h, transpose, A2, B2, (E,), out, dev)
+    _check(_lib.nf4_fp8_matmul_grouped(a, f, s, M, w, ws, E, o, h, off, tr, a2, b2, R, C.data_ptr(),
+                                       _raw_stream(dev)), "nf4_fp8_matmul_grouped")
     return C
 
 
@@ -600,25 +637,33 @@ def rmsnorm_fwd(X: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, residual: t
                 want_y: bool = True, want_fp8: bool = False, want_rstd: bool = False, outs=None):
     """nf4_rmsnorm_fwd of bf16 X [M][H] (+ residual): (Y bf16, h bf16, codes e4m3, scales fp32, rstd fp32), None for
     what is not asked for (h: without a residual).  `outs`: the same five, given instead of allocated."""
-    M, H = _need(X, torch.bfloat16, (None, None), "X").shape
-    _need(w, torch.bfloat16, (H,), "w")
-    if residual is not None:
-        _need(residual, torch.bfloat16, (M, H), "residual")
-    shapes = (("Y", want_y, torch.bfloat16, (M, H)), ("h", residual is not None, torch.bfloat16, (M, H)),
-              ("codes", want_fp8, torch.float8_e4m3fn, (M, H)), ("scales", want_fp8, torch.float32, (M, _blocks(H))),
-              ("rstd", want_rstd, torch.float32, (M,)))
+    M, H = _matrix(X, "X")
+    dev = torch.cuda.current_device()
+    bf16, f32, e4m3, device = torch.bfloat16, torch.float32, torch.float8_e4m3fn, X.device
+    x = _held(X, bf16, (M, H), dev, "X")
+    wp = _held(w, bf16, (H,), dev, "w")
+    res = None if residual is None else _held(residual, bf16, (M, H), dev, "residual")
+    want = (want_y, residual is not None, want_fp8, want_fp8, want_rstd)
     if outs is None:
-        outs = tuple(torch.empty(shape, dtype=dt, device=X.device) if want else None
-                     for _, want, dt, shape in shapes)
+        Y = torch.empty((M, H), dtype=bf16, device=device) if want_y else None
+        h = None if residual is None else torch.empty((M, H), dtype=bf16, device=device)
+        codes = torch.empty((M, H), dtype=e4m3, device=device) if want_fp8 else None
+        scales = torch.empty((M, _blocks(H)), dtype=f32, device=device) if want_fp8 else None
+        rstd = torch.empty((M,), dtype=f32, device=device) if want_rstd else None
+        outs = (Y, h, codes, scales, rstd)
     else:
-        for t, (name, want, dt, shape) in zip(outs, shapes):
-            if want != (t is not None):
-                raise ValueError(f"outs.{name}: {'missing' if want else 'given, but not asked for'}")
-            if want:
-                _need(t, dt, shape, f"outs.{name}")
-    Y, h, codes, scales, rstd = outs
-    _check(_lib.nf4_rmsnorm_fwd(_ptr(X), _ptr(residual), _ptr(w), M, H, eps, _ptr(h), _ptr(Y), _ptr(codes),
-                                _ptr(scales), _ptr(rstd), _stream()), "nf4_rmsnorm_fwd")
+        names = ("Y", "h", "codes", "scales", "rstd")
+        kinds = ((bf16, (M, H)), (bf16, (M, H)), (e4m3, (M, H)), (f32, (M, _blocks(H))), (f32, (M,)))
+        for t, asked, name, (dtype, shape) in zip(outs, want, names, kinds):
+            if bool(asked) != (t is not None):
+                raise ValueError(f"outs.{name}: {'missing' if asked else 'given, but not asked for'}")
+            if asked:
+                _held(t, dtype, shape, dev, f"outs.{name}")
+        Y, h, codes, scales, rstd = outs
+    _check(_lib.nf4_rmsnorm_fwd(x, res, wp, M, H, eps, None if h is None else h.data_ptr(),
+                                None if Y is None else Y.data_ptr(), None if codes is None else codes.data_ptr(),
+                                None if scales is None else scales.data_ptr(),
+                                None if rstd is None else rstd.data_ptr(), _raw_stream(dev)), "nf4_rmsnorm_fwd")
     return outs
 
 
@@ -632,22 +677,22 @@ def rmsnorm_bwd(dY: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rstd: torch.
                 dH: torch.Tensor | None = None, ws: torch.Tensor | None = None, outs=None):
     """nf4_rmsnorm_bwd: (dX bf16 [M][H], the gradient of X and of the residual alike, dw fp32 [H]) from the forward's
     h (X without a residual) and rstd; dH is the gradient that reaches h along the residual stream."""
-    M, H = _need(dY, torch.bfloat16, (None, None), "dY").shape
-    _need(h, torch.bfloat16, (M, H), "h")
-    _need(w, torch.bfloat16, (H,), "w")
-    _need(rstd, torch.float32, (M,), "rstd")
-    if dH is not None:
-        _need(dH, torch.bfloat16, (M, H), "dH")
+    M, H = _matrix(dY, "dY")
+    dev = torch.cuda.current_device()
+    bf16, f32 = torch.bfloat16, torch.float32
+    g = _held(dY, bf16, (M, H), dev, "dY")
+    hp = _held(h, bf16, (M, H), dev, "h")
+    wp = _held(w, bf16, (H,), dev, "w")
+    r = _held(rstd, f32, (M,), dev, "rstd")
+    d = None if dH is None else _held(dH, bf16, (M, H), dev, "dH")
     if outs is None:
-        dX = torch.empty(M, H, dtype=torch.bfloat16, device=dY.device)
-        dw = torch.empty(H, dtype=torch.float32, device=dY.device)
-    else:
-        dX = _need(outs[0], torch.bfloat16, (M, H), "outs.dX")
-        dw = _need(outs[1], torch.float32, (H,), "outs.dw")
+        outs = (torch.empty((M, H), dtype=bf16, device=dY.device), torch.empty((H,), dtype=f32, device=dY.device))
+    dX, dw = outs
     ws = _need_ws(ws) if ws is not None else \
-        torch.empty(rmsnorm_workspace_bytes(M, H), dtype=torch.uint8, device=dY.device)
-    _check(_lib.nf4_rmsnorm_bwd(_ptr(dY), _ptr(h), _ptr(w), _ptr(rstd), _ptr(dH), M, H, _ptr(dX), _ptr(dw), _ptr(ws),
-                                ws.numel(), _stream()), "nf4_rmsnorm_bwd")
+        torch.empty((rmsnorm_workspace_bytes(M, H),), dtype=torch.uint8, device=dY.device)
+    _check(_lib.nf4_rmsnorm_bwd(g, hp, wp, r, d, M, H, _held(dX, bf16, (M, H), dev, "outs.dX"),
+                                _held(dw, f32, (H,), dev, "outs.dw"), ws.data_ptr(), ws.numel(), _raw_stream(dev)),
+           "nf4_rmsnorm_bwd")
     return dX, dw
 
 
