@@ -90,6 +90,7 @@ __device__ __forceinline__ bool find_tile(const Args& p, int bm, int t, int& e, 
   return false;
 }
 
+constexpr int kWaitLds = 15 | (3 << 14) | (0x7 << 4);  // lgkmcnt(0), vmcnt as it is
 constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8); }
 
 // The tile of this workgroup.  Workgroups are dealt to the 8 XCDs round-robin;
@@ -121,14 +122,27 @@ __global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
   constexpr int WN = 16 * NI;  // columns of a wave
   constexpr int HW = WN / 2;   // and of a half of them
   constexpr int AI = BM / 64;  // 1 KB copies of A per wave
+  // operand buffers: three where a step is short, so that copies run two steps
+  // ahead; two 256 x 256 steps are all that fits.  W<step><half>
+  constexpr int NB3 = NI == 8 ? 2 : 3;
+  constexpr int X2 = NB3 == 3 ? 1 : 0;
   __shared__ __attribute__((aligned(1024))) uint8_t A0[BM * 128];
   __shared__ __attribute__((aligned(1024))) uint8_t A1[BM * 128];
-  __shared__ __attribute__((aligned(1024))) uint8_t W00[BN * 64];  // W<step % 2><half>
+  __shared__ __attribute__((aligned(1024))) uint8_t A2[X2 ? BM * 128 : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t W00[BN * 64];
   __shared__ __attribute__((aligned(1024))) uint8_t W01[BN * 64];
   __shared__ __attribute__((aligned(1024))) uint8_t W10[BN * 64];
   __shared__ __attribute__((aligned(1024))) uint8_t W11[BN * 64];
+  __shared__ __attribute__((aligned(1024))) uint8_t W20[X2 ? BN * 64 : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t W21[X2 ? BN * 64 : 16];
   __shared__ __attribute__((aligned(1024))) float S0[NW * 64];
   __shared__ __attribute__((aligned(1024))) float S1[NW * 64];
+  __shared__ __attribute__((aligned(1024))) float S2[X2 ? NW * 64 : 16];
+  auto abuf = [&](int b) -> uint8_t* { return b == 0 ? A0 : b == 1 ? A1 : A2; };
+  auto wbuf = [&](int b, int h) -> uint8_t* {
+    return h == 0 ? (b == 0 ? W00 : b == 1 ? W10 : W20) : (b == 0 ? W01 : b == 1 ? W11 : W21);
+  };
+  auto sbuf = [&](int b) -> float* { return b == 0 ? S0 : b == 1 ? S1 : S2; };
   constexpr int SR = BM / NW;  // A scales a wave copies
 
   const int lane = threadIdx.x & 63;
@@ -177,32 +191,28 @@ __global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
   const uint32_t s_off = lane < SR ? (uint32_t)((wave * SR + lane) * KB * 4) : kOOB;
   // Steps behind the last one load its tile once more, so the loop has no
   // branches and every wait counts the same loads.
-  auto copy_a = [&](int kt, uint8_t* Ad, float* Sd) {
+  auto copy_a = [&](int kt, int b, int i) {
     kt = min(kt, KB - 1);
     const uint32_t off = kt * 128 + c_chunk * 16 < K ? a_off : kOOB;
-#pragma unroll
-    for (int i = 0; i < AI; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (lds_ptr_t)(Ad + (i * NW + wave) * 1024), 16, off,
-                                               kt * 128 + i * 64 * K, 0, 0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (lds_ptr_t)(Sd + wave * 64), 4, s_off, kt * 4, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (lds_ptr_t)(abuf(b) + (i * NW + wave) * 1024), 16, off,
+                                             kt * 128 + i * 64 * K, 0, 0);
   };
-  auto copy_w = [&](int kt, int h, uint8_t* Wd) {
+  auto copy_s = [&](int kt, int b) {
     kt = min(kt, KB - 1);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (lds_ptr_t)(sbuf(b) + wave * 64), 4, s_off, kt * 4, 0, 0);
+  };
+  auto copy_w = [&](int kt, int b, int h, int i) {
+    kt = min(kt, KB - 1);
+    const lds_ptr_t to = (lds_ptr_t)(wbuf(b, h) + (i * NW + wave) * 1024);
     if constexpr (TR) {
       const __amdgpu_buffer_rsrc_t wr =
           make_rsrc(W + (int64_t)kt * 128 * N, (uint32_t)(min(128, K - kt * 128) * (int64_t)N));
       const uint32_t off = col0 + h * HW < N ? w_off : kOOB;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_ptr_t)(Wd + (i * NW + wave) * 1024), 16, off,
-                                                 h * HW + i * 64 * N, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, to, 16, off, h * HW + i * 64 * N, 0, 0);
     } else {
       const __amdgpu_buffer_rsrc_t wr = make_rsrc(W + (int64_t)n0 * K, (uint32_t)((int64_t)nrows * K));
       const uint32_t off = kt * 128 + c_chunk * 16 < K ? w_off : kOOB;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_ptr_t)(Wd + (i * NW + wave) * 1024), 16, off,
-                                                 kt * 128 + (i * 128 + h * HW) * K, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, to, 16, off, kt * 128 + (i * 128 + h * HW) * K, 0, 0);
     }
   };
   const int nb = min((n0 + wn * WN) >> 7, NB - 1);
@@ -265,18 +275,20 @@ __global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
   // barrier before each.  The group's W fragment is read during the group before
   // it; the next step's A fragments replace this step's as the last group is done
   // with them; the multiply-adds of a group run beside the next one's MFMAs.
-  // Copies of step kt:   before the 2nd half: A and scales (kt + 2), W (kt + 2) first half
-  //                      before the 1st half: W (kt + 1) second half
-  // each into memory whose readers the barrier has seen through, a step and more
-  // ahead of its own.
+  // Copies, B the number of buffers:
+  //   before the 1st half of step kt: the 2nd half of W (kt + B - 1),
+  //   before the 2nd half:            A, its scales and the 1st half of W (kt + B),
+  // each into memory whose readers that barrier has seen through, and B - 1 steps
+  // before the barrier that waits for it.
   auto barrier = [&](auto outstanding) {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(wait_vm(decltype(outstanding)::value));
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  constexpr std::integral_constant<int, 2> kHalf0{};  // the copies issued in a 1st half
-  constexpr std::integral_constant<int, 3 + AI> kHalf1{};  // and in a 2nd half
+  constexpr int C0 = 2, C1 = 3 + AI;  // copies issued before a 1st and a 2nd half
+  constexpr std::integral_constant<int, (NB3 - 1) * C1 + (NB3 - 2) * C0> kHalf1{};  // may be under way at a 1st half
+  constexpr std::integral_constant<int, (NB3 - 1) * C0 + (NB3 - 2) * C1> kHalf0{};  // and at a 2nd half
   i32x8 fa[MI], fw[2];
   floatx4 d[2][MI];
   float s[MI], sc[MI];
@@ -287,19 +299,15 @@ __global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
 #pragma unroll
       for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(dd[i][v], sc[i], acc[i][j][v]);
   };
-  auto step = [&](int kt, uint8_t* Ac, uint8_t* An, uint8_t* Wc0, uint8_t* Wc1, uint8_t* Wn0, uint8_t* Wn1, float* Sc,
-                  const float* Sn) {
+  auto step = [&](int kt, int b) {  // b = kt % NB3, a constant in every copy of the step
+    uint8_t* const An = abuf((b + 1) % NB3);
+    uint8_t* const Wc0 = wbuf(b, 0);
+    uint8_t* const Wc1 = wbuf(b, 1);
+    uint8_t* const Wn0 = wbuf((b + 1) % NB3, 0);
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
-      if (j == 0) {
-        barrier(kHalf1);
-        copy_w(kt + 1, 1, Wn1);
-      }
-      if (j == NI / 2) {
-        barrier(kHalf0);
-        copy_w(kt + 2, 0, Wc0);
-        copy_a(kt + 2, Ac, Sc);
-      }
+      if (j == 0) barrier(kHalf1);
+      if (j == NI / 2) barrier(kHalf0);
       __builtin_amdgcn_sched_barrier(0);
       fw[(j + 1) & 1] = j + 1 < NI / 2 ? frag_w(Wc0, j + 1) : j + 1 < NI ? frag_w(Wc1, j + 1 - NI / 2) : frag_w(Wn0, 0);
 #pragma unroll
@@ -315,7 +323,7 @@ __global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
 #pragma unroll
         for (int i = 0; i < MI; ++i) sc[i] = s[i] * w;
       }
-      if (j == NI - 1) read_s(Sn, s);
+      if (j == NI - 1) read_s(sbuf((b + 1) % NB3), s);
 #pragma unroll
       for (int i = 0; i < MI; ++i) asm volatile("" : "+v"(acc[i][(j + NI - 1) % NI]));
       __builtin_amdgcn_sched_group_barrier(0x100, TR ? 4 : 2, 0);
@@ -325,14 +333,42 @@ __global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
         __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
+      // this half's copies, spread over its groups: a burst would hold up every wave
+      constexpr int H = NI / 2;
+      if (j < H) {
+#pragma unroll
+        for (int c = j * C0 / H; c < (j + 1) * C0 / H; ++c) copy_w(kt + NB3 - 1, (b + NB3 - 1) % NB3, 1, c);
+      } else {
+#pragma unroll
+        for (int c = (j - H) * C1 / H; c < (j - H + 1) * C1 / H; ++c) {
+          if (c < 2) copy_w(kt + NB3, b, 0, c);
+          else if (c < 2 + AI) copy_a(kt + NB3, b, c - 2);
+          else copy_s(kt + NB3, b);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if (((kt + 1) & 63) == 0) wsr = load_ws(kt + 1);
+    if (((kt + 1) & 63) == 0) {
+      wsr = load_ws(kt + 1);
+      // waited for here, or every step's use would wait for the copies under way
+      __builtin_amdgcn_s_waitcnt(wait_vm(0));
+    }
   };
-  copy_w(0, 0, W00);
-  copy_w(0, 1, W01);
-  copy_a(0, A0, S0);
-  copy_w(1, 0, W10);
-  copy_a(1, A1, S1);
+  // in the order that the loop would have issued them
+  auto first = [&](int b) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) copy_w(b, b, 0, c);
+#pragma unroll
+    for (int c = 0; c < AI; ++c) copy_a(b, b, c);
+    copy_s(b, b);
+  };
+  first(0);
+#pragma unroll
+  for (int b = 1; b < NB3; ++b) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) copy_w(b - 1, b - 1, 1, c);
+    first(b);
+  }
   barrier(kHalf1);
   fw[0] = frag_w(W00, 0);
 #pragma unroll
@@ -344,11 +380,12 @@ __global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
     d[1][i] = floatx4{0.f, 0.f, 0.f, 0.f};
   }
   int kt = 0;
-  for (; kt + 2 <= KB; kt += 2) {
-    step(kt, A0, A1, W00, W01, W10, W11, S0, S1);
-    step(kt + 1, A1, A0, W10, W11, W00, W01, S1, S0);
+  for (; kt + NB3 <= KB; kt += NB3) {
+#pragma unroll
+    for (int b = 0; b < NB3; ++b) step(kt + b, b);
   }
-  if (kt < KB) step(kt, A0, A1, W00, W01, W10, W11, S0, S1);
+  if (kt < KB) step(kt, 0);
+  if (NB3 == 3 && kt + 1 < KB) step(kt + 1, 1);
   fold(NI - 1, d[(NI - 1) & 1]);
   __builtin_amdgcn_s_waitcnt(wait_vm(0));
 
@@ -408,71 +445,275 @@ __global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
   }
 }
 
+// Few rows, or few tiles.  A workgroup makes a tile of 16 MT rows by 16 NT columns;
+// its NWV waves take every NWV-th block of the contraction and join their sums
+// through LDS in a fixed order at the end.  A wave stages its own operands: rows
+// of 128 bytes (TR: k rows of 64 bytes) copied straight into its part of LDS, ST
+// rounds in flight, so the loop has no barrier.  (Fragments loaded from memory
+// into registers take four times as long: the address path joins neighbouring
+// lanes only, and a fragment's neighbouring lanes are different rows.)
+template <int MT, int NT, int NWV, int ST, bool TR, bool E5M2, bool GROUPED>
+__global__ __launch_bounds__(NWV * 64) void k_fp8_rows(Args p) {
+  static_assert(!TR || NT == 4, "64 bytes of each k row");
+  constexpr int BM = 16 * MT, BN = 16 * NT;
+  constexpr int WB = (MT + NT) * 2048 + 256;  // a wave's bytes of one round: A, W, A scales
+  constexpr int WOFF = MT * 2048, SOFF = (MT + NT) * 2048;
+  __shared__ __attribute__((aligned(1024))) uint8_t L0[NWV * WB];
+  __shared__ __attribute__((aligned(1024))) uint8_t L1[NWV * WB];
+  __shared__ __attribute__((aligned(1024))) uint8_t L2[ST > 2 ? NWV * WB : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t L3[ST > 3 ? NWV * WB : 16];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, l16 = lane & 15;
+  const int tiles_m = (int)gridDim.x / p.tiles_n;
+  int id = blockIdx.x;
+  if ((gridDim.x & 7) == 0) id = (id & 7) * (gridDim.x >> 3) + (id >> 3);
+  const int tm = GROUPED ? id / p.tiles_n : id % tiles_m;
+  const int n0 = (GROUPED ? id % p.tiles_n : id / tiles_m) * BN;
+  const int N = p.N, K = p.K;
+  const int KB = (K + 127) / 128;
+  const int NB = (N + 127) / 128;
+  int e = 0;
+  int64_t m0, m1;
+  if constexpr (GROUPED) {
+    if (!find_tile(p, BM, tm, e, m0, m1)) return;
+  } else {
+    m0 = (int64_t)tm * BM;
+    m1 = min(m0 + BM, p.M);
+  }
+  const int mrows = (int)(m1 - m0);
+  const int nrows = min(BN, N - n0);
+  const uint8_t* W = p.W + (GROUPED ? (int64_t)e * N * K : 0);
+  const float* ws = p.ws + (GROUPED ? (int64_t)e * NB * KB : 0);
+  const __amdgpu_buffer_rsrc_t ar = make_rsrc(p.A + m0 * K, (uint32_t)((int64_t)mrows * K));
+  const __amdgpu_buffer_rsrc_t sr = make_rsrc(p.as + m0 * KB, (uint32_t)((int64_t)mrows * KB * 4));
+
+  // copies: 8 lanes a row, chunks XORed with the row's low bits (see k_fp8_wide)
+  const int c_row = lane >> 3, c_k = ((lane & 7) ^ c_row) * 16;
+  const uint32_t a_off = (uint32_t)(c_row * K + c_k);
+  // TR: 4 lanes a k row, chunk c of row r at place c ^ (r / 4 % 4)
+  const int t_row = lane >> 2;
+  const int t_col = n0 + ((lane & 3) ^ ((t_row >> 2) & 3)) * 16;
+  const uint32_t t_off = t_col < N ? (uint32_t)(t_row * N + t_col) : kOOB;
+  auto lbuf = [&](int b) -> uint8_t* { return (b == 0 ? L0 : b == 1 ? L1 : b == 2 ? L2 : L3) + wave * WB; };
+  constexpr int LOADS = 2 * MT + 2 * NT + 1;
+  auto copy = [&](int kt, int b) {
+    kt = min(kt, KB - 1);  // a round behind the last copies it once more, and is not used
+    uint8_t* const to = lbuf(b);
+    const bool in = kt * 128 + c_k < K;
+    const uint32_t off = in ? a_off : kOOB;
+    if constexpr (TR) {
+      const __amdgpu_buffer_rsrc_t wr =
+          make_rsrc(W + (int64_t)kt * 128 * N, (uint32_t)(min(128, K - kt * 128) * (int64_t)N));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_ptr_t)(to + WOFF + i * 1024), 16, t_off, i * 16 * N, 0, 0);
+    } else {
+      const __amdgpu_buffer_rsrc_t wr = make_rsrc(W + (int64_t)n0 * K, (uint32_t)((int64_t)nrows * K));
+#pragma unroll
+      for (int i = 0; i < 2 * NT; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_ptr_t)(to + WOFF + i * 1024), 16, off, kt * 128 + i * 8 * K,
+                                                 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (lds_ptr_t)(to + i * 1024), 16, off, kt * 128 + i * 8 * K, 0, 0);
+    if (lane < BM)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (lds_ptr_t)(to + SOFF), 4, (uint32_t)(lane * KB * 4), kt * 4, 0, 0);
+  };
+  // W scales of this wave's rounds, one a lane
+  const int nb = n0 >> 7;
+  auto load_ws = [&](int r) -> float {
+    const int k = min((r + lane) * NWV + wave, KB - 1);
+    return TR ? ws[(int64_t)k * NB + nb] : ws[(int64_t)nb * KB + k];
+  };
+
+  floatx4 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+  const uint32_t f_lo = (uint32_t)(l16 * 128 + ((g ^ (l16 & 7)) << 4));
+  auto frag = [&](const uint8_t* at) -> i32x8 {
+    const u32x4 lo = *(const u32x4*)(at + f_lo);
+    const u32x4 hi = *(const u32x4*)(at + (f_lo ^ 64));
+    return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+  };
+  auto frag_t = [&](uint8_t* at, int j) -> i32x8 {  // k rows of 64 bytes
+    i32x8 f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = (q >> 1) * 64 + 16 * g + (q & 1) * 8 + (l16 >> 1);
+      const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+          (lds_i32x2_ptr)(at + r * 64 + ((j ^ ((r >> 2) & 3)) << 4) + (l16 & 1) * 8));
+      f[2 * q] = v.x;
+      f[2 * q + 1] = v.y;
+    }
+    return f;
+  };
+
+  const int rounds = (KB - wave + NWV - 1) / NWV;  // of this wave; 0 when it has none
+  float wsr = load_ws(0);
+#pragma unroll
+  for (int b = 0; b < ST - 1; ++b) copy(b * NWV + wave, b);
+  auto round = [&](int r, int b) {
+    copy((r + ST - 1) * NWV + wave, (b + ST - 1) % ST);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(wait_vm((ST - 1) * LOADS));  // all but the rounds ahead
+    asm volatile("" ::: "memory");
+    uint8_t* const at = lbuf(b);
+    const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wsr), r & 63));
+    i32x8 fw[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) fw[j] = TR ? frag_t(at + WOFF, j) : frag(at + WOFF + j * 2048);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const i32x8 fa = frag(at + i * 2048);
+      const float s = *(const float*)(at + SOFF + (i * 16 + l16) * 4) * w;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const floatx4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[j], fa, floatx4{0.f, 0.f, 0.f, 0.f}, 0,
+                                                                           E5M2 ? 1 : 0, 0, 0, 0, 0);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(d[v], s, acc[i][j][v]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(acc[i][j]));
+    // the reads of this round are done before its memory is copied to again
+    __builtin_amdgcn_s_waitcnt(kWaitLds);
+    if (((r + 1) & 63) == 0) {
+      wsr = load_ws(r + 1);
+      __builtin_amdgcn_s_waitcnt(wait_vm(0));
+    }
+  };
+  int r = 0;
+  for (; r + ST <= rounds; r += ST) {
+#pragma unroll
+    for (int b = 0; b < ST; ++b) round(r + b, b);
+  }
+#pragma unroll
+  for (int b = 0; b < ST - 1; ++b)
+    if (r + b < rounds) round(r + b, b);
+  __builtin_amdgcn_s_waitcnt(wait_vm(0));
+
+  // the low-rank term: runs of 32 of its columns, dealt to the waves
+  for (int k0 = wave * 32; k0 < p.R; k0 += NWV * 32) {
+    const __amdgpu_buffer_rsrc_t a2 = make_rsrc(p.A2 + m0 * p.R, (uint32_t)((int64_t)mrows * p.R * 2));
+    const __amdgpu_buffer_rsrc_t b2 =
+        make_rsrc(p.B2 + ((GROUPED ? (int64_t)e * N : 0) + n0) * p.R, (uint32_t)((int64_t)nrows * p.R * 2));
+    const int k = k0 + 8 * g;
+    const uint32_t o = k < p.R ? (uint32_t)((l16 * p.R + k) * 2) : kOOB;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const bf16x8 fb = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(b2, o, j * 16 * p.R * 2, 0));
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const bf16x8 fa = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(a2, o, i * 16 * p.R * 2, 0));
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb, fa, acc[i][j], 0, 0, 0);
+      }
+    }
+  }
+
+  __syncthreads();  // every wave is done with its rounds: their memory holds the sums
+  static_assert(MT * NT * 1024 <= WB, "a wave's sums fit its part");
+  floatx4* const part = (floatx4*)L0;
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) part[(wave * MT * NT + i * NT + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+  for (int q = threadIdx.x; q < MT * NT * 64; q += NWV * 64) {
+    const int t = q >> 6, l = q & 63;
+    floatx4 s = part[q];
+#pragma unroll
+    for (int w = 1; w < NWV; ++w) s += part[w * MT * NT * 64 + q];
+    const int row = t / NT * 16 + (l & 15);
+    const int n = n0 + t % NT * 16 + 4 * (l >> 4);
+    if (row < mrows && n < N)
+      *(uint2*)(p.C + (m0 + row) * N + n) = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
+  }
+}
+
+// one launch of tile kind `kind` over all of p's rows
+hipError_t launch_part(const Fp8Gemm& q, Args p, int kind, hipStream_t st) {
+  const Fp8Kind& k = fp8_kinds()[kind];
+  p.tiles_n = (p.N + k.bn - 1) / k.bn;
+  // every expert's last tile may be partly filled
+  const int64_t tiles = q.experts ? p.M / k.bm + std::min<int64_t>(q.experts, p.M) : (p.M + k.bm - 1) / k.bm;
+  if (tiles * p.tiles_n > (int64_t)0xFFFFFFFF / k.threads) return hipErrorInvalidValue;
+  const dim3 gr((unsigned)(tiles * p.tiles_n)), bl((unsigned)k.threads);
+#define NF4K_LAUNCH(...) hipLaunchKernelGGL((__VA_ARGS__), gr, bl, 0, st, p)
+#define NF4K_FLAGS(KERNEL, ...)                                                     \
+  do {                                                                              \
+    if (q.experts) {                                                                \
+      if (q.a_e5m2) NF4K_LAUNCH(KERNEL<__VA_ARGS__, true, true>);                   \
+      else NF4K_LAUNCH(KERNEL<__VA_ARGS__, false, true>);                           \
+    } else {                                                                        \
+      if (q.a_e5m2) NF4K_LAUNCH(KERNEL<__VA_ARGS__, true, false>);                  \
+      else NF4K_LAUNCH(KERNEL<__VA_ARGS__, false, false>);                          \
+    }                                                                               \
+  } while (0)
+#define NF4K_WIDE(NI)                                       \
+  do {                                                      \
+    if (q.transpose) NF4K_FLAGS(k_fp8_wide, NI, true);      \
+    else NF4K_FLAGS(k_fp8_wide, NI, false);                 \
+  } while (0)
+  switch (kind) {
+    case kFp8Wide8: NF4K_WIDE(8); break;
+    case kFp8Wide4: NF4K_WIDE(4); break;
+    case kFp8Wide2: NF4K_WIDE(2); break;
+    case kFp8Rows11: NF4K_FLAGS(k_fp8_rows, 1, 1, 4, 4, false); break;
+    case kFp8Rows14: NF4K_FLAGS(k_fp8_rows, 1, 4, 4, 3, false); break;
+    case kFp8Rows22: NF4K_FLAGS(k_fp8_rows, 2, 2, 8, 2, false); break;
+    case kFp8Rows42: NF4K_FLAGS(k_fp8_rows, 4, 2, 4, 3, false); break;
+    case kFp8Rows44: NF4K_FLAGS(k_fp8_rows, 4, 4, 4, 2, false); break;
+    case kFp8Rows14T: NF4K_FLAGS(k_fp8_rows, 1, 4, 4, 3, true); break;
+    case kFp8Rows24T: NF4K_FLAGS(k_fp8_rows, 2, 4, 4, 3, true); break;
+    default: NF4K_FLAGS(k_fp8_rows, 4, 4, 4, 2, true); break;
+  }
+#undef NF4K_WIDE
+#undef NF4K_FLAGS
+#undef NF4K_LAUNCH
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_fp8_gemm(const Fp8Gemm& q, hipStream_t st) {
-  constexpr int BN = 256, NT = 512;
   Args p{};
-  p.A = q.A;
-  p.as = q.a_scales;
   p.W = q.W;
   p.ws = q.w_scales;
   p.offsets = q.offsets;
-  p.A2 = q.A2;
   p.B2 = q.B2;
-  p.C = q.C;
-  p.M = q.M;
   p.N = (int)(q.transpose ? q.cols : q.rows);
   p.K = (int)(q.transpose ? q.rows : q.cols);
   p.R = q.R;
   p.experts = q.experts;
-  p.tiles_n = (p.N + BN - 1) / BN;
   const int KB = (p.K + 127) / 128;
-#define NF4K_FP8(NI, GR)                                                                                    \
-  do {                                                                                                      \
-    if (q.transpose) {                                                                                      \
-      if (q.a_e5m2) hipLaunchKernelGGL((k_fp8_wide<NI, true, true, GR>), gr, dim3(NT), 0, st, p);           \
-      else hipLaunchKernelGGL((k_fp8_wide<NI, true, false, GR>), gr, dim3(NT), 0, st, p);                   \
-    } else {                                                                                                \
-      if (q.a_e5m2) hipLaunchKernelGGL((k_fp8_wide<NI, false, true, GR>), gr, dim3(NT), 0, st, p);          \
-      else hipLaunchKernelGGL((k_fp8_wide<NI, false, false, GR>), gr, dim3(NT), 0, st, p);                  \
-    }                                                                                                       \
-  } while (0)
-#define NF4K_FP8_NI(GR)            \
-  do {                             \
-    if (ni == 8) NF4K_FP8(8, GR);  \
-    else if (ni == 4) NF4K_FP8(4, GR); \
-    else NF4K_FP8(2, GR);          \
-  } while (0)
-  if (q.experts) {
-    const int ni = fp8_tile_ni(std::max<int64_t>(1, q.M / q.experts), p.N, q.experts);
-    // every expert's last tile may be partly filled
-    const int64_t tiles = q.M / (32 * ni) + std::min<int64_t>(q.experts, q.M);
-    if (tiles * p.tiles_n > (int64_t)0xFFFFFFFF / NT) return hipErrorInvalidValue;
-    const dim3 gr((unsigned)(tiles * p.tiles_n));
-    NF4K_FP8_NI(true);
-    return hipGetLastError();
-  }
-  const int ni = fp8_tile_ni(q.M, p.N, 1);
-  const int BM = 32 * ni;
-  // at most 2^32 - 1 work-items a launch: more tiles run as ranges of row panels
-  const int64_t tiles_m = (q.M + BM - 1) / BM;
-  const int64_t panels = std::max<int64_t>(1, (int64_t)0xFFFFFFFF / NT / p.tiles_n);
-  for (int64_t t0 = 0; t0 < tiles_m; t0 += panels) {
-    const int64_t r0 = t0 * BM;
-    p.A = q.A + r0 * p.K;
-    p.as = q.a_scales + r0 * KB;
-    p.A2 = q.A2 ? q.A2 + r0 * q.R : nullptr;
-    p.C = q.C + r0 * p.N;
-    p.M = std::min(panels * BM, q.M - r0);
-    const dim3 gr((unsigned)(std::min(panels, tiles_m - t0) * p.tiles_n));
-    NF4K_FP8_NI(false);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+  Fp8Part parts[2];
+  const int n = plan_fp8(q.M, p.N, p.K, q.transpose, q.experts, parts);
+  int64_t r0 = 0;
+  for (int i = 0; i < n; ++i) {
+    // a launch holds at most 2^32 - 1 work-items: more tiles run as ranges of rows
+    const Fp8Kind& k = fp8_kinds()[parts[i].kind];
+    const int64_t tiles_n = (p.N + k.bn - 1) / k.bn;
+    const int64_t most = q.experts ? q.M : std::max<int64_t>(1, (int64_t)0xFFFFFFFF / k.threads / tiles_n) * k.bm;
+    for (const int64_t end = r0 + parts[i].rows; r0 < end;) {
+      const int64_t rows = std::min(most, end - r0);
+      p.A = q.A + r0 * p.K;
+      p.as = q.a_scales + r0 * KB;
+      p.A2 = q.A2 ? q.A2 + r0 * q.R : nullptr;
+      p.C = q.C + r0 * p.N;
+      p.M = rows;
+      const hipError_t e = launch_part(q, p, parts[i].kind, st);
+      if (e != hipSuccess) return e;
+      r0 += rows;
+    }
   }
   return hipSuccess;
-#undef NF4K_FP8_NI
-#undef NF4K_FP8
 }
 
 }  // namespace nf4k

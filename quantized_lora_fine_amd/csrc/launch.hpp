@@ -196,10 +196,24 @@ struct Fp8Gemm {
   int R;
   uint16_t* C;
 };
-// tile of a product with M rows (of each expert, on average) and N columns: ni
-// of 8, 4 or 2 for 256, 128 or 64 rows by 256 columns, whichever fills the
-// compute units in the least time
-int fp8_tile_ni(int64_t M, int N, int experts);
+// The product's tile kinds (rows bm by columns bn a workgroup of `threads`), and
+// what one costs; plan_fp8 picks the kind, or two for two ranges of rows, that
+// the costs say takes the least time.  Returns the number of parts (their rows
+// add up to M).  experts > 0: one kind for all.
+enum {
+  kFp8Wide8, kFp8Wide4, kFp8Wide2, kFp8Rows11, kFp8Rows14, kFp8Rows22, kFp8Rows42, kFp8Rows44,
+  kFp8Rows14T, kFp8Rows24T, kFp8Rows44T, kFp8Kinds
+};
+struct Fp8Kind {
+  int bm, bn, threads;
+  double u0, u1;
+};
+struct Fp8Part {
+  int kind;
+  int64_t rows;
+};
+const Fp8Kind* fp8_kinds();
+int plan_fp8(int64_t M, int N, int K, bool transpose, int experts, Fp8Part parts[2]);
 NF4K_WEAK hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t st);
 
 }  // namespace nf4k

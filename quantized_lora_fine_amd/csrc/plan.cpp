@@ -90,22 +90,93 @@ int rmsnorm_parts(int64_t M, int H) {
   return (int)(groups < 512 ? groups : 512);
 }
 
-int fp8_tile_ni(int64_t M, int N, int experts) {
-  // microseconds per 128 of the contraction for a full set of tiles on the 256
-  // compute units: 256 x 256 tiles (ni = 8), 128 x 256 (4) and 64 x 256 (2)
-  static const double cost[3] = {2.0, 1.22, 0.8};
-  int best = 8;
-  double least = 0;
-  for (int i = 0; i < 3; ++i) {
-    const int ni = 8 >> i, bm = 32 * ni;
-    const int64_t tiles = (M + bm - 1) / bm * ((N + 255) / 256) * experts;
-    const double t = (double)((tiles + 255) / 256) * cost[i];
-    if (i == 0 || t < least) {
-      least = t;
-      best = ni;
+// Tiles of the block-scaled product.  u0 and u1: microseconds a tile takes for
+// 128 of the contraction when few compute units have one and when all do.
+const Fp8Kind* fp8_kinds() {
+  static const Fp8Kind kinds[kFp8Kinds] = {
+      {256, 256, 512, 1.20, 1.95},  // kFp8Wide8
+      {128, 256, 512, 0.75, 1.18},  // kFp8Wide4
+      {64, 256, 512, 0.55, 0.85},   // kFp8Wide2
+      {16, 16, 256, 0.05, 0.063},   // kFp8Rows11
+      {16, 64, 256, 0.11, 0.185},   // kFp8Rows14
+      {32, 32, 512, 0.10, 0.154},   // kFp8Rows22
+      {64, 32, 256, 0.18, 0.244},   // kFp8Rows42
+      {64, 64, 256, 0.27, 0.34},    // kFp8Rows44
+      {16, 64, 256, 0.25, 0.31},    // kFp8Rows14T
+      {32, 64, 256, 0.29, 0.345},   // kFp8Rows24T
+      {64, 64, 256, 0.40, 0.457},   // kFp8Rows44T
+  };
+  return kinds;
+}
+
+namespace {
+
+constexpr int kCUs = 256;
+constexpr double kFp8Start = 4.0;  // microseconds before and after the loop of a tile, launch included
+
+// whole sets of tiles over the compute units, and how full the last (or only) one makes them
+double fp8_time(int kind, int64_t tiles_m, int N, int K) {
+  const Fp8Kind& k = fp8_kinds()[kind];
+  const int64_t tiles = tiles_m * ((N + k.bn - 1) / k.bn);
+  const double fill = tiles >= kCUs ? 1.0 : (double)tiles / kCUs;
+  return kFp8Start + (double)((tiles + kCUs - 1) / kCUs) * ((K + 127) / 128) * (k.u0 + (k.u1 - k.u0) * fill);
+}
+
+int fp8_best(int64_t M, int N, int K, bool transpose, int experts, double* time) {
+  // up to 4 rows the weight's stream is all: the narrowest tiles keep the most of it under way
+  const bool few = M <= 4 && !transpose && !experts;
+  int best = kFp8Rows11;
+  double least = -1.0;
+  for (int i = 0; i < kFp8Kinds; ++i) {
+    const bool t = i >= kFp8Rows14T, wide = i <= kFp8Wide2;
+    if (few ? i != kFp8Rows11 : !wide && t != transpose) continue;
+    const int64_t bm = fp8_kinds()[i].bm;
+    int64_t tiles_m = (M + bm - 1) / bm;
+    if (experts) {
+      // the rows' tiles, and half a tile more for every expert that can have rows
+      const int64_t used = M < experts ? M : experts;
+      tiles_m = M / bm + used / 2;
+      if (tiles_m < used) tiles_m = used;
+    }
+    const double x = fp8_time(i, tiles_m, N, K);
+    if (least < 0 || x < least) {
+      least = x;
+      best = i;
     }
   }
+  *time = least;
   return best;
+}
+
+}  // namespace
+
+int plan_fp8(int64_t M, int N, int K, bool transpose, int experts, Fp8Part parts[2]) {
+  double least;
+  parts[0].kind = fp8_best(M, N, K, transpose, experts, &least);
+  parts[0].rows = M;
+  int n = 1;
+  if (experts) return n;
+  // or whole sets of wide tiles, and the rows that are left by themselves: a few
+  // rows past a set would hold every compute unit for another whole one
+  for (int i = kFp8Wide8; i <= kFp8Wide2; ++i) {
+    const Fp8Kind& k = fp8_kinds()[i];
+    const int64_t tiles_n = (N + k.bn - 1) / k.bn;
+    const int64_t sets = (M / k.bm) * tiles_n / kCUs;
+    const int64_t rows = sets * kCUs / tiles_n * k.bm;
+    if (rows <= 0 || rows >= M) continue;
+    double rest;
+    const int kind = fp8_best(M - rows, N, K, transpose, 0, &rest);
+    const double x = fp8_time(i, rows / k.bm, N, K) + rest;
+    if (x < 0.95 * least) {  // a second launch has to be worth it
+      least = x;
+      n = 2;
+      parts[0].kind = i;
+      parts[0].rows = rows;
+      parts[1].kind = kind;
+      parts[1].rows = M - rows;
+    }
+  }
+  return n;
 }
 
 int error_batch_chunk(const int64_t* rows, const int64_t* cols, int32_t n, int32_t c0, int64_t* g0) {
