@@ -666,6 +666,7 @@ hipError_t launch_part(const Fp8Gemm& q, Args p, int kind, hipStream_t st) {
     case kFp8Wide4: NF4K_WIDE(4); break;
     case kFp8Wide2: NF4K_WIDE(2); break;
     case kFp8Rows11: NF4K_FLAGS(k_fp8_rows, 1, 1, 4, 4, false); break;
+    case kFp8Rows12: NF4K_FLAGS(k_fp8_rows, 1, 2, 4, 3, false); break;
     case kFp8Rows14: NF4K_FLAGS(k_fp8_rows, 1, 4, 4, 3, false); break;
     case kFp8Rows22: NF4K_FLAGS(k_fp8_rows, 2, 2, 8, 2, false); break;
     case kFp8Rows42: NF4K_FLAGS(k_fp8_rows, 4, 2, 4, 3, false); break;

@@ -90,21 +90,24 @@ int rmsnorm_parts(int64_t M, int H) {
   return (int)(groups < 512 ? groups : 512);
 }
 
-// Tiles of the block-scaled product.  u0 and u1: microseconds a tile takes for
-// 128 of the contraction when few compute units have one and when all do.
+// Tiles of the block-scaled product, with what one was measured to take on an
+// MI355X: `start` microseconds around its loop, and u0 to u1 microseconds for
+// every 128 of the contraction, u0 when few compute units have a tile and u1 when
+// all do (4096- to 28672-column weights, 1 to 16384 rows).
 const Fp8Kind* fp8_kinds() {
   static const Fp8Kind kinds[kFp8Kinds] = {
-      {256, 256, 512, 1.20, 1.95},  // kFp8Wide8
-      {128, 256, 512, 0.75, 1.18},  // kFp8Wide4
-      {64, 256, 512, 0.55, 0.85},   // kFp8Wide2
-      {16, 16, 256, 0.05, 0.063},   // kFp8Rows11
-      {16, 64, 256, 0.11, 0.185},   // kFp8Rows14
-      {32, 32, 512, 0.10, 0.154},   // kFp8Rows22
-      {64, 32, 256, 0.18, 0.244},   // kFp8Rows42
-      {64, 64, 256, 0.27, 0.34},    // kFp8Rows44
-      {16, 64, 256, 0.25, 0.31},    // kFp8Rows14T
-      {32, 64, 256, 0.29, 0.345},   // kFp8Rows24T
-      {64, 64, 256, 0.40, 0.457},   // kFp8Rows44T
+      {256, 256, 512, 4.0, 1.20, 1.83},   // kFp8Wide8
+      {128, 256, 512, 3.0, 0.75, 1.10},   // kFp8Wide4
+      {64, 256, 512, 2.5, 0.52, 0.80},    // kFp8Wide2
+      {16, 16, 256, 0.2, 0.045, 0.060},   // kFp8Rows11
+      {16, 32, 256, 0.85, 0.06, 0.120},   // kFp8Rows12
+      {16, 64, 256, 0.8, 0.10, 0.170},    // kFp8Rows14
+      {32, 32, 512, 1.2, 0.09, 0.134},    // kFp8Rows22
+      {64, 32, 256, 1.0, 0.17, 0.225},    // kFp8Rows42
+      {64, 64, 256, 2.2, 0.24, 0.297},    // kFp8Rows44
+      {16, 64, 256, 1.0, 0.23, 0.280},    // kFp8Rows14T
+      {32, 64, 256, 1.2, 0.27, 0.310},    // kFp8Rows24T
+      {64, 64, 256, 2.2, 0.36, 0.400},    // kFp8Rows44T
   };
   return kinds;
 }
@@ -112,24 +115,30 @@ const Fp8Kind* fp8_kinds() {
 namespace {
 
 constexpr int kCUs = 256;
-constexpr double kFp8Start = 4.0;  // microseconds before and after the loop of a tile, launch included
+constexpr double kFp8Launch = 3.0;  // microseconds
 
-// whole sets of tiles over the compute units, and how full the last (or only) one makes them
+// the launch and every set of tiles that the compute units hold at once
 double fp8_time(int kind, int64_t tiles_m, int N, int K) {
   const Fp8Kind& k = fp8_kinds()[kind];
   const int64_t tiles = tiles_m * ((N + k.bn - 1) / k.bn);
   const double fill = tiles >= kCUs ? 1.0 : (double)tiles / kCUs;
-  return kFp8Start + (double)((tiles + kCUs - 1) / kCUs) * ((K + 127) / 128) * (k.u0 + (k.u1 - k.u0) * fill);
+  return kFp8Launch +
+         (double)((tiles + kCUs - 1) / kCUs) * (k.start + ((K + 127) / 128) * (k.u0 + (k.u1 - k.u0) * fill));
 }
 
 int fp8_best(int64_t M, int N, int K, bool transpose, int experts, double* time) {
-  // up to 4 rows the weight's stream is all: the narrowest tiles keep the most of it under way
-  const bool few = M <= 4 && !transpose && !experts;
-  int best = kFp8Rows11;
-  double least = -1.0;
+  int best = -1;
+  double least = 0;
   for (int i = 0; i < kFp8Kinds; ++i) {
-    const bool t = i >= kFp8Rows14T, wide = i <= kFp8Wide2;
-    if (few ? i != kFp8Rows11 : !wide && t != transpose) continue;
+    const bool wide = i <= kFp8Wide2, t = i >= kFp8Rows14T;
+    if (!wide && t != transpose) continue;
+    // Bound by the weight's stream, not by the tiles' own time: the kinds that put
+    // two workgroups on a compute unit, whose starts hide behind each other.  Up
+    // to 8 rows of one weight the narrowest (28672 x 8192, 1 row: 42 us against 45
+    // and 47 for 32 and 64 columns), few rows of many experts the next one (64
+    // experts of 1536 x 4096, 48 rows: 42 us against 52 and 46).
+    if (!transpose && !experts && M <= 8 && i != kFp8Rows11) continue;
+    if (!transpose && experts && M <= 4 * (int64_t)experts && i != kFp8Rows12) continue;
     const int64_t bm = fp8_kinds()[i].bm;
     int64_t tiles_m = (M + bm - 1) / bm;
     if (experts) {
@@ -139,7 +148,7 @@ int fp8_best(int64_t M, int N, int K, bool transpose, int experts, double* time)
       if (tiles_m < used) tiles_m = used;
     }
     const double x = fp8_time(i, tiles_m, N, K);
-    if (least < 0 || x < least) {
+    if (best < 0 || x < least) {
       least = x;
       best = i;
     }
