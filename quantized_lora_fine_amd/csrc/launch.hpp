@@ -166,8 +166,9 @@ NF4K_WEAK hipError_t launch_fp8_quantize(const void* X, bool bf16, int64_t rows,
 NF4K_WEAK hipError_t launch_fp8_dequantize(const uint8_t* codes, const float* scales, int64_t rows, int64_t cols,
                                            bool e5m2, int block_rows, bool bf16, void* out, hipStream_t st);
 
-// threads that hold one row of width H (16, 64, 256, 512 or 1024)
+// threads of a workgroup of the norm for rows of width H, and the rows it holds
 int rmsnorm_threads(int H);
+int rmsnorm_teams(int H);
 // workgroups of the norm's gradient, each with a partial dw [H]
 int rmsnorm_parts(int64_t M, int H);
 constexpr int kMaxNormWidth = 32768;  // 1024 threads, 4 chunks of 8 columns

@@ -33,22 +33,32 @@ __device__ __forceinline__ u32x4 narrow8(const float (&v)[8]) {
   return r;
 }
 
-// Sum over the TPR threads of a row, in a fixed order; every thread gets it.
-// TPR of 16 and 64 stay inside a wave; a larger TPR is the whole workgroup, and
-// `red` (one float per wave) must not be the one of the previous call.
+// How a row is held: TPR = 16 or 64 threads of a wave (several rows a workgroup,
+// no barrier), or TPR = 0: the whole workgroup, of as many waves as the row needs.
+// Every thread has NC chunks of 8 neighbouring columns, a row's width apart.
 template <int TPR>
-__device__ __forceinline__ float row_sum(float x, float* red) {
+__device__ __forceinline__ int row_threads() { return TPR ? TPR : (int)blockDim.x; }
+
+// Sum over the threads of a row, in a fixed order; every thread gets it.  `red`
+// (TPR = 0: a float for each of up to 16 waves, the unused ones zero) must not be
+// the one of the previous call.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float x, floatx4 (&red)[4]) {
 #pragma unroll
-  for (int o = 1; o < (TPR < 64 ? TPR : 64); o <<= 1) x += __shfl_xor(x, o);
-  if constexpr (TPR > 64) {
-    constexpr int W = TPR / 64;
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+  for (int o = 1; o < (TPR == 16 ? 16 : 64); o <<= 1) x += __shfl_xor(x, o);
+  if constexpr (TPR == 0) {
+    if ((threadIdx.x & 63) == 0) ((float*)red)[threadIdx.x >> 6] = x;
     __syncthreads();
-    x = red[0];
+    x = 0.f;
 #pragma unroll
-    for (int i = 1; i < W; ++i) x += red[i];
+    for (int i = 0; i < 4; ++i) x += (red[i].x + red[i].y) + (red[i].z + red[i].w);
   }
   return x;
+}
+template <int TPR>
+__device__ __forceinline__ void row_sum_init(floatx4 (&red)[4]) {
+  // waves that the workgroup does not have count as zero; the barrier in row_sum orders this
+  if (TPR == 0 && threadIdx.x < 16 && threadIdx.x >= (blockDim.x >> 6)) ((float*)red)[threadIdx.x] = 0.f;
 }
 
 struct NormArgs {
@@ -65,20 +75,21 @@ struct NormArgs {
   float* rstd;  // or NULL
 };
 
-// TPR threads hold a row in registers, NC chunks of 8 columns each; 16
-// neighbouring threads hold one block of the 8-bit output.
+// The row stays in registers; 16 neighbouring threads hold one block of the 8-bit
+// output.
 template <int TPR, int NC>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm(NormArgs p) {
-  constexpr int NT = TPR < 256 ? 256 : TPR;
-  __shared__ float red[TPR / 64 + 1];
-  const int64_t row = (int64_t)blockIdx.x * (NT / TPR) + threadIdx.x / TPR;
-  const int t = threadIdx.x % TPR;
-  if (row >= p.rows) return;  // whole rows of threads; with TPR > 64 the whole workgroup
+__global__ __launch_bounds__(TPR ? 256 : 1024) void k_rmsnorm(NormArgs p) {
+  __shared__ floatx4 red[4];
+  row_sum_init<TPR>(red);
+  const int T = row_threads<TPR>();
+  const int64_t row = TPR ? (int64_t)blockIdx.x * (256 / (TPR ? TPR : 1)) + threadIdx.x / (TPR ? TPR : 1) : blockIdx.x;
+  const int t = TPR ? threadIdx.x % (TPR ? TPR : 1) : threadIdx.x;
+  if (row >= p.rows) return;  // whole rows of threads (TPR = 0: no workgroup)
   const int64_t base = row * p.H;
   u32x4 hb[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int col = (c * TPR + t) * 8;
+    const int col = (c * T + t) * 8;
     hb[c] = u32x4{0u, 0u, 0u, 0u};
     if (col < p.H) hb[c] = *(const u32x4*)(p.X + base + col);
   }
@@ -86,7 +97,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm(NormArgs p) {
     u32x4 rb[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int col = (c * TPR + t) * 8;
+      const int col = (c * T + t) * 8;
       rb[c] = u32x4{0u, 0u, 0u, 0u};
       if (col < p.H) rb[c] = *(const u32x4*)(p.R + base + col);
     }
@@ -98,7 +109,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm(NormArgs p) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) a[j] += b[j];
       hb[c] = narrow8(a);
-      const int col = (c * TPR + t) * 8;
+      const int col = (c * T + t) * 8;
       if (col < p.H) *(u32x4*)(p.Hout + base + col) = hb[c];
     }
   }
@@ -116,7 +127,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm(NormArgs p) {
   const int64_t kb = (p.H + 127) / 128;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int col = (c * TPR + t) * 8;
+    const int col = (c * T + t) * 8;
     const bool in = col < p.H;
     float a[8], w[8];
     widen8(hb[c], a);
@@ -154,48 +165,76 @@ struct NormGradArgs {
   float* part;  // [gridDim.x][H]
 };
 
-// A workgroup takes every gridDim.x-th group of NT / TPR rows; each thread
-// keeps its columns' share of dw in registers over all of them.
+// A workgroup takes every gridDim.x-th row (TPR > 0: group of 256 / TPR rows), the
+// next one's loads under way while it works on one; each thread keeps its
+// columns' share of dw in registers over all of them.
 template <int TPR, int NC>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm_grad(NormGradArgs p) {
-  constexpr int NT = TPR < 256 ? 256 : TPR;
-  constexpr int TEAMS = NT / TPR;
-  __shared__ float red[2][TPR / 64 + 1];
-  const int team = threadIdx.x / TPR;
-  const int t = threadIdx.x % TPR;
+__global__ __launch_bounds__(TPR ? 256 : 1024) void k_rmsnorm_grad(NormGradArgs p) {
+  constexpr int TEAMS = TPR ? 256 / (TPR ? TPR : 1) : 1;
+  __shared__ floatx4 red[2][4];
+  row_sum_init<TPR>(red[0]);
+  row_sum_init<TPR>(red[1]);
+  const int T = row_threads<TPR>();
+  const int team = TPR ? threadIdx.x / (TPR ? TPR : 1) : 0;
+  const int t = TPR ? threadIdx.x % (TPR ? TPR : 1) : threadIdx.x;
+  constexpr bool kAhead = NC == 1;  // wider rows fill the registers as they are
   float dw[NC][8];
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[c][j] = 0.f;
+  // w stays in registers, or (NC = 4) comes from the caches for every row; a load
+  // in the loop waits for the next row's, which are older
+  u32x4 wb[NC];
+  auto load_weight = [&](int c) {
+    const int col = (c * T + t) * 8;
+    wb[c] = u32x4{0u, 0u, 0u, 0u};
+    if (col < p.H) wb[c] = *(const u32x4*)(p.w + col);
+  };
+#pragma unroll
+  for (int c = 0; c < NC; ++c) load_weight(c);
+  auto weight = [&](int c, float (&w)[8]) {
+    if constexpr (NC == 4) load_weight(c);
+    widen8(wb[c], w);
+  };
   const float invH = 1.f / (float)p.H;
-  int flip = 0;
-  for (int64_t row = (int64_t)blockIdx.x * TEAMS + team; row < p.rows; row += (int64_t)gridDim.x * TEAMS) {
+  const int64_t stride = (int64_t)gridDim.x * TEAMS;
+  struct Row {
+    u32x4 g[NC], h[NC], d[NC];
+    float rstd;
+  };
+  auto load = [&](int64_t row, Row& r) {
     const int64_t base = row * p.H;
-    const float rstd = p.rstd[row];
-    u32x4 gb[NC], hb[NC];
+    r.rstd = p.rstd[row];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int col = (c * TPR + t) * 8;
-      gb[c] = hb[c] = u32x4{0u, 0u, 0u, 0u};
+      const int col = (c * T + t) * 8;
+      r.g[c] = r.h[c] = r.d[c] = u32x4{0u, 0u, 0u, 0u};
       if (col < p.H) {
-        gb[c] = *(const u32x4*)(p.dY + base + col);
-        hb[c] = *(const u32x4*)(p.Hs + base + col);
+        r.g[c] = *(const u32x4*)(p.dY + base + col);
+        r.h[c] = *(const u32x4*)(p.Hs + base + col);
+        if (p.dH) r.d[c] = *(const u32x4*)(p.dH + base + col);
       }
     }
+  };
+  int flip = 0;
+  int64_t row = (int64_t)blockIdx.x * TEAMS + team;
+  Row cur;
+  if (kAhead && row < p.rows) load(row, cur);
+  for (; row < p.rows; row += stride) {
+    Row next;  // past the last row: that one again, so that no branch keeps the loads back
+    if constexpr (kAhead) load(min(row + stride, p.rows - 1), next);
+    else load(row, cur);
     float dot = 0.f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int col = (c * TPR + t) * 8;
       float g[8], h[8], w[8];
-      u32x4 wb = {0u, 0u, 0u, 0u};
-      if (col < p.H) wb = *(const u32x4*)(p.w + col);
-      widen8(gb[c], g);
-      widen8(hb[c], h);
-      widen8(wb, w);
+      widen8(cur.g[c], g);
+      widen8(cur.h[c], h);
+      weight(c, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float xhat = h[j] * rstd;
+        const float xhat = h[j] * cur.rstd;
         dot = __builtin_fmaf(g[j] * w[j], xhat, dot);
         dw[c][j] = __builtin_fmaf(g[j], xhat, dw[c][j]);
       }
@@ -204,17 +243,18 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm_grad(NormGrad
     flip ^= 1;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int col = (c * TPR + t) * 8;
+      const int col = (c * T + t) * 8;
       if (col >= p.H) continue;
-      float g[8], h[8], w[8], d[8] = {};
-      widen8(gb[c], g);
-      widen8(hb[c], h);
-      widen8(*(const u32x4*)(p.w + col), w);
-      if (p.dH) widen8(*(const u32x4*)(p.dH + base + col), d);
+      float g[8], h[8], d[8], w[8];
+      widen8(cur.g[c], g);
+      widen8(cur.h[c], h);
+      widen8(cur.d[c], d);
+      weight(c, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = __builtin_fmaf(rstd, g[j] * w[j] - h[j] * rstd * dot, d[j]);
-      *(u32x4*)(p.dX + base + col) = narrow8(d);
+      for (int j = 0; j < 8; ++j) d[j] = __builtin_fmaf(cur.rstd, g[j] * w[j] - h[j] * cur.rstd * dot, d[j]);
+      *(u32x4*)(p.dX + row * p.H + col) = narrow8(d);
     }
+    if constexpr (kAhead) cur = next;
   }
   if constexpr (TEAMS > 1) {
     __shared__ float sum[TEAMS][TPR * NC * 8];
@@ -223,15 +263,15 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm_grad(NormGrad
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum[team][(c * TPR + t) * 8 + j] = dw[c][j];
     __syncthreads();
-    for (int col = threadIdx.x; col < p.H; col += NT) {
-      float s = sum[0][col];
-      for (int k = 1; k < TEAMS; ++k) s += sum[k][col];
-      p.part[(int64_t)blockIdx.x * p.H + col] = s;
+    for (int col = threadIdx.x; col < p.H; col += 256) {
+      float x = sum[0][col];
+      for (int k = 1; k < TEAMS; ++k) x += sum[k][col];
+      p.part[(int64_t)blockIdx.x * p.H + col] = x;
     }
   } else {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int col = (c * TPR + t) * 8;
+      const int col = (c * T + t) * 8;
       if (col >= p.H) continue;
       floatx4* dst = (floatx4*)(p.part + (int64_t)blockIdx.x * p.H + col);
       dst[0] = floatx4{dw[c][0], dw[c][1], dw[c][2], dw[c][3]};
@@ -240,39 +280,52 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm_grad(NormGrad
   }
 }
 
-// dw[col] = sum of the parts in a fixed order: 16 waves, each every 16th part
+// dw[col] = sum of the n parts in a fixed order.  32 columns a workgroup, so that a
+// width of 4096 has 128 of them; 32 runs of lanes each take every 32nd part, 8
+// loads at a time.
 __global__ __launch_bounds__(1024) void k_rmsnorm_dw(const float* __restrict__ part, int n, int H,
                                                      float* __restrict__ dw) {
-  __shared__ float red[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int col = blockIdx.x * 64 + lane;
+  __shared__ float red[32][33];
+  const int l = threadIdx.x & 31, run = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + l;
   float s = 0.f;
-  if (col < H)
-    for (int i = wave; i < n; i += 16) s += part[(int64_t)i * H + col];
-  red[wave][lane] = s;
-  __syncthreads();
-  if (wave == 0 && col < H) {
-    for (int i = 1; i < 16; ++i) s += red[i][lane];
-    dw[col] = s;
+  if (col < H) {
+    for (int i0 = run; i0 < n; i0 += 32 * 8) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = i0 + 32 * u < n ? part[(int64_t)(i0 + 32 * u) * H + col] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += v[u];
+    }
   }
+  red[run][l] = s;
+  __syncthreads();
+  // run r of the workgroup joins column r: lane l has its share l
+  float x = red[l][run];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor(x, o);
+  if (l == 0 && blockIdx.x * 32 + run < H) dw[blockIdx.x * 32 + run] = x;
 }
 
 }  // namespace
 
-// the kernels' (threads per row, chunks) by width; see rmsnorm_threads
-#define NF4K_NORM_SHAPES(CALL)                         \
-  do {                                                 \
-    if (tpr == 16) CALL(16, 1);                        \
-    else if (tpr == 64) { if (H <= 512) CALL(64, 1); else CALL(64, 4); } \
-    else if (tpr == 256) { if (H <= 4096) CALL(256, 2); else CALL(256, 4); } \
-    else if (tpr == 512) CALL(512, 4);                 \
-    else CALL(1024, 4);                                \
+// the kernel for a width: rows by 16 or 64 threads of a wave up to 2048 columns, by
+// the workgroup beyond, with at most 1024 threads
+#define NF4K_NORM_SHAPES(CALL)         \
+  do {                                 \
+    if (H <= 128) CALL(16, 1);         \
+    else if (H <= 512) CALL(64, 1);    \
+    else if (H <= 1024) CALL(64, 2);   \
+    else if (H <= 2048) CALL(64, 4);   \
+    else if (H <= 8192) CALL(0, 1);    \
+    else if (H <= 16384) CALL(0, 2);   \
+    else CALL(0, 4);                   \
   } while (0)
 
 hipError_t launch_rmsnorm_fwd(const uint16_t* X, const uint16_t* R, const uint16_t* w, int64_t M, int H, float eps,
                               uint16_t* Hout, uint16_t* Y, uint8_t* codes, float* scales, float* rstd,
                               hipStream_t st) {
-  const int tpr = rmsnorm_threads(H), nt = std::max(tpr, 256), teams = nt / tpr;
+  const int nt = rmsnorm_threads(H), teams = rmsnorm_teams(H);
   const int64_t kb = (H + 127) / 128;
   constexpr int64_t kMost = (int64_t)1 << 21;  // workgroups a launch: its work-items stay below 2^32
   for (int64_t r0 = 0; r0 < M; r0 += kMost * teams) {
@@ -292,7 +345,7 @@ hipError_t launch_rmsnorm_fwd(const uint16_t* X, const uint16_t* R, const uint16
 hipError_t launch_rmsnorm_bwd(const uint16_t* dY, const uint16_t* Hs, const uint16_t* w, const float* rstd,
                               const uint16_t* dH, int64_t M, int H, uint16_t* dX, float* dw, float* part,
                               hipStream_t st) {
-  const int tpr = rmsnorm_threads(H), nt = std::max(tpr, 256);
+  const int nt = rmsnorm_threads(H);
   const int parts = rmsnorm_parts(M, H);
   NormGradArgs a{dY, Hs, w, rstd, dH, M, H, dX, part};
   const dim3 gr((unsigned)parts), bl(nt);
@@ -301,7 +354,7 @@ hipError_t launch_rmsnorm_bwd(const uint16_t* dY, const uint16_t* Hs, const uint
 #undef NF4K_CALL
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_rmsnorm_dw, dim3((unsigned)((H + 63) / 64)), dim3(1024), 0, st, part, parts, H, dw);
+  hipLaunchKernelGGL(k_rmsnorm_dw, dim3((unsigned)((H + 31) / 32)), dim3(1024), 0, st, part, parts, H, dw);
   return hipGetLastError();
 }
 
