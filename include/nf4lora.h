@@ -476,7 +476,9 @@ nf4_status nf4_probe_mfma_peak(int32_t iters, int32_t workgroups, float *out_dev
  *                      [ceil(rows / 128)][ceil(cols / 128)] (weights).
  *                Blocks at the right and lower edge are shorter.
  * cols is a multiple of 16 and at most 2^22; for the products the weight's rows
- * are too, and rows * cols is at most 2^32.
+ * are too, and rows * cols is at most 2^32.  Scales, rstd and offsets need 4-byte
+ * alignment only (an expert's part of a stack of scales starts anywhere); the
+ * other device pointers 16, as everywhere.
  */
 enum { NF4_FP8_E4M3 = 0, NF4_FP8_E5M2 = 1 };
 

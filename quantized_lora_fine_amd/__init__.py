@@ -552,11 +552,14 @@ def fp8_quantize(X: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = torc
     sshape = (rows if block_rows == 1 else _blocks(rows), _blocks(cols))
     if codes is None:
         codes = torch.empty((rows, cols), dtype=dtype, device=X.device)
+    else:
+        _held(codes, dtype, (rows, cols), dev, "codes")
     if scales is None:
         scales = torch.empty(sshape, dtype=torch.float32, device=X.device)
-    _check(_lib.nf4_fp8_quantize(x, bf16, rows, cols, f, block_rows, _held(codes, dtype, (rows, cols), dev, "codes"),
-                                 _held(scales, torch.float32, sshape, dev, "scales"), _raw_stream(dev)),
-           "nf4_fp8_quantize")
+    else:
+        _held(scales, torch.float32, sshape, dev, "scales")
+    _check(_lib.nf4_fp8_quantize(x, bf16, rows, cols, f, block_rows, codes.data_ptr(), scales.data_ptr(),
+                                 _raw_stream(dev)), "nf4_fp8_quantize")
     return codes, scales
 
 

@@ -21,6 +21,7 @@ constexpr int64_t kGroup = 256;
 constexpr size_t kCheckWorkspace = 256;  // nf4_check_finite: one int flag
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }  // scales and offsets: read and written one by one
 
 struct Range {
   uintptr_t lo, hi;
@@ -514,8 +515,8 @@ nf4_status fp8_product(const Fp8Gemm& q, int32_t a_format, void* stream) {
   if (q.M == 0) return NF4_OK;
   if (!q.A || !q.a_scales || !q.W || !q.w_scales || !q.C || (q.R > 0 && (!q.A2 || !q.B2))) return NF4_ERR_NULL;
   if (q.experts && !q.offsets) return NF4_ERR_NULL;
-  if (!aligned16(q.A) || !aligned16(q.a_scales) || !aligned16(q.W) || !aligned16(q.w_scales) || !aligned16(q.C) ||
-      (q.R > 0 && (!aligned16(q.A2) || !aligned16(q.B2))) || (q.experts && !aligned16(q.offsets)))
+  if (!aligned16(q.A) || !aligned4(q.a_scales) || !aligned16(q.W) || !aligned4(q.w_scales) || !aligned16(q.C) ||
+      (q.R > 0 && (!aligned16(q.A2) || !aligned16(q.B2))) || (q.experts && !aligned4(q.offsets)))
     return NF4_ERR_ALIGN;
   const int64_t K = q.transpose ? q.rows : q.cols, N = q.transpose ? q.cols : q.rows;
   const int64_t E = q.experts ? q.experts : 1;
@@ -940,7 +941,7 @@ nf4_status nf4_fp8_quantize(const void* X, int32_t x_is_bf16, int64_t rows, int6
   const int64_t n = rows * cols;
   if (n == 0) return NF4_OK;
   if (!X || !codes || !scales) return NF4_ERR_NULL;
-  if (!aligned16(X) || !aligned16(codes) || !aligned16(scales)) return NF4_ERR_ALIGN;
+  if (!aligned16(X) || !aligned16(codes) || !aligned4(scales)) return NF4_ERR_ALIGN;
   const Range ins[] = {rng(X, (size_t)n * (x_is_bf16 ? 2 : 4))};
   const Range outs[] = {rng(codes, (size_t)n), rng(scales, fp8_scale_bytes(rows, cols, block_rows))};
   st = check_alias(ins, outs);
@@ -957,7 +958,7 @@ nf4_status nf4_fp8_dequantize(const uint8_t* codes, const float* scales, int64_t
   const int64_t n = rows * cols;
   if (n == 0) return NF4_OK;
   if (!codes || !scales || !out) return NF4_ERR_NULL;
-  if (!aligned16(codes) || !aligned16(scales) || !aligned16(out)) return NF4_ERR_ALIGN;
+  if (!aligned16(codes) || !aligned4(scales) || !aligned16(out)) return NF4_ERR_ALIGN;
   const Range ins[] = {rng(codes, (size_t)n), rng(scales, fp8_scale_bytes(rows, cols, block_rows))};
   const Range outs[] = {rng(out, (size_t)n * (out_is_bf16 ? 2 : 4))};
   st = check_alias(ins, outs);
@@ -997,7 +998,7 @@ nf4_status nf4_rmsnorm_fwd(const uint16_t* X, const uint16_t* res, const uint16_
   if ((codes == nullptr) != (scales == nullptr) || (!Y && !codes)) return NF4_ERR_NULL;
   if (!res) H_out = nullptr;
   if (!aligned16(X) || !aligned16(res) || !aligned16(w) || !aligned16(H_out) || !aligned16(Y) || !aligned16(codes) ||
-      !aligned16(scales) || !aligned16(rstd))
+      !aligned4(scales) || !aligned4(rstd))
     return NF4_ERR_ALIGN;
   const size_t b = (size_t)(M * H * 2);
   const Range ins[] = {rng(X, b), rng(res, res ? b : 0), rng(w, (size_t)H * 2)};
@@ -1027,7 +1028,7 @@ nf4_status nf4_rmsnorm_bwd(const uint16_t* dY, const uint16_t* h, const uint16_t
   const size_t need = norm_ws(M, H);
   if (!ws || ws_bytes < need) return NF4_ERR_WORKSPACE;
   if (!aligned16(dw) || !aligned16(ws) ||
-      (M > 0 && (!aligned16(dY) || !aligned16(h) || !aligned16(w) || !aligned16(rstd) || !aligned16(dH) ||
+      (M > 0 && (!aligned16(dY) || !aligned16(h) || !aligned16(w) || !aligned4(rstd) || !aligned16(dH) ||
                  !aligned16(dX))))
     return NF4_ERR_ALIGN;
   const size_t b = (size_t)(M * H * 2);

@@ -20,6 +20,11 @@ GB = 1 << 30
 A, S, W, T, C, A2, B2, OFF = ((i + 1) * 64 * GB for i in range(8))  # aligned fake addresses, far apart
 
 
+def odd(name):
+    """An address that is not aligned enough: 4 bytes for scales, rstd and offsets, 16 for the others."""
+    return 64 * GB * 9 + (2 if name in ("scales", "s", "ws", "off", "rstd") else 8)
+
+
 def quantize(X=A, bf16=0, rows=8, cols=272, fmt=0, block_rows=1, codes=C, scales=S):
     return lib.nf4_fp8_quantize(X, bf16, rows, cols, fmt, block_rows, codes, scales, None)
 
@@ -50,7 +55,7 @@ def test_quantize_refuses(call, inp, out):
     for bad in ({"cols": 24}, {"rows": -1}, {"cols": -16}, {"cols": (1 << 22) + 16}, {"rows": (1 << 31), "cols": 1024}):
         assert call(**bad) == nf4.NF4_ERR_SHAPE, bad
     for p in (inp, "scales", out):
-        assert call(**{p: None}) == nf4.NF4_ERR_NULL and call(**{p: 64 * GB * 9 + 4}) == nf4.NF4_ERR_ALIGN
+        assert call(**{p: None}) == nf4.NF4_ERR_NULL and call(**{p: odd(p)}) == nf4.NF4_ERR_ALIGN
     assert call(**{out: A + 16}) == nf4.NF4_ERR_ALIAS
     assert call(rows=0) == nf4.NF4_OK and call(cols=0) == nf4.NF4_OK
     if call is quantize:
@@ -66,7 +71,7 @@ def test_products_refuse(call):
     ptrs = ["a", "s", "w", "ws", "a2", "b2", "c"] + (["off"] if call is grouped else [])
     for p in ptrs:
         assert call(**{p: None}) == nf4.NF4_ERR_NULL, p
-        assert call(**{p: 64 * GB * 9 + 8}) == nf4.NF4_ERR_ALIGN, p
+        assert call(**{p: odd(p)}) == nf4.NF4_ERR_ALIGN, p
     for p in ptrs[:-2] + ptrs[-1:]:
         if p != "c":
             assert call(c={"a": A, "s": S, "w": W, "ws": T, "a2": A2, "b2": B2, "off": OFF}[p]) == nf4.NF4_ERR_ALIAS, p
@@ -91,7 +96,7 @@ def test_norm_refuses():
                 {"Y": None, "codes": None, "scales": None}):
         assert norm(**bad) == nf4.NF4_ERR_NULL, bad
     for p in ("X", "res", "w", "h", "Y", "codes", "scales", "rstd"):
-        assert norm(**{p: 64 * GB * 9 + 4}) == nf4.NF4_ERR_ALIGN, p
+        assert norm(**{p: odd(p)}) == nf4.NF4_ERR_ALIGN, p
     for bad in ({"Y": A}, {"h": S}, {"codes": A + 64}, {"rstd": W}, {"h": C + 16}):
         assert norm(**bad) == nf4.NF4_ERR_ALIAS, bad
     assert norm(M=0) == nf4.NF4_OK
@@ -101,7 +106,7 @@ def test_norm_grad_refuses():
     for p in ("dY", "h", "w", "rstd", "dX", "dw"):
         assert norm_grad(**{p: None}) == nf4.NF4_ERR_NULL, p
     for p in ("dY", "h", "w", "rstd", "dH", "dX", "dw", "ws"):
-        assert norm_grad(**{p: 64 * GB * 9 + 4}) == nf4.NF4_ERR_ALIGN, p
+        assert norm_grad(**{p: odd(p)}) == nf4.NF4_ERR_ALIGN, p
     need = nf4.rmsnorm_workspace_bytes(8, 272)
     assert norm_grad(n=need - 1) == nf4.NF4_ERR_WORKSPACE and norm_grad(ws=None) == nf4.NF4_ERR_WORKSPACE
     for bad in ({"dX": A}, {"dX": C}, {"dw": T}, {"ws": S}, {"dw": OFF + 16}):

@@ -260,6 +260,38 @@ def test_matmul(M, o, h, R, fmt, transpose):
     assert torch.equal(nf4.fp8_matmul(*args).view(torch.int16), C.view(torch.int16))
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 48, 33024), (3, 272, 16400), (17, 144, 33040), (40, 80, 65680), (64, 272, 8208),
+                                   (300, 528, 16400), (520, 400, 8320), (1030, 1296, 9232)])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_matmul_long_contraction(M, N, K, transpose):
+    # beyond 64 blocks of the contraction the weight's scales are fetched again
+    o, h = (K, N) if transpose else (N, K)
+    a, s, w, ws, A2, B2 = product_case(M + K, M, o, h, transpose, 16, "e4m3")
+    want = fp8.matmul(a, s, "e4m3", w[0], ws[0], transpose, f64(A2), f64(B2[0]))
+    C = nf4.fp8_matmul(t8(a), torch.from_numpy(s).to(DEV), t8(w[0]), torch.from_numpy(ws[0]).to(DEV), transpose,
+                       A2.to(DEV), B2[0].to(DEV))
+    check_product(C, want, K, 16)
+
+
+@pytest.mark.parametrize("M,N,K,transpose", [  # one of every kind of tile, and of split rows
+    (8, 4096, 512, False), (16, 11008, 256, False), (32, 16384, 256, False), (64, 4096, 400, False),
+    (128, 4096, 272, False), (256, 8192, 272, False), (600, 11008, 144, False), (2048, 4096, 272, False),
+    (4096, 4096, 272, False), (4099, 4096, 1040, False), (16, 4096, 256, True), (128, 4096, 272, True),
+    (64, 11008, 272, True), (300, 8192, 144, True), (1024, 4096, 272, True), (2048, 4096, 272, True),
+    (4099, 4096, 1040, True), (64, 4096, 4096, False), (256, 4096, 4096, False), (32, 8192, 4096, False)])
+def test_matmul_tiles(M, N, K, transpose):
+    rng = np.random.default_rng(M + N)
+    o, h = (K, N) if transpose else (N, K)
+    X = torch.from_numpy(rows_of(rng, M, K)).to(DEV)
+    a, s = nf4.fp8_quantize(X)
+    w, ws = nf4.fp8_quantize(torch.from_numpy(0.02 * rng.standard_normal((o, h)).astype(np.float32)).to(DEV), 128)
+    C = nf4.fp8_matmul(a, s, w, ws, transpose)
+    # all of it against the dequantized values' product in fp64 on the device
+    A, W = nf4.fp8_dequantize(a, s).double(), nf4.fp8_dequantize(w, ws, 128).double()
+    W = W if transpose else W.t().contiguous()
+    check_product(C, (f64(A @ W), f64(A.abs() @ W.abs()), f64(((A * A) @ (W * W)).sqrt())), K, 0)
+
+
 @pytest.mark.parametrize("transpose", [False, True])
 def test_matmul_zero_blocks_and_nan(transpose):
     # a zero row and zero weight blocks give exact zeros; a NaN stays in its row
@@ -276,7 +308,7 @@ def test_matmul_zero_blocks_and_nan(transpose):
 
 GROUPED = [  # counts, rows before the first and behind the last
     ([5], 0, 0), ([0, 7, 0, 1], 0, 3), ([130, 0, 1, 64, 17], 2, 5), ([1] * 70, 0, 0), ([0] * 66 + [3], 1, 1),
-    ([300, 5, 129, 0, 0, 40], 0, 9), ([0, 0], 0, 4),
+    ([300, 5, 129, 0, 0, 40], 0, 9), ([0, 0], 0, 4), ([700, 0, 1], 5, 0), ([0] * 130 + [5, 0, 40], 0, 2),
 ]
 
 
@@ -301,6 +333,33 @@ def test_matmul_grouped(counts, before, after, o, h, R, fmt, transpose):
             check_product(out[r], want, h if not transpose else o, R)
     rest = torch.cat([out[:ends[0]], out[ends[-1]:]])
     assert torch.all(rest == 3.0)
+
+
+@pytest.mark.parametrize("counts,N,K", [([40] * 8, 1040, 1040), ([100, 0, 300, 7], 2064, 528), ([900, 0, 33, 1200], 2048, 272),
+                                        ([2000, 0, 1500, 33], 4096, 144), ([5000, 1, 0, 3000], 4096, 144)])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_matmul_grouped_tiles(counts, N, K, transpose):
+    rng = np.random.default_rng(sum(counts) + N)
+    E, M = len(counts), sum(counts) + 5
+    o, h = (K, N) if transpose else (N, K)
+    a, s = nf4.fp8_quantize(torch.from_numpy(rows_of(rng, M, K)).to(DEV))
+    W = torch.empty(E, o, h, dtype=torch.float8_e4m3fn, device=DEV)
+    ws = torch.empty(E, -(-o // 128), -(-h // 128), device=DEV)
+    for e in range(E):
+        x = torch.from_numpy(0.02 * rng.standard_normal((o, h)).astype(np.float32)).to(DEV)
+        nf4.fp8_quantize(x, 128, codes=W[e], scales=ws[e])
+    ends = np.concatenate([[0], np.cumsum(counts)])
+    offsets = torch.from_numpy(ends.astype(np.int32)).to(DEV)
+    out = torch.full((M, N), 3.0, dtype=torch.bfloat16, device=DEV)
+    nf4.fp8_matmul_grouped(a, s, W, ws, offsets, transpose, out=out)
+    A = nf4.fp8_dequantize(a, s).double()
+    for e in range(E):
+        if counts[e]:
+            D, X = nf4.fp8_dequantize(W[e], ws[e], 128).double(), A[ends[e]:ends[e + 1]]
+            D = D if transpose else D.t().contiguous()
+            check_product(out[ends[e]:ends[e + 1]],
+                          (f64(X @ D), f64(X.abs() @ D.abs()), f64(((X * X) @ (D * D)).sqrt())), K, 0)
+    assert torch.all(out[ends[-1]:] == 3.0)
 
 
 def test_matmul_grouped_offsets_outside():
