@@ -21,7 +21,8 @@
  *   L2 [r][o] are row-major bf16; dL1 [h][r] and dL2 [r][o] are fp32.
  * - Every pointer argument except the nf4_tensor descriptor itself and the
  *   host scalars is a DEVICE pointer, and every device base pointer must be
- *   16-byte aligned (NF4_ERR_ALIGN otherwise).
+ *   16-byte aligned (NF4_ERR_ALIGN otherwise; the scales of 8-bit storage need
+ *   4 bytes, see there).
  * - The caller owns every buffer.  The library allocates and frees nothing,
  *   keeps no mutable global state, and is safe to call from several host
  *   threads (calls on one stream run in stream order).
@@ -530,8 +531,8 @@ nf4_status nf4_fp8_matmul(const uint8_t *A, int32_t a_format, const float *a_sca
  *             Read by the kernels, so nothing waits for the routing.  Rows before
  *             offsets[0] and from offsets[experts] on are neither read nor
  *             written.  Offsets outside [0, M] are taken as the nearest of the
- *             two; where they do not ascend, which rows of C are written is
- *             unspecified (never any outside C).
+ *             two; where they do not ascend, which rows of C are written, and
+ *             with what, is unspecified (never any outside C).
  *   experts : 1 .. 4096;  M <= 2^31 - 1.
  * Errors as nf4_fp8_matmul.
  */

@@ -83,7 +83,8 @@ __device__ __forceinline__ bool find_tile(const Args& p, int bm, int t, int& e, 
       e = e0 + l;
       m0 = (int64_t)l0 + (int64_t)(t - first) * bm;
       m1 = min(m0 + bm, (int64_t)l0 + ln);
-      return true;
+      // (offsets that do not ascend can make the counts overflow: still inside)
+      return m0 >= l0 && m0 < m1;
     }
     base += __builtin_amdgcn_readlane(incl, 63);
   }

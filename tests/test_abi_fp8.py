@@ -8,7 +8,8 @@ import sys
 
 import pytest
 
-from tests.test_host_sanitized import GXX, ROCM, ROOT, SAN_ENV, _run, san_build  # noqa: F401  (the fixture)
+from tests.test_host_sanitized import (COMMON, CSRC, GXX, HOST, ROCM, ROOT, SAN, SAN_ENV, _run,  # noqa: F401
+                                       san_build)
 
 nf4 = pytest.importorskip("quantized_lora_fine_amd", reason="libnf4lora.so not built")
 lib = nf4._lib
@@ -138,3 +139,10 @@ def test_sanitized_build_without_kernels_reports_hip(san_build):  # noqa: F811
     env = {**os.environ, **SAN_ENV, "NF4LORA_LIB": san_build[0], "LD_PRELOAD": asan}
     assert "ok" in _run([sys.executable, "-c", code], env=env, cwd=ROOT)
 
+
+
+@needs_host_build
+def test_plan_units_sanitized(tmp_path):
+    exe = str(tmp_path / "fp8_plan_units")
+    _run([GXX, *COMMON, *SAN, "-o", exe, os.path.join(HOST, "fp8_plan_units.cpp"), os.path.join(CSRC, "plan.cpp")])
+    assert "fp8 plan units: ok" in _run([exe], env={**os.environ, **SAN_ENV})
