@@ -486,7 +486,7 @@ enum { NF4_FP8_E4M3 = 0, NF4_FP8_E5M2 = 1 };
 /*
  * Quantize X [rows][cols] (bf16 when x_is_bf16, else fp32).  Per block:
  *   amax  = max(max |x|, 2^-100),  scale = fl32(amax / F),
- *   code  = the nearest 8-bit value to fl32(x * fl32(F / amax)), ties to even.
+ *   code  = the nearest 8-bit value to fl32(x * fl32(F * fl32(1 / amax))), ties to even.
  * A block of zeros has codes 0 and the scale 2^-100 / F.  A NaN becomes a NaN
  * code and leaves its block's scale alone; an infinity makes its whole block
  * NaN when dequantized.  rows * cols is at most 2^40.

@@ -4,7 +4,7 @@ Codes are OCP 8-bit floats in blocks of 128 columns of one row (block_rows = 1)
 or of 128 rows (block_rows = 128), one fp32 scale per block:
 
     amax = max(max |x|, 2^-100), scale = fl32(amax / F),
-    code = nearest 8-bit value to fl32(x * fl32(F / amax)), ties to even.
+    code = nearest 8-bit value to fl32(x * fl32(F * fl32(1 / amax))), ties to even.
 
 A NaN keeps its sign-less NaN code and does not count for its block's amax.
 """
@@ -67,7 +67,7 @@ def block_scales(x: np.ndarray, block_rows: int, fmt: str):
             amax[i, j] = b.max() if b.size else 0.0
     amax = np.maximum(amax, FLOOR)
     with np.errstate(over="ignore"):
-        return (amax / F).astype(np.float32), (F / amax).astype(np.float32)
+        return (amax / F).astype(np.float32), F * (np.float32(1.0) / amax)
 
 
 def quantize(x: np.ndarray, block_rows: int, fmt: str):

@@ -60,12 +60,16 @@ __device__ __forceinline__ float row16_max(float x) {
 
 // Scale and multiplier of a block whose largest magnitude is amax: codes are
 // rne8(fl32(x * mul)) and stand for code * scale.  Both quotients are IEEE
-// divisions, so another implementation of the format gives the same codes.
+// divisions, and the multiplier is the reciprocal's product with F, which is
+// what an array library computes for `F / amax` with a plain number F: such a
+// program gets the same codes.  (F / amax rounded once instead differs in the
+// last bit for a part of the blocks, and a code in a million falls on the other
+// side of a tie.)
 template <bool E5M2>
 __device__ __forceinline__ void fp8_scale(float amax, float& scale, float& mul) {
   const float m = fmaxf(amax, kFp8Floor);
   scale = m / fp8_max<E5M2>();
-  mul = fp8_max<E5M2>() / m;
+  mul = fp8_max<E5M2>() * (1.f / m);
 }
 
 __device__ __forceinline__ float abs_max4(float a, float b, float c, float d) {

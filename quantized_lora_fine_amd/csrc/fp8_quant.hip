@@ -4,8 +4,8 @@
 // the blocks at the right and lower edge are shorter.  With F the format's
 // largest value,
 //     amax = max(max |x| over the block, 2^-100),  scale = amax / F,
-//     code = rne8(x * (F / amax)),
-// the quotients and the product rounded to fp32.
+//     code = rne8(x * (F * (1 / amax))),
+// each quotient and product rounded to fp32.
 #include <algorithm>
 #include <type_traits>
 

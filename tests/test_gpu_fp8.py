@@ -80,6 +80,17 @@ def test_quantize(rows, cols, bf16, block_rows, fmt):
     assert torch.equal(db.cpu().view(torch.int16), bf16_np(dw).view(torch.int16))
 
 
+@pytest.mark.parametrize("fmt,most", [("e4m3", 448.0), ("e5m2", 57344.0)])
+def test_quantize_as_an_array_expression(fmt, most):
+    # enough values that a multiplier off by its last bit would move some codes over a tie
+    g = torch.Generator(device=DEV).manual_seed(11)
+    x = torch.randn(4096, 4096, generator=g, device=DEV)
+    b = x.view(4096, 32, 128)
+    amax = b.abs().amax(2, keepdim=True).clamp_min(2.0 ** -100)
+    codes, _ = nf4.fp8_quantize(x, 1, DTYPES[fmt])
+    assert np.array_equal(bits(codes), bits((b * (most / amax)).to(DTYPES[fmt]).view(4096, 4096)))
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 def test_quantize_every_code_and_tie(fmt):
     # a block whose largest value is F has scale 1: its codes are the rounding itself
