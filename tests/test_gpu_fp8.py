@@ -174,6 +174,22 @@ def test_rmsnorm(M, H, residual):
     assert np.array_equal(bits(c1), bits(codes)) and torch.equal(s1, scales)
 
 
+def test_rmsnorm_rounds_once():
+    # codes against those of y in 64 bits: a fp32 value of y and its product with the multiplier, at most 2^-23 off
+    # together, move a value over a tie where it lies within 2^-23 * |v| of one; ties are 2^-4 |v| apart or more, so
+    # at most 2 * 2^-23 * 2^4 of the values lie there: 4 of a million, 1.3 of these.  (With rstd and the
+    # two products in fp32 as well, it is 50 of a million.)
+    rng = np.random.default_rng(5)
+    M, H = 84, 4096
+    X, w = bf16_np(rows_of(rng, M, H)), bf16_np(1 + 0.1 * rng.standard_normal(H))
+    _, _, codes, _, rstd = nf4.rmsnorm_fwd(X.to(DEV), w.to(DEV), 1e-6, want_y=False, want_fp8=True, want_rstd=True)
+    y, r = fp8.rmsnorm(f64(X), f64(w), 1e-6)
+    _, mul = fp8.block_scales(y.astype(np.float32), 1, "e4m3")
+    want = fp8.encode((y * fp8._spread(mul, 1, M, H).astype(np.float64)).astype(np.float32), "e4m3")
+    assert np.sum(bits(codes) != want) <= 6  # of 1.3 expected at most, more than 6 in one of 10^3 draws
+    check_within("rstd", rstd, r, np.abs(r) * 2.0 ** -24 * (1 + 2.0 ** -16))
+
+
 def test_rmsnorm_rows_of_zeros():
     X = torch.zeros(3, 256, dtype=torch.bfloat16, device=DEV)
     X[1] = 2.0
