@@ -496,6 +496,9 @@ __global__ __launch_bounds__(NWV * 64) void k_fp8_rows(Args p) {
   const int t_row = lane >> 2;
   const int t_col = n0 + ((lane & 3) ^ ((t_row >> 2) & 3)) * 16;
   const uint32_t t_off = t_col < N ? (uint32_t)(t_row * N + t_col) : kOOB;
+  // (a branch around the other lanes would make the compiler's own waits count this
+  // load as one that may not be there)
+  const uint32_t s_off = lane < BM ? (uint32_t)(lane * KB * 4) : kOOB;
   auto lbuf = [&](int b) -> uint8_t* { return (b == 0 ? L0 : b == 1 ? L1 : b == 2 ? L2 : L3) + wave * WB; };
   constexpr int LOADS = 2 * MT + 2 * NT + 1;
   auto copy = [&](int kt, int b) {
@@ -519,8 +522,7 @@ __global__ __launch_bounds__(NWV * 64) void k_fp8_rows(Args p) {
 #pragma unroll
     for (int i = 0; i < 2 * MT; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (lds_ptr_t)(to + i * 1024), 16, off, kt * 128 + i * 8 * K, 0, 0);
-    if (lane < BM)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (lds_ptr_t)(to + SOFF), 4, (uint32_t)(lane * KB * 4), kt * 4, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (lds_ptr_t)(to + SOFF), 4, s_off, kt * 4, 0, 0);
   };
   // W scales of this wave's rounds, one a lane
   const int nb = n0 >> 7;
@@ -638,6 +640,208 @@ __global__ __launch_bounds__(NWV * 64) void k_fp8_rows(Args p) {
   }
 }
 
+// Tiles of 128 x 128 and 128 x 64, not transposed, for products whose 256-column
+// tiles would leave compute units without one.  8 waves share the operands of a
+// step, which go through a ring of ST buffers, ST - 1 steps under way.  A step has
+// one barrier; its fragments were read during the step before it.  Bound by LDS: a
+// step of a 128 x 64 tile takes 0.33 us, of which 64 KB of fragments and 24 KB of
+// copies are 0.3.  (4 waves with tiles twice as large read less, but wait for
+// themselves: 0.53 us.  64 x 64 tiles, 0.20 us, are no better than k_fp8_rows';
+// transposed, the 8-byte reads of W make a step 0.75 us, more than k_fp8_rows
+// needs.)  128 rows by 9104 x 5888: 33 us, 415 TFLOP/s, against 39 for the best of
+// the other tiles; 512 rows by 4096 x 4096: 18 against 23.
+template <int BM, int BN, int ST, bool E5M2, bool GROUPED>
+__global__ __launch_bounds__(512) void k_fp8_ring(Args p) {
+  constexpr int NW = 8;
+  constexpr int WR = BN == 64 ? 4 : 2, WC = NW / WR;  // waves below and beside each other
+  constexpr int MI = BM / WR / 16, NI = BN / WC / 16;
+  constexpr int AI = BM / 64, WI = BN / 64;  // 1 KB copies of a wave and step
+  constexpr int SR = BM / NW;                // A scales a wave copies
+  constexpr int WOFF = BM * 128, SOFF = WOFF + BN * 128, SB = SOFF + NW * 256;
+  static_assert(ST % 2 == 0, "the fragments' registers alternate with the buffers");
+  __shared__ __attribute__((aligned(1024))) uint8_t L0[SB];
+  __shared__ __attribute__((aligned(1024))) uint8_t L1[SB];
+  __shared__ __attribute__((aligned(1024))) uint8_t L2[SB];
+  __shared__ __attribute__((aligned(1024))) uint8_t L3[SB];
+  __shared__ __attribute__((aligned(1024))) uint8_t L4[ST > 4 ? SB : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t L5[ST > 4 ? SB : 16];
+  auto lbuf = [&](int b) -> uint8_t* {
+    return b == 0 ? L0 : b == 1 ? L1 : b == 2 ? L2 : b == 3 ? L3 : b == 4 ? L4 : L5;
+  };
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % WR, wn = wave / WR;
+  const int g = lane >> 4, l16 = lane & 15;
+  const int tiles_m = (int)gridDim.x / p.tiles_n;
+  int tm, tn;
+  tile_of(GROUPED, tiles_m, p.tiles_n, tm, tn);
+  const int n0 = tn * BN;
+  const int N = p.N, K = p.K;
+  const int KB = (K + 127) / 128;
+  const int NB = (N + 127) / 128;
+  int e = 0;
+  int64_t m0, m1;
+  if constexpr (GROUPED) {
+    if (!find_tile(p, BM, tm, e, m0, m1)) return;
+  } else {
+    m0 = (int64_t)tm * BM;
+    m1 = min(m0 + BM, p.M);
+  }
+  const int mrows = (int)(m1 - m0);
+  const int nrows = min(BN, N - n0);
+  const uint8_t* W = p.W + (GROUPED ? (int64_t)e * N * K : 0);
+  const float* ws = p.ws + (GROUPED ? (int64_t)e * NB * KB : 0);
+  const __amdgpu_buffer_rsrc_t ar = make_rsrc(p.A + m0 * K, (uint32_t)((int64_t)mrows * K));
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc(W + (int64_t)n0 * K, (uint32_t)((int64_t)nrows * K));
+  const __amdgpu_buffer_rsrc_t sr = make_rsrc(p.as + m0 * KB, (uint32_t)((int64_t)mrows * KB * 4));
+
+  // copies and fragments as in k_fp8_wide
+  const int c_row = wave * 8 + (lane >> 3);  // of copy i: plus i * 64
+  const int c_chunk = (lane & 7) ^ (c_row & 7);
+  const uint32_t c_off = (uint32_t)(c_row * K + c_chunk * 16);
+  const uint32_t s_off = lane < SR ? (uint32_t)((wave * SR + lane) * KB * 4) : kOOB;
+  constexpr int C = AI + WI + 1;  // loads a step
+  auto copy = [&](int kt, int b) {
+    kt = min(kt, KB - 1);  // a step behind the last copies it once more, and is not used
+    uint8_t* const to = lbuf(b);
+    const uint32_t off = kt * 128 + c_chunk * 16 < K ? c_off : kOOB;
+#pragma unroll
+    for (int i = 0; i < AI; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (lds_ptr_t)(to + (i * NW + wave) * 1024), 16, off,
+                                               kt * 128 + i * 64 * K, 0, 0);
+#pragma unroll
+    for (int i = 0; i < WI; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_ptr_t)(to + WOFF + (i * NW + wave) * 1024), 16, off,
+                                               kt * 128 + i * 64 * K, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (lds_ptr_t)(to + SOFF + wave * 256), 4, s_off, kt * 4, 0, 0);
+  };
+  const int nb = n0 >> 7;
+  auto load_ws = [&](int kt) -> float {
+    return ws[(int64_t)nb * KB + min(kt + lane, KB - 1)];
+  };
+
+  constexpr int WN = BN / WC;  // columns of a wave
+  const uint32_t fa_at = (uint32_t)((wm * MI * 16 + l16) * 128 + ((g ^ (l16 & 7)) << 4));
+  const uint32_t fw_at = (uint32_t)((wn * WN + l16) * 128 + ((g ^ (l16 & 7)) << 4));
+  auto frag = [&](const uint8_t* at, uint32_t o, int i) -> i32x8 {
+    const u32x4 lo = *(const u32x4*)(at + o + i * 2048);
+    const u32x4 hi = *(const u32x4*)(at + (o ^ 64) + i * 2048);
+    return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+  };
+  floatx4 acc[MI][NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+  i32x8 fa[2][MI], fw[2][NI];
+  float s[2][MI];
+  auto read = [&](int b, int x) {
+    uint8_t* const at = lbuf(b);
+#pragma unroll
+    for (int j = 0; j < NI; ++j) fw[x][j] = frag(at + WOFF, fw_at, j);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      fa[x][i] = frag(at, fa_at, i);
+      const int r = (wm * MI + i) * 16 + l16;
+      s[x][i] = *(const float*)(at + SOFF + r / SR * 256 + r % SR * 4);
+    }
+  };
+  // every wave's copies but those of the `ahead` newest steps are there, and every
+  // wave's reads so far are done
+  auto barrier = [&](auto ahead) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(wait_vm(decltype(ahead)::value * C) & kWaitLds);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  float wsr = load_ws(0);
+#pragma unroll
+  for (int b = 0; b < ST; ++b) copy(b, b);
+  barrier(std::integral_constant<int, ST - 1>{});
+  read(0, 0);
+  auto step = [&](int kt, int b) {
+    const int x = b & 1;
+    __builtin_amdgcn_sched_barrier(0);
+    barrier(std::integral_constant<int, ST - 2>{});  // step kt + 1 is there, the reads of step kt are done
+    copy(kt + ST, b);
+    __builtin_amdgcn_sched_barrier(0);
+    read((b + 1) % ST, x ^ 1);
+    const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wsr), kt & 63));
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const float sc = s[x][i] * w;
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        const floatx4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            fw[x][j], fa[x][i], floatx4{0.f, 0.f, 0.f, 0.f}, 0, E5M2 ? 1 : 0, 0, 0, 0, 0);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(d[v], sc, acc[i][j][v]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) asm volatile("" : "+v"(acc[i][j]));
+    if (((kt + 1) & 63) == 0) {
+      wsr = load_ws(kt + 1);
+      __builtin_amdgcn_s_waitcnt(wait_vm(0));
+    }
+  };
+  int kt = 0;
+  for (; kt + ST <= KB; kt += ST) {
+#pragma unroll
+    for (int b = 0; b < ST; ++b) step(kt + b, b);
+  }
+#pragma unroll
+  for (int b = 0; b < ST - 1; ++b)
+    if (kt + b < KB) step(kt + b, b);
+  __builtin_amdgcn_s_waitcnt(wait_vm(0));
+
+  if (p.R) {
+    const __amdgpu_buffer_rsrc_t a2 = make_rsrc(p.A2 + m0 * p.R, (uint32_t)((int64_t)mrows * p.R * 2));
+    const __amdgpu_buffer_rsrc_t b2 =
+        make_rsrc(p.B2 + ((GROUPED ? (int64_t)e * N : 0) + n0) * p.R, (uint32_t)((int64_t)nrows * p.R * 2));
+    for (int k0 = 0; k0 < p.R; k0 += 32) {
+      const int k = k0 + 8 * g;
+      bf16x8 fb[NI];
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+        fb[j] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(
+            b2, k < p.R ? (uint32_t)(((wn * WN + j * 16 + l16) * p.R + k) * 2) : kOOB, 0, 0));
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const bf16x8 f = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(
+            a2, k < p.R ? (uint32_t)((((wm * MI + i) * 16 + l16) * p.R + k) * 2) : kOOB, 0, 0));
+#pragma unroll
+        for (int j = 0; j < NI; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], f, acc[i][j], 0, 0, 0);
+      }
+    }
+  }
+
+  __syncthreads();  // every wave is done with the buffers: the result tile goes through the first
+  constexpr int PC = BN / 8;  // 16-byte pieces of a row
+  static_assert(BM * BN * 2 <= SB, "the result tile fits");
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const int r = (wm * MI + i) * 16 + l16;
+      const int piece = wn * (WN / 8) + j * 2 + (g >> 1);
+      uint2 o;
+      o.x = pack_bf16x2(acc[i][j][0], acc[i][j][1]);
+      o.y = pack_bf16x2(acc[i][j][2], acc[i][j][3]);
+      *(uint2*)(L0 + r * (BN * 2) + ((piece ^ (r & (PC - 1))) << 4) + (g & 1) * 8) = o;
+    }
+  __syncthreads();
+#pragma unroll
+  for (int q = threadIdx.x; q < BM * PC; q += 512) {
+    const int r = q / PC, piece = q % PC;
+    const int n = n0 + piece * 8;
+    if (r < mrows && n < N)
+      *(u32x4*)(p.C + (m0 + r) * N + n) = *(const u32x4*)(L0 + r * (BN * 2) + ((piece ^ (r & (PC - 1))) << 4));
+  }
+}
+
 // one launch of tile kind `kind` over all of p's rows
 hipError_t launch_part(const Fp8Gemm& q, Args p, int kind, hipStream_t st) {
   const Fp8Kind& k = fp8_kinds()[kind];
@@ -666,9 +870,10 @@ hipError_t launch_part(const Fp8Gemm& q, Args p, int kind, hipStream_t st) {
     case kFp8Wide8: NF4K_WIDE(8); break;
     case kFp8Wide4: NF4K_WIDE(4); break;
     case kFp8Wide2: NF4K_WIDE(2); break;
+    case kFp8Ring22: NF4K_FLAGS(k_fp8_ring, 128, 128, 4); break;
+    case kFp8Ring21: NF4K_FLAGS(k_fp8_ring, 128, 64, 6); break;
     case kFp8Rows11: NF4K_FLAGS(k_fp8_rows, 1, 1, 4, 4, false); break;
     case kFp8Rows12: NF4K_FLAGS(k_fp8_rows, 1, 2, 4, 3, false); break;
-    case kFp8Rows14: NF4K_FLAGS(k_fp8_rows, 1, 4, 4, 3, false); break;
     case kFp8Rows22: NF4K_FLAGS(k_fp8_rows, 2, 2, 8, 2, false); break;
     case kFp8Rows42: NF4K_FLAGS(k_fp8_rows, 4, 2, 4, 3, false); break;
     case kFp8Rows44: NF4K_FLAGS(k_fp8_rows, 4, 4, 4, 2, false); break;

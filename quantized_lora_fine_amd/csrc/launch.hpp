@@ -202,7 +202,7 @@ struct Fp8Gemm {
 // the costs say takes the least time.  Returns the number of parts (their rows
 // add up to M).  experts > 0: one kind for all.
 enum {
-  kFp8Wide8, kFp8Wide4, kFp8Wide2, kFp8Rows11, kFp8Rows12, kFp8Rows14, kFp8Rows22, kFp8Rows42, kFp8Rows44,
+  kFp8Wide8, kFp8Wide4, kFp8Wide2, kFp8Ring22, kFp8Ring21, kFp8Rows11, kFp8Rows12, kFp8Rows22, kFp8Rows42, kFp8Rows44,
   kFp8Rows14T, kFp8Rows24T, kFp8Rows44T, kFp8Kinds
 };
 struct Fp8Kind {

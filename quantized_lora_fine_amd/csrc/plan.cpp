@@ -95,24 +95,27 @@ int rmsnorm_parts(int64_t M, int H) {
   return (int)(groups < most ? groups : most);
 }
 
-// Tiles of the block-scaled product, with what one was measured to take on an
-// MI355X: `start` microseconds around its loop, and u0 to u1 microseconds for
-// every 128 of the contraction, u0 when few compute units have a tile and u1 when
-// all do (4096- to 28672-column weights, 1 to 16384 rows).
+// Tiles of the block-scaled product, with what one takes on an MI355X: `start`
+// microseconds around its loop, and u0 to u1 microseconds for every 128 of the
+// contraction, u0 when few compute units have a tile and u1 when all do.  Fitted
+// to the times of every kind for 1 to 8192 rows by 12 weights of 560 x 1200 to
+// 28672 x 8192, each way; the kind that these costs choose is 1 % slower than the
+// fastest one in the mean, 23 % at worst (160 rows by 9104 x 5888).
 const Fp8Kind* fp8_kinds() {
   static const Fp8Kind kinds[kFp8Kinds] = {
-      {256, 256, 512, 4.0, 1.20, 1.83},   // kFp8Wide8
-      {128, 256, 512, 3.0, 0.75, 1.10},   // kFp8Wide4
-      {64, 256, 512, 2.5, 0.52, 0.80},    // kFp8Wide2
-      {16, 16, 256, 0.2, 0.045, 0.060},   // kFp8Rows11
-      {16, 32, 256, 0.85, 0.06, 0.120},   // kFp8Rows12
-      {16, 64, 256, 0.8, 0.10, 0.170},    // kFp8Rows14
-      {32, 32, 512, 1.2, 0.09, 0.134},    // kFp8Rows22
-      {64, 32, 256, 1.0, 0.17, 0.225},    // kFp8Rows42
-      {64, 64, 256, 2.2, 0.24, 0.297},    // kFp8Rows44
-      {16, 64, 256, 1.0, 0.23, 0.280},    // kFp8Rows14T
-      {32, 64, 256, 1.2, 0.27, 0.310},    // kFp8Rows24T
-      {64, 64, 256, 2.2, 0.36, 0.400},    // kFp8Rows44T
+      {256, 256, 512, 4.6, 1.11, 1.66},   // kFp8Wide8
+      {128, 256, 512, 2.3, 0.81, 1.04},   // kFp8Wide4
+      {64, 256, 512, 1.1, 0.69, 0.78},    // kFp8Wide2
+      {128, 128, 512, 1.3, 0.54, 0.71},   // kFp8Ring22
+      {128, 64, 512, 1.2, 0.33, 0.47},    // kFp8Ring21
+      {16, 16, 256, 0.4, 0.040, 0.053},   // kFp8Rows11
+      {16, 32, 256, 0.3, 0.070, 0.080},   // kFp8Rows12
+      {32, 32, 512, 0.3, 0.083, 0.144},   // kFp8Rows22
+      {64, 32, 256, 1.2, 0.133, 0.197},   // kFp8Rows42
+      {64, 64, 256, 1.8, 0.234, 0.291},   // kFp8Rows44
+      {16, 64, 256, 0.8, 0.220, 0.259},   // kFp8Rows14T
+      {32, 64, 256, 1.3, 0.259, 0.320},   // kFp8Rows24T
+      {64, 64, 256, 2.0, 0.349, 0.420},   // kFp8Rows44T
   };
   return kinds;
 }
