@@ -143,16 +143,18 @@ int fp8_best(int64_t M, int N, int K, bool transpose, int experts, double* time)
     // Bound by the weight's stream, not by the tiles' own time: the kinds that put
     // two workgroups on a compute unit, whose starts hide behind each other.  Up
     // to 8 rows of one weight the narrowest (28672 x 8192, 1 row: 42 us against 45
-    // and 47 for 32 and 64 columns), few rows of many experts the next one (64
-    // experts of 1536 x 4096, 48 rows: 42 us against 52 and 46).
+    // and 51 for 32 columns by 16 and by 32 rows), few rows of many experts the next
+    // one (64 experts of 1536 x 4096, 48 rows: 34 us against 39 and 43).
     if (!transpose && !experts && M <= 8 && i != kFp8Rows11) continue;
     if (!transpose && experts && M <= 4 * (int64_t)experts && i != kFp8Rows12) continue;
     const int64_t bm = fp8_kinds()[i].bm;
     int64_t tiles_m = (M + bm - 1) / bm;
     if (experts) {
-      // the rows' tiles, and half a tile more for every expert that can have rows
+      // the rows' tiles, half a tile more for every expert that can have rows, and a
+      // tenth: the counts are not known, and one tile past a set costs a set (32
+      // experts of 2048 x 4096, 4096 rows: 90 us against 115 without it)
       const int64_t used = M < experts ? M : experts;
-      tiles_m = M / bm + used / 2;
+      tiles_m = (M / bm + used / 2) * 11 / 10;
       if (tiles_m < used) tiles_m = used;
     }
     const double x = fp8_time(i, tiles_m, N, K);
