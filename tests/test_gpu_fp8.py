@@ -319,6 +319,58 @@ def test_matmul_tiles(M, N, K, transpose):
     check_product(C, (f64(A @ W), f64(A.abs() @ W.abs()), f64(((A * A) @ (W * W)).sqrt())), K, 0)
 
 
+EVERY_TILE = [  # M, N, K, transpose, experts: each kind of tile, dense and grouped
+    (5000, 1552, 1040, False, 0), (4099, 1040, 1040, False, 0), (390, 8208, 1040, False, 0),
+    (130, 8208, 1040, False, 0), (70, 8208, 1040, False, 0), (5, 272, 1040, False, 0), (260, 272, 1040, False, 0),
+    (520, 272, 1040, False, 0), (1030, 272, 1040, False, 0), (1030, 528, 1040, False, 0),
+    (5000, 1552, 1040, True, 0), (6200, 528, 1040, True, 0), (70, 8208, 1040, True, 0), (5, 272, 1040, True, 0),
+    (1030, 272, 1040, True, 0), (1030, 528, 1040, True, 0),
+    (4099, 1040, 9232, False, 0), (390, 8208, 9232, False, 0), (200, 8208, 9232, False, 0), (70, 8208, 9232, False, 0),
+    (1030, 272, 9232, False, 0), (200, 2064, 9232, False, 0), (2050, 528, 9232, True, 0), (1030, 272, 9232, True, 0),
+    (1030, 528, 9232, True, 0), (6200, 528, 9232, True, 0),
+    (5000, 1552, 1040, False, 5), (520, 6160, 1040, False, 5), (100, 8208, 1040, False, 5), (200, 4112, 1040, False, 5),
+    (3000, 272, 1040, False, 5), (24, 272, 1040, False, 5), (5, 272, 1040, False, 5), (520, 272, 1040, False, 5),
+    (130, 1552, 1040, False, 5), (1030, 528, 1040, False, 5), (6200, 1040, 1040, True, 5), (5000, 528, 1040, True, 5),
+    (5, 8208, 1040, True, 5), (5, 272, 1040, True, 5), (130, 1552, 1040, True, 5), (1500, 272, 1040, True, 5),
+    (4099, 1552, 9232, True, 5), (1030, 6160, 9232, False, 5), (6200, 272, 9232, False, 5),
+]
+
+
+@pytest.mark.parametrize("R,fmt", [(64, "e5m2"), (16, "e4m3")])
+@pytest.mark.parametrize("M,N,K,transpose,experts", EVERY_TILE)
+def test_matmul_every_tile(M, N, K, transpose, experts, R, fmt):
+    g = torch.Generator(device=DEV).manual_seed(M + N + K)
+    E = experts or 1
+    o, h = (K, N) if transpose else (N, K)
+    a, s = nf4.fp8_quantize(torch.randn(M, K, generator=g, device=DEV) *
+                            torch.exp(torch.randn(M, 1, generator=g, device=DEV)), 1, DTYPES[fmt])
+    W = torch.empty(E, o, h, dtype=torch.float8_e4m3fn, device=DEV)
+    ws = torch.empty(E, -(-o // 128), -(-h // 128), device=DEV)
+    for e in range(E):
+        nf4.fp8_quantize(0.02 * torch.randn(o, h, generator=g, device=DEV), 128, codes=W[e], scales=ws[e])
+    A2 = torch.randn(M, R, generator=g, device=DEV).bfloat16()
+    B2 = (0.05 * torch.randn(E, N, R, generator=g, device=DEV)).bfloat16()
+    if experts:
+        counts = [M // 2, 0, 1, M - M // 2 - 3, 0]  # two rows behind
+        ends = np.concatenate([[0], np.cumsum(counts)])
+        C = torch.full((M, N), 3.0, dtype=torch.bfloat16, device=DEV)
+        nf4.fp8_matmul_grouped(a, s, W, ws, torch.from_numpy(ends.astype(np.int32)).to(DEV), transpose, A2, B2, out=C)
+        assert torch.all(C[M - 2:] == 3.0)
+    else:
+        ends = np.array([0, M])
+        C = nf4.fp8_matmul(a, s, W[0], ws[0], transpose, A2, B2[0])
+    A, D2 = nf4.fp8_dequantize(a, s).double(), A2.double()
+    for e in range(E):
+        r = slice(int(ends[e]), int(ends[e + 1]))
+        if ends[e] == ends[e + 1]:
+            continue
+        D = nf4.fp8_dequantize(W[e], ws[e], 128).double()
+        D = D if transpose else D.t().contiguous()
+        X, T, U = A[r], D2[r], B2[e].double().t().contiguous()
+        check_product(C[r], (f64(X @ D + T @ U), f64(X.abs() @ D.abs() + T.abs() @ U.abs()),
+                             f64(((X * X) @ (D * D) + (T * T) @ (U * U)).sqrt())), K, R)
+
+
 @pytest.mark.parametrize("transpose", [False, True])
 def test_matmul_zero_blocks_and_nan(transpose):
     # a zero row and zero weight blocks give exact zeros; a NaN stays in its row
