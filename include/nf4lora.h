@@ -534,7 +534,8 @@ nf4_status nf4_fp8_matmul(const uint8_t *A, int32_t a_format, const float *a_sca
  *             written.  Offsets outside [0, M] are taken as the nearest of the
  *             two; where they do not ascend, which rows of C are written, and
  *             with what, is unspecified (never any outside C).
- *   experts : 1 .. 4096;  M <= 2^31 - 1.
+ *   experts : 1 .. 4096;  M <= 2^30, and (M / 256 + min(experts, M)) * ceil(N / 256)
+ *             < 2^23 (one launch), N the columns of C.
  * Errors as nf4_fp8_matmul.
  */
 nf4_status nf4_fp8_matmul_grouped(const uint8_t *A, int32_t a_format, const float *a_scales, int64_t M,

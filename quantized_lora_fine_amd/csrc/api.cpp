@@ -510,9 +510,11 @@ nf4_status fp8_product(const Fp8Gemm& q, int32_t a_format, void* stream) {
   if (a_format != NF4_FP8_E4M3 && a_format != NF4_FP8_E5M2) return NF4_ERR_ARG;
   if (q.rows <= 0 || q.cols <= 0 || q.rows % 16 != 0 || q.cols % 16 != 0) return NF4_ERR_SHAPE;
   if (q.rows > kMaxLayerDim || q.cols > kMaxLayerDim || q.rows * q.cols > kMaxLayerWeights) return NF4_ERR_SHAPE;
-  const int64_t mmax = q.experts ? (int64_t)INT32_MAX : (int64_t)1 << 31;
+  const int64_t mmax = (int64_t)1 << (q.experts ? 30 : 31);
   if (q.M < 0 || q.M > mmax || q.R < 0 || q.R > 256 || q.R % 16 != 0) return NF4_ERR_SHAPE;
   if (q.M == 0) return NF4_OK;
+  if (q.experts && !fp8_grouped_fits(kFp8Wide8, q.M, (int)(q.transpose ? q.cols : q.rows), q.experts))
+    return NF4_ERR_SHAPE;
   if (!q.A || !q.a_scales || !q.W || !q.w_scales || !q.C || (q.R > 0 && (!q.A2 || !q.B2))) return NF4_ERR_NULL;
   if (q.experts && !q.offsets) return NF4_ERR_NULL;
   if (!aligned16(q.A) || !aligned4(q.a_scales) || !aligned16(q.W) || !aligned4(q.w_scales) || !aligned16(q.C) ||

@@ -874,10 +874,9 @@ __global__ __launch_bounds__(512) void k_fp8_ring(Args p) {
 hipError_t launch_part(const Fp8Gemm& q, Args p, int kind, hipStream_t st) {
   const Fp8Kind& k = fp8_kinds()[kind];
   p.tiles_n = (p.N + k.bn - 1) / k.bn;
-  // every expert's last tile may be partly filled
-  const int64_t tiles = q.experts ? p.M / k.bm + std::min<int64_t>(q.experts, p.M) : (p.M + k.bm - 1) / k.bm;
-  if (tiles * p.tiles_n > (int64_t)0xFFFFFFFF / k.threads) return hipErrorInvalidValue;
-  const dim3 gr((unsigned)(tiles * p.tiles_n)), bl((unsigned)k.threads);
+  const int64_t tiles =
+      q.experts ? fp8_grouped_tiles(kind, p.M, p.N, q.experts) : (p.M + k.bm - 1) / k.bm * p.tiles_n;
+  const dim3 gr((unsigned)tiles), bl((unsigned)k.threads);
 #define NF4K_LAUNCH(...) hipLaunchKernelGGL((__VA_ARGS__), gr, bl, 0, st, p)
 #define NF4K_FLAGS(KERNEL, ...)                                                     \
   do {                                                                              \

@@ -214,6 +214,11 @@ struct Fp8Part {
   int64_t rows;
 };
 const Fp8Kind* fp8_kinds();
+// A grouped product is one launch: its workgroups (every expert's last tile may be
+// partly filled), and whether their work-items stay below 2^32.  plan_fp8 needs
+// the largest kind, kFp8Wide8, to fit.
+int64_t fp8_grouped_tiles(int kind, int64_t M, int N, int experts);
+bool fp8_grouped_fits(int kind, int64_t M, int N, int experts);
 int plan_fp8(int64_t M, int N, int K, bool transpose, int experts, Fp8Part parts[2]);
 NF4K_WEAK hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t st);
 

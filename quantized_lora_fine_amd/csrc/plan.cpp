@@ -120,6 +120,15 @@ const Fp8Kind* fp8_kinds() {
   return kinds;
 }
 
+int64_t fp8_grouped_tiles(int kind, int64_t M, int N, int experts) {
+  const Fp8Kind& k = fp8_kinds()[kind];
+  return (M / k.bm + (M < experts ? M : experts)) * ((N + k.bn - 1) / k.bn);
+}
+
+bool fp8_grouped_fits(int kind, int64_t M, int N, int experts) {
+  return fp8_grouped_tiles(kind, M, N, experts) <= (int64_t)0xFFFFFFFF / fp8_kinds()[kind].threads;
+}
+
 namespace {
 
 constexpr int kCUs = 256;
@@ -146,7 +155,9 @@ int fp8_best(int64_t M, int N, int K, bool transpose, int experts, double* time)
     // and 51 for 32 columns by 16 and by 32 rows), few rows of many experts the next
     // one (64 experts of 1536 x 4096, 48 rows: 34 us against 39 and 43).
     if (!transpose && !experts && M <= 8 && i != kFp8Rows11) continue;
-    if (!transpose && experts && M <= 4 * (int64_t)experts && i != kFp8Rows12) continue;
+    if (!transpose && experts && M <= 4 * (int64_t)experts && i != kFp8Rows12 &&
+        fp8_grouped_fits(kFp8Rows12, M, N, experts))
+      continue;
     const int64_t bm = fp8_kinds()[i].bm;
     int64_t tiles_m = (M + bm - 1) / bm;
     if (experts) {
@@ -156,6 +167,7 @@ int fp8_best(int64_t M, int N, int K, bool transpose, int experts, double* time)
       const int64_t used = M < experts ? M : experts;
       tiles_m = (M / bm + used / 2) * 11 / 10;
       if (tiles_m < used) tiles_m = used;
+      if (!fp8_grouped_fits(i, M, N, experts)) continue;
     }
     const double x = fp8_time(i, tiles_m, N, K);
     if (best < 0 || x < least) {

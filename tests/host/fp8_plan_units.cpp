@@ -33,6 +33,7 @@ int main() {
     const int N = 16 * (int)pick(1, pick(0, 3) ? 1024 : 262144), K = 16 * (int)pick(1, pick(0, 3) ? 1024 : 262144);
     const bool t = pick(0, 1);
     const int experts = pick(0, 2) ? 0 : (int)pick(1, 4096);
+    if (experts && !fp8_grouped_fits(kFp8Wide8, M, N, experts)) continue;  // refused before
     Fp8Part parts[2];
     const int c = plan_fp8(M, N, K, t, experts, parts);
     CHECK(c == 1 || (c == 2 && !experts));
@@ -40,6 +41,7 @@ int main() {
     for (int i = 0; i < c; ++i) {
       CHECK(parts[i].rows > 0 && parts[i].kind >= 0 && parts[i].kind < kFp8Kinds);
       CHECK(wide(parts[i].kind) || transposed(parts[i].kind) == t);
+      CHECK(!experts || fp8_grouped_fits(parts[i].kind, M, N, experts));
       rows += parts[i].rows;
       reached[parts[i].kind] = true;
     }
@@ -61,6 +63,11 @@ int main() {
   CHECK(plan_fp8(48, 1536, 4096, false, 64, p) == 1 && p[0].kind == kFp8Rows12);
   // 16384 x 28672: 7168 large tiles are 28 whole sets of 256
   CHECK(plan_fp8(16384, 28672, 8192, false, 0, p) == 1 && p[0].kind == kFp8Wide8);
+  // a grouped product of narrow rows and many of them takes the kinds that one launch holds
+  CHECK(!fp8_grouped_fits(kFp8Rows11, (int64_t)1 << 30, 16, 1) && fp8_grouped_fits(kFp8Wide8, (int64_t)1 << 30, 16, 4096));
+  for (bool t : {false, true})
+    CHECK(plan_fp8((int64_t)1 << 30, 16, 16, t, 4096, p) == 1 && fp8_grouped_fits(p[0].kind, (int64_t)1 << 30, 16, 4096));
+  CHECK(plan_fp8(16384, 1 << 22, 16, false, 4096, p) == 1 || !fp8_grouped_fits(kFp8Wide8, 16384, 1 << 22, 4096));
   // three rows past a whole set of 256-row tiles go by themselves
   CHECK(plan_fp8(4099, 4096, 11008, true, 0, p) == 2 && p[0].rows == 4096 && p[0].kind == kFp8Wide8 &&
         transposed(p[1].kind));

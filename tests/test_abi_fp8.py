@@ -83,7 +83,9 @@ def test_products_refuse(call):
 def test_grouped_refuses():
     for E in (0, -1, 4097):
         assert grouped(E=E) == nf4.NF4_ERR_SHAPE
-    assert grouped(M=1 << 31) == nf4.NF4_ERR_SHAPE
+    assert grouped(M=1 << 31) == nf4.NF4_ERR_SHAPE and grouped(M=(1 << 30) + 1) == nf4.NF4_ERR_SHAPE
+    # more tiles than one launch holds
+    assert grouped(M=1 << 30, rows=1 << 20, cols=16) == nf4.NF4_ERR_SHAPE
     # the last expert's weight counts as input
     assert grouped(c=W + 3 * 144 * 272) == nf4.NF4_ERR_ALIAS
 

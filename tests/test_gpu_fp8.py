@@ -450,6 +450,88 @@ def test_matmul_grouped_offsets_outside():
     assert torch.equal(nf4.fp8_matmul_grouped(*args, wide), nf4.fp8_matmul_grouped(*args, good))
 
 
+def tall(M, H):
+    """bf16 [M][H] whose rows all differ, made without a host copy."""
+    g = torch.Generator(device=DEV).manual_seed(H)
+    base = torch.randn(512, H, generator=g, device=DEV).bfloat16()
+    x = torch.empty(M, H, dtype=torch.bfloat16, device=DEV)
+    for r0 in range(0, M, 512):
+        n = min(512, M - r0)
+        x[r0:r0 + n] = base[:n] * (1 + r0 / M)
+    return x
+
+
+def test_rows_past_32_bits():
+    # more than 2^32 values: the last rows are what they are by themselves
+    M, H = 131300, 32768
+    X, w = tall(M, H), bf16_np(1 + 0.1 * np.random.default_rng(1).standard_normal(H)).to(DEV)
+    ends = [slice(0, 65), slice(65500, 65600), slice(131050, 131090), slice(M - 70, M)]
+    codes, scales = nf4.fp8_quantize(X)
+    for r in ends:
+        c, s = nf4.fp8_quantize(X[r])
+        assert np.array_equal(bits(codes[r]), bits(c)) and torch.equal(scales[r], s)
+    back = nf4.fp8_dequantize(codes, scales, bf16=True)
+    for r in ends:
+        assert torch.equal(back[r], nf4.fp8_dequantize(codes[r], scales[r], bf16=True))
+    Y, h, nc, ns, rstd = nf4.rmsnorm_fwd(X, w, 1e-6, back, want_fp8=True, want_rstd=True)
+    for r in ends:
+        one = nf4.rmsnorm_fwd(X[r], w, 1e-6, back[r], want_fp8=True, want_rstd=True)
+        for t, u in zip((Y, h, nc, ns, rstd), one):
+            assert torch.equal(t[r].view(torch.uint8), u.view(torch.uint8))
+    del codes, scales, nc, ns, back
+    dX, dw = nf4.rmsnorm_bwd(Y, h, w, rstd, X)
+    for r in ends:
+        assert torch.equal(dX[r].view(torch.int16),
+                           nf4.rmsnorm_bwd(Y[r].contiguous(), h[r], w, rstd[r], X[r])[0].view(torch.int16))
+    dw64, size = torch.zeros(H, dtype=torch.float64, device=DEV), torch.zeros(H, dtype=torch.float64, device=DEV)
+    for r0 in range(0, M, 4096):
+        t = Y[r0:r0 + 4096].double() * h[r0:r0 + 4096].double() * rstd[r0:r0 + 4096, None].double()
+        dw64 += t.sum(0)
+        size += t.abs().sum(0)
+    # a workgroup's rows in turn (at most ceil(M / 256)), then the parts
+    check_within("dw", dw, f64(dw64), f64(size) * (-(-M // 256) + 64) * EPS32)
+    del X, Y, h, dX
+    x = tall(128 * 1024 + 200, 32768).float()  # and by blocks of 128 rows
+    codes, scales = nf4.fp8_quantize(x, 128)
+    r = slice(128 * 1024, None)
+    c, s = nf4.fp8_quantize(x[r], 128)
+    assert np.array_equal(bits(codes[r]), bits(c)) and torch.equal(scales[1024:], s)
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_products_past_32_bits(transpose):
+    # A and C of more than 2^32 bytes
+    M, N, K = 263000, 16400, 16512
+    o, h = (K, N) if transpose else (N, K)
+    a, s = nf4.fp8_quantize(tall(M, K))
+    w, ws = nf4.fp8_quantize(tall(o, h), 128)
+    C = nf4.fp8_matmul(a, s, w, ws, transpose)
+    W = nf4.fp8_dequantize(w, ws, 128)
+    rows = torch.tensor([0, 131071, 131072, 260096, 262143, 262144, M - 1], device=DEV)
+    cols = torch.cat([torch.arange(0, 300, device=DEV), torch.arange(N - 300, N, device=DEV)])
+    B = (W[:, cols] if transpose else W[cols].t()).double().contiguous()
+
+    def check(C, rows, B):
+        A = nf4.fp8_dequantize(a[rows].contiguous(), s[rows].contiguous()).double()
+        check_product(C[rows][:, cols].contiguous(), (f64(A @ B), f64(A.abs() @ B.abs()),
+                                                      f64(((A * A) @ (B * B)).sqrt())), K, 0)
+
+    check(C, rows, B)
+    # and a stack of weights of more than 2^32 bytes, the last expert with rows
+    E = 17
+    W17 = torch.empty(E, o, h, dtype=torch.float8_e4m3fn, device=DEV)
+    s17 = torch.zeros(E, -(-o // 128), -(-h // 128), device=DEV)
+    W17.view(torch.uint8)[:E - 1] = 0x7F  # NaN
+    W17.view(torch.uint8)[E - 1] = w.view(torch.uint8)
+    s17[E - 1] = ws
+    offsets = torch.full((E + 1,), M - 300, dtype=torch.int32, device=DEV)
+    offsets[E] = M
+    C.fill_(3.0)
+    nf4.fp8_matmul_grouped(a, s, W17, s17, offsets, transpose, out=C)
+    assert torch.all(C[M - 1000:M - 300] == 3.0)
+    check(C, torch.tensor([M - 300, M - 44, M - 1], device=DEV), B)
+
+
 def test_empty():
     a = torch.empty(0, 272, dtype=torch.float8_e4m3fn, device=DEV)
     s = torch.empty(0, 3, device=DEV)
