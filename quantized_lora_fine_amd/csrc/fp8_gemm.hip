@@ -60,33 +60,32 @@ struct Args {
 __device__ __forceinline__ bool find_tile(const Args& p, int bm, int t, int& e, int64_t& m0, int64_t& m1) {
   const int lane = threadIdx.x & 63;
   const int M = (int)p.M;
-  int base = 0;
+  uint32_t base = 0;  // (counts may wrap where offsets do not ascend; the rows stay inside all the same)
   for (int e0 = 0; e0 < p.experts; e0 += 64) {
     const int i = e0 + lane;
     int lo = 0, n = 0;
     if (i < p.experts) {
       lo = min(max(p.offsets[i], 0), M);
-      n = max(min(p.offsets[i + 1], M) - lo, 0);
+      n = max(min(max(p.offsets[i + 1], 0), M) - lo, 0);  // lo + n <= M
     }
-    const int tiles = (int)(((int64_t)n + bm - 1) / bm);
-    int incl = tiles;
+    const uint32_t tiles = (uint32_t)(((int64_t)n + bm - 1) / bm);
+    uint32_t incl = tiles;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(incl, o);
+      const uint32_t v = __shfl_up(incl, o);
       if (lane >= o) incl += v;
     }
-    const uint64_t hit = __ballot(base + incl > t);
+    const uint64_t hit = __ballot(base + incl > (uint32_t)t);
     if (hit) {
       const int l = __builtin_ctzll(hit);
-      const int first = base + __builtin_amdgcn_readlane(incl - tiles, l);
+      const uint32_t first = base + (uint32_t)__builtin_amdgcn_readlane((int)(incl - tiles), l);
       const int l0 = __builtin_amdgcn_readlane(lo, l), ln = __builtin_amdgcn_readlane(n, l);
       e = e0 + l;
-      m0 = (int64_t)l0 + (int64_t)(t - first) * bm;
+      m0 = (int64_t)l0 + (int64_t)((uint32_t)t - first) * bm;
       m1 = min(m0 + bm, (int64_t)l0 + ln);
-      // (offsets that do not ascend can make the counts overflow: still inside)
-      return m0 >= l0 && m0 < m1;
+      return m0 < m1;
     }
-    base += __builtin_amdgcn_readlane(incl, 63);
+    base += (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
   }
   return false;
 }

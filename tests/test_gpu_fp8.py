@@ -450,6 +450,70 @@ def test_matmul_grouped_offsets_outside():
     assert torch.equal(nf4.fp8_matmul_grouped(*args, wide), nf4.fp8_matmul_grouped(*args, good))
 
 
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("counts", [[5, 0, 12], [300, 0, 129], [2000, 0, 1500]])
+def test_matmul_grouped_reads_its_rows_alone(counts, transpose):
+    # NaN in the rows before and behind, and in the weights of experts without rows
+    rng = np.random.default_rng(sum(counts))
+    o, h = (528, 1040)
+    K, N = (o, h) if transpose else (h, o)
+    M = 3 + sum(counts) + 130
+    a, s = nf4.fp8_quantize(torch.from_numpy(rows_of(rng, M, K)).to(DEV))
+    W = torch.empty(3, o, h, dtype=torch.float8_e4m3fn, device=DEV)
+    ws = torch.empty(3, -(-o // 128), -(-h // 128), device=DEV)
+    for e in range(3):
+        nf4.fp8_quantize(torch.from_numpy(0.02 * rng.standard_normal((o, h)).astype(np.float32)).to(DEV), 128,
+                         codes=W[e], scales=ws[e])
+    A2 = torch.from_numpy(rng.standard_normal((M, 48))).to(DEV).bfloat16()
+    B2 = torch.from_numpy(0.05 * rng.standard_normal((3, N, 48))).to(DEV).bfloat16()
+    offsets = torch.from_numpy((3 + np.concatenate([[0], np.cumsum(counts)])).astype(np.int32)).to(DEV)
+    want = nf4.fp8_matmul_grouped(a, s, W, ws, offsets, transpose, A2, B2, out=torch.full((M, N), 3.0, device=DEV).bfloat16())
+    for r in (slice(0, 3), slice(3 + sum(counts), M)):
+        a.view(torch.uint8)[r] = 0x7F
+        s[r] = float("nan")
+        A2[r] = float("nan")
+    W.view(torch.uint8)[1] = 0x7F
+    ws[1] = float("inf")
+    B2[1] = float("nan")
+    got = nf4.fp8_matmul_grouped(a, s, W, ws, offsets, transpose, A2, B2, out=torch.full((M, N), 3.0, device=DEV).bfloat16())
+    assert torch.isfinite(got).all() and torch.equal(got, want)
+
+
+def test_matmul_grouped_offsets_that_do_not_ascend():
+    # which rows are written is unspecified, but none outside C
+    a, s, w, ws, _, _ = product_case(10, 40, 144, 272, False, 0, "e4m3", 4)
+    args = (t8(a), torch.from_numpy(s).to(DEV), t8(np.stack(w)), torch.from_numpy(np.stack(ws)).to(DEV))
+    for ends in ([0, 40, 5, 38, 40], [40, 30, 20, 10, 0], [0, -7, 90, -2147483648, 2147483647], [7, 7, 7, 7, 7]):
+        room = torch.full((120, 144), 3.0, dtype=torch.bfloat16, device=DEV)
+        nf4.fp8_matmul_grouped(*args, torch.tensor(ends, dtype=torch.int32, device=DEV), out=room[40:80])
+        assert torch.all(room[:40] == 3.0) and torch.all(room[80:] == 3.0)
+
+
+def test_matmul_grouped_replayed_with_other_offsets():
+    a, s, w, ws, A2, B2 = product_case(11, 200, 272, 400, False, 16, "e4m3", 5)
+    args = [t8(a), torch.from_numpy(s).to(DEV), t8(np.stack(w)), torch.from_numpy(np.stack(ws)).to(DEV)]
+    more = (False, A2.to(DEV), torch.stack(B2).to(DEV))
+    splits = [[0, 0, 200, 200, 200, 200], [0, 1, 2, 3, 4, 5], [10, 60, 61, 61, 190, 200], [200] * 6]
+    offsets = torch.tensor(splits[0], dtype=torch.int32, device=DEV)
+    out = torch.zeros(200, 272, dtype=torch.bfloat16, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        nf4.fp8_matmul_grouped(*args, offsets, *more, out=out)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        nf4.fp8_matmul_grouped(*args, offsets, *more, out=out)
+    for ends in splits + splits[::-1]:
+        offsets.copy_(torch.tensor(ends, dtype=torch.int32))
+        out.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = nf4.fp8_matmul_grouped(*args, torch.tensor(ends, dtype=torch.int32, device=DEV), *more,
+                                      out=torch.full_like(out, 3.0))
+        assert torch.equal(out, want), ends
+
+
 def tall(M, H):
     """bf16 [M][H] whose rows all differ, made without a host copy."""
     g = torch.Generator(device=DEV).manual_seed(H)
@@ -619,6 +683,21 @@ def test_another_stream():
         got = layer(*args)
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_two_streams_at_once():
+    cases = [layer_case(M=130), layer_case(M=700)]
+    want = [layer(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(8):
+        for c, st in zip(cases, streams):
+            with torch.cuda.stream(st):
+                got.append(layer(*c))
+    torch.cuda.synchronize()
+    for k, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[k % 2])), k
 
 
 def test_binding_refuses():
