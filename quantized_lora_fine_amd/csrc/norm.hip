@@ -166,11 +166,15 @@ __global__ __launch_bounds__(TPR ? 256 : 1024) void k_rmsnorm(NormArgs p) {
     for (int j = 0; j < 8; ++j) ss = __builtin_fma((double)a[j], (double)a[j], ss);
   }
   ss = row_sum<TPR>(ss, red);
-  // one step of Newton's from the fp32 root; a root of 0 or infinity stands as it is
-  const double mean = __builtin_fma(ss, p.inv_H, (double)p.eps);
-  const float hi = 1.f / sqrtf((float)mean);
-  const float e = (float)__builtin_fma(-mean, (double)hi * (double)hi, 1.);
-  const float lo = fabsf(e) < 1.f ? 0.5f * hi * e : 0.f;
+  // one step of Newton's from the fp32 root of mean / 4^k, which is 1/4 or more and
+  // below 1; a root of 0 or infinity stands as it is
+  double mean = __builtin_fma(ss, p.inv_H, (double)p.eps);
+  const int k = (__builtin_amdgcn_frexp_exp(mean) + 1) >> 1;
+  mean = __builtin_amdgcn_ldexp(mean, -2 * k);
+  const float root = 1.f / sqrtf((float)mean);
+  const float e = (float)__builtin_fma(-mean, (double)root * (double)root, 1.);
+  const float hi = ldexpf(root, -k);
+  const float lo = fabsf(e) < 1.f ? ldexpf(0.5f * root * e, -k) : 0.f;
   if (p.rstd && t == 0) p.rstd[row] = hi + lo;
   const int64_t kb = (p.H + 127) / 128;
 #pragma unroll

@@ -174,6 +174,23 @@ def test_rmsnorm(M, H, residual):
     assert np.array_equal(bits(c1), bits(codes)) and torch.equal(s1, scales)
 
 
+def test_rmsnorm_any_magnitude():
+    # squares past and below fp32's range; an infinity or NaN stays in its row
+    rng = np.random.default_rng(6)
+    M, H = 12, 1040
+    x = rng.standard_normal((M, H)) * np.array([1e30, 1e25, 1e19, 1e18, 1, 1e-10, 1e-18, 1e-19, 1e-22, 1e-30, 1, 1])[:, None]
+    X, w = bf16_np(x), bf16_np(1 + 0.1 * rng.standard_normal(H))
+    X[10, 7], X[11, 9] = float("inf"), float("nan")
+    Y, _, codes, scales, rstd = nf4.rmsnorm_fwd(X.to(DEV), w.to(DEV), 0.0, want_fp8=True, want_rstd=True)
+    y, r = fp8.rmsnorm(f64(X[:10]), f64(w), 0.0)
+    check_within("rstd", rstd[:10], r, np.abs(r) * 2.0 ** -24 * (1 + 2.0 ** -16))
+    check_within("y", Y[:10], y, np.abs(y) * BF16 * (1 + 2.0 ** -8))
+    d = f64(nf4.fp8_dequantize(codes, scales)[:10])
+    sw = fp8._spread(fp8.block_scales(y.astype(np.float32), 1, "e4m3")[0], 1, 10, H)
+    assert np.all(np.abs(d - y) <= np.maximum(np.abs(y) * E4M3, sw * 2.0 ** -10) * (1 + 2.0 ** -8))
+    assert torch.isnan(Y[10, 7]) and torch.isnan(Y[11]).all() and float(rstd[10]) == 0 and torch.isnan(rstd[11])
+
+
 def test_rmsnorm_rounds_once():
     # codes against those of y in 64 bits: a fp32 value of y and its product with the multiplier, at most 2^-23 off
     # together, move a value over a tie where it lies within 2^-23 * |v| of one; ties are 2^-4 |v| apart or more, so
