@@ -154,6 +154,9 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current device from torch's C layer (a tensor on a GPU is checked against it, so the runtime is up)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
 # the current stream's handle straight from torch's C layer: building the Stream object around it takes longer than
 # a launch
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
@@ -547,15 +550,15 @@ def fp8_quantize(X: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = torc
     bf16 = X.dtype is torch.bfloat16
     if not bf16 and X.dtype is not torch.float32:
         raise ValueError(f"X: expected bf16 or fp32, got {X.dtype}")
-    dev = torch.cuda.current_device()
+    dev = _device()
     x = _held(X, X.dtype, (rows, cols), dev, "X")
     sshape = (rows if block_rows == 1 else _blocks(rows), _blocks(cols))
     if codes is None:
-        codes = torch.empty((rows, cols), dtype=dtype, device=X.device)
+        codes = torch.empty(rows, cols, dtype=dtype, device=X.device)
     else:
         _held(codes, dtype, (rows, cols), dev, "codes")
     if scales is None:
-        scales = torch.empty(sshape, dtype=torch.float32, device=X.device)
+        scales = torch.empty(*sshape, dtype=torch.float32, device=X.device)
     else:
         _held(scales, torch.float32, sshape, dev, "scales")
     _check(_lib.nf4_fp8_quantize(x, bf16, rows, cols, f, block_rows, codes.data_ptr(), scales.data_ptr(),
@@ -568,12 +571,12 @@ def fp8_dequantize(codes: torch.Tensor, scales: torch.Tensor, block_rows: int = 
     """nf4_fp8_dequantize into fp32 (or bf16) [rows][cols], into `out` when given."""
     f = _fp8_format(getattr(codes, "dtype", None), "codes")
     rows, cols = _matrix(codes, "codes")
-    dev = torch.cuda.current_device()
+    dev = _device()
     c = _held(codes, codes.dtype, (rows, cols), dev, "codes")
     s = _held(scales, torch.float32, (rows if block_rows == 1 else _blocks(rows), _blocks(cols)), dev, "scales")
     odt = torch.bfloat16 if bf16 else torch.float32
     if out is None:
-        out = torch.empty((rows, cols), dtype=odt, device=codes.device)
+        out = torch.empty(rows, cols, dtype=odt, device=codes.device)
     _check(_lib.nf4_fp8_dequantize(c, s, rows, cols, f, block_rows, _held(out, odt, (rows, cols), dev, "out"),
                                    1 if bf16 else 0, _raw_stream(dev)), "nf4_fp8_dequantize")
     return out
@@ -595,7 +598,7 @@ def _fp8_product(A, a_scales, o: int, h: int, transpose, A2, B2, experts: tuple,
         a2 = _held(A2, torch.bfloat16, (M, R), dev, "A2")
         b2 = _held(B2, torch.bfloat16, (*experts, N, R), dev, "B2")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=A.device)
     else:
         _held(out, torch.bfloat16, (M, N), dev, "out")
     return a, f, s, M, 1 if transpose else 0, a2, b2, R, out
@@ -608,7 +611,7 @@ def fp8_matmul(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scale
     A [M][K] and a_scales as fp8_quantize(X) gives them (either format), W [o][h] (e4m3) and w_scales as
     fp8_quantize(W, 128) does."""
     o, h = _matrix(W, "W")
-    dev = torch.cuda.current_device()
+    dev = _device()
     w = _held(W, torch.float8_e4m3fn, (o, h), dev, "W")
     ws = _held(w_scales, torch.float32, (_blocks(o), _blocks(h)), dev, "w_scales")
     a, f, s, M, tr, a2, b2, R, C = _fp8_product(A, a_scales, o, h, transpose, A2, B2, (), out, dev)
@@ -626,7 +629,7 @@ def fp8_matmul_grouped(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor,
     if not isinstance(W, torch.Tensor) or W.dim() != 3:
         raise ValueError("W: expected a tensor of three dimensions, [experts][o][h]")
     E, o, h = W.shape
-    dev = torch.cuda.current_device()
+    dev = _device()
     w = _held(W, torch.float8_e4m3fn, (E, o, h), dev, "W")
     ws = _held(w_scales, torch.float32, (E, _blocks(o), _blocks(h)), dev, "w_scales")
     off = _held(offsets, torch.int32, (E + 1,), dev, "offsets")
@@ -641,18 +644,18 @@ def rmsnorm_fwd(X: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, residual: t
     """nf4_rmsnorm_fwd of bf16 X [M][H] (+ residual): (Y bf16, h bf16, codes e4m3, scales fp32, rstd fp32), None for
     what is not asked for (h: without a residual).  `outs`: the same five, given instead of allocated."""
     M, H = _matrix(X, "X")
-    dev = torch.cuda.current_device()
+    dev = _device()
     bf16, f32, e4m3, device = torch.bfloat16, torch.float32, torch.float8_e4m3fn, X.device
     x = _held(X, bf16, (M, H), dev, "X")
     wp = _held(w, bf16, (H,), dev, "w")
     res = None if residual is None else _held(residual, bf16, (M, H), dev, "residual")
     want = (want_y, residual is not None, want_fp8, want_fp8, want_rstd)
     if outs is None:
-        Y = torch.empty((M, H), dtype=bf16, device=device) if want_y else None
-        h = None if residual is None else torch.empty((M, H), dtype=bf16, device=device)
-        codes = torch.empty((M, H), dtype=e4m3, device=device) if want_fp8 else None
-        scales = torch.empty((M, _blocks(H)), dtype=f32, device=device) if want_fp8 else None
-        rstd = torch.empty((M,), dtype=f32, device=device) if want_rstd else None
+        Y = torch.empty(M, H, dtype=bf16, device=device) if want_y else None
+        h = None if residual is None else torch.empty(M, H, dtype=bf16, device=device)
+        codes = torch.empty(M, H, dtype=e4m3, device=device) if want_fp8 else None
+        scales = torch.empty(M, _blocks(H), dtype=f32, device=device) if want_fp8 else None
+        rstd = torch.empty(M, dtype=f32, device=device) if want_rstd else None
         outs = (Y, h, codes, scales, rstd)
     else:
         names = ("Y", "h", "codes", "scales", "rstd")
@@ -681,7 +684,7 @@ def rmsnorm_bwd(dY: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rstd: torch.
     """nf4_rmsnorm_bwd: (dX bf16 [M][H], the gradient of X and of the residual alike, dw fp32 [H]) from the forward's
     h (X without a residual) and rstd; dH is the gradient that reaches h along the residual stream."""
     M, H = _matrix(dY, "dY")
-    dev = torch.cuda.current_device()
+    dev = _device()
     bf16, f32 = torch.bfloat16, torch.float32
     g = _held(dY, bf16, (M, H), dev, "dY")
     hp = _held(h, bf16, (M, H), dev, "h")
@@ -689,10 +692,10 @@ def rmsnorm_bwd(dY: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rstd: torch.
     r = _held(rstd, f32, (M,), dev, "rstd")
     d = None if dH is None else _held(dH, bf16, (M, H), dev, "dH")
     if outs is None:
-        outs = (torch.empty((M, H), dtype=bf16, device=dY.device), torch.empty((H,), dtype=f32, device=dY.device))
+        outs = (torch.empty(M, H, dtype=bf16, device=dY.device), torch.empty(H, dtype=f32, device=dY.device))
     dX, dw = outs
     ws = _need_ws(ws) if ws is not None else \
-        torch.empty((rmsnorm_workspace_bytes(M, H),), dtype=torch.uint8, device=dY.device)
+        torch.empty(rmsnorm_workspace_bytes(M, H), dtype=torch.uint8, device=dY.device)
     _check(_lib.nf4_rmsnorm_bwd(g, hp, wp, r, d, M, H, _held(dX, bf16, (M, H), dev, "outs.dX"),
                                 _held(dw, f32, (H,), dev, "outs.dw"), ws.data_ptr(), ws.numel(), _raw_stream(dev)),
            "nf4_rmsnorm_bwd")
