@@ -518,11 +518,23 @@ nf4_status nf4_fp8_dequantize(const uint8_t *codes, const float *scales, int64_t
  * B2 NULL only when R == 0 (an adapter's s T and L2^T, or G and L1).  M == 0 does
  * nothing.  One row or a few (a decoded token) take a kernel of their own that
  * streams the weight.
- * Errors: NF4_ERR_NULL, _SHAPE, _ARG (a_format, transpose), _ALIGN, _ALIAS, _HIP.
+ *   ws : nf4_fp8_matmul_workspace_bytes bytes, or NULL.  With it a product of few
+ *        tiles and a long contraction splits the contraction over workgroups and
+ *        joins their fp32 sums in a fixed order; without it nothing is split.
+ * Errors: NF4_ERR_NULL, _SHAPE, _ARG (a_format, transpose), _ALIGN, _WORKSPACE,
+ * _ALIAS, _HIP.
  */
 nf4_status nf4_fp8_matmul(const uint8_t *A, int32_t a_format, const float *a_scales, int64_t M, const uint8_t *W,
                           const float *w_scales, int64_t rows, int64_t cols, int32_t transpose, const uint16_t *A2,
-                          const uint16_t *B2, int32_t R, uint16_t *C, void *stream);
+                          const uint16_t *B2, int32_t R, uint16_t *C, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Workspace bytes of nf4_fp8_matmul (experts = 0) and nf4_fp8_matmul_grouped (host
+ * output *bytes): 0 for most products, at most 64 MiB.  Errors: NF4_ERR_NULL,
+ * _SHAPE, _ARG (transpose).
+ */
+nf4_status nf4_fp8_matmul_workspace_bytes(int64_t M, int64_t rows, int64_t cols, int32_t transpose, int32_t experts,
+                                          size_t *bytes);
 
 /*
  * nf4_fp8_matmul for rows sorted by expert: rows offsets[e] .. offsets[e + 1] - 1
@@ -541,7 +553,7 @@ nf4_status nf4_fp8_matmul(const uint8_t *A, int32_t a_format, const float *a_sca
 nf4_status nf4_fp8_matmul_grouped(const uint8_t *A, int32_t a_format, const float *a_scales, int64_t M,
                                   const uint8_t *W, const float *w_scales, int32_t experts, int64_t rows,
                                   int64_t cols, const int32_t *offsets, int32_t transpose, const uint16_t *A2,
-                                  const uint16_t *B2, int32_t R, uint16_t *C, void *stream);
+                                  const uint16_t *B2, int32_t R, uint16_t *C, void *ws, size_t ws_bytes, void *stream);
 
 /*
  * The norm in front of a linear, with the residual's addition and the linear's

@@ -9,6 +9,7 @@ the library returns.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -86,9 +87,11 @@ _SIGS = {
     "nf4_stack_bwd": ([_LP, _i32, _i32, _i64, _vp, _sz, _vp], ctypes.c_int),
     "nf4_fp8_quantize": ([_vp, _i32, _i64, _i64, _i32, _i32, _vp, _vp, _vp], ctypes.c_int),
     "nf4_fp8_dequantize": ([_vp, _vp, _i64, _i64, _i32, _i32, _vp, _i32, _vp], ctypes.c_int),
-    "nf4_fp8_matmul": ([_vp, _i32, _vp, _i64, _vp, _vp, _i64, _i64, _i32, _vp, _vp, _i32, _vp, _vp], ctypes.c_int),
-    "nf4_fp8_matmul_grouped": ([_vp, _i32, _vp, _i64, _vp, _vp, _i32, _i64, _i64, _vp, _i32, _vp, _vp, _i32, _vp, _vp],
-                               ctypes.c_int),
+    "nf4_fp8_matmul_workspace_bytes": ([_i64, _i64, _i64, _i32, _i32, ctypes.POINTER(_sz)], ctypes.c_int),
+    "nf4_fp8_matmul": ([_vp, _i32, _vp, _i64, _vp, _vp, _i64, _i64, _i32, _vp, _vp, _i32, _vp, _vp, _sz, _vp],
+                       ctypes.c_int),
+    "nf4_fp8_matmul_grouped": ([_vp, _i32, _vp, _i64, _vp, _vp, _i32, _i64, _i64, _vp, _i32, _vp, _vp, _i32, _vp, _vp,
+                                _sz, _vp], ctypes.c_int),
     "nf4_rmsnorm_fwd": ([_vp, _vp, _vp, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
     "nf4_rmsnorm_workspace_bytes": ([_i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
     "nf4_rmsnorm_bwd": ([_vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
@@ -582,6 +585,27 @@ def fp8_dequantize(codes: torch.Tensor, scales: torch.Tensor, block_rows: int = 
     return out
 
 
+@functools.lru_cache(maxsize=4096)
+def fp8_matmul_workspace_bytes(M: int, o: int, h: int, transpose: bool = False, experts: int = 0) -> int:
+    """Bytes of the workspace of fp8_matmul (experts = 0) or fp8_matmul_grouped, a function of the sizes alone."""
+    b = _sz()
+    _check(_lib.nf4_fp8_matmul_workspace_bytes(M, o, h, 1 if transpose else 0, experts, ctypes.byref(b)),
+           "nf4_fp8_matmul_workspace_bytes")
+    return b.value
+
+
+def _fp8_ws(ws, M: int, o: int, h: int, transpose: int, experts: int, device):
+    """(tensor, address, bytes) of the product's workspace: the given one, or a new one where one helps."""
+    if ws is None:
+        n = fp8_matmul_workspace_bytes(M, o, h, transpose, experts)
+        if not n:
+            return None, None, 0
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+    else:
+        _need_ws(ws)
+    return ws, ws.data_ptr(), ws.numel()
+
+
 def _fp8_product(A, a_scales, o: int, h: int, transpose, A2, B2, experts: tuple, out, dev: int):
     """Checks the product's tensors against W [o][h]; returns (A, a_format, a_scales, M, transpose, A2, B2, R, C tensor)
     as the C calls take them."""
@@ -606,23 +630,25 @@ def _fp8_product(A, a_scales, o: int, h: int, transpose, A2, B2, experts: tuple,
 
 def fp8_matmul(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
                transpose: bool = False, A2: torch.Tensor | None = None, B2: torch.Tensor | None = None,
-               out: torch.Tensor | None = None) -> torch.Tensor:
+               out: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
     """nf4_fp8_matmul: A * W^T (+ A2 * B2^T), or A * W (+ ...) with transpose=True, bf16 [M][N].
     A [M][K] and a_scales as fp8_quantize(X) gives them (either format), W [o][h] (e4m3) and w_scales as
-    fp8_quantize(W, 128) does."""
+    fp8_quantize(W, 128) does.  ws: a workspace of fp8_matmul_workspace_bytes, else allocated where one helps."""
     o, h = _matrix(W, "W")
     dev = _device()
     w = _held(W, torch.float8_e4m3fn, (o, h), dev, "W")
-    ws = _held(w_scales, torch.float32, (_blocks(o), _blocks(h)), dev, "w_scales")
+    sw = _held(w_scales, torch.float32, (_blocks(o), _blocks(h)), dev, "w_scales")
     a, f, s, M, tr, a2, b2, R, C = _fp8_product(A, a_scales, o, h, transpose, A2, B2, (), out, dev)
-    _check(_lib.nf4_fp8_matmul(a, f, s, M, w, ws, o, h, tr, a2, b2, R, C.data_ptr(), _raw_stream(dev)),
+    ws, wp, wn = _fp8_ws(ws, M, o, h, tr, 0, C.device)
+    _check(_lib.nf4_fp8_matmul(a, f, s, M, w, sw, o, h, tr, a2, b2, R, C.data_ptr(), wp, wn, _raw_stream(dev)),
            "nf4_fp8_matmul")
     return C
 
 
 def fp8_matmul_grouped(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
                        offsets: torch.Tensor, transpose: bool = False, A2: torch.Tensor | None = None,
-                       B2: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+                       B2: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                       ws: torch.Tensor | None = None) -> torch.Tensor:
     """nf4_fp8_matmul_grouped: fp8_matmul of the rows offsets[e] .. offsets[e + 1] - 1 with expert e's W[e]
     [experts][o][h] (w_scales [experts][..][..], B2 [experts][N][R]); offsets is a cuda int32 [experts + 1].
     Rows outside the experts' are not written (undefined in a result that this call allocates)."""
@@ -631,10 +657,11 @@ def fp8_matmul_grouped(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor,
     E, o, h = W.shape
     dev = _device()
     w = _held(W, torch.float8_e4m3fn, (E, o, h), dev, "W")
-    ws = _held(w_scales, torch.float32, (E, _blocks(o), _blocks(h)), dev, "w_scales")
+    sw = _held(w_scales, torch.float32, (E, _blocks(o), _blocks(h)), dev, "w_scales")
     off = _held(offsets, torch.int32, (E + 1,), dev, "offsets")
     a, f, s, M, tr, a2, b2, R, C = _fp8_product(A, a_scales, o, h, transpose, A2, B2, (E,), out, dev)
-    _check(_lib.nf4_fp8_matmul_grouped(a, f, s, M, w, ws, E, o, h, off, tr, a2, b2, R, C.data_ptr(),
+    ws, wp, wn = _fp8_ws(ws, M, o, h, tr, E, C.device)
+    _check(_lib.nf4_fp8_matmul_grouped(a, f, s, M, w, sw, E, o, h, off, tr, a2, b2, R, C.data_ptr(), wp, wn,
                                        _raw_stream(dev)), "nf4_fp8_matmul_grouped")
     return C
 

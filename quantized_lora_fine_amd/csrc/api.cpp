@@ -505,21 +505,41 @@ nf4_status check_alias(const Range (&ins)[NI], const Range (&outs)[NO]) {
   return NF4_OK;
 }
 
-// both products; q.experts == 0 is the dense one
-nf4_status fp8_product(const Fp8Gemm& q, int32_t a_format, void* stream) {
-  if (a_format != NF4_FP8_E4M3 && a_format != NF4_FP8_E5M2) return NF4_ERR_ARG;
-  if (q.rows <= 0 || q.cols <= 0 || q.rows % 16 != 0 || q.cols % 16 != 0) return NF4_ERR_SHAPE;
-  if (q.rows > kMaxLayerDim || q.cols > kMaxLayerDim || q.rows * q.cols > kMaxLayerWeights) return NF4_ERR_SHAPE;
-  const int64_t mmax = (int64_t)1 << (q.experts ? 30 : 31);
-  if (q.M < 0 || q.M > mmax || q.R < 0 || q.R > 256 || q.R % 16 != 0) return NF4_ERR_SHAPE;
-  if (q.M == 0) return NF4_OK;
-  if (q.experts && !fp8_grouped_fits(kFp8Wide8, q.M, (int)(q.transpose ? q.cols : q.rows), q.experts))
+// sizes of both products; experts == 0 is the dense one
+nf4_status check_fp8_product(int64_t M, int64_t rows, int64_t cols, int32_t transpose, int32_t experts) {
+  if (transpose != 0 && transpose != 1) return NF4_ERR_ARG;
+  if (rows <= 0 || cols <= 0 || rows % 16 != 0 || cols % 16 != 0) return NF4_ERR_SHAPE;
+  if (rows > kMaxLayerDim || cols > kMaxLayerDim || rows * cols > kMaxLayerWeights) return NF4_ERR_SHAPE;
+  if (experts < 0 || experts > 4096) return NF4_ERR_SHAPE;
+  if (M < 0 || M > (int64_t)1 << (experts ? 30 : 31)) return NF4_ERR_SHAPE;
+  if (M > 0 && experts && !fp8_grouped_fits(kFp8Wide8, M, (int)(transpose ? cols : rows), experts))
     return NF4_ERR_SHAPE;
+  return NF4_OK;
+}
+
+size_t fp8_product_ws(int64_t M, int64_t rows, int64_t cols, int32_t transpose, int32_t experts) {
+  if (M == 0) return 0;
+  return (size_t)fp8_split_bytes(M, (int)(transpose ? cols : rows), (int)(transpose ? rows : cols), transpose == 1,
+                                 experts);
+}
+
+nf4_status fp8_product(Fp8Gemm q, int32_t a_format, int32_t transpose, void* wsp, size_t ws_bytes, void* stream) {
+  if (a_format != NF4_FP8_E4M3 && a_format != NF4_FP8_E5M2) return NF4_ERR_ARG;
+  nf4_status st = check_fp8_product(q.M, q.rows, q.cols, transpose, q.experts);
+  if (st != NF4_OK) return st;
+  if (q.R < 0 || q.R > 256 || q.R % 16 != 0) return NF4_ERR_SHAPE;
+  if (q.M == 0) return NF4_OK;
   if (!q.A || !q.a_scales || !q.W || !q.w_scales || !q.C || (q.R > 0 && (!q.A2 || !q.B2))) return NF4_ERR_NULL;
   if (q.experts && !q.offsets) return NF4_ERR_NULL;
   if (!aligned16(q.A) || !aligned4(q.a_scales) || !aligned16(q.W) || !aligned4(q.w_scales) || !aligned16(q.C) ||
       (q.R > 0 && (!aligned16(q.A2) || !aligned16(q.B2))) || (q.experts && !aligned4(q.offsets)))
     return NF4_ERR_ALIGN;
+  const size_t need = wsp ? fp8_product_ws(q.M, q.rows, q.cols, transpose, q.experts) : 0;
+  if (need) {
+    if (ws_bytes < need) return NF4_ERR_WORKSPACE;
+    if (!aligned16(wsp)) return NF4_ERR_ALIGN;
+    q.part = (float*)wsp;
+  }
   const int64_t K = q.transpose ? q.rows : q.cols, N = q.transpose ? q.cols : q.rows;
   const int64_t E = q.experts ? q.experts : 1;
   const Range ins[] = {rng(q.A, (size_t)(q.M * K)),
@@ -529,8 +549,8 @@ nf4_status fp8_product(const Fp8Gemm& q, int32_t a_format, void* stream) {
                        rng(q.A2, (size_t)(q.M * q.R * 2)),
                        rng(q.B2, (size_t)(E * N * q.R * 2)),
                        rng(q.offsets, q.experts ? (size_t)(E + 1) * 4 : 0)};
-  const Range outs[] = {rng(q.C, (size_t)(q.M * N * 2))};
-  const nf4_status st = check_alias(ins, outs);
+  const Range outs[] = {rng(q.C, (size_t)(q.M * N * 2)), rng(q.part, need)};
+  st = check_alias(ins, outs);
   if (st != NF4_OK) return st;
   if (!launch_fp8_gemm) return NF4_ERR_HIP;
   return hip_status(launch_fp8_gemm(q, (hipStream_t)stream));
@@ -970,24 +990,31 @@ nf4_status nf4_fp8_dequantize(const uint8_t* codes, const float* scales, int64_t
                                           out_is_bf16 != 0, out, (hipStream_t)stream));
 }
 
+nf4_status nf4_fp8_matmul_workspace_bytes(int64_t M, int64_t rows, int64_t cols, int32_t transpose, int32_t experts,
+                                          size_t* bytes) {
+  if (!bytes) return NF4_ERR_NULL;
+  const nf4_status st = check_fp8_product(M, rows, cols, transpose, experts);
+  if (st != NF4_OK) return st;
+  *bytes = fp8_product_ws(M, rows, cols, transpose, experts);
+  return NF4_OK;
+}
+
 nf4_status nf4_fp8_matmul(const uint8_t* A, int32_t a_format, const float* a_scales, int64_t M, const uint8_t* W,
                           const float* w_scales, int64_t rows, int64_t cols, int32_t transpose, const uint16_t* A2,
-                          const uint16_t* B2, int32_t R, uint16_t* C, void* stream) {
-  if (transpose != 0 && transpose != 1) return NF4_ERR_ARG;
+                          const uint16_t* B2, int32_t R, uint16_t* C, void* ws, size_t ws_bytes, void* stream) {
   const Fp8Gemm q{A, a_format == NF4_FP8_E5M2, a_scales, M, W, w_scales, rows, cols, transpose == 1, 0, nullptr, A2, B2,
-                  R, C};
-  return fp8_product(q, a_format, stream);
+                  R, C, nullptr};
+  return fp8_product(q, a_format, transpose, ws, ws_bytes, stream);
 }
 
 nf4_status nf4_fp8_matmul_grouped(const uint8_t* A, int32_t a_format, const float* a_scales, int64_t M,
                                   const uint8_t* W, const float* w_scales, int32_t experts, int64_t rows, int64_t cols,
                                   const int32_t* offsets, int32_t transpose, const uint16_t* A2, const uint16_t* B2,
-                                  int32_t R, uint16_t* C, void* stream) {
-  if (transpose != 0 && transpose != 1) return NF4_ERR_ARG;
-  if (experts < 1 || experts > 4096) return NF4_ERR_SHAPE;
+                                  int32_t R, uint16_t* C, void* ws, size_t ws_bytes, void* stream) {
+  if (experts < 1) return NF4_ERR_SHAPE;
   const Fp8Gemm q{A, a_format == NF4_FP8_E5M2, a_scales, M, W, w_scales, rows, cols, transpose == 1, experts, offsets,
-                  A2, B2, R, C};
-  return fp8_product(q, a_format, stream);
+                  A2, B2, R, C, nullptr};
+  return fp8_product(q, a_format, transpose, ws, ws_bytes, stream);
 }
 
 nf4_status nf4_rmsnorm_fwd(const uint16_t* X, const uint16_t* res, const uint16_t* w, int64_t M, int64_t H, float eps,

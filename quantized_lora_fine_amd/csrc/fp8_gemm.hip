@@ -51,7 +51,18 @@ struct Args {
   int N, K, R;
   int experts;
   int tiles_n;
+  float* part;  // [gridDim.y][M][N], where the contraction is split over gridDim.y workgroups
 };
+
+// This workgroup's blocks of the contraction: kb of them from kb0 on.
+__device__ __forceinline__ void k_range(int blocks, int& kb0, int& kb) {
+  kb0 = 0;
+  kb = blocks;
+  if (gridDim.y == 1) return;
+  const uint32_t y = blockIdx.y;
+  kb0 = (int)(blocks * y / gridDim.y);
+  kb = (int)(blocks * (y + 1) / gridDim.y) - kb0;
+}
 
 // Tile `t` of a product grouped by expert: its expert and rows [m0, m1).  Every
 // wave finds it by itself: 64 experts at a time, a scan of their tile counts.
@@ -88,6 +99,11 @@ __device__ __forceinline__ bool find_tile(const Args& p, int bm, int t, int& e, 
     base += (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
   }
   return false;
+}
+
+// four neighbouring sums of a split contraction
+__device__ __forceinline__ void store_part(const Args& p, int64_t m0, int mrows, int row, int n, floatx4 s) {
+  if (row < mrows && n < p.N) *(floatx4*)(p.part + (blockIdx.y * p.M + m0 + row) * p.N + n) = s;
 }
 
 constexpr int kWaitLds = 15 | (3 << 14) | (0x7 << 4);  // lgkmcnt(0), vmcnt as it is
@@ -168,7 +184,10 @@ __global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
   tile_of(GROUPED, tiles_m, p.tiles_n, tm, tn);
   const int n0 = tn * BN;
   const int N = p.N, K = p.K;
-  const int KB = (K + 127) / 128;
+  const int KS = (K + 127) / 128;
+  int kb0, KB;
+  k_range(KS, kb0, KB);
+  const int KL = K - kb0 * 128;  // columns from this workgroup's first on
   const int NB = (N + 127) / 128;
   int e = 0;
   int64_t m0, m1;
@@ -179,11 +198,11 @@ __global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
     m1 = min(m0 + BM, p.M);
   }
   const int mrows = (int)(m1 - m0);
-  const uint8_t* W = p.W + (GROUPED ? (int64_t)e * N * K : 0);
-  const float* ws = p.ws + (GROUPED ? (int64_t)e * NB * KB : 0);
+  const uint8_t* W = p.W + (GROUPED ? (int64_t)e * N * K : 0) + (TR ? (int64_t)kb0 * 128 * N : kb0 * 128);
+  const float* ws = p.ws + (GROUPED ? (int64_t)e * NB * KS : 0) + (TR ? (int64_t)kb0 * NB : kb0);
 
-  const __amdgpu_buffer_rsrc_t ar = make_rsrc(p.A + m0 * K, (uint32_t)((int64_t)mrows * K));
-  const __amdgpu_buffer_rsrc_t sr = make_rsrc(p.as + m0 * KB, (uint32_t)((int64_t)mrows * KB * 4));
+  const __amdgpu_buffer_rsrc_t ar = make_rsrc(p.A + m0 * K + kb0 * 128, (uint32_t)((int64_t)mrows * K - kb0 * 128));
+  const __amdgpu_buffer_rsrc_t sr = make_rsrc(p.as + m0 * KS + kb0, (uint32_t)(((int64_t)mrows * KS - kb0) * 4));
   const int nrows = min(BN, N - n0);
   // The buffer range covers the rows that exist, and its check takes the scalar
   // offset in, so one lane offset serves all of a wave's copies.
@@ -201,12 +220,12 @@ __global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
   } else {
     w_off = (uint32_t)(((c_row / HW) * WN + c_row % HW) * K + c_chunk * 16);  // copy 1: + 128 rows
   }
-  const uint32_t s_off = lane < SR ? (uint32_t)((wave * SR + lane) * KB * 4) : kOOB;
+  const uint32_t s_off = lane < SR ? (uint32_t)((wave * SR + lane) * KS * 4) : kOOB;
   // Steps behind the last one load its tile once more, so the loop has no
   // branches and every wait counts the same loads.
   auto copy_a = [&](int kt, int b, int i) {
     kt = min(kt, KB - 1);
-    const uint32_t off = kt * 128 + c_chunk * 16 < K ? a_off : kOOB;
+    const uint32_t off = kt * 128 + c_chunk * 16 < KL ? a_off : kOOB;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (lds_ptr_t)(abuf(b) + (i * NW + wave) * 1024), 16, off,
                                              kt * 128 + i * 64 * K, 0, 0);
   };
@@ -219,19 +238,19 @@ __global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
     const lds_ptr_t to = (lds_ptr_t)(wbuf(b, h) + (i * NW + wave) * 1024);
     if constexpr (TR) {
       const __amdgpu_buffer_rsrc_t wr =
-          make_rsrc(W + (int64_t)kt * 128 * N, (uint32_t)(min(128, K - kt * 128) * (int64_t)N));
+          make_rsrc(W + (int64_t)kt * 128 * N, (uint32_t)(min(128, KL - kt * 128) * (int64_t)N));
       const uint32_t off = col0 + h * HW < N ? w_off : kOOB;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, to, 16, off, h * HW + i * 64 * N, 0, 0);
     } else {
-      const __amdgpu_buffer_rsrc_t wr = make_rsrc(W + (int64_t)n0 * K, (uint32_t)((int64_t)nrows * K));
-      const uint32_t off = kt * 128 + c_chunk * 16 < K ? w_off : kOOB;
+      const __amdgpu_buffer_rsrc_t wr = make_rsrc(W + (int64_t)n0 * K, (uint32_t)((int64_t)nrows * K - kb0 * 128));
+      const uint32_t off = kt * 128 + c_chunk * 16 < KL ? w_off : kOOB;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, to, 16, off, kt * 128 + (i * 128 + h * HW) * K, 0, 0);
     }
   };
   const int nb = min((n0 + wn * WN) >> 7, NB - 1);
   auto load_ws = [&](int kt) -> float {
     const int k = min(kt + lane, KB - 1);
-    return TR ? ws[(int64_t)k * NB + nb] : ws[(int64_t)nb * KB + k];
+    return TR ? ws[(int64_t)k * NB + nb] : ws[(int64_t)nb * KS + k];
   };
 
   // LDS places of this lane's fragment pieces; subtile i adds 2 KB, or (TR) flips
@@ -402,7 +421,7 @@ __global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
   fold(NI - 1, d[(NI - 1) & 1]);
   __builtin_amdgcn_s_waitcnt(wait_vm(0));
 
-  if (p.R) {
+  if (p.R && blockIdx.y == 0) {
     const __amdgpu_buffer_rsrc_t a2 = make_rsrc(p.A2 + m0 * p.R, (uint32_t)((int64_t)mrows * p.R * 2));
     const __amdgpu_buffer_rsrc_t b2 =
         make_rsrc(p.B2 + ((GROUPED ? (int64_t)e * N : 0) + n0) * p.R, (uint32_t)((int64_t)nrows * p.R * 2));
@@ -423,6 +442,14 @@ __global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
     }
   }
 
+  if (gridDim.y > 1) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+        store_part(p, m0, mrows, wm * 64 + i * 16 + l16, n0 + wn * WN + j * 16 + 4 * g, acc[i][j]);
+    return;
+  }
   __syncthreads();
   // the result tile of a wave in its own part of the operand buffers
   constexpr int WB = 64 * WN * 2, PA = BM * 128 / WB, PW = 16384 / WB;
@@ -472,7 +499,7 @@ __global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
 // 11008 x 4096.  32 or 128 bytes of each k row instead of 64 are within 10 % of it
 // either way, and copies issued before a round's products instead of after are no
 // faster.
-template <int MT, int NT, int NWV, int ST, bool TR, bool E5M2, bool GROUPED>
+template <int MT, int NT, int NWV, int ST, bool TR, bool SPLIT, bool E5M2, bool GROUPED>
 __global__ __launch_bounds__(NWV * 64) void k_fp8_rows(Args p) {
   static_assert(!TR || NT == 4, "64 bytes of each k row");
   constexpr int BM = 16 * MT, BN = 16 * NT;
@@ -499,7 +526,10 @@ __global__ __launch_bounds__(NWV * 64) void k_fp8_rows(Args p) {
   const int tm = GROUPED ? id / p.tiles_n : id % tiles_m;
   const int n0 = (GROUPED ? id % p.tiles_n : id / tiles_m) * BN;
   const int N = p.N, K = p.K;
-  const int KB = (K + 127) / 128;
+  const int KS = (K + 127) / 128;
+  int kb0 = 0, KB = KS;
+  if constexpr (SPLIT) k_range(KS, kb0, KB);
+  const int KL = K - kb0 * 128;  // columns from this workgroup's first on
   const int NB = (N + 127) / 128;
   int e = 0;
   int64_t m0, m1;
@@ -511,10 +541,10 @@ __global__ __launch_bounds__(NWV * 64) void k_fp8_rows(Args p) {
   }
   const int mrows = (int)(m1 - m0);
   const int nrows = min(BN, N - n0);
-  const uint8_t* W = p.W + (GROUPED ? (int64_t)e * N * K : 0);
-  const float* ws = p.ws + (GROUPED ? (int64_t)e * NB * KB : 0);
-  const __amdgpu_buffer_rsrc_t ar = make_rsrc(p.A + m0 * K, (uint32_t)((int64_t)mrows * K));
-  const __amdgpu_buffer_rsrc_t sr = make_rsrc(p.as + m0 * KB, (uint32_t)((int64_t)mrows * KB * 4));
+  const uint8_t* W = p.W + (GROUPED ? (int64_t)e * N * K : 0) + (TR ? (int64_t)kb0 * 128 * N : kb0 * 128);
+  const float* ws = p.ws + (GROUPED ? (int64_t)e * NB * KS : 0) + (TR ? (int64_t)kb0 * NB : kb0);
+  const __amdgpu_buffer_rsrc_t ar = make_rsrc(p.A + m0 * K + kb0 * 128, (uint32_t)((int64_t)mrows * K - kb0 * 128));
+  const __amdgpu_buffer_rsrc_t sr = make_rsrc(p.as + m0 * KS + kb0, (uint32_t)(((int64_t)mrows * KS - kb0) * 4));
 
   // copies: 8 lanes a row, chunks XORed with the row's low bits (see k_fp8_wide)
   const int c_row = lane >> 3, c_k = ((lane & 7) ^ c_row) * 16;
@@ -525,22 +555,22 @@ __global__ __launch_bounds__(NWV * 64) void k_fp8_rows(Args p) {
   const uint32_t t_off = t_col < N ? (uint32_t)(t_row * N + t_col) : kOOB;
   // (a branch around the other lanes would make the compiler's own waits count this
   // load as one that may not be there)
-  const uint32_t s_off = lane < BM ? (uint32_t)(lane * KB * 4) : kOOB;
+  const uint32_t s_off = lane < BM ? (uint32_t)(lane * KS * 4) : kOOB;
   auto lbuf = [&](int b) -> uint8_t* { return (b == 0 ? L0 : b == 1 ? L1 : b == 2 ? L2 : L3) + wave * WB; };
   constexpr int LOADS = 2 * MT + 2 * NT + 1;
   auto copy = [&](int kt, int b) {
     kt = min(kt, KB - 1);  // a round behind the last copies it once more, and is not used
     uint8_t* const to = lbuf(b);
-    const bool in = kt * 128 + c_k < K;
+    const bool in = kt * 128 + c_k < KL;
     const uint32_t off = in ? a_off : kOOB;
     if constexpr (TR) {
       const __amdgpu_buffer_rsrc_t wr =
-          make_rsrc(W + (int64_t)kt * 128 * N, (uint32_t)(min(128, K - kt * 128) * (int64_t)N));
+          make_rsrc(W + (int64_t)kt * 128 * N, (uint32_t)(min(128, KL - kt * 128) * (int64_t)N));
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_ptr_t)(to + WOFF + i * 1024), 16, t_off, i * 16 * N, 0, 0);
     } else {
-      const __amdgpu_buffer_rsrc_t wr = make_rsrc(W + (int64_t)n0 * K, (uint32_t)((int64_t)nrows * K));
+      const __amdgpu_buffer_rsrc_t wr = make_rsrc(W + (int64_t)n0 * K, (uint32_t)((int64_t)nrows * K - kb0 * 128));
 #pragma unroll
       for (int i = 0; i < 2 * NT; ++i)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_ptr_t)(to + WOFF + i * 1024), 16, off, kt * 128 + i * 8 * K,
@@ -555,7 +585,7 @@ __global__ __launch_bounds__(NWV * 64) void k_fp8_rows(Args p) {
   const int nb = n0 >> 7;
   auto load_ws = [&](int r) -> float {
     const int k = min((r + lane) * NWV + wave, KB - 1);
-    return TR ? ws[(int64_t)k * NB + nb] : ws[(int64_t)nb * KB + k];
+    return TR ? ws[(int64_t)k * NB + nb] : ws[(int64_t)nb * KS + k];
   };
 
   floatx4 acc[MT][NT];
@@ -630,7 +660,7 @@ __global__ __launch_bounds__(NWV * 64) void k_fp8_rows(Args p) {
   __builtin_amdgcn_s_waitcnt(wait_vm(0));
 
   // the low-rank term: runs of 32 of its columns, dealt to the waves
-  for (int k0 = wave * 32; k0 < p.R; k0 += NWV * 32) {
+  for (int k0 = wave * 32; k0 < (SPLIT && blockIdx.y ? 0 : p.R); k0 += NWV * 32) {
     const __amdgpu_buffer_rsrc_t a2 = make_rsrc(p.A2 + m0 * p.R, (uint32_t)((int64_t)mrows * p.R * 2));
     const __amdgpu_buffer_rsrc_t b2 =
         make_rsrc(p.B2 + ((GROUPED ? (int64_t)e * N : 0) + n0) * p.R, (uint32_t)((int64_t)nrows * p.R * 2));
@@ -662,7 +692,8 @@ __global__ __launch_bounds__(NWV * 64) void k_fp8_rows(Args p) {
     for (int w = 1; w < NWV; ++w) s += part[w * MT * NT * 64 + q];
     const int row = t / NT * 16 + (l & 15);
     const int n = n0 + t % NT * 16 + 4 * (l >> 4);
-    if (row < mrows && n < N)
+    if constexpr (SPLIT) store_part(p, m0, mrows, row, n, s);
+    else if (row < mrows && n < N)
       *(uint2*)(p.C + (m0 + row) * N + n) = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
   }
 }
@@ -704,7 +735,10 @@ __global__ __launch_bounds__(512) void k_fp8_ring(Args p) {
   tile_of(GROUPED, tiles_m, p.tiles_n, tm, tn);
   const int n0 = tn * BN;
   const int N = p.N, K = p.K;
-  const int KB = (K + 127) / 128;
+  const int KS = (K + 127) / 128;
+  int kb0, KB;
+  k_range(KS, kb0, KB);
+  const int KL = K - kb0 * 128;  // columns from this workgroup's first on
   const int NB = (N + 127) / 128;
   int e = 0;
   int64_t m0, m1;
@@ -716,22 +750,22 @@ __global__ __launch_bounds__(512) void k_fp8_ring(Args p) {
   }
   const int mrows = (int)(m1 - m0);
   const int nrows = min(BN, N - n0);
-  const uint8_t* W = p.W + (GROUPED ? (int64_t)e * N * K : 0);
-  const float* ws = p.ws + (GROUPED ? (int64_t)e * NB * KB : 0);
-  const __amdgpu_buffer_rsrc_t ar = make_rsrc(p.A + m0 * K, (uint32_t)((int64_t)mrows * K));
-  const __amdgpu_buffer_rsrc_t wr = make_rsrc(W + (int64_t)n0 * K, (uint32_t)((int64_t)nrows * K));
-  const __amdgpu_buffer_rsrc_t sr = make_rsrc(p.as + m0 * KB, (uint32_t)((int64_t)mrows * KB * 4));
+  const uint8_t* W = p.W + (GROUPED ? (int64_t)e * N * K : 0) + kb0 * 128;
+  const float* ws = p.ws + (GROUPED ? (int64_t)e * NB * KS : 0) + kb0;
+  const __amdgpu_buffer_rsrc_t ar = make_rsrc(p.A + m0 * K + kb0 * 128, (uint32_t)((int64_t)mrows * K - kb0 * 128));
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc(W + (int64_t)n0 * K, (uint32_t)((int64_t)nrows * K - kb0 * 128));
+  const __amdgpu_buffer_rsrc_t sr = make_rsrc(p.as + m0 * KS + kb0, (uint32_t)(((int64_t)mrows * KS - kb0) * 4));
 
   // copies and fragments as in k_fp8_wide
   const int c_row = wave * 8 + (lane >> 3);  // of copy i: plus i * 64
   const int c_chunk = (lane & 7) ^ (c_row & 7);
   const uint32_t c_off = (uint32_t)(c_row * K + c_chunk * 16);
-  const uint32_t s_off = lane < SR ? (uint32_t)((wave * SR + lane) * KB * 4) : kOOB;
+  const uint32_t s_off = lane < SR ? (uint32_t)((wave * SR + lane) * KS * 4) : kOOB;
   constexpr int C = AI + WI + 1;  // loads a step
   auto copy = [&](int kt, int b) {
     kt = min(kt, KB - 1);  // a step behind the last copies it once more, and is not used
     uint8_t* const to = lbuf(b);
-    const uint32_t off = kt * 128 + c_chunk * 16 < K ? c_off : kOOB;
+    const uint32_t off = kt * 128 + c_chunk * 16 < KL ? c_off : kOOB;
 #pragma unroll
     for (int i = 0; i < AI; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (lds_ptr_t)(to + (i * NW + wave) * 1024), 16, off,
@@ -744,7 +778,7 @@ __global__ __launch_bounds__(512) void k_fp8_ring(Args p) {
   };
   const int nb = n0 >> 7;
   auto load_ws = [&](int kt) -> float {
-    return ws[(int64_t)nb * KB + min(kt + lane, KB - 1)];
+    return ws[(int64_t)nb * KS + min(kt + lane, KB - 1)];
   };
 
   constexpr int WN = BN / WC;  // columns of a wave
@@ -824,7 +858,7 @@ __global__ __launch_bounds__(512) void k_fp8_ring(Args p) {
     if (kt + b < KB) step(kt + b, b);
   __builtin_amdgcn_s_waitcnt(wait_vm(0));
 
-  if (p.R) {
+  if (p.R && blockIdx.y == 0) {
     const __amdgpu_buffer_rsrc_t a2 = make_rsrc(p.A2 + m0 * p.R, (uint32_t)((int64_t)mrows * p.R * 2));
     const __amdgpu_buffer_rsrc_t b2 =
         make_rsrc(p.B2 + ((GROUPED ? (int64_t)e * N : 0) + n0) * p.R, (uint32_t)((int64_t)nrows * p.R * 2));
@@ -845,6 +879,14 @@ __global__ __launch_bounds__(512) void k_fp8_ring(Args p) {
     }
   }
 
+  if (gridDim.y > 1) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+        store_part(p, m0, mrows, (wm * MI + i) * 16 + l16, n0 + wn * WN + j * 16 + 4 * g, acc[i][j]);
+    return;
+  }
   __syncthreads();  // every wave is done with the buffers: the result tile goes through the first
   constexpr int PC = BN / 8;  // 16-byte pieces of a row
   static_assert(BM * BN * 2 <= SB, "the result tile fits");
@@ -869,13 +911,35 @@ __global__ __launch_bounds__(512) void k_fp8_ring(Args p) {
   }
 }
 
+// C = bf16(sum of the parts), in their order; of a grouped product the experts' rows
+// alone.  8 values a lane.
+__global__ __launch_bounds__(256) void k_fp8_join(const float* __restrict__ part, int splits, int64_t M, int N,
+                                                  const int32_t* __restrict__ offsets, int experts,
+                                                  uint16_t* __restrict__ C) {
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;  // M * N / 8 < 2^31
+  const uint32_t per_row = (uint32_t)N / 8;
+  if (i >= (uint32_t)M * per_row) return;
+  if (offsets) {
+    const int row = (int)(i / per_row);
+    if (row < offsets[0] || row >= offsets[experts]) return;
+  }
+  floatx4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+  for (int k = 0; k < splits; ++k) {
+    const floatx4* at = (const floatx4*)(part + k * M * N + (int64_t)i * 8);
+    lo += at[0];
+    hi += at[1];
+  }
+  *(u32x4*)(C + (int64_t)i * 8) = u32x4{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[0], hi[1]),
+                                        pack_bf16x2(hi[2], hi[3])};
+}
+
 // one launch of tile kind `kind` over all of p's rows
-hipError_t launch_part(const Fp8Gemm& q, Args p, int kind, hipStream_t st) {
+hipError_t launch_part(const Fp8Gemm& q, Args p, int kind, int splits, hipStream_t st) {
   const Fp8Kind& k = fp8_kinds()[kind];
   p.tiles_n = (p.N + k.bn - 1) / k.bn;
   const int64_t tiles =
       q.experts ? fp8_grouped_tiles(kind, p.M, p.N, q.experts) : (p.M + k.bm - 1) / k.bm * p.tiles_n;
-  const dim3 gr((unsigned)tiles), bl((unsigned)k.threads);
+  const dim3 gr((unsigned)tiles, (unsigned)splits), bl((unsigned)k.threads);
 #define NF4K_LAUNCH(...) hipLaunchKernelGGL((__VA_ARGS__), gr, bl, 0, st, p)
 #define NF4K_FLAGS(KERNEL, ...)                                                     \
   do {                                                                              \
@@ -892,24 +956,35 @@ hipError_t launch_part(const Fp8Gemm& q, Args p, int kind, hipStream_t st) {
     if (q.transpose) NF4K_FLAGS(k_fp8_wide, NI, true);      \
     else NF4K_FLAGS(k_fp8_wide, NI, false);                 \
   } while (0)
+// (without the split's few instructions one row by 4096 x 4096 is 4 % faster)
+#define NF4K_ROWS(...)                                              \
+  do {                                                              \
+    if (splits > 1) NF4K_FLAGS(k_fp8_rows, __VA_ARGS__, true);      \
+    else NF4K_FLAGS(k_fp8_rows, __VA_ARGS__, false);                \
+  } while (0)
   switch (kind) {
     case kFp8Wide8: NF4K_WIDE(8); break;
     case kFp8Wide4: NF4K_WIDE(4); break;
     case kFp8Wide2: NF4K_WIDE(2); break;
     case kFp8Ring22: NF4K_FLAGS(k_fp8_ring, 128, 128, 4); break;
     case kFp8Ring21: NF4K_FLAGS(k_fp8_ring, 128, 64, 6); break;
-    case kFp8Rows11: NF4K_FLAGS(k_fp8_rows, 1, 1, 4, 4, false); break;
-    case kFp8Rows12: NF4K_FLAGS(k_fp8_rows, 1, 2, 4, 3, false); break;
-    case kFp8Rows22: NF4K_FLAGS(k_fp8_rows, 2, 2, 8, 2, false); break;
-    case kFp8Rows42: NF4K_FLAGS(k_fp8_rows, 4, 2, 4, 3, false); break;
-    case kFp8Rows44: NF4K_FLAGS(k_fp8_rows, 4, 4, 4, 2, false); break;
-    case kFp8Rows14T: NF4K_FLAGS(k_fp8_rows, 1, 4, 4, 3, true); break;
-    case kFp8Rows24T: NF4K_FLAGS(k_fp8_rows, 2, 4, 4, 3, true); break;
-    default: NF4K_FLAGS(k_fp8_rows, 4, 4, 4, 2, true); break;
+    case kFp8Rows11: NF4K_ROWS(1, 1, 4, 4, false); break;
+    case kFp8Rows12: NF4K_ROWS(1, 2, 4, 3, false); break;
+    case kFp8Rows22: NF4K_ROWS(2, 2, 8, 2, false); break;
+    case kFp8Rows42: NF4K_ROWS(4, 2, 4, 3, false); break;
+    case kFp8Rows44: NF4K_ROWS(4, 4, 4, 2, false); break;
+    case kFp8Rows14T: NF4K_ROWS(1, 4, 4, 3, true); break;
+    case kFp8Rows24T: NF4K_ROWS(2, 4, 4, 3, true); break;
+    default: NF4K_ROWS(4, 4, 4, 2, true); break;
   }
+#undef NF4K_ROWS
 #undef NF4K_WIDE
 #undef NF4K_FLAGS
 #undef NF4K_LAUNCH
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits == 1) return e;
+  hipLaunchKernelGGL(k_fp8_join, dim3((unsigned)((p.M * (p.N / 8) + 255) / 256)), dim3(256), 0, st, p.part, splits, p.M,
+                     p.N, q.experts ? q.offsets : nullptr, q.experts, p.C);
   return hipGetLastError();
 }
 
@@ -927,7 +1002,8 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& q, hipStream_t st) {
   p.experts = q.experts;
   const int KB = (p.K + 127) / 128;
   Fp8Part parts[2];
-  const int n = plan_fp8(q.M, p.N, p.K, q.transpose, q.experts, parts);
+  p.part = q.part;
+  const int n = plan_fp8(q.M, p.N, p.K, q.transpose, q.experts, q.part != nullptr, parts);
   int64_t r0 = 0;
   for (int i = 0; i < n; ++i) {
     // a launch holds at most 2^32 - 1 work-items: more tiles run as ranges of rows
@@ -941,7 +1017,7 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& q, hipStream_t st) {
       p.A2 = q.A2 ? q.A2 + r0 * q.R : nullptr;
       p.C = q.C + r0 * p.N;
       p.M = rows;
-      const hipError_t e = launch_part(q, p, parts[i].kind, st);
+      const hipError_t e = launch_part(q, p, parts[i].kind, parts[i].splits, st);
       if (e != hipSuccess) return e;
       r0 += rows;
     }

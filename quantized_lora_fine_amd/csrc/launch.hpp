@@ -196,6 +196,7 @@ struct Fp8Gemm {
   const uint16_t* B2;
   int R;
   uint16_t* C;
+  float* part;  // fp8_split_bytes of it, or NULL: no contraction is split
 };
 // The product's tile kinds (rows bm by columns bn a workgroup of `threads`), and
 // what one costs; plan_fp8 picks the kind, or two for two ranges of rows, that
@@ -212,6 +213,7 @@ struct Fp8Kind {
 struct Fp8Part {
   int kind;
   int64_t rows;
+  int splits;  // workgroups that share a tile's contraction
 };
 const Fp8Kind* fp8_kinds();
 // A grouped product is one launch: its workgroups (every expert's last tile may be
@@ -219,7 +221,9 @@ const Fp8Kind* fp8_kinds();
 // the largest kind, kFp8Wide8, to fit.
 int64_t fp8_grouped_tiles(int kind, int64_t M, int N, int experts);
 bool fp8_grouped_fits(int kind, int64_t M, int N, int experts);
-int plan_fp8(int64_t M, int N, int K, bool transpose, int experts, Fp8Part parts[2]);
+int plan_fp8(int64_t M, int N, int K, bool transpose, int experts, bool may_split, Fp8Part parts[2]);
+// bytes of the fp32 parts that plan_fp8 with may_split wants (0: it splits nothing)
+int64_t fp8_split_bytes(int64_t M, int N, int K, bool transpose, int experts);
 NF4K_WEAK hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t st);
 
 }  // namespace nf4k

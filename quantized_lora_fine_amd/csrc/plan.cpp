@@ -134,18 +134,28 @@ namespace {
 constexpr int kCUs = 256;
 constexpr double kFp8Launch = 3.0;  // microseconds
 
+constexpr double kFp8Join = 2.5, kFp8JoinRate = 4e6;  // the join's launch, and bytes a microsecond of it
+constexpr int64_t kFp8SplitBytes = (int64_t)1 << 26;
+
 // the launch and every set of tiles that the compute units hold at once
-double fp8_time(int kind, int64_t tiles_m, int N, int K) {
+double fp8_time(int kind, int64_t tiles_m, int N, int K, int splits) {
   const Fp8Kind& k = fp8_kinds()[kind];
-  const int64_t tiles = tiles_m * ((N + k.bn - 1) / k.bn);
+  const int64_t tiles = tiles_m * ((N + k.bn - 1) / k.bn) * splits;
   const double fill = tiles >= kCUs ? 1.0 : (double)tiles / kCUs;
-  return kFp8Launch +
-         (double)((tiles + kCUs - 1) / kCUs) * (k.start + ((K + 127) / 128) * (k.u0 + (k.u1 - k.u0) * fill));
+  const int64_t steps = ((K + 127) / 128 + splits - 1) / splits;
+  return kFp8Launch + (double)((tiles + kCUs - 1) / kCUs) * (k.start + steps * (k.u0 + (k.u1 - k.u0) * fill));
 }
 
-int fp8_best(int64_t M, int N, int K, bool transpose, int experts, double* time) {
+// The kind, and over how many workgroups a tile's contraction is split: where
+// there are fewer tiles than compute units, as long as each part has 4 blocks, the
+// parts fit 64 MB, and a tenth is gained by the costs: no split beats the weights'
+// own stream, and the join is a launch more (3 rows by 11008 x 4096 transposed 28
+// -> 16.5 us, 900 rows over two experts of 6144 x 1328 transposed 60 -> 31).
+int fp8_best(int64_t M, int N, int K, bool transpose, int experts, bool may_split, double* time, int* splits) {
   int best = -1;
   double least = 0;
+  *splits = 1;
+  const double stream = (double)(experts ? std::min<int64_t>(M, experts) : 1) * N * K / 5.5e6;  // the weights, once
   for (int i = 0; i < kFp8Kinds; ++i) {
     const bool wide = i <= kFp8Wide2, t = i >= kFp8Rows14T;
     if (!wide && t != transpose) continue;
@@ -169,10 +179,17 @@ int fp8_best(int64_t M, int N, int K, bool transpose, int experts, double* time)
       if (tiles_m < used) tiles_m = used;
       if (!fp8_grouped_fits(i, M, N, experts)) continue;
     }
-    const double x = fp8_time(i, tiles_m, N, K);
-    if (best < 0 || x < least) {
-      least = x;
-      best = i;
+    const int64_t tiles = tiles_m * ((N + fp8_kinds()[i].bn - 1) / fp8_kinds()[i].bn);
+    for (int s : {1, 2, 3, 4, 6, 8}) {
+      if (s > 1 && (!may_split || s > K / 512 || s * tiles > 2 * kCUs || s * M * N * 4 > kFp8SplitBytes)) break;
+      double x = fp8_time(i, tiles_m, N, K, s);
+      if (s > 1)
+        x = 1.1 * (std::max(x, kFp8Launch + stream) + kFp8Join + (double)(M * N * (8 * s + 2)) / kFp8JoinRate);
+      if (best < 0 || x < least) {
+        least = x;
+        best = i;
+        *splits = s;
+      }
     }
   }
   *time = least;
@@ -181,9 +198,9 @@ int fp8_best(int64_t M, int N, int K, bool transpose, int experts, double* time)
 
 }  // namespace
 
-int plan_fp8(int64_t M, int N, int K, bool transpose, int experts, Fp8Part parts[2]) {
+int plan_fp8(int64_t M, int N, int K, bool transpose, int experts, bool may_split, Fp8Part parts[2]) {
   double least;
-  parts[0].kind = fp8_best(M, N, K, transpose, experts, &least);
+  parts[0].kind = fp8_best(M, N, K, transpose, experts, may_split, &least, &parts[0].splits);
   parts[0].rows = M;
   int n = 1;
   if (experts) return n;
@@ -196,18 +213,31 @@ int plan_fp8(int64_t M, int N, int K, bool transpose, int experts, Fp8Part parts
     const int64_t rows = sets * kCUs / tiles_n * k.bm;
     if (rows <= 0 || rows >= M) continue;
     double rest;
-    const int kind = fp8_best(M - rows, N, K, transpose, 0, &rest);
-    const double x = fp8_time(i, rows / k.bm, N, K) + rest;
+    int splits;
+    const int kind = fp8_best(M - rows, N, K, transpose, 0, may_split, &rest, &splits);
+    const double x = fp8_time(i, rows / k.bm, N, K, 1) + rest;
     if (x < 0.95 * least) {  // a second launch has to be worth it
       least = x;
       n = 2;
       parts[0].kind = i;
       parts[0].rows = rows;
+      parts[0].splits = 1;
       parts[1].kind = kind;
       parts[1].rows = M - rows;
+      parts[1].splits = splits;
     }
   }
   return n;
+}
+
+int64_t fp8_split_bytes(int64_t M, int N, int K, bool transpose, int experts) {
+  Fp8Part parts[2];
+  const int n = plan_fp8(M, N, K, transpose, experts, true, parts);
+  int64_t most = 0;
+  for (int i = 0; i < n; ++i)
+    if (parts[i].splits > 1 && parts[i].splits * parts[i].rows * N * 4 > most)
+      most = parts[i].splits * parts[i].rows * N * 4;
+  return most;
 }
 
 int error_batch_chunk(const int64_t* rows, const int64_t* cols, int32_t n, int32_t c0, int64_t* g0) {

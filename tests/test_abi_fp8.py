@@ -34,12 +34,13 @@ def dequantize(codes=A, scales=S, rows=8, cols=272, fmt=0, block_rows=1, out=C, 
     return lib.nf4_fp8_dequantize(codes, scales, rows, cols, fmt, block_rows, out, bf16, None)
 
 
-def matmul(a=A, fmt=0, s=S, M=8, w=W, ws=T, rows=144, cols=272, tr=0, a2=A2, b2=B2, R=16, c=C):
-    return lib.nf4_fp8_matmul(a, fmt, s, M, w, ws, rows, cols, tr, a2, b2, R, c, None)
+def matmul(a=A, fmt=0, s=S, M=8, w=W, ws=T, rows=144, cols=272, tr=0, a2=A2, b2=B2, R=16, c=C, work=None, n=0):
+    return lib.nf4_fp8_matmul(a, fmt, s, M, w, ws, rows, cols, tr, a2, b2, R, c, work, n, None)
 
 
-def grouped(a=A, fmt=0, s=S, M=8, w=W, ws=T, E=4, rows=144, cols=272, off=OFF, tr=0, a2=A2, b2=B2, R=16, c=C):
-    return lib.nf4_fp8_matmul_grouped(a, fmt, s, M, w, ws, E, rows, cols, off, tr, a2, b2, R, c, None)
+def grouped(a=A, fmt=0, s=S, M=8, w=W, ws=T, E=4, rows=144, cols=272, off=OFF, tr=0, a2=A2, b2=B2, R=16, c=C,
+            work=None, n=0):
+    return lib.nf4_fp8_matmul_grouped(a, fmt, s, M, w, ws, E, rows, cols, off, tr, a2, b2, R, c, work, n, None)
 
 
 def norm(X=A, res=S, w=W, M=8, H=272, eps=1e-6, h=T, Y=C, codes=A2, scales=B2, rstd=OFF):
@@ -78,6 +79,26 @@ def test_products_refuse(call):
             assert call(c={"a": A, "s": S, "w": W, "ws": T, "a2": A2, "b2": B2, "off": OFF}[p]) == nf4.NF4_ERR_ALIAS, p
     assert call(M=0) == nf4.NF4_OK
     assert call(M=0, a=None, c=None) == nf4.NF4_OK
+
+
+def test_product_workspace():
+    n = ctypes.c_size_t()
+    size = lib.nf4_fp8_matmul_workspace_bytes
+    assert size(8, 144, 272, 0, 0, None) == nf4.NF4_ERR_NULL
+    assert size(8, 144, 272, 2, 0, ctypes.byref(n)) == nf4.NF4_ERR_ARG
+    for bad in ((8, 8, 272, 0, 0), (8, 144, 24, 0, 0), (-1, 144, 272, 0, 0), (8, 144, 272, 0, 4097), (8, 144, 272, 0, -1),
+                ((1 << 30) + 1, 144, 272, 0, 4), ((1 << 31) + 1, 144, 272, 0, 0)):
+        assert size(*bad, ctypes.byref(n)) == nf4.NF4_ERR_SHAPE, bad
+    assert nf4.fp8_matmul_workspace_bytes(0, 144, 272) == 0
+    # few tiles and a long contraction: split
+    for call, E in ((matmul, 0), (grouped, 2)):
+        need = nf4.fp8_matmul_workspace_bytes(64, 512, 16384, False, E)
+        assert 0 < need <= 1 << 26
+        big = {"M": 64, "rows": 512, "cols": 16384, **({"E": 2} if E else {})}
+        assert call(**big, work=64 * GB * 10, n=need - 1) == nf4.NF4_ERR_WORKSPACE
+        assert call(**big, work=64 * GB * 10 + 8, n=need) == nf4.NF4_ERR_ALIGN
+        for at in (A, S, W, T, A2, B2, C):
+            assert call(**big, work=at, n=need) == nf4.NF4_ERR_ALIAS
 
 
 def test_grouped_refuses():

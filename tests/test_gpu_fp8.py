@@ -353,9 +353,8 @@ EVERY_TILE = [  # M, N, K, transpose, experts: each kind of tile, dense and grou
 ]
 
 
-@pytest.mark.parametrize("R,fmt", [(64, "e5m2"), (16, "e4m3")])
-@pytest.mark.parametrize("M,N,K,transpose,experts", EVERY_TILE)
-def test_matmul_every_tile(M, N, K, transpose, experts, R, fmt):
+def check_tiles(M, N, K, transpose, experts, R, fmt, spoil=False):
+    """A product against fp64 on the device; spoil: with a workspace full of NaN, and again without one."""
     g = torch.Generator(device=DEV).manual_seed(M + N + K)
     E = experts or 1
     o, h = (K, N) if transpose else (N, K)
@@ -368,14 +367,31 @@ def test_matmul_every_tile(M, N, K, transpose, experts, R, fmt):
     A2 = torch.randn(M, R, generator=g, device=DEV).bfloat16()
     B2 = (0.05 * torch.randn(E, N, R, generator=g, device=DEV)).bfloat16()
     if experts:
-        counts = [M // 2, 0, 1, M - M // 2 - 3, 0]  # two rows behind
+        counts = [M // 2, 0, 1, M - M // 2 - 3, 0] if experts == 5 else [M // 2, 0, M - M // 2 - 2]  # two rows behind
         ends = np.concatenate([[0], np.cumsum(counts)])
         C = torch.full((M, N), 3.0, dtype=torch.bfloat16, device=DEV)
-        nf4.fp8_matmul_grouped(a, s, W, ws, torch.from_numpy(ends.astype(np.int32)).to(DEV), transpose, A2, B2, out=C)
-        assert torch.all(C[M - 2:] == 3.0)
+        offsets = torch.from_numpy(ends.astype(np.int32)).to(DEV)
     else:
         ends = np.array([0, M])
-        C = nf4.fp8_matmul(a, s, W[0], ws[0], transpose, A2, B2[0])
+        C = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+
+    def product(work=None):
+        if experts:
+            nf4.fp8_matmul_grouped(a, s, W, ws, offsets, transpose, A2, B2, out=C, ws=work)
+            assert torch.all(C[M - 2:] == 3.0)
+        else:
+            nf4.fp8_matmul(a, s, W[0], ws[0], transpose, A2, B2[0], out=C, ws=work)
+        return C.clone()
+
+    if spoil:
+        n = nf4.fp8_matmul_workspace_bytes(M, o, h, transpose, experts)
+        assert n > 0
+        work = torch.full((n + 16,), 0xFF, dtype=torch.uint8, device=DEV)
+        got = product(work)
+        assert torch.all(work[n:] == 0xFF)
+        assert torch.equal(product().view(torch.int16), got.view(torch.int16))  # one of its own
+    else:
+        product()
     A, D2 = nf4.fp8_dequantize(a, s).double(), A2.double()
     for e in range(E):
         r = slice(int(ends[e]), int(ends[e + 1]))
@@ -386,6 +402,31 @@ def test_matmul_every_tile(M, N, K, transpose, experts, R, fmt):
         X, T, U = A[r], D2[r], B2[e].double().t().contiguous()
         check_product(C[r], (f64(X @ D + T @ U), f64(X.abs() @ D.abs() + T.abs() @ U.abs()),
                              f64(((X * X) @ (D * D) + (T * T) @ (U * U)).sqrt())), K, R)
+
+
+@pytest.mark.parametrize("R,fmt", [(64, "e5m2"), (16, "e4m3")])
+@pytest.mark.parametrize("M,N,K,transpose,experts", EVERY_TILE)
+def test_matmul_every_tile(M, N, K, transpose, experts, R, fmt):
+    check_tiles(M, N, K, transpose, experts, R, fmt)
+
+
+SPLIT_TILES = [  # M, N, K, transpose, experts: each kind of tile with its contraction split
+    (4099, 528, 16400, False, 0), (3000, 144, 33040, False, 0), (130, 2064, 16400, False, 0), (260, 4112, 16400, False, 0),
+    (300, 1552, 33040, False, 0), (200, 784, 16400, False, 0), (1, 16, 16400, False, 0), (5, 1552, 65552, False, 0),
+    (130, 80, 16400, False, 0), (260, 80, 33040, False, 0), (4099, 16, 16400, False, 0), (520, 144, 33040, False, 0),
+    (3000, 272, 33040, True, 0), (3000, 80, 8208, True, 0), (2050, 80, 8208, True, 0), (48, 4112, 16400, True, 0),
+    (1, 16, 4112, True, 0), (5, 144, 33040, True, 0), (700, 16, 4112, True, 0), (2050, 16, 4112, True, 0),
+    (2050, 1040, 16400, False, 3), (4099, 144, 16400, False, 3), (200, 1552, 16400, False, 3), (1290, 784, 16400, False, 3),
+    (1030, 144, 16400, False, 3), (17, 16, 16400, False, 3), (260, 80, 33040, False, 3), (4099, 16, 16400, False, 3),
+    (800, 144, 16400, False, 3), (5, 528, 16400, False, 3), (3000, 272, 33040, True, 3), (1030, 1040, 16400, True, 3),
+    (1290, 80, 8208, True, 3), (17, 1040, 4112, True, 3), (700, 16, 4112, True, 3), (2050, 16, 4112, True, 3),
+]
+
+
+@pytest.mark.parametrize("R,fmt", [(64, "e5m2"), (16, "e4m3")])
+@pytest.mark.parametrize("M,N,K,transpose,experts", SPLIT_TILES)
+def test_matmul_split_contraction(M, N, K, transpose, experts, R, fmt):
+    check_tiles(M, N, K, transpose, experts, R, fmt, spoil=True)
 
 
 @pytest.mark.parametrize("transpose", [False, True])
@@ -731,7 +772,7 @@ def test_binding_refuses():
         lambda: nf4.fp8_quantize(x.half()), lambda: nf4.fp8_quantize(x.cpu()), lambda: nf4.fp8_quantize(x.t()),
         lambda: nf4.fp8_quantize(x, 1, torch.float16), lambda: nf4.fp8_quantize(x, 1, scales=s[:4]),
         lambda: nf4.fp8_quantize(x, 1, codes=a.view(torch.uint8)),
-        lambda: nf4.fp8_dequantize(x, s), lambda: nf4.fp8_dequantize(a, ws), lambda: nf4.fp8_dequantize(a, s, out=b),
+        lambda: nf4.fp8_dequantize(x, s), lambda: nf4.fp8_dequantize(a, ws), lambda: nf4.fp8_dequantize(a, s, out=b), lambda: nf4.fp8_matmul(a, s, W, ws, ws=x),
         lambda: nf4.fp8_matmul(a, ws, W, ws), lambda: nf4.fp8_matmul(a, s, W, ws, True),
         lambda: nf4.fp8_matmul(a, s, W.view(torch.float8_e5m2), ws), lambda: nf4.fp8_matmul(x, s, W, ws),
         lambda: nf4.fp8_matmul(a, s, W, ws, A2=A2), lambda: nf4.fp8_matmul(a, s, W, ws, A2=A2, B2=B2.t()),
