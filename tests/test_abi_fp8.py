@@ -91,10 +91,10 @@ def test_product_workspace():
         assert size(*bad, ctypes.byref(n)) == nf4.NF4_ERR_SHAPE, bad
     assert nf4.fp8_matmul_workspace_bytes(0, 144, 272) == 0
     # few tiles and a long contraction: split
-    for call, E in ((matmul, 0), (grouped, 2)):
-        need = nf4.fp8_matmul_workspace_bytes(64, 512, 16384, False, E)
+    for call, E in ((matmul, 0), (grouped, 3)):
+        need = nf4.fp8_matmul_workspace_bytes(260, 80, 33040, False, E)
         assert 0 < need <= 1 << 26
-        big = {"M": 64, "rows": 512, "cols": 16384, **({"E": 2} if E else {})}
+        big = {"M": 260, "rows": 80, "cols": 33040, **({"E": 3} if E else {})}
         assert call(**big, work=64 * GB * 10, n=need - 1) == nf4.NF4_ERR_WORKSPACE
         assert call(**big, work=64 * GB * 10 + 8, n=need) == nf4.NF4_ERR_ALIGN
         for at in (A, S, W, T, A2, B2, C):
