@@ -140,7 +140,7 @@ __device__ __forceinline__ void tile_of(bool grouped, int tiles_m, int tiles_n, 
 // kernel without the multiply-adds of the scales are 17 % faster, without the copies
 // of the operands 22 %, without the barriers 2 %.  The library's 8-bit product with
 // one scale for a whole matrix takes 2.5 ms.
-// 2048 rows by 4096 x 4096 (128 x 256 tiles, one a compute unit): 36 us, 1.9 PFLOP/s.
+// 2048 rows by 4096 x 4096 (128 x 256 tiles, one a compute unit): 37 us, 1.9 PFLOP/s.
 // Transposed, W's fragments are 8-byte transposing reads at half the rate of the
 // 16-byte ones: 4096 rows by 11008 x 4096: 168 us, 2.2 PFLOP/s.
 template <int NI, bool TR, bool E5M2, bool GROUPED>
@@ -496,7 +496,7 @@ __global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
 // a copy reaches; by 4096 x 4096 5.4 us, of which the launch and the first loads are
 // 3.  Transposed a workgroup's time goes with its k rows (1.5 ns each, whatever it
 // takes of a row's 128-byte line), so few rows are slower there: 29 us by
-// 11008 x 4096.  32 or 128 bytes of each k row instead of 64 are within 10 % of it
+// 11008 x 4096, 16 with the contraction split over 4.  32 or 128 bytes of each k row instead of 64 are within 10 % of it
 // either way, and copies issued before a round's products instead of after are no
 // faster.
 template <int MT, int NT, int NWV, int ST, bool TR, bool SPLIT, bool E5M2, bool GROUPED>
@@ -912,8 +912,10 @@ __global__ __launch_bounds__(512) void k_fp8_ring(Args p) {
 }
 
 // C = bf16(sum of the parts), in their order; of a grouped product the experts' rows
-// alone.  8 values a lane.
-__global__ __launch_bounds__(256) void k_fp8_join(const float* __restrict__ part, int splits, int64_t M, int N,
+// alone.  8 values a lane, whose parts are all loaded at once (512 columns by 11008
+// transposed, one row: 8.9 us with the product, against 10.4 for a loop over them).
+template <int SPLITS>
+__global__ __launch_bounds__(256) void k_fp8_join(const float* __restrict__ part, int64_t M, int N,
                                                   const int32_t* __restrict__ offsets, int experts,
                                                   uint16_t* __restrict__ C) {
   const uint32_t i = blockIdx.x * 256 + threadIdx.x;  // M * N / 8 < 2^31
@@ -923,11 +925,18 @@ __global__ __launch_bounds__(256) void k_fp8_join(const float* __restrict__ part
     const int row = (int)(i / per_row);
     if (row < offsets[0] || row >= offsets[experts]) return;
   }
-  floatx4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
-  for (int k = 0; k < splits; ++k) {
+  floatx4 v[SPLITS][2];
+#pragma unroll
+  for (int k = 0; k < SPLITS; ++k) {
     const floatx4* at = (const floatx4*)(part + k * M * N + (int64_t)i * 8);
-    lo += at[0];
-    hi += at[1];
+    v[k][0] = at[0];
+    v[k][1] = at[1];
+  }
+  floatx4 lo = v[0][0], hi = v[0][1];
+#pragma unroll
+  for (int k = 1; k < SPLITS; ++k) {
+    lo += v[k][0];
+    hi += v[k][1];
   }
   *(u32x4*)(C + (int64_t)i * 8) = u32x4{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[0], hi[1]),
                                         pack_bf16x2(hi[2], hi[3])};
@@ -983,8 +992,17 @@ hipError_t launch_part(const Fp8Gemm& q, Args p, int kind, int splits, hipStream
 #undef NF4K_LAUNCH
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
-  hipLaunchKernelGGL(k_fp8_join, dim3((unsigned)((p.M * (p.N / 8) + 255) / 256)), dim3(256), 0, st, p.part, splits, p.M,
-                     p.N, q.experts ? q.offsets : nullptr, q.experts, p.C);
+#define NF4K_JOIN(S)                                                                                               \
+  hipLaunchKernelGGL(k_fp8_join<S>, dim3((unsigned)((p.M * (p.N / 8) + 255) / 256)), dim3(256), 0, st, p.part, p.M, \
+                     p.N, q.experts ? q.offsets : nullptr, q.experts, p.C)
+  switch (splits) {
+    case 2: NF4K_JOIN(2); break;
+    case 3: NF4K_JOIN(3); break;
+    case 4: NF4K_JOIN(4); break;
+    case 6: NF4K_JOIN(6); break;
+    default: NF4K_JOIN(8); break;
+  }
+#undef NF4K_JOIN
   return hipGetLastError();
 }
 

@@ -213,7 +213,7 @@ struct Fp8Kind {
 struct Fp8Part {
   int kind;
   int64_t rows;
-  int splits;  // workgroups that share a tile's contraction
+  int splits;  // workgroups that share a tile's contraction: 1, 2, 3, 4, 6 or 8
 };
 const Fp8Kind* fp8_kinds();
 // A grouped product is one launch: its workgroups (every expert's last tile may be

@@ -43,7 +43,9 @@ int main() {
       CHECK(parts[i].rows > 0 && parts[i].kind >= 0 && parts[i].kind < kFp8Kinds);
       CHECK(wide(parts[i].kind) || transposed(parts[i].kind) == t);
       CHECK(!experts || fp8_grouped_fits(parts[i].kind, M, N, experts));
-      CHECK(parts[i].splits >= 1 && (may_split || parts[i].splits == 1));
+      const int k = parts[i].splits;
+      CHECK(k == 1 || k == 2 || k == 3 || k == 4 || k == 6 || k == 8);  // the join's kinds
+      CHECK((may_split || parts[i].splits == 1));
       if (parts[i].splits > 1) {
         joined = true;
         // no part of the contraction is empty, and the workspace holds the sums
