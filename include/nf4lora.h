@@ -521,6 +521,7 @@ nf4_status nf4_fp8_dequantize(const uint8_t *codes, const float *scales, int64_t
  *   ws : nf4_fp8_matmul_workspace_bytes bytes, or NULL.  With it a product of few
  *        tiles and a long contraction splits the contraction over workgroups and
  *        joins their fp32 sums in a fixed order; without it nothing is split.
+ *        Calls that may overlap (on several streams) need one each.
  * Errors: NF4_ERR_NULL, _SHAPE, _ARG (a_format, transpose), _ALIGN, _WORKSPACE,
  * _ALIAS, _HIP.
  */
@@ -584,7 +585,8 @@ nf4_status nf4_rmsnorm_workspace_bytes(int64_t M, int64_t H, size_t *bytes);
  * dX is the gradient of x and of res alike.  dH (bf16 [M][H], or NULL) is the
  * gradient that reaches h along the residual stream.  dw is summed in a fixed
  * order.  M == 0 writes zeros to dw.
- *   ws : nf4_rmsnorm_workspace_bytes(M, H) bytes.
+ *   ws : nf4_rmsnorm_workspace_bytes(M, H) bytes; one each for calls that may
+ *        overlap.
  * Errors: NF4_ERR_NULL, _SHAPE, _ALIGN, _WORKSPACE, _ALIAS, _HIP.
  */
 nf4_status nf4_rmsnorm_bwd(const uint16_t *dY, const uint16_t *h, const uint16_t *w, const float *rstd,

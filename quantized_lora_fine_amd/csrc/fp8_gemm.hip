@@ -496,7 +496,7 @@ __global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
 // a copy reaches; by 4096 x 4096 5.4 us, of which the launch and the first loads are
 // 3.  Transposed a workgroup's time goes with its k rows (1.5 ns each, whatever it
 // takes of a row's 128-byte line), so few rows are slower there: 29 us by
-// 11008 x 4096, 16 with the contraction split over 4.  32 or 128 bytes of each k row instead of 64 are within 10 % of it
+// 11008 x 4096, 16 with the contraction split over 3.  32 or 128 bytes of each k row instead of 64 are within 10 % of it
 // either way, and copies issued before a round's products instead of after are no
 // faster.
 template <int MT, int NT, int NWV, int ST, bool TR, bool SPLIT, bool E5M2, bool GROUPED>

@@ -743,6 +743,38 @@ def test_another_stream():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("transpose", [False, True])
+def test_split_captured_and_replayed(transpose):
+    # its workspace comes from the graph's pool, or is the caller's, shared by two graphs that run in turn
+    M, N, K = (260, 80, 33040) if not transpose else (5, 144, 33040)
+    o, h = (K, N) if transpose else (N, K)
+    a, s, w, ws, A2, B2 = product_case(21, M, o, h, transpose, 16, "e4m3")
+    args = (t8(a), torch.from_numpy(s).to(DEV), t8(w[0]), torch.from_numpy(ws[0]).to(DEV), transpose, A2.to(DEV),
+            B2[0].to(DEV))
+    eager = nf4.fp8_matmul(*args)
+    work = torch.empty(nf4.fp8_matmul_workspace_bytes(M, o, h, transpose), dtype=torch.uint8, device=DEV)
+    assert work.numel()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        nf4.fp8_matmul(*args)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = []
+    for given in (None, work, work):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = nf4.fp8_matmul(*args, ws=given)
+        graphs.append((g, out))
+    for k in range(4):
+        for g, out in graphs:
+            out.zero_()
+            g.replay()
+        torch.cuda.synchronize()
+        for g, out in graphs:
+            assert torch.equal(out, eager), k
+        assert torch.equal(nf4.fp8_matmul(*args), eager)
+
+
 def test_two_streams_at_once():
     cases = [layer_case(M=130), layer_case(M=700)]
     want = [layer(*c) for c in cases]
