@@ -140,7 +140,7 @@ __device__ __forceinline__ void tile_of(bool grouped, int tiles_m, int tiles_n, 
 // kernel without the multiply-adds of the scales are 17 % faster, without the copies
 // of the operands 22 %, without the barriers 2 %.  The library's 8-bit product with
 // one scale for a whole matrix takes 2.5 ms.
-// 2048 rows by 4096 x 4096 (128 x 256 tiles, one a compute unit): 37 us, 1.9 PFLOP/s.
+// 2048 rows by 4096 x 4096 (128 x 256 tiles, one a compute unit): 37 to 39 us, 1.8 PFLOP/s.
 // Transposed, W's fragments are 8-byte transposing reads at half the rate of the
 // 16-byte ones: 4096 rows by 11008 x 4096: 168 us, 2.2 PFLOP/s.
 template <int NI, bool TR, bool E5M2, bool GROUPED>
