@@ -565,10 +565,12 @@ nf4_status nf4_fp8_matmul_grouped(const uint8_t *A, int32_t a_format, const floa
  * y goes to Y as bf16 (for bf16 consumers: nf4lora_fwd, the adapter product) and
  * / or to codes and scales as e4m3 in blocks of one row, quantized from y before
  * any rounding as nf4_fp8_quantize does.  Y may be NULL, and codes and scales
- * both; one of the two forms must be there.  Each output is rounded once; h * w is
- * formed in fp32 first and must not overflow there.  H is a multiple of 16, at most
- * 32768; eps is finite and >= 0 (with eps = 0 a row of zeros is NaN).  M == 0 does
- * nothing.
+ * both; one of the two forms must be there.  Each output is rounded once.  Rows of
+ * any magnitude are in range, with any eps: a row or block of zeros has zeros and codes 0,
+ * and y does not depend on rstd being an fp32 value (rstd itself is written as
+ * infinity past fp32's range: eps = 0 and a root mean square below 2^-128).  H is a
+ * multiple of 16, at most 32768; eps is finite and >= 0 (with eps = 0 a row of zeros is
+ * NaN).  M == 0 does nothing.
  * Errors: NF4_ERR_NULL, _SHAPE, _ARG (eps), _ALIGN, _ALIAS, _HIP.
  */
 nf4_status nf4_rmsnorm_fwd(const uint16_t *X, const uint16_t *res, const uint16_t *w, int64_t M, int64_t H, float eps,

@@ -6,10 +6,12 @@
 //     rstd = 1 / sqrt(mean(h^2) + eps),   y = h * rstd * w;
 // y leaves as bf16, as 8-bit codes with a scale per 128 columns (quantized from
 // y, not from its bf16 rounding), or both.  A product h * w of bf16 values is exact
-// in fp32; the sum of squares is fp64, rstd the sum of two fp32 values, hi + lo, so
-// that fma(hw, hi, hw * lo) rounds y once: of 600 rows of 4096, 5 have a code that
-// y in 64 bits puts on the other side of a tie, and 178 with fp32 throughout.  It
-// costs 2 % at 16384 x 8192 (219 -> 225 us; y and the root in fp64: 240 us).
+// in fp32; the sum of squares is fp64, and rstd = 2^-k (hi + lo) with two fp32 values,
+// so that with h 2^-k in h's place fma(hw, hi, hw * lo) is y rounded once, to fp32, at
+// any magnitude of the row: of 600 rows of 4096, 5 have a code that y in 64 bits puts
+// on the other side of a tie, and 178 with fp32 throughout.  Replayed graphs at
+// 16384 x 8192: 219 us with fp32 throughout, 225 so, 240 with y and the root in fp64;
+// the factor 2^-k apart is within 1 % of one rstd.
 // Gradient, with xhat = h * rstd and u = dy * w:
 //     dx = rstd * (u - xhat * mean(u * xhat)) + dh,   dw = sum over rows dy * xhat.
 // The gradient's sums are fp32.
@@ -44,7 +46,7 @@ template <int TPR>
 __device__ __forceinline__ int row_threads() { return TPR ? TPR : (int)blockDim.x; }
 
 // Sum over 16 lanes or the wave; every lane gets it.  Lane exchanges in the vector
-// unit, not LDS permutes (16384 x 8192 forward 228.5 -> 225 us).
+// unit, not LDS permutes (16384 x 8192 forward 228.5 -> 225 us by replayed graphs).
 template <int N, class F>
 __device__ __forceinline__ F wave_add(F x) {
   constexpr int W = sizeof(F) / 4;
@@ -167,15 +169,17 @@ __global__ __launch_bounds__(TPR ? 256 : 1024) void k_rmsnorm(NormArgs p) {
   }
   ss = row_sum<TPR>(ss, red);
   // one step of Newton's from the fp32 root of mean / 4^k, which is 1/4 or more and
-  // below 1; a root of 0 or infinity stands as it is
+  // below 1; a root of 0 or infinity stands as it is.  The row is multiplied by
+  // 2^-k and its root, from 1 to 2, apart: rstd itself may lie past fp32's range (a
+  // row of bf16's subnormals), and so may its product with a block's multiplier (up
+  // to 448 * 2^100, for a block of zeros) or h * w
   double mean = __builtin_fma(ss, p.inv_H, (double)p.eps);
   const int k = (__builtin_amdgcn_frexp_exp(mean) + 1) >> 1;
   mean = __builtin_amdgcn_ldexp(mean, -2 * k);
-  const float root = 1.f / sqrtf((float)mean);
-  const float e = (float)__builtin_fma(-mean, (double)root * (double)root, 1.);
-  const float hi = ldexpf(root, -k);
-  const float lo = fabsf(e) < 1.f ? ldexpf(0.5f * root * e, -k) : 0.f;
-  if (p.rstd && t == 0) p.rstd[row] = hi + lo;
+  const float hi = 1.f / sqrtf((float)mean);
+  const float e = (float)__builtin_fma(-mean, (double)hi * (double)hi, 1.);
+  const float lo = fabsf(e) < 1.f ? 0.5f * hi * e : 0.f;
+  if (p.rstd && t == 0) p.rstd[row] = ldexpf(hi + lo, -k);
   const int64_t kb = (p.H + 127) / 128;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
@@ -188,7 +192,7 @@ __global__ __launch_bounds__(TPR ? 256 : 1024) void k_rmsnorm(NormArgs p) {
     widen8(wb, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      w[j] *= a[j];
+      w[j] *= __builtin_ldexpf(a[j], -k);
       a[j] = __builtin_fmaf(w[j], hi, w[j] * lo);
     }
     if (p.Y && in) *(u32x4*)(p.Y + base + col) = narrow8(a);
@@ -199,7 +203,7 @@ __global__ __launch_bounds__(TPR ? 256 : 1024) void k_rmsnorm(NormArgs p) {
       fp8_scale<false>(row16_max(m), scale, mul);
       if (in) {
         uint2 o;
-        const float mhi = hi * mul, mlo = __builtin_fmaf(hi, mul, -mhi) + lo * mul;  // rstd * mul
+        const float mhi = hi * mul, mlo = __builtin_fmaf(hi, mul, -mhi) + lo * mul;
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] = __builtin_fmaf(w[j], mhi, w[j] * mlo);
         o.x = pack_fp8x4<false>(a[0], a[1], a[2], a[3]);
