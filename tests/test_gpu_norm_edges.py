@@ -113,3 +113,12 @@ def test_codes_of_small_rows_through_a_product(H):
     W, ws = nf4.fp8_quantize(torch.from_numpy(rng.standard_normal((144, H)).astype(np.float32)).to(DEV), 128)
     C = nf4.fp8_matmul(codes, scales, W, ws)
     assert torch.isfinite(C).all() and torch.all(C[2] == 0) and torch.all(C[6] == 0) and torch.all(C[1] != 0)
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("M", [1, 21])
+@pytest.mark.parametrize("H", [16, 128, 144, 512, 528, 1024, 1040, 2048, 2064, 4096, 5120, 8192, 8208, 16384, 16400, 32768])
+def test_every_width_to_one_rounding(H, M, residual):
+    rng = np.random.default_rng(M + H)
+    rows = lambda: bf16_np(rng.standard_normal((M, H)) * np.exp(3 * rng.standard_normal((M, 1))))
+    check_norm(rows(), bf16_np(1 + 0.1 * rng.standard_normal(H)), 1e-6, rows() if residual else None)
