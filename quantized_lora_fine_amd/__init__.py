@@ -157,7 +157,7 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-# the current device from torch's C layer (a tensor on a GPU is checked against it, so the runtime is up)
+# the current device from torch's C layer; it needs a runtime that is up (see _device_for)
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 # the current stream's handle straight from torch's C layer: building the Stream object around it takes longer than
@@ -524,6 +524,13 @@ def _held(t, dtype, shape, dev: int, name: str):
     return t.data_ptr()
 
 
+def _device_for(t, name: str) -> int:
+    """The current device, for a tensor `t` on a GPU (one in host memory is refused before the runtime is asked)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: expected a tensor on the current cuda device, got {getattr(t, 'device', type(t).__name__)}")
+    return _device()
+
+
 def _matrix(t, name: str):
     """(rows, cols) of a tensor of two dimensions; the rest is for the caller to check."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
@@ -553,7 +560,7 @@ def fp8_quantize(X: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = torc
     bf16 = X.dtype is torch.bfloat16
     if not bf16 and X.dtype is not torch.float32:
         raise ValueError(f"X: expected bf16 or fp32, got {X.dtype}")
-    dev = _device()
+    dev = _device_for(X, "X")
     x = _held(X, X.dtype, (rows, cols), dev, "X")
     sshape = (rows if block_rows == 1 else _blocks(rows), _blocks(cols))
     if codes is None:
@@ -574,7 +581,7 @@ def fp8_dequantize(codes: torch.Tensor, scales: torch.Tensor, block_rows: int = 
     """nf4_fp8_dequantize into fp32 (or bf16) [rows][cols], into `out` when given."""
     f = _fp8_format(getattr(codes, "dtype", None), "codes")
     rows, cols = _matrix(codes, "codes")
-    dev = _device()
+    dev = _device_for(codes, "codes")
     c = _held(codes, codes.dtype, (rows, cols), dev, "codes")
     s = _held(scales, torch.float32, (rows if block_rows == 1 else _blocks(rows), _blocks(cols)), dev, "scales")
     odt = torch.bfloat16 if bf16 else torch.float32
@@ -635,7 +642,7 @@ def fp8_matmul(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scale
     A [M][K] and a_scales as fp8_quantize(X) gives them (either format), W [o][h] (e4m3) and w_scales as
     fp8_quantize(W, 128) does.  ws: a workspace of fp8_matmul_workspace_bytes, else allocated where one helps."""
     o, h = _matrix(W, "W")
-    dev = _device()
+    dev = _device_for(W, "W")
     w = _held(W, torch.float8_e4m3fn, (o, h), dev, "W")
     sw = _held(w_scales, torch.float32, (_blocks(o), _blocks(h)), dev, "w_scales")
     a, f, s, M, tr, a2, b2, R, C = _fp8_product(A, a_scales, o, h, transpose, A2, B2, (), out, dev)
@@ -655,7 +662,7 @@ def fp8_matmul_grouped(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor,
     if not isinstance(W, torch.Tensor) or W.dim() != 3:
         raise ValueError("W: expected a tensor of three dimensions, [experts][o][h]")
     E, o, h = W.shape
-    dev = _device()
+    dev = _device_for(W, "W")
     w = _held(W, torch.float8_e4m3fn, (E, o, h), dev, "W")
     sw = _held(w_scales, torch.float32, (E, _blocks(o), _blocks(h)), dev, "w_scales")
     off = _held(offsets, torch.int32, (E + 1,), dev, "offsets")
@@ -671,7 +678,7 @@ def rmsnorm_fwd(X: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, residual: t
     """nf4_rmsnorm_fwd of bf16 X [M][H] (+ residual): (Y bf16, h bf16, codes e4m3, scales fp32, rstd fp32), None for
     what is not asked for (h: without a residual).  `outs`: the same five, given instead of allocated."""
     M, H = _matrix(X, "X")
-    dev = _device()
+    dev = _device_for(X, "X")
     bf16, f32, e4m3, device = torch.bfloat16, torch.float32, torch.float8_e4m3fn, X.device
     x = _held(X, bf16, (M, H), dev, "X")
     wp = _held(w, bf16, (H,), dev, "w")
@@ -711,7 +718,7 @@ def rmsnorm_bwd(dY: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rstd: torch.
     """nf4_rmsnorm_bwd: (dX bf16 [M][H], the gradient of X and of the residual alike, dw fp32 [H]) from the forward's
     h (X without a residual) and rstd; dH is the gradient that reaches h along the residual stream."""
     M, H = _matrix(dY, "dY")
-    dev = _device()
+    dev = _device_for(dY, "dY")
     bf16, f32 = torch.bfloat16, torch.float32
     g = _held(dY, bf16, (M, H), dev, "dY")
     hp = _held(h, bf16, (M, H), dev, "h")
