@@ -511,7 +511,8 @@ nf4_status nf4_fp8_dequantize(const uint8_t *codes, const float *scales, int64_t
  * [rows][cols] in blocks of 128 x 128.  transpose = 1 is the input gradient
  * dX = dY W of the same stored weight, dY quantized along the outputs.  Every
  * block's products are summed by the matrix cores, multiplied by the two scales
- * and added in fp32; C is bf16.  (The matrix cores add 8-bit products of 8
+ * (whose product is formed first, in fp32; it is a normal value wherever the largest
+ * magnitudes of both blocks lie between 2^-50 and 2^60) and added in fp32; C is bf16.  (The matrix cores add 8-bit products of 8
  * neighbouring k aligned to the largest of them, p, cutting each off below
  * 2^-13 p, and add these sums in fp32: far below what 8-bit codes round away.)
  * The low-rank term is nf4_matmul's: bf16, R a multiple of 16 in [0, 256], A2 and
@@ -563,10 +564,12 @@ nf4_status nf4_fp8_matmul_grouped(const uint8_t *A, int32_t a_format, const floa
  *   rstd = 1 / sqrt(mean(h^2) + eps)        (fp32, to rstd [M] unless NULL)
  *   y    = h * rstd * w                     (w bf16 [H])
  * y goes to Y as bf16 (for bf16 consumers: nf4lora_fwd, the adapter product) and
- * / or to codes and scales as e4m3 in blocks of one row, quantized from y before
- * any rounding as nf4_fp8_quantize does.  Y may be NULL, and codes and scales
- * both; one of the two forms must be there.  Each output is rounded once.  Rows of
- * any magnitude are in range, with any eps: a row or block of zeros has zeros and codes 0,
+ * / or to codes and scales as e4m3 in blocks of one row, quantized from y (not from
+ * Y) as nf4_fp8_quantize does.  Y may be NULL, and codes and scales both; one of
+ * the two forms must be there.  y and rstd are within one fp32 rounding of their exact
+ * values (2^-24), and y is narrowed from there: a bf16 value or a code differs
+ * from the rounding of the exact y only next to a tie, by one step, and a scale by
+ * an fp32 step or two.  Rows of any magnitude are in range, with any eps: a row or block of zeros has zeros and codes 0,
  * and y does not depend on rstd being an fp32 value (rstd itself is written as
  * infinity past fp32's range: eps = 0 and a root mean square below 2^-128).  H is a
  * multiple of 16, at most 32768; eps is finite and >= 0 (with eps = 0 a row of zeros is

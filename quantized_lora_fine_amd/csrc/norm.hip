@@ -8,7 +8,7 @@
 // y, not from its bf16 rounding), or both.  A product h * w of bf16 values is exact
 // in fp32; the sum of squares is fp64, and rstd = 2^-k (hi + lo) with two fp32 values,
 // so that with h 2^-k in h's place fma(hw, hi, hw * lo) is y rounded once, to fp32, at
-// any magnitude of the row: of 600 rows of 4096, 5 have a code that y in 64 bits puts
+// any magnitude of the row (bf16 values, codes and scales are rounded from there): of 600 rows of 4096, 5 have a code that y in 64 bits puts
 // on the other side of a tie, and 178 with fp32 throughout.  Replayed graphs at
 // 16384 x 8192: 219 us with fp32 throughout, 225 so, 240 with y and the root in fp64;
 // the factor 2^-k apart is within 1 % of one rstd.
