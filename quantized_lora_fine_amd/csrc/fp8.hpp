@@ -26,7 +26,7 @@ __device__ __forceinline__ uint32_t pack_fp8x4(float a, float b, float c, float 
   return (uint32_t)v;
 }
 
-// Byte `i` (a constant) of a code word as fp32 (exact).
+// The four codes of a word as fp32 (exact).
 template <bool E5M2>
 __device__ __forceinline__ void unpack_fp8x4(uint32_t w, float (&v)[4]) {
   typedef float f32x2 __attribute__((ext_vector_type(2)));

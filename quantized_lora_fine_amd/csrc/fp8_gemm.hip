@@ -132,7 +132,7 @@ __device__ __forceinline__ void tile_of(bool grouped, int tiles_m, int tiles_n, 
 
 // Tiles of 256, 128 or 64 rows by 256 columns (NI = 8, 4, 2) for products with enough
 // of them: 8 waves, each 64 rows by 16 NI columns.  A step is one block of 128 k.
-// Its fragments take LDS 16 (4 + NI) KB, its copies 8 (NI + 8) KB, its MFMAs 256 NI
+// Its fragments take LDS 16 (4 + NI) KB, its copies 4 (NI + 8) KB, its MFMAs 256 NI
 // cycles: the 256 x 256 tile is the largest whose accumulators (128 registers) and
 // two steps of operands (132 KB) fit, and the one that LDS holds up least.
 // 16384 rows by 28672 x 8192: 3.3 ms, 2.35 PFLOP/s.  The chip runs at 1.6 GHz there
@@ -140,9 +140,14 @@ __device__ __forceinline__ void tile_of(bool grouped, int tiles_m, int tiles_n, 
 // kernel without the multiply-adds of the scales are 17 % faster, without the copies
 // of the operands 22 %, without the barriers 2 %.  The library's 8-bit product with
 // one scale for a whole matrix takes 2.5 ms.
-// 2048 rows by 4096 x 4096 (128 x 256 tiles, one a compute unit): 37 to 39 us, 1.8 PFLOP/s.
+// 2048 rows by 4096 x 4096 (128 x 256 tiles, one a compute unit): 39 us with the weight
+// in the caches, 41 from memory, 1.7 PFLOP/s.  No unit is full there: the matrix cores
+// are busy 35 % of the cycles, LDS 21 %; of the waves' cycles a third go to
+// instructions, 30 % to waits for copies, LDS and barriers, and in the rest a wave
+// could go on but for the issue.
 // Transposed, W's fragments are 8-byte transposing reads at half the rate of the
-// 16-byte ones: 4096 rows by 11008 x 4096: 168 us, 2.2 PFLOP/s.
+// 16-byte ones: 4096 rows by 11008 x 4096: 163 to 169 us, 2.2 PFLOP/s, the matrix cores
+// busy 57 % of the cycles, LDS 38 % with 14 % of conflicts.
 template <int NI, bool TR, bool E5M2, bool GROUPED>
 __global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
   constexpr int WGM = NI / 2, NW = 8;  // 16 / NI waves beside each other
@@ -492,13 +497,13 @@ __global__ __launch_bounds__(512, 2) void k_fp8_wide(Args p) {
 // rounds in flight, so the loop has no barrier.  (Fragments loaded from memory
 // into registers take four times as long: the address path joins neighbouring
 // lanes only, and a fragment's neighbouring lanes are different rows.)
-// One row by 28672 x 8192: 42 us with the weight out of the caches, 5.6 TB/s, what
-// a copy reaches; by 4096 x 4096 5.4 us, of which the launch and the first loads are
-// 3.  Transposed a workgroup's time goes with its k rows (1.5 ns each, whatever it
-// takes of a row's 128-byte line), so few rows are slower there: 29 us by
-// 11008 x 4096, 16 with the contraction split over 3.  32 or 128 bytes of each k row instead of 64 are within 10 % of it
-// either way, and copies issued before a round's products instead of after are no
-// faster.
+// One row by 28672 x 8192: 40 to 42 us with the weight out of the caches, 5.6 TB/s,
+// what a copy reaches; by 4096 x 4096 5.4 to 5.6 us, of which the launch and the first
+// loads are 3.  Transposed a workgroup's time goes with its k rows (1.5 ns each, whatever
+// it takes of a row's 128-byte line), so few rows are slower there: 3 rows by
+// 11008 x 4096 39 us with the weight out of the caches, 20 with the contraction split
+// over 3.  32 or 128 bytes of each k row instead of 64 are within 10 % of it either way,
+// and copies issued before a round's products instead of after are no faster.
 template <int MT, int NT, int NWV, int ST, bool TR, bool SPLIT, bool E5M2, bool GROUPED>
 __global__ __launch_bounds__(NWV * 64) void k_fp8_rows(Args p) {
   static_assert(!TR || NT == 4, "64 bytes of each k row");
@@ -706,8 +711,9 @@ __global__ __launch_bounds__(NWV * 64) void k_fp8_rows(Args p) {
 // copies are 0.3.  (4 waves with tiles twice as large read less, but wait for
 // themselves: 0.53 us.  64 x 64 tiles, 0.20 us, are no better than k_fp8_rows';
 // transposed, the 8-byte reads of W make a step 0.75 us, more than k_fp8_rows
-// needs.)  128 rows by 9104 x 5888: 33 us, 415 TFLOP/s, against 39 for the best of
-// the other tiles; 512 rows by 4096 x 4096: 18 against 23.
+// needs.)  With the weight out of the caches 128 rows by 9104 x 5888 take 33 us, 415
+// TFLOP/s, against 39 for the best of the other tiles; with it in them 512 rows by
+// 4096 x 4096 18 us against 23.
 template <int BM, int BN, int ST, bool E5M2, bool GROUPED>
 __global__ __launch_bounds__(512) void k_fp8_ring(Args p) {
   constexpr int NW = 8;

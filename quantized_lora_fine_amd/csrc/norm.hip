@@ -9,9 +9,10 @@
 // in fp32; the sum of squares is fp64, and rstd = 2^-k (hi + lo) with two fp32 values,
 // so that with h 2^-k in h's place fma(hw, hi, hw * lo) is y rounded once, to fp32, at
 // any magnitude of the row (bf16 values, codes and scales are rounded from there): of 600 rows of 4096, 5 have a code that y in 64 bits puts
-// on the other side of a tie, and 178 with fp32 throughout.  Replayed graphs at
-// 16384 x 8192: 219 us with fp32 throughout, 225 so, 240 with y and the root in fp64;
-// the factor 2^-k apart is within 1 % of one rstd.
+// on the other side of a tie, and 178 with fp32 throughout.  By
+// replayed graphs at 16384 x 8192 with a residual and both outputs: 209 us with fp32
+// throughout, 211 so, 217 with y and the root in fp64; 16384 x 4096 with the 8-bit
+// output alone 83.5, 88.5 and 95.  The factor 2^-k apart is within 1 % of one rstd.
 // Gradient, with xhat = h * rstd and u = dy * w:
 //     dx = rstd * (u - xhat * mean(u * xhat)) + dh,   dw = sum over rows dy * xhat.
 // The gradient's sums are fp32.
@@ -46,7 +47,7 @@ template <int TPR>
 __device__ __forceinline__ int row_threads() { return TPR ? TPR : (int)blockDim.x; }
 
 // Sum over 16 lanes or the wave; every lane gets it.  Lane exchanges in the vector
-// unit, not LDS permutes (16384 x 8192 forward 228.5 -> 225 us by replayed graphs).
+// unit, not LDS permutes (1.5 % less at 16384 x 8192, forward).
 template <int N, class F>
 __device__ __forceinline__ F wave_add(F x) {
   constexpr int W = sizeof(F) / 4;
@@ -122,7 +123,8 @@ struct NormArgs {
 
 // The row stays in registers, so each byte moves once; 16 neighbouring threads hold
 // one block of the 8-bit output.  Bound by memory: 16384 x 8192 with a residual and
-// both outputs 210 us, 5.8 TB/s; one row of 4096 4.5 us, the launch and three waits.
+// both outputs 211 us, 5.8 TB/s; one row of 4096 3.1 us by replayed graphs, the launch
+// and three waits.
 template <int TPR, int NC>
 __global__ __launch_bounds__(TPR ? 256 : 1024) void k_rmsnorm(NormArgs p) {
   __shared__ __align__(16) double red[16];
@@ -230,8 +232,9 @@ struct NormGradArgs {
 // A workgroup takes every gridDim.x-th row (TPR > 0: group of 256 / TPR rows), the
 // next one's loads under way while it works on one; each thread keeps its
 // columns' share of dw in registers over all of them.  Bound by memory: 16384 x 8192
-// with dH 195 us, 5.5 TB/s; 1999 x 5120 17 us (256 workgroups have 7 or 8 rows each:
-// the first row's wait and the parts' join are a third of it).
+// with dH 193 to 196 us, 5.5 TB/s, without 151; 1999 x 5120 with dH 17 to 19 us (256
+// workgroups have 7 or 8 rows each: the first row's wait and the parts' join are a
+// third of it).
 template <int TPR, int NC>
 __global__ __launch_bounds__(TPR ? 256 : 1024) void k_rmsnorm_grad(NormGradArgs p) {
   constexpr int TEAMS = TPR ? 256 / (TPR ? TPR : 1) : 1;

@@ -88,9 +88,10 @@ int rmsnorm_threads(int H) {
 int rmsnorm_parts(int64_t M, int H) {
   const int teams = rmsnorm_teams(H);
   const int64_t groups = (M + teams - 1) / teams;
-  // one workgroup a compute unit where it holds a whole row (16384 x 8192: 148 us
-  // against 153 and 157 for 512 and 1024, whose parts of dw are more), two where
-  // its waves hold several
+  // one workgroup a compute unit where it holds a whole row (16384 x 8192 with dH:
+  // 193 us against 198 and 203 for 512 and 1024, whose parts of dw are more, without dH
+  // 151 against 154 and 156; 1999 x 5120 with dH: 18.6 against 21.3 and 25.4; by replayed
+  // graphs), two where its waves hold several
   const int64_t most = teams > 1 ? 512 : 256;
   return (int)(groups < most ? groups : most);
 }
@@ -100,7 +101,9 @@ int rmsnorm_parts(int64_t M, int H) {
 // contraction, u0 when few compute units have a tile and u1 when all do.  Fitted
 // to the times of every kind for 1 to 8192 rows by 12 weights of 560 x 1200 to
 // 28672 x 8192, each way; the kind that these costs choose is 1 % slower than the
-// fastest one in the mean, 23 % at worst (160 rows by 9104 x 5888).
+// fastest one in the mean, 23 % at worst (160 rows by 9104 x 5888).  Unsplit, nothing
+// stands for the weight's own stream: with the weight in the caches the times hold (64
+// rows by 28672 x 8192: 43 us predicted, 43 measured), from memory it takes longer (66).
 const Fp8Kind* fp8_kinds() {
   static const Fp8Kind kinds[kFp8Kinds] = {
       {256, 256, 512, 4.6, 1.11, 1.66},   // kFp8Wide8
@@ -149,8 +152,9 @@ double fp8_time(int kind, int64_t tiles_m, int N, int K, int splits) {
 // The kind, and over how many workgroups a tile's contraction is split: where
 // there are fewer tiles than compute units, as long as each part has 4 blocks, the
 // parts fit 64 MB, and a tenth is gained by the costs: no split beats the weights'
-// own stream, and the join is a launch more (3 rows by 11008 x 4096 transposed 28
-// -> 16.5 us, 900 rows over two experts of 6144 x 1328 transposed 60 -> 31).
+// own stream, and the join is a launch more (3 rows by 11008 x 4096 transposed, by
+// replayed graphs: 25 -> 14.4 us with the weight in the caches, 39 -> 20.2 from memory;
+// 900 rows by 6144 x 1328 transposed 47 -> 28 and 61 -> 30).
 int fp8_best(int64_t M, int N, int K, bool transpose, int experts, bool may_split, double* time, int* splits) {
   int best = -1;
   double least = 0;
