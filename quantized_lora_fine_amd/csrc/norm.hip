@@ -7,12 +7,13 @@
 // y leaves as bf16, as 8-bit codes with a scale per 128 columns (quantized from
 // y, not from its bf16 rounding), or both.  A product h * w of bf16 values is exact
 // in fp32; the sum of squares is fp64, and rstd = 2^-k (hi + lo) with two fp32 values,
-// so that with h 2^-k in h's place fma(hw, hi, hw * lo) is y rounded once, to fp32, at
-// any magnitude of the row (bf16 values, codes and scales are rounded from there): of 600 rows of 4096, 5 have a code that y in 64 bits puts
-// on the other side of a tie, and 178 with fp32 throughout.  By
-// replayed graphs at 16384 x 8192 with a residual and both outputs: 209 us with fp32
-// throughout, 211 so, 217 with y and the root in fp64; 16384 x 4096 with the 8-bit
-// output alone 83.5, 88.5 and 95.  The factor 2^-k apart is within 1 % of one rstd.
+// so that fma(hw, hi, hw * lo) is y rounded once, to fp32; bf16 values, codes and
+// scales are rounded from there.  Of 600 rows of 4096, 5 have a code that y in 64 bits
+// puts on the other side of a tie, and 178 with fp32 throughout.  By replayed graphs at
+// 16384 x 8192 with a residual and both outputs: 209 us with fp32 throughout, 211 so,
+// 217 with y and the root in fp64; at 16384 x 4096 with the 8-bit output alone 83.5, 89
+// and 95.  The factor 2^-k goes with the pair, or, for rows far from 1, with h (for all
+// rows that would take 1 % more time).
 // Gradient, with xhat = h * rstd and u = dy * w:
 //     dx = rstd * (u - xhat * mean(u * xhat)) + dh,   dw = sum over rows dy * xhat.
 // The gradient's sums are fp32.
@@ -171,17 +172,20 @@ __global__ __launch_bounds__(TPR ? 256 : 1024) void k_rmsnorm(NormArgs p) {
   }
   ss = row_sum<TPR>(ss, red);
   // one step of Newton's from the fp32 root of mean / 4^k, which is 1/4 or more and
-  // below 1; a root of 0 or infinity stands as it is.  The row is multiplied by
-  // 2^-k and its root, from 1 to 2, apart: rstd itself may lie past fp32's range (a
-  // row of bf16's subnormals), and so may its product with a block's multiplier (up
-  // to 448 * 2^100, for a block of zeros) or h * w
+  // below 1; a root of 0 or infinity stands as it is.  Far from 1, rstd may lie past
+  // fp32's range (a row of bf16's subnormals), and so may its product with a block's
+  // multiplier (up to 448 * 2^100, for a block of zeros) or h * w: there h is multiplied
+  // by 2^-k and the products take the root, from 1 to 2, alone.  Up to 2^17 rstd's
+  // product with a multiplier is below 2^126, and the factor stays with it.
   double mean = __builtin_fma(ss, p.inv_H, (double)p.eps);
   const int k = (__builtin_amdgcn_frexp_exp(mean) + 1) >> 1;
   mean = __builtin_amdgcn_ldexp(mean, -2 * k);
-  const float hi = 1.f / sqrtf((float)mean);
-  const float e = (float)__builtin_fma(-mean, (double)hi * (double)hi, 1.);
-  const float lo = fabsf(e) < 1.f ? 0.5f * hi * e : 0.f;
-  if (p.rstd && t == 0) p.rstd[row] = ldexpf(hi + lo, -k);
+  const float root = 1.f / sqrtf((float)mean);
+  const float e = (float)__builtin_fma(-mean, (double)root * (double)root, 1.);
+  const float rest = fabsf(e) < 1.f ? 0.5f * root * e : 0.f;
+  if (p.rstd && t == 0) p.rstd[row] = ldexpf(root + rest, -k);
+  const int far = (unsigned)(k + 16) <= 32u ? 0 : k;
+  const float hi = ldexpf(root, far - k), lo = ldexpf(rest, far - k);
   const int64_t kb = (p.H + 127) / 128;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
@@ -192,9 +196,13 @@ __global__ __launch_bounds__(TPR ? 256 : 1024) void k_rmsnorm(NormArgs p) {
     u32x4 wb = {0u, 0u, 0u, 0u};
     if (in) wb = *(const u32x4*)(p.w + col);
     widen8(wb, w);
+    if (far) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j] = ldexpf(a[j], -far);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      w[j] *= __builtin_ldexpf(a[j], -k);
+      w[j] *= a[j];
       a[j] = __builtin_fmaf(w[j], hi, w[j] * lo);
     }
     if (p.Y && in) *(u32x4*)(p.Y + base + col) = narrow8(a);

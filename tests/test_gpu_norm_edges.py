@@ -91,6 +91,20 @@ def test_a_zero_block_beside_others(scale, H, eps):
     check_norm(X, w, eps)
 
 
+@pytest.mark.parametrize("H", [64, 272, 2064])
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -34, 2.0 ** -36, 1e-9])
+def test_rows_of_every_power(H, eps):
+    # one launch of rows whose sizes differ by powers of two, some zeros among them: neighbours in a wave may differ
+    rng = np.random.default_rng(H)
+    x = rng.standard_normal((161, H)) * 2.0 ** np.arange(-40, 121, dtype=np.float64)[:, None]
+    x[::3, :min(H // 2, 128)] = 0
+    if eps:
+        x[5::16] = 0
+    w = bf16_np(1 + 0.1 * rng.standard_normal(H))
+    check_norm(bf16_np(x[:160]), w, eps)
+    check_norm(bf16_np(x[160:]), w, eps)
+
+
 @pytest.mark.parametrize("value", [2.0 ** -133, 2.0 ** -126, 2.0 ** -125, 2.0 ** 127])
 @pytest.mark.parametrize("H", [16, 144, 4096])
 def test_rows_of_one_value_without_eps(H, value):
