@@ -599,6 +599,58 @@ nf4_status nf4_rmsnorm_bwd(const uint16_t *dY, const uint16_t *h, const uint16_t
                            const uint16_t *dH, int64_t M, int64_t H, uint16_t *dX, float *dw, void *ws,
                            size_t ws_bytes, void *stream);
 
+/*
+ * The layer norm, with the outputs of nf4_rmsnorm_fwd.  Per row of X bf16 [M][H]:
+ *   h    = bf16(x + res), written to H_out  (res NULL: h = x, H_out unused)
+ *   mean = sum(h) / H,  rstd = 1 / sqrt(sum((h - mean)^2) / H + eps)
+ *                                (fp32, to mean [M] and rstd [M] unless NULL)
+ *   y    = (h - mean) * rstd * w + b       (w, b bf16 [H]; b NULL: 0)
+ * y goes to Y as bf16 and / or to codes and scales as e4m3 in blocks of one row, as
+ * nf4_fp8_quantize writes them for y in fp32.  Y may be NULL, and codes and scales both;
+ * one of the two forms must be there.  mean, rstd and y are computed in 64 bits and
+ * rounded to fp32 once; a bf16 value or a code differs from the rounding of the exact y
+ * only next to a tie, by one step.  A row of equal values gives b exactly where eps > 0,
+ * and NaN where eps = 0.  Sizes, eps and errors as nf4_rmsnorm_fwd.
+ */
+nf4_status nf4_layernorm_fwd(const uint16_t *X, const uint16_t *res, const uint16_t *w, const uint16_t *b, int64_t M,
+                             int64_t H, float eps, uint16_t *H_out, uint16_t *Y, uint8_t *codes, float *scales,
+                             float *mean, float *rstd, void *stream);
+
+/* Workspace bytes of nf4_layernorm_bwd (host output *bytes).  Errors: NF4_ERR_NULL, _SHAPE. */
+nf4_status nf4_layernorm_workspace_bytes(int64_t M, int64_t H, size_t *bytes);
+
+/*
+ * The layer norm's gradient, from the forward's h (H_out, or X without a residual), mean
+ * and rstd:  with xhat = (h - mean) * rstd and u = dY * w,
+ *   dX = rstd * (u - mean(u) - xhat * mean(u * xhat)) + dH   -> bf16 [M][H]
+ *   dw = sum over rows of dY * xhat,  db = sum over rows of dY  -> fp32 [H]
+ * dX is the gradient of x and of res alike; dH (bf16 [M][H], or NULL) is the gradient
+ * that reaches h along the residual stream.  db may be NULL.  dw and db are summed in a
+ * fixed order.  M == 0 writes zeros to them.
+ *   ws : nf4_layernorm_workspace_bytes(M, H) bytes; one each for calls that may overlap.
+ * Errors as nf4_rmsnorm_bwd.
+ */
+nf4_status nf4_layernorm_bwd(const uint16_t *dY, const uint16_t *h, const uint16_t *w, const float *mean,
+                             const float *rstd, const uint16_t *dH, int64_t M, int64_t H, uint16_t *dX, float *dw,
+                             float *db, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Rows sorted by id, for the calls that are grouped by expert or by adapter.  ids is
+ * DEVICE int32 [M].
+ *   order   : int32 [M], the rows of id 0, then those of id 1, and so on, each id's in
+ *             ascending order; behind them the rows whose id is outside [0, n).
+ *   offsets : int32 [n + 1]; the rows of id i are order[offsets[i]] to
+ *             order[offsets[i + 1] - 1], and offsets[n] counts the rows with an id.
+ *   ws      : nf4_route_workspace_bytes(M, n) bytes (0 up to some thousands of rows),
+ *             16-byte aligned; one each for calls that may overlap.
+ * 1 <= n <= 4096, 0 <= M <= 2^30.  ids, order and offsets need 4-byte alignment.
+ * Errors: NF4_ERR_NULL, _SHAPE, _ALIGN, _WORKSPACE, _ALIAS, _HIP.
+ */
+nf4_status nf4_route(const int32_t *ids, int64_t M, int32_t n, int32_t *order, int32_t *offsets, void *ws,
+                     size_t ws_bytes, void *stream);
+/* Workspace bytes of nf4_route (host output *bytes).  Errors: NF4_ERR_NULL, _SHAPE. */
+nf4_status nf4_route_workspace_bytes(int64_t M, int32_t n, size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif

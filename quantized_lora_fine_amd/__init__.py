@@ -95,6 +95,11 @@ _SIGS = {
     "nf4_rmsnorm_fwd": ([_vp, _vp, _vp, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
     "nf4_rmsnorm_workspace_bytes": ([_i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
     "nf4_rmsnorm_bwd": ([_vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "nf4_layernorm_fwd": ([_vp, _vp, _vp, _vp, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "nf4_layernorm_workspace_bytes": ([_i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
+    "nf4_layernorm_bwd": ([_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "nf4_route_workspace_bytes": ([_i64, _i32, ctypes.POINTER(_sz)], ctypes.c_int),
+    "nf4_route": ([_vp, _i64, _i32, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
 }
 for _name, (_args, _res) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -734,6 +739,109 @@ def rmsnorm_bwd(dY: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rstd: torch.
                                 _held(dw, f32, (H,), dev, "outs.dw"), ws.data_ptr(), ws.numel(), _raw_stream(dev)),
            "nf4_rmsnorm_bwd")
     return dX, dw
+
+
+def layernorm_fwd(X: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None = None, eps: float = 1e-5,
+                  residual: torch.Tensor | None = None, want_y: bool = True, want_fp8: bool = False,
+                  want_stats: bool = False, outs=None):
+    """nf4_layernorm_fwd of bf16 X [M][H] (+ residual): (Y bf16, h bf16, codes e4m3, scales fp32, mean fp32, rstd fp32),
+    None for what is not asked for (h: without a residual).  `outs`: the same six, given instead of allocated."""
+    M, H = _matrix(X, "X")
+    dev = _device_for(X, "X")
+    bf16, f32, e4m3, device = torch.bfloat16, torch.float32, torch.float8_e4m3fn, X.device
+    x = _held(X, bf16, (M, H), dev, "X")
+    wp = _held(w, bf16, (H,), dev, "w")
+    bp = None if b is None else _held(b, bf16, (H,), dev, "b")
+    res = None if residual is None else _held(residual, bf16, (M, H), dev, "residual")
+    if outs is None:
+        outs = (torch.empty(M, H, dtype=bf16, device=device) if want_y else None,
+                None if residual is None else torch.empty(M, H, dtype=bf16, device=device),
+                torch.empty(M, H, dtype=e4m3, device=device) if want_fp8 else None,
+                torch.empty(M, _blocks(H), dtype=f32, device=device) if want_fp8 else None,
+                torch.empty(M, dtype=f32, device=device) if want_stats else None,
+                torch.empty(M, dtype=f32, device=device) if want_stats else None)
+    else:
+        want = (want_y, residual is not None, want_fp8, want_fp8, want_stats, want_stats)
+        names = ("Y", "h", "codes", "scales", "mean", "rstd")
+        kinds = ((bf16, (M, H)), (bf16, (M, H)), (e4m3, (M, H)), (f32, (M, _blocks(H))), (f32, (M,)), (f32, (M,)))
+        for t, asked, name, (dtype, shape) in zip(outs, want, names, kinds, strict=True):
+            if bool(asked) != (t is not None):
+                raise ValueError(f"outs.{name}: {'missing' if asked else 'given, but not asked for'}")
+            if asked:
+                _held(t, dtype, shape, dev, f"outs.{name}")
+    Y, h, codes, scales, mean, rstd = (None if t is None else t.data_ptr() for t in outs)
+    _check(_lib.nf4_layernorm_fwd(x, res, wp, bp, M, H, eps, h, Y, codes, scales, mean, rstd, _raw_stream(dev)),
+           "nf4_layernorm_fwd")
+    return outs
+
+
+@functools.lru_cache(maxsize=4096)
+def layernorm_workspace_bytes(M: int, H: int) -> int:
+    b = _sz()
+    _check(_lib.nf4_layernorm_workspace_bytes(M, H, ctypes.byref(b)), "nf4_layernorm_workspace_bytes")
+    return b.value
+
+
+def layernorm_bwd(dY: torch.Tensor, h: torch.Tensor, w: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                  dH: torch.Tensor | None = None, want_db: bool = True, ws: torch.Tensor | None = None, outs=None):
+    """nf4_layernorm_bwd: (dX bf16 [M][H], the gradient of X and of the residual alike, dw fp32 [H], db fp32 [H] or None)
+    from the forward's h (X without a residual), mean and rstd; dH is the gradient that reaches h along the residual
+    stream."""
+    M, H = _matrix(dY, "dY")
+    dev = _device_for(dY, "dY")
+    bf16, f32 = torch.bfloat16, torch.float32
+    g = _held(dY, bf16, (M, H), dev, "dY")
+    hp = _held(h, bf16, (M, H), dev, "h")
+    wp = _held(w, bf16, (H,), dev, "w")
+    mp = _held(mean, f32, (M,), dev, "mean")
+    r = _held(rstd, f32, (M,), dev, "rstd")
+    d = None if dH is None else _held(dH, bf16, (M, H), dev, "dH")
+    if outs is None:
+        outs = (torch.empty(M, H, dtype=bf16, device=dY.device), torch.empty(H, dtype=f32, device=dY.device),
+                torch.empty(H, dtype=f32, device=dY.device) if want_db else None)
+    dX, dw, db = outs
+    if bool(want_db) != (db is not None):
+        raise ValueError(f"outs.db: {'missing' if want_db else 'given, but not asked for'}")
+    ws = _need_ws(ws) if ws is not None else \
+        torch.empty(layernorm_workspace_bytes(M, H), dtype=torch.uint8, device=dY.device)
+    _check(_lib.nf4_layernorm_bwd(g, hp, wp, mp, r, d, M, H, _held(dX, bf16, (M, H), dev, "outs.dX"),
+                                  _held(dw, f32, (H,), dev, "outs.dw"),
+                                  None if db is None else _held(db, f32, (H,), dev, "outs.db"), ws.data_ptr(),
+                                  ws.numel(), _raw_stream(dev)), "nf4_layernorm_bwd")
+    return dX, dw, db
+
+
+# ---------------------------------------------------------------------------
+# rows sorted by id, and the adapters of many requests beside a shared projection
+# ---------------------------------------------------------------------------
+
+@functools.lru_cache(maxsize=4096)
+def route_workspace_bytes(M: int, n: int) -> int:
+    b = _sz()
+    _check(_lib.nf4_route_workspace_bytes(M, n, ctypes.byref(b)), "nf4_route_workspace_bytes")
+    return b.value
+
+
+def route(ids: torch.Tensor, n: int, ws: torch.Tensor | None = None, outs=None):
+    """nf4_route: (order int32 [M], offsets int32 [n + 1]) of the cuda int32 ids [M]: the rows of each id 0 .. n - 1 one
+    after another, those without one (an id outside [0, n)) behind them; `outs`: the same two, given."""
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 1:
+        raise ValueError("ids: expected a tensor of one dimension")
+    dev = _device_for(ids, "ids")
+    M, i32 = ids.shape[0], torch.int32
+    i = _held(ids, i32, (M,), dev, "ids")
+    need = route_workspace_bytes(M, n)
+    if outs is None:
+        outs = torch.empty(M, dtype=i32, device=ids.device), torch.empty(n + 1, dtype=i32, device=ids.device)
+    order, offsets = outs
+    if ws is not None:
+        _need_ws(ws)
+    elif need:
+        ws = torch.empty(need, dtype=torch.uint8, device=ids.device)
+    _check(_lib.nf4_route(i, M, n, _held(order, i32, (M,), dev, "outs.order"),
+                          _held(offsets, i32, (n + 1,), dev, "outs.offsets"), None if ws is None else ws.data_ptr(),
+                          0 if ws is None else ws.numel(), _raw_stream(dev)), "nf4_route")
+    return order, offsets
 
 
 # ---------------------------------------------------------------------------

@@ -40,10 +40,11 @@ EXTRA = {"quant.hip": ["-ffp-contract=off"],
          "merge.hip": ["-ffp-contract=off"],
          # the 8-bit codes and scales round as the format defines; the fused multiply-adds are written out
          "fp8_quant.hip": ["-ffp-contract=off"],
-         "norm.hip": ["-ffp-contract=off"]}
+         "norm.hip": ["-ffp-contract=off"],
+         "layernorm.hip": ["-ffp-contract=off"]}
 
 HIP_SOURCES = ["quant.hip", "gemm.hip", "skinny.hip", "merge.hip", "probe.hip", "scratch.hip", "fp8_quant.hip", "fp8_gemm.hip",
-               "norm.hip"]
+               "norm.hip", "layernorm.hip", "route.hip"]
 CPP_SOURCES = ["api.cpp", "nf4_table.cpp", "plan.cpp"]
 
 

@@ -1076,4 +1076,89 @@ nf4_status nf4_rmsnorm_bwd(const uint16_t* dY, const uint16_t* h, const uint16_t
       launch_rmsnorm_bwd(dY, h, w, rstd, dH, M, (int)H, dX, dw, (float*)ws, (hipStream_t)stream));
 }
 
+nf4_status nf4_layernorm_fwd(const uint16_t* X, const uint16_t* res, const uint16_t* w, const uint16_t* b, int64_t M,
+                             int64_t H, float eps, uint16_t* H_out, uint16_t* Y, uint8_t* codes, float* scales,
+                             float* mean, float* rstd, void* stream) {
+  nf4_status st = check_norm(M, H);
+  if (st != NF4_OK) return st;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return NF4_ERR_ARG;
+  if (M == 0) return NF4_OK;
+  if (!X || !w || (res && !H_out)) return NF4_ERR_NULL;
+  if ((codes == nullptr) != (scales == nullptr) || (!Y && !codes)) return NF4_ERR_NULL;
+  if (!res) H_out = nullptr;
+  if (!aligned16(X) || !aligned16(res) || !aligned16(w) || !aligned16(b) || !aligned16(H_out) || !aligned16(Y) ||
+      !aligned16(codes) || !aligned4(scales) || !aligned4(mean) || !aligned4(rstd))
+    return NF4_ERR_ALIGN;
+  const size_t n = (size_t)(M * H * 2);
+  const Range ins[] = {rng(X, n), rng(res, res ? n : 0), rng(w, (size_t)H * 2), rng(b, b ? (size_t)H * 2 : 0)};
+  const Range outs[] = {rng(H_out, H_out ? n : 0), rng(Y, Y ? n : 0), rng(codes, codes ? (size_t)(M * H) : 0),
+                        rng(scales, scales ? fp8_scale_bytes(M, H, 1) : 0), rng(mean, mean ? (size_t)M * 4 : 0),
+                        rng(rstd, rstd ? (size_t)M * 4 : 0)};
+  st = check_alias(ins, outs);
+  if (st != NF4_OK) return st;
+  if (!launch_layernorm_fwd) return NF4_ERR_HIP;
+  return hip_status(
+      launch_layernorm_fwd(X, res, w, b, M, (int)H, eps, H_out, Y, codes, scales, mean, rstd, (hipStream_t)stream));
+}
+
+nf4_status nf4_layernorm_workspace_bytes(int64_t M, int64_t H, size_t* bytes) {
+  if (!bytes) return NF4_ERR_NULL;
+  const nf4_status st = check_norm(M, H);
+  if (st != NF4_OK) return st;
+  *bytes = 2 * norm_ws(M, H);
+  return NF4_OK;
+}
+
+nf4_status nf4_layernorm_bwd(const uint16_t* dY, const uint16_t* h, const uint16_t* w, const float* mean,
+                             const float* rstd, const uint16_t* dH, int64_t M, int64_t H, uint16_t* dX, float* dw,
+                             float* db, void* ws, size_t ws_bytes, void* stream) {
+  nf4_status st = check_norm(M, H);
+  if (st != NF4_OK) return st;
+  if (!dw || (M > 0 && (!dY || !h || !w || !mean || !rstd || !dX))) return NF4_ERR_NULL;
+  const size_t need = 2 * norm_ws(M, H);
+  if (!ws || ws_bytes < need) return NF4_ERR_WORKSPACE;
+  if (!aligned16(dw) || !aligned16(db) || !aligned16(ws) ||
+      (M > 0 && (!aligned16(dY) || !aligned16(h) || !aligned16(w) || !aligned4(mean) || !aligned4(rstd) ||
+                 !aligned16(dH) || !aligned16(dX))))
+    return NF4_ERR_ALIGN;
+  const size_t n = (size_t)(M * H * 2);
+  const Range ins[] = {rng(dY, n), rng(h, n), rng(w, M > 0 ? (size_t)H * 2 : 0), rng(mean, (size_t)M * 4),
+                       rng(rstd, (size_t)M * 4), rng(dH, dH ? n : 0)};
+  const Range outs[] = {rng(dX, n), rng(dw, (size_t)H * 4), rng(db, db ? (size_t)H * 4 : 0), rng(ws, need)};
+  st = check_alias(ins, outs);
+  if (st != NF4_OK) return st;
+  if (M == 0) {
+    PrepArgs pa{};
+    pa.zero[0] = ZeroJob{(uint32_t*)dw, H};
+    if (db) pa.zero[1] = ZeroJob{(uint32_t*)db, H};
+    return hip_status(launch_prep(pa, (hipStream_t)stream));
+  }
+  if (!launch_layernorm_bwd) return NF4_ERR_HIP;
+  return hip_status(
+      launch_layernorm_bwd(dY, h, w, mean, rstd, dH, M, (int)H, dX, dw, db, (float*)ws, (hipStream_t)stream));
+}
+
+nf4_status nf4_route_workspace_bytes(int64_t M, int32_t n, size_t* bytes) {
+  if (!bytes) return NF4_ERR_NULL;
+  if (M < 0 || M > kMaxRoutedRows || n < 1 || n > kMaxIds) return NF4_ERR_SHAPE;
+  *bytes = align256((size_t)route_counts(M, n) * 4);
+  return NF4_OK;
+}
+
+nf4_status nf4_route(const int32_t* ids, int64_t M, int32_t n, int32_t* order, int32_t* offsets, void* ws,
+                     size_t ws_bytes, void* stream) {
+  size_t need = 0;
+  nf4_status st = nf4_route_workspace_bytes(M, n, &need);
+  if (st != NF4_OK) return st;
+  if (!offsets || (M > 0 && (!ids || !order))) return NF4_ERR_NULL;
+  if (need && (!ws || ws_bytes < need)) return NF4_ERR_WORKSPACE;
+  if (!aligned4(ids) || !aligned4(order) || !aligned4(offsets) || (need && !aligned16(ws))) return NF4_ERR_ALIGN;
+  const Range ins[] = {rng(ids, (size_t)M * 4)};
+  const Range outs[] = {rng(order, (size_t)M * 4), rng(offsets, (size_t)(n + 1) * 4), rng(ws, need)};
+  st = check_alias(ins, outs);
+  if (st != NF4_OK) return st;
+  if (!launch_route) return NF4_ERR_HIP;
+  return hip_status(launch_route(ids, M, n, order, offsets, (int*)ws, (hipStream_t)stream));
+}
+
 }  // extern "C"

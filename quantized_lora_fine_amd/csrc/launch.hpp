@@ -179,6 +179,24 @@ NF4K_WEAK hipError_t launch_rmsnorm_bwd(const uint16_t* dY, const uint16_t* Hs, 
                                         const uint16_t* dH, int64_t M, int H, uint16_t* dX, float* dw, float* part,
                                         hipStream_t st);
 
+// Layer norm; `part` of its gradient is rmsnorm_parts(M, H) rows of H for dw, and as many for db.
+NF4K_WEAK hipError_t launch_layernorm_fwd(const uint16_t* X, const uint16_t* R, const uint16_t* w, const uint16_t* b,
+                                          int64_t M, int H, float eps, uint16_t* Hout, uint16_t* Y, uint8_t* codes,
+                                          float* scales, float* mean, float* rstd, hipStream_t st);
+NF4K_WEAK hipError_t launch_layernorm_bwd(const uint16_t* dY, const uint16_t* Hs, const uint16_t* w, const float* mean,
+                                          const float* rstd, const uint16_t* dH, int64_t M, int H, uint16_t* dX,
+                                          float* dw, float* db, float* part, hipStream_t st);
+
+// ---- rows sorted by id, and the adapters of many requests ----
+constexpr int kMaxIds = 4096;
+constexpr int64_t kMaxRoutedRows = (int64_t)1 << 30;
+// How the rows are split into runs, one a wave: true where one workgroup takes them all.
+bool plan_route(int64_t M, int n, int* runs, int64_t* run);
+// ints of the counts that several workgroups share (0: one workgroup takes all rows)
+int64_t route_counts(int64_t M, int n);
+NF4K_WEAK hipError_t launch_route(const int32_t* ids, int64_t M, int n, int32_t* order, int32_t* offsets, int* counts,
+                                  hipStream_t st);
+
 // C [M][N] = A W^T (or A W) in 8 bits, scaled by block, plus A2 B2^T; with
 // `offsets` grouped by expert (rows offsets[e] .. offsets[e + 1] by W[e], B2[e])
 struct Fp8Gemm {

@@ -4,6 +4,8 @@
 // link it without a GPU.
 #include "launch.hpp"
 
+#include <algorithm>
+
 namespace nf4k {
 
 // split-K factor for an NT skinny product over M rows (64 rows per
@@ -94,6 +96,23 @@ int rmsnorm_parts(int64_t M, int H) {
   // graphs), two where its waves hold several
   const int64_t most = teams > 1 ? 512 : 256;
   return (int)(groups < most ? groups : most);
+}
+
+// Runs are of 512 rows, 8 loads of a lane under way, while they are 2048 at most.  One
+// workgroup takes up to 16 of them where their counts fit in 64 KB of LDS.
+bool plan_route(int64_t M, int n, int* runs, int64_t* run) {
+  const int64_t fit = std::min<int64_t>(16, 16384 / ((int64_t)n + 1));
+  const bool one = M <= 512 * fit;
+  *run = one ? 64 * ((M + 64 * fit - 1) / (64 * fit)) : 512 * ((M + 512 * 2048 - 1) / (512 * 2048));
+  if (*run < 64) *run = 64;
+  *runs = (int)std::max<int64_t>(1, (M + *run - 1) / *run);
+  return one;
+}
+
+int64_t route_counts(int64_t M, int n) {
+  int runs;
+  int64_t run;
+  return plan_route(M, n, &runs, &run) ? 0 : ((int64_t)n + 1) * (runs + 1);
 }
 
 // Tiles of the block-scaled product, with what one takes on an MI355X: `start`
