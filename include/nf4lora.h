@@ -651,6 +651,66 @@ nf4_status nf4_route(const int32_t *ids, int64_t M, int32_t n, int32_t *order, i
 /* Workspace bytes of nf4_route (host output *bytes).  Errors: NF4_ERR_NULL, _SHAPE. */
 nf4_status nf4_route_workspace_bytes(int64_t M, int32_t n, size_t *bytes);
 
+/*
+ * Low-rank adapters of many requests beside a shared projection: the second term of
+ * equation (3), Y = X W + s X L1 L2, with each row's own adapter.  The projection X W is
+ * any of the library's products (or none), made for all rows at once; `base` is its
+ * result.  For a row m of adapter a:
+ *     T[m] = X[m] L1[a]                        (fp32)
+ *     Y[m] = bf16(base[m] + s[a] T[m] L2[a])
+ *   L1      : bf16 [n][cols][r];  L2 : bf16 [n][r][rows];  s : fp32 [n].  A pool of n
+ *             adapters of one rank r, a multiple of 8 in [8, 256] (a smaller one has
+ *             columns of zeros).  1 <= n <= 4096.
+ *   offsets, order : DEVICE int32, as nf4_route writes them: adapter a's rows are
+ *             order[offsets[a]] to order[offsets[a + 1] - 1], in [0, M); order NULL: the
+ *             rows offsets[a] to offsets[a + 1] - 1 themselves.  Read by the kernels, so
+ *             nothing waits for the routing.  Rows that no adapter has are neither read nor
+ *             written.  Offsets outside [0, M] are taken as the nearest of the two, and
+ *             entries of order outside [0, M) name no row; where offsets do not ascend, or
+ *             a row is listed twice, which rows are written, and with what, is unspecified
+ *             (never any outside the buffers).
+ *   X       : bf16 [M][cols];  base : bf16 [M][rows], Y itself (in place), or NULL for 0;
+ *   Y       : bf16 [M][rows];  T_out : fp32 [M][r] for nf4_adapters_bwd, or NULL.
+ * rows and cols are multiples of 16, at most 2^22; M <= 2^26.  Products are of bf16
+ * operands with fp32 sums; T stays fp32 (as two bf16 values in the second product, which
+ * leave 2^-17 of each).  Adapters hold finite values.  M == 0 does nothing.
+ *   ws      : nf4_adapters_workspace_bytes(NF4_OP_FWD, ...) bytes; one each for calls
+ *             that may overlap.
+ * s, order and offsets need 4-byte alignment, the other pointers 16.
+ * Errors: NF4_ERR_NULL, _SHAPE, _ALIGN, _WORKSPACE, _ALIAS, _HIP.
+ */
+nf4_status nf4_adapters_fwd(const uint16_t *X, int64_t M, const uint16_t *L1, const uint16_t *L2, const float *s,
+                            int32_t n, int64_t rows, int64_t cols, int32_t r, const int32_t *order,
+                            const int32_t *offsets, const uint16_t *base, uint16_t *Y, float *T_out, void *ws,
+                            size_t ws_bytes, void *stream);
+
+/* Workspace bytes of nf4_adapters_fwd (op = NF4_OP_FWD) and nf4_adapters_bwd (NF4_OP_BWD; host output *bytes).
+ * Errors: NF4_ERR_NULL, _SHAPE, _ARG (op). */
+nf4_status nf4_adapters_workspace_bytes(int32_t op, int64_t M, int64_t rows, int64_t cols, int32_t n, int32_t r,
+                                        size_t *bytes);
+
+/*
+ * The gradients of nf4_adapters_fwd, from its T and either its X or an 8-bit checkpoint of
+ * X: the codes and scales in blocks of one row that the norms or nf4_fp8_quantize wrote (for
+ * the frozen product, say), read as they are.  With G[m] = s[a] dY[m] L2[a]^T (fp32):
+ *     dL2[a] = s[a] sum over a's rows of T[m]^T dY[m]   -> fp32 [n][r][rows]
+ *     dL1[a] = sum over a's rows of X[m]^T G[m]         -> fp32 [n][cols][r]
+ *     dX[m]  = bf16(base[m] + G[m] L1[a]^T)             -> bf16 [M][cols], optional
+ *   X, x_scales, x_format : bf16 [M][cols] with x_scales NULL, or codes [M][cols] of
+ *             x_format (NF4_FP8_E4M3, _E5M2) with scales [M][ceil(cols / 128)].
+ *   dY      : bf16 [M][rows];  T : fp32 [M][r].
+ *   base    : bf16 [M][cols], the gradient through the shared projection (dY W), dX itself
+ *             (in place), or NULL for 0.  dX NULL: no input gradient.
+ * An adapter without rows gets zeros.  Sums are fp32 in a fixed order; G and T enter the
+ * products for dL1 and dL2 with all their bits (as three bf16 values).  M == 0 writes zeros to dL1 and dL2.
+ * Everything else, and errors (_ARG: x_format), as nf4_adapters_fwd.
+ */
+nf4_status nf4_adapters_bwd(const void *X, const float *x_scales, int32_t x_format, const uint16_t *dY, const float *T,
+                            int64_t M, const uint16_t *L1, const uint16_t *L2, const float *s, int32_t n,
+                            int64_t rows, int64_t cols, int32_t r, const int32_t *order, const int32_t *offsets,
+                            const uint16_t *base, uint16_t *dX, float *dL1, float *dL2, void *ws, size_t ws_bytes,
+                            void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -40,37 +40,37 @@ def _listed(order, offsets, a, M):
 
 
 def adapters_fwd(x, l1, l2, s, order, offsets, base):
-    """(y, t, S, Q): the outputs for listed rows (others: base, or 0 without one, and t = 0), the sum of the magnitudes of
-    the terms of s T L2, and the same of X L1."""
+    """(y, t, S, Q, R): the outputs for listed rows (others: base, or 0 without one, and t = 0); S the sum of the
+    magnitudes of the terms of s T L2, Q the same of X L1, and R what Q becomes in Y."""
     x, l1, l2, s = (np.asarray(v, np.float64) for v in (x, l1, l2, s))
     M, n, r, o = x.shape[0], l1.shape[0], l1.shape[2], l2.shape[2]
     y = np.zeros((M, o)) if base is None else np.array(base, np.float64)
-    t, S, Q = np.zeros((M, r)), np.zeros((M, o)), np.zeros((M, r))
+    t, S, Q, R = np.zeros((M, r)), np.zeros((M, o)), np.zeros((M, r)), np.zeros((M, o))
     for a in range(n):
         rows = _listed(order, offsets, a, M)
         t[rows] = x[rows] @ l1[a]
         Q[rows] = np.abs(x[rows]) @ np.abs(l1[a])
         y[rows] += s[a] * (t[rows] @ l2[a])
         S[rows] = abs(s[a]) * (np.abs(t[rows]) @ np.abs(l2[a]))
-    return y, t, S, Q
+        R[rows] = abs(s[a]) * (Q[rows] @ np.abs(l2[a]))
+    return y, t, S, Q, R
 
 
 def adapters_bwd(dy, x, t, l1, l2, s, order, offsets, base):
-    """(dx, dl1, dl2) and, of each, the sum of the magnitudes of its terms; with G, and the same of it."""
+    """(dx, dl1, dl2), each with the sum of the magnitudes of its terms (G's own terms in the first two)."""
     dy, x, t, l1, l2, s = (np.asarray(v, np.float64) for v in (dy, x, t, l1, l2, s))
     M, n, h, r, o = x.shape[0], l1.shape[0], l1.shape[1], l1.shape[2], l2.shape[2]
     dx = np.zeros((M, h)) if base is None else np.array(base, np.float64)
     Sx, dl1, S1, dl2, S2 = np.zeros((M, h)), np.zeros((n, h, r)), np.zeros((n, h, r)), np.zeros((n, r, o)), \
         np.zeros((n, r, o))
-    g, Sg = np.zeros((M, r)), np.zeros((M, r))
     for a in range(n):
         rows = _listed(order, offsets, a, M)
-        g[rows] = s[a] * (dy[rows] @ l2[a].T)
-        Sg[rows] = abs(s[a]) * (np.abs(dy[rows]) @ np.abs(l2[a]).T)
+        g = s[a] * (dy[rows] @ l2[a].T)
+        Sg = abs(s[a]) * (np.abs(dy[rows]) @ np.abs(l2[a]).T)
         dl2[a] = s[a] * (t[rows].T @ dy[rows])
         S2[a] = abs(s[a]) * (np.abs(t[rows]).T @ np.abs(dy[rows]))
-        dl1[a] = x[rows].T @ g[rows]
-        S1[a] = np.abs(x[rows]).T @ Sg[rows]
-        dx[rows] += g[rows] @ l1[a].T
-        Sx[rows] = Sg[rows] @ np.abs(l1[a]).T
+        dl1[a] = x[rows].T @ g
+        S1[a] = np.abs(x[rows]).T @ Sg
+        dx[rows] += g @ l1[a].T
+        Sx[rows] = Sg @ np.abs(l1[a]).T
     return (dx, Sx), (dl1, S1), (dl2, S2)

@@ -99,6 +99,11 @@ _SIGS = {
     "nf4_layernorm_workspace_bytes": ([_i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
     "nf4_layernorm_bwd": ([_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
     "nf4_route_workspace_bytes": ([_i64, _i32, ctypes.POINTER(_sz)], ctypes.c_int),
+    "nf4_adapters_workspace_bytes": ([_i32, _i64, _i64, _i64, _i32, _i32, ctypes.POINTER(_sz)], ctypes.c_int),
+    "nf4_adapters_fwd": ([_vp, _i64, _vp, _vp, _vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+                         ctypes.c_int),
+    "nf4_adapters_bwd": ([_vp, _vp, _i32, _vp, _vp, _i64, _vp, _vp, _vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp,
+                          _vp, _vp, _sz, _vp], ctypes.c_int),
     "nf4_route": ([_vp, _i64, _i32, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
 }
 for _name, (_args, _res) in _SIGS.items():
@@ -842,6 +847,91 @@ def route(ids: torch.Tensor, n: int, ws: torch.Tensor | None = None, outs=None):
                           _held(offsets, i32, (n + 1,), dev, "outs.offsets"), None if ws is None else ws.data_ptr(),
                           0 if ws is None else ws.numel(), _raw_stream(dev)), "nf4_route")
     return order, offsets
+
+
+@functools.lru_cache(maxsize=4096)
+def adapters_workspace_bytes(op: int, M: int, o: int, h: int, n: int, r: int) -> int:
+    """Bytes of the workspace of adapters_fwd (op = NF4_OP_FWD) or adapters_bwd (NF4_OP_BWD)."""
+    b = _sz()
+    _check(_lib.nf4_adapters_workspace_bytes(op, M, o, h, n, r, ctypes.byref(b)), "nf4_adapters_workspace_bytes")
+    return b.value
+
+
+def _adapters(L1, L2, s, offsets, order, M: int, dev: int):
+    """Checks a pool's tensors and the rows' lists; returns (n, o, h, r, L1, L2, s, order, offsets) as the C calls take
+    them."""
+    if not isinstance(L1, torch.Tensor) or L1.dim() != 3:
+        raise ValueError("L1: expected a tensor of three dimensions, [n][h][r]")
+    if not isinstance(L2, torch.Tensor) or L2.dim() != 3:
+        raise ValueError("L2: expected a tensor of three dimensions, [n][r][o]")
+    n, h, r = L1.shape
+    o = L2.shape[2]
+    return (n, o, h, r, _held(L1, torch.bfloat16, (n, h, r), dev, "L1"), _held(L2, torch.bfloat16, (n, r, o), dev, "L2"),
+            _held(s, torch.float32, (n,), dev, "s"),
+            None if order is None else _held(order, torch.int32, (M,), dev, "order"),
+            _held(offsets, torch.int32, (n + 1,), dev, "offsets"))
+
+
+def _adapters_ws(ws, op: int, M: int, o: int, h: int, n: int, r: int, device):
+    if ws is not None:
+        return _need_ws(ws)
+    return torch.empty(adapters_workspace_bytes(op, M, o, h, n, r), dtype=torch.uint8, device=device)
+
+
+def adapters_fwd(X: torch.Tensor, L1: torch.Tensor, L2: torch.Tensor, s: torch.Tensor, offsets: torch.Tensor,
+                 order: torch.Tensor | None = None, base: torch.Tensor | None = None, want_T: bool = True,
+                 out: torch.Tensor | None = None, T_out: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """nf4_adapters_fwd: (Y bf16 [M][o], T fp32 [M][r] or None), Y = base + s[a] (X L1[a]) L2[a] for the rows of each
+    adapter a of the pool L1 [n][h][r], L2 [n][r][o], s fp32 [n].  offsets (and order) as route() gives them; base bf16
+    [M][o] is the shared projection's result, or None for 0, and `out` may be base itself.  Rows that no adapter has
+    are not written (undefined in results that this call allocates)."""
+    M, h = _matrix(X, "X")
+    dev = _device_for(X, "X")
+    n, o, hl, r, l1, l2, sp, ordp, off = _adapters(L1, L2, s, offsets, order, M, dev)
+    x = _held(X, torch.bfloat16, (M, hl), dev, "X")
+    b = None if base is None else _held(base, torch.bfloat16, (M, o), dev, "base")
+    if out is None:
+        out = torch.empty(M, o, dtype=torch.bfloat16, device=X.device)
+    if T_out is None and want_T:
+        T_out = torch.empty(M, r, dtype=torch.float32, device=X.device)
+    t = None if T_out is None else _held(T_out, torch.float32, (M, r), dev, "T_out")
+    ws = _adapters_ws(ws, NF4_OP_FWD, M, o, h, n, r, X.device)
+    _check(_lib.nf4_adapters_fwd(x, M, l1, l2, sp, n, o, h, r, ordp, off, b, _held(out, torch.bfloat16, (M, o), dev, "out"),
+                                 t, ws.data_ptr(), ws.numel(), _raw_stream(dev)), "nf4_adapters_fwd")
+    return out, T_out
+
+
+def adapters_bwd(dY: torch.Tensor, X: torch.Tensor, T: torch.Tensor, L1: torch.Tensor, L2: torch.Tensor, s: torch.Tensor,
+                 offsets: torch.Tensor, order: torch.Tensor | None = None, x_scales: torch.Tensor | None = None,
+                 base: torch.Tensor | None = None, want_dX: bool = True, dX: torch.Tensor | None = None,
+                 dL1: torch.Tensor | None = None, dL2: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """nf4_adapters_bwd: (dX bf16 [M][h] or None, dL1 fp32 [n][h][r], dL2 fp32 [n][r][o]) from the forward's T and X, or
+    from an 8-bit checkpoint of X: codes and x_scales as the norms and fp8_quantize give them.  base bf16 [M][h] is the
+    gradient through the shared projection, or None for 0, and `dX` may be base itself."""
+    M, o = _matrix(dY, "dY")
+    dev = _device_for(dY, "dY")
+    n, ol, h, r, l1, l2, sp, ordp, off = _adapters(L1, L2, s, offsets, order, M, dev)
+    bf16, f32 = torch.bfloat16, torch.float32
+    g = _held(dY, bf16, (M, ol), dev, "dY")
+    if x_scales is None:
+        f, sx, x = 0, None, _held(X, bf16, (M, h), dev, "X")
+    else:
+        f = _fp8_format(getattr(X, "dtype", None), "X")
+        sx, x = _held(x_scales, f32, (M, _blocks(h)), dev, "x_scales"), _held(X, X.dtype, (M, h), dev, "X")
+    t = _held(T, f32, (M, r), dev, "T")
+    if dX is None and want_dX:
+        dX = torch.empty(M, h, dtype=bf16, device=dY.device)
+    dx = None if dX is None else _held(dX, bf16, (M, h), dev, "dX")
+    b = None if base is None else _held(base, bf16, (M, h), dev, "base")
+    if dL1 is None:
+        dL1 = torch.empty(n, h, r, dtype=f32, device=dY.device)
+    if dL2 is None:
+        dL2 = torch.empty(n, r, o, dtype=f32, device=dY.device)
+    ws = _adapters_ws(ws, NF4_OP_BWD, M, o, h, n, r, dY.device)
+    _check(_lib.nf4_adapters_bwd(x, sx, f, g, t, M, l1, l2, sp, n, o, h, r, ordp, off, b, dx,
+                                 _held(dL1, f32, (n, h, r), dev, "dL1"), _held(dL2, f32, (n, r, o), dev, "dL2"),
+                                 ws.data_ptr(), ws.numel(), _raw_stream(dev)), "nf4_adapters_bwd")
+    return dX, dL1, dL2
 
 
 # ---------------------------------------------------------------------------

@@ -44,7 +44,7 @@ EXTRA = {"quant.hip": ["-ffp-contract=off"],
          "layernorm.hip": ["-ffp-contract=off"]}
 
 HIP_SOURCES = ["quant.hip", "gemm.hip", "skinny.hip", "merge.hip", "probe.hip", "scratch.hip", "fp8_quant.hip", "fp8_gemm.hip",
-               "norm.hip", "layernorm.hip", "route.hip"]
+               "norm.hip", "layernorm.hip", "route.hip", "adapters.hip"]
 CPP_SOURCES = ["api.cpp", "nf4_table.cpp", "plan.cpp"]
 
 

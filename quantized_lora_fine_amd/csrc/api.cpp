@@ -562,6 +562,22 @@ nf4_status check_norm(int64_t M, int64_t H) {
   return NF4_OK;
 }
 
+// ---- the adapters of many requests ----
+nf4_status check_adapters(int64_t M, int64_t rows, int64_t cols, int32_t n, int32_t r) {
+  if (M < 0 || M > kMaxAdapterRows || n < 1 || n > kMaxIds) return NF4_ERR_SHAPE;
+  if (rows <= 0 || cols <= 0 || rows % 16 != 0 || cols % 16 != 0 || rows > kMaxLayerDim || cols > kMaxLayerDim)
+    return NF4_ERR_SHAPE;
+  if (r < 8 || r > 256 || r % 8 != 0) return NF4_ERR_SHAPE;
+  return NF4_OK;
+}
+
+size_t adapters_ws(int32_t op, int64_t M, int64_t rows, int64_t cols, int32_t n, int32_t r) {
+  if (M == 0) return 0;
+  if (op == NF4_OP_FWD) return (size_t)plan_adapters_rows(M, n, cols).splits * M * r * 4;
+  return (size_t)plan_adapters_rows(M, n, rows).splits * M * r * 4 +
+         (size_t)plan_adapters_items(M, n, cols, rows, r).items * r * (rows + cols) * 4;
+}
+
 size_t norm_ws(int64_t M, int64_t H) { return align256((size_t)std::max(rmsnorm_parts(M, (int)H), 1) * H * 4); }
 
 }  // namespace
@@ -1159,6 +1175,87 @@ nf4_status nf4_route(const int32_t* ids, int64_t M, int32_t n, int32_t* order, i
   if (st != NF4_OK) return st;
   if (!launch_route) return NF4_ERR_HIP;
   return hip_status(launch_route(ids, M, n, order, offsets, (int*)ws, (hipStream_t)stream));
+}
+
+nf4_status nf4_adapters_workspace_bytes(int32_t op, int64_t M, int64_t rows, int64_t cols, int32_t n, int32_t r,
+                                        size_t* bytes) {
+  if (!bytes) return NF4_ERR_NULL;
+  if (op != NF4_OP_FWD && op != NF4_OP_BWD) return NF4_ERR_ARG;
+  const nf4_status st = check_adapters(M, rows, cols, n, r);
+  if (st != NF4_OK) return st;
+  *bytes = adapters_ws(op, M, rows, cols, n, r);
+  return NF4_OK;
+}
+
+nf4_status nf4_adapters_fwd(const uint16_t* X, int64_t M, const uint16_t* L1, const uint16_t* L2, const float* s,
+                            int32_t n, int64_t rows, int64_t cols, int32_t r, const int32_t* order,
+                            const int32_t* offsets, const uint16_t* base, uint16_t* Y, float* T_out, void* ws,
+                            size_t ws_bytes, void* stream) {
+  nf4_status st = check_adapters(M, rows, cols, n, r);
+  if (st != NF4_OK) return st;
+  if (M == 0) return NF4_OK;
+  if (!X || !L1 || !L2 || !s || !offsets || !Y) return NF4_ERR_NULL;
+  const size_t need = adapters_ws(NF4_OP_FWD, M, rows, cols, n, r);
+  if (!ws || ws_bytes < need) return NF4_ERR_WORKSPACE;
+  if (!aligned16(X) || !aligned16(L1) || !aligned16(L2) || !aligned4(s) || !aligned4(order) || !aligned4(offsets) ||
+      !aligned16(base) || !aligned16(Y) || !aligned16(T_out) || !aligned16(ws))
+    return NF4_ERR_ALIGN;
+  const size_t y = (size_t)(M * rows * 2);
+  const Range ins[] = {rng(X, (size_t)(M * cols * 2)), rng(L1, (size_t)n * cols * r * 2),
+                       rng(L2, (size_t)n * rows * r * 2), rng(s, (size_t)n * 4),
+                       rng(order, order ? (size_t)M * 4 : 0), rng(offsets, (size_t)(n + 1) * 4),
+                       rng(base, base && base != Y ? y : 0)};
+  const Range outs[] = {rng(Y, y), rng(T_out, T_out ? (size_t)M * r * 4 : 0), rng(ws, need)};
+  st = check_alias(ins, outs);
+  if (st != NF4_OK) return st;
+  if (!launch_adapters_fwd) return NF4_ERR_HIP;
+  const AdapterCall c{{offsets, order, n, M}, L1, L2, s, rows, cols, r};
+  return hip_status(launch_adapters_fwd(c, X, base, Y, T_out, ws, (hipStream_t)stream));
+}
+
+nf4_status nf4_adapters_bwd(const void* X, const float* x_scales, int32_t x_format, const uint16_t* dY, const float* T,
+                            int64_t M, const uint16_t* L1, const uint16_t* L2, const float* s, int32_t n,
+                            int64_t rows, int64_t cols, int32_t r, const int32_t* order, const int32_t* offsets,
+                            const uint16_t* base, uint16_t* dX, float* dL1, float* dL2, void* ws, size_t ws_bytes,
+                            void* stream) {
+  nf4_status st = check_adapters(M, rows, cols, n, r);
+  if (st != NF4_OK) return st;
+  if (x_scales && x_format != NF4_FP8_E4M3 && x_format != NF4_FP8_E5M2) return NF4_ERR_ARG;
+  if (!dL1 || !dL2) return NF4_ERR_NULL;
+  if (M > 0 && (!X || !dY || !T || !L1 || !L2 || !s || !offsets)) return NF4_ERR_NULL;
+  if (!aligned16(dL1) || !aligned16(dL2)) return NF4_ERR_ALIGN;
+  const size_t need = adapters_ws(NF4_OP_BWD, M, rows, cols, n, r);
+  const size_t b1 = (size_t)n * cols * r * 4, b2 = (size_t)n * rows * r * 4;
+  if (M == 0) {
+    if (overlap(rng(dL1, b1), rng(dL2, b2))) return NF4_ERR_ALIAS;
+    PrepArgs pa{};
+    pa.zero[0] = ZeroJob{(uint32_t*)dL1, (int64_t)(b1 / 4)};
+    pa.zero[1] = ZeroJob{(uint32_t*)dL2, (int64_t)(b2 / 4)};
+    return hip_status(launch_prep(pa, (hipStream_t)stream));
+  }
+  if (!ws || ws_bytes < need) return NF4_ERR_WORKSPACE;
+  if (!aligned16(X) || !aligned4(x_scales) || !aligned16(dY) || !aligned16(T) || !aligned16(L1) || !aligned16(L2) ||
+      !aligned4(s) || !aligned4(order) || !aligned4(offsets) || !aligned16(base) || !aligned16(dX) || !aligned16(ws))
+    return NF4_ERR_ALIGN;
+  const size_t x = (size_t)(M * cols * 2);
+  if (!dX) base = nullptr;
+  const Range ins[] = {rng(X, x_scales ? x / 2 : x),
+                       rng(x_scales, x_scales ? fp8_scale_bytes(M, cols, 1) : 0),
+                       rng(dY, (size_t)(M * rows * 2)),
+                       rng(T, (size_t)M * r * 4),
+                       rng(L1, b1 / 2),
+                       rng(L2, b2 / 2),
+                       rng(s, (size_t)n * 4),
+                       rng(order, order ? (size_t)M * 4 : 0),
+                       rng(offsets, (size_t)(n + 1) * 4),
+                       rng(base, base && base != dX ? x : 0)};
+  const Range outs[] = {rng(dX, dX ? x : 0), rng(dL1, b1), rng(dL2, b2), rng(ws, need)};
+  st = check_alias(ins, outs);
+  if (st != NF4_OK) return st;
+  if (!launch_adapters_bwd) return NF4_ERR_HIP;
+  const AdapterCall c{{offsets, order, n, M}, L1, L2, s, rows, cols, r};
+  const int x8 = !x_scales ? 0 : x_format == NF4_FP8_E5M2 ? 2 : 1;
+  return hip_status(launch_adapters_bwd(c, X, x8, x_scales, dY, T, base, dX, dL1, dL2, ws, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -197,6 +197,78 @@ int64_t route_counts(int64_t M, int n);
 NF4K_WEAK hipError_t launch_route(const int32_t* ids, int64_t M, int n, int32_t* order, int32_t* offsets, int* counts,
                                   hipStream_t st);
 
+// The adapters of many requests (adapters.hip).  Their rows: adapter a's are
+// order[offsets[a] .. offsets[a + 1]), or these numbers themselves without an order.
+struct AdapterRows {
+  const int32_t* offsets;
+  const int32_t* order;  // or NULL
+  int n;
+  int64_t M;
+};
+struct AdapterCall {
+  AdapterRows rows;
+  const uint16_t* L1;  // [n][h][r]
+  const uint16_t* L2;  // [n][r][o]
+  const float* s;      // [n]
+  int64_t o, h;
+  int r;
+};
+struct AdapterNarrow {
+  AdapterRows rows;
+  const uint16_t* A;  // [M][K]
+  const uint16_t* L;
+  int64_t K;
+  int r;
+  int64_t krange;
+  float* part;  // [splits][M][r]
+};
+struct AdapterWide {
+  AdapterRows rows;
+  const float* part;  // [splits][M][r]
+  int splits;
+  const uint16_t* L;
+  int64_t N;
+  int r;
+  const float* s;
+  const uint16_t* base;  // or NULL
+  uint16_t* out;
+  float* T_out;  // the joined parts, or NULL
+};
+struct AdapterGrad {
+  const void* Q;          // [M][N], bf16 or codes
+  const float* q_scales;  // of codes
+  int64_t N;
+  const float* P;  // [splits][M][r]
+  int splits, r;
+  const float* s;
+  int item;       // rows an item, a multiple of 64
+  int64_t items;  // at most
+  int trans;      // out [n][N][r], else [n][r][N]
+  float* part;    // [items][r * N]
+  float* out;
+};
+constexpr int64_t kMaxAdapterRows = (int64_t)1 << 26;  // tiles of 16 rows stay one launch
+// Tiles of rows of the products of one row, and the splits of a contraction over K.
+struct AdapterPlan {
+  int bm;         // rows a tile: 16 or 64
+  int64_t tiles;  // at most
+  int splits;
+  int64_t krange;
+};
+AdapterPlan plan_adapters_rows(int64_t M, int n, int64_t K);
+// Rows of an item of the adapters' gradients, and the items there are at most.
+struct AdapterItems {
+  int item;
+  int64_t items;
+};
+AdapterItems plan_adapters_items(int64_t M, int n, int64_t h, int64_t o, int r);
+NF4K_WEAK hipError_t launch_adapters_fwd(const AdapterCall& c, const uint16_t* X, const uint16_t* base, uint16_t* Y,
+                                         float* T_out, void* ws, hipStream_t st);
+// x8: 0 X is bf16, 1 e4m3, 2 e5m2
+NF4K_WEAK hipError_t launch_adapters_bwd(const AdapterCall& c, const void* X, int x8, const float* x_scales,
+                                         const uint16_t* dY, const float* T, const uint16_t* base, uint16_t* dX,
+                                         float* dL1, float* dL2, void* ws, hipStream_t st);
+
 // C [M][N] = A W^T (or A W) in 8 bits, scaled by block, plus A2 B2^T; with
 // `offsets` grouped by expert (rows offsets[e] .. offsets[e + 1] by W[e], B2[e])
 struct Fp8Gemm {

@@ -115,6 +115,30 @@ int64_t route_counts(int64_t M, int n) {
   return plan_route(M, n, &runs, &run) ? 0 : ((int64_t)n + 1) * (runs + 1);
 }
 
+// Tiles of 16 rows where an adapter has few in the mean, else of 64.  About 1024
+// workgroups, each with 256 of the contraction or more: 4 waves with 2 steps of 32.
+AdapterPlan plan_adapters_rows(int64_t M, int n, int64_t K) {
+  AdapterPlan p;
+  const int64_t used = std::min<int64_t>(M, n);
+  p.bm = M <= 16 * used ? 16 : 64;
+  p.tiles = std::min<int64_t>(M, M / p.bm + used);
+  const int64_t most = std::max<int64_t>(1, (K + 255) / 256);
+  const int64_t want = std::min(most, (1024 + p.tiles - 1) / std::max<int64_t>(p.tiles, 1));
+  p.krange = ((K + want - 1) / want + 255) / 256 * 256;
+  p.splits = (int)((K + p.krange - 1) / p.krange);
+  return p;
+}
+
+AdapterItems plan_adapters_items(int64_t M, int n, int64_t h, int64_t o, int r) {
+  AdapterItems p;
+  const int64_t tiles = ((h + 127) / 128 + (o + 127) / 128) * ((r + 63) / 64);
+  const int64_t used = std::min<int64_t>(M, n);
+  const int64_t rows = std::max<int64_t>(128, M * tiles / 1024);
+  p.item = (int)((std::min<int64_t>(rows, std::max<int64_t>(M, 64)) + 63) / 64 * 64);
+  p.items = std::min<int64_t>(M, M / p.item + used);
+  return p;
+}
+
 // Tiles of the block-scaled product, with what one takes on an MI355X: `start`
 // microseconds around its loop, and u0 to u1 microseconds for every 128 of the
 // contraction, u0 when few compute units have a tile and u1 when all do.  Fitted
