@@ -29,7 +29,7 @@ namespace nf4k {
 
 namespace {
 
-constexpr int kAhead = 2;  // steps of 32 columns whose loads are under way in k_adapters_narrow
+constexpr int kAhead = 2;  // steps of 32 columns whose loads are under way in k_adapters_narrow_few
 
 // Tile t of `bm` rows: its adapter, positions [p0, p1), and whether they are all of the
 // adapter's.  Every wave scans the tile counts of 64 adapters at a time.
@@ -99,15 +99,16 @@ __device__ __forceinline__ void split4(floatx4 x, uint2 (&part)[W]) {
 
 // ---------------------------------------------------------------------------
 // part[split][m][j] = sum over the split's k of A[m][k] L[a][k][j] (KMAJOR: L1
-// [n][K][r]) or A[m][k] L[a][j][k] (L2 [n][r][K]).  A workgroup has 16 NM rows,
+// [n][K][r]) or A[m][k] L[a][j][k] (L2 [n][r][K]), for tiles of 16 rows.  A workgroup has
 // 16 NJ columns of the rank (blockIdx.z: which 64) and a range of k (blockIdx.y).  Its 4
 // waves take every fourth step of 32 k, kAhead steps' loads under way, and their sums are
 // added in LDS in wave order.  A's rows are the MFMA's second operand, so a lane ends with
 // 4 neighbouring columns of one row; a row or column past the end repeats a valid one and
 // is not written.  L1 goes through LDS for transposing reads, each wave's own part.
 // ---------------------------------------------------------------------------
-template <bool KMAJOR, int NJ, int NM>
-__global__ __launch_bounds__(256) void k_adapters_narrow(AdapterNarrow p) {
+template <bool KMAJOR, int NJ>
+__global__ __launch_bounds__(256) void k_adapters_narrow_few(AdapterNarrow p) {
+  constexpr int NM = 1;
   constexpr int RP = 16 * NJ, BM = 16 * NM;
   constexpr int ROW = RP * 2 + (NJ == 1 ? 0 : 16);                      // LDS bytes of a k row of L1
   constexpr int STAGE = KMAJOR ? 32 * ROW * kAhead : 0;                 // a wave's
@@ -196,32 +197,234 @@ __global__ __launch_bounds__(256) void k_adapters_narrow(AdapterNarrow p) {
   }
 }
 
-// sum of a value's splits, in their order
+// ---------------------------------------------------------------------------
+// The same for tiles of BM = 64 MW rows: both operands are copied straight into LDS, 64 of
+// k a step through a ring of three buffers, two steps under way.  A wave owns 16 MW rows,
+// so nothing is joined.  16-byte pieces of a row of 128 bytes stand XORed by the row, so
+// that fragments of 16 rows fall on different banks; rows of L1 are as long as the rank,
+// and only those of 128 bytes need that.  A step past K repeats valid memory, and its
+// fragments are zeroed.
+// ---------------------------------------------------------------------------
+constexpr int kWaitLds = 15 | (3 << 14) | (0x7 << 4);  // lgkmcnt(0), vmcnt as it is
+constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8); }
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+typedef __attribute__((address_space(1))) const void* global_ptr_t;
+
+template <bool KMAJOR, int NJ, int MW>
+__global__ __launch_bounds__(256) void k_adapters_narrow(AdapterNarrow p) {
+  constexpr int RP = 16 * NJ, BM = 64 * MW;
+  constexpr int XB = BM * 128, SB = XB + RP * 128 + 128;
+  constexpr int XI = 2 * MW, LI = NJ == 1 ? 1 : NJ / 2;  // copies of a wave and step
+  __shared__ __attribute__((aligned(1024))) uint8_t S0[SB];
+  __shared__ __attribute__((aligned(1024))) uint8_t S1[SB];
+  __shared__ __attribute__((aligned(1024))) uint8_t S2[SB];
+  auto buf = [&](int b) -> uint8_t* { return b == 0 ? S0 : b == 1 ? S1 : S2; };
+  Tile tile;
+  if (!find_tile(p.rows, BM, blockIdx.x, tile)) return;
+  const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int j0 = blockIdx.z * 64, r = p.r, rw = min(r - j0, 64);  // columns of the rank here
+  const int64_t K = p.K;
+  const int64_t k0 = (int64_t)blockIdx.y * p.krange, k1 = min(k0 + p.krange, K);
+  const int steps = (int)((k1 - k0 + 63) / 64);
+  // X: copy i has rows 32 i + tid / 8
+  const uint16_t* xp[XI];
+  const int xc = 8 * ((tid & 7) ^ ((tid >> 3) & 7));
+#pragma unroll
+  for (int i = 0; i < XI; ++i)
+    xp[i] = p.A + max(row_at(p.rows, tile, tile.p0 + 32 * i + (tid >> 3)), (int64_t)0) * K + k0;
+  const uint16_t* L = p.L + (int64_t)tile.a * K * r;
+  const uint16_t* lp[LI];
+  int lk[LI];  // KMAJOR: the row of k within a step
+#pragma unroll
+  for (int i = 0; i < LI; ++i) {
+    int e = NJ == 1 ? tid & 127 : 256 * i + tid;
+    if constexpr (KMAJOR) {
+      e = min(e, 8 * rw - 1);
+      const int per = rw / 8;
+      lk[i] = e / per;
+      int c = e - lk[i] * per;
+      if (rw == 64) c ^= ((lk[i] >> 1) & 1) << 1;
+      lp[i] = L + k0 * r + j0 + 8 * c;
+    } else {
+      lp[i] = L + (int64_t)(j0 + min(e >> 3, rw - 1)) * K + k0;
+    }
+  }
+  auto copy = [&](int t, int b) {
+    t = min(t, steps - 1);  // a step behind the last copies it once more, and is not used
+    uint8_t* const to = buf(b);
+    const int64_t k = 64 * (int64_t)t, left = K - k0 - k;  // from here to the row's end
+    const int64_t x = k + (xc < left ? xc : 0);
+#pragma unroll
+    for (int i = 0; i < XI; ++i)
+      __builtin_amdgcn_global_load_lds((global_ptr_t)(xp[i] + x), (lds_ptr_t)(to + (4 * i + wave) * 1024), 16, 0, 0);
+#pragma unroll
+    for (int i = 0; i < LI; ++i) {
+      const uint16_t* from = KMAJOR ? lp[i] + (k + min((int64_t)lk[i], left - 1)) * r : lp[i] + x;
+      __builtin_amdgcn_global_load_lds((global_ptr_t)from,
+                                       (lds_ptr_t)(to + XB + (NJ == 1 ? wave & 1 : 4 * i + wave) * 1024), 16, 0, 0);
+    }
+  };
+  floatx4 acc[NJ][MW];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int i = 0; i < MW; ++i) acc[j][i] = floatx4{0.f, 0.f, 0.f, 0.f};
+  const int rb = KMAJOR ? 2 * rw : 128;
+  const int e = li >> 2, q = li & 3, swz = rw == 64 && e >= 2 ? 2 : 0;
+  auto compute = [&](int t, int b) {
+    uint8_t* const at = buf(b);
+    const int64_t left = k1 - k0 - 64 * (int64_t)t;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const bool in = 32 * ks + 8 * g < left;
+      const int piece = ((4 * ks + g) ^ (li & 7)) << 4;
+      bf16x8 fx[MW];
+#pragma unroll
+      for (int i = 0; i < MW; ++i) {
+        u32x4 v = *(const u32x4*)(at + (wave * 16 * MW + 16 * i + li) * 128 + piece);
+        if (!in) v = u32x4{0u, 0u, 0u, 0u};
+        fx[i] = __builtin_bit_cast(bf16x8, v);
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        u32x4 v;
+        if constexpr (KMAJOR)
+          v = __builtin_bit_cast(u32x4, lds_tr8(at + XB + (32 * ks + 8 * g + e) * rb +
+                                                    (((2 * j + (q >> 1)) ^ swz) << 4) + ((q & 1) << 3), rb));
+        else v = *(const u32x4*)(at + XB + (16 * j + li) * 128 + piece);
+        if (!in) v = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < MW; ++i)
+          acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v), fx[i], acc[j][i], 0, 0, 0);
+      }
+    }
+  };
+  auto step = [&](int t, int b) {
+    // this step's copies are there, everybody's, and the reads of the step before are done
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(wait_vm(XI + LI) & kWaitLds);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    copy(t + 2, (b + 2) % 3);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(t, b);
+  };
+  copy(0, 0);
+  copy(1, 1);
+  for (int t = 0; t < steps; t += 3) {
+    step(t, 0);
+    if (t + 1 < steps) step(t + 1, 1);
+    if (t + 2 < steps) step(t + 2, 2);
+  }
+#pragma unroll
+  for (int i = 0; i < MW; ++i) {
+    const int64_t row = row_at(p.rows, tile, tile.p0 + wave * 16 * MW + 16 * i + li);
+    if (row < 0) continue;
+    float* to = p.part + ((int64_t)blockIdx.y * p.rows.M + row) * r + j0;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      if (16 * j + 4 * g < rw) *(floatx4*)(to + 16 * j + 4 * g) = acc[j][i];
+  }
+  __builtin_amdgcn_s_waitcnt(0);  // no copy is on its way into LDS that is no longer this workgroup's
+}
+
+// sum of a value's splits, in their order, 4 loads at a time
 __device__ __forceinline__ floatx4 join4(const float* part, int64_t stride, int splits) {
   floatx4 s = *(const floatx4*)part;
-  for (int q = 1; q < splits; ++q) s += *(const floatx4*)(part + q * stride);
+  for (int q = 1; q < splits; q += 4) {
+    floatx4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = *(const floatx4*)(part + min(q + u, splits - 1) * stride);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (q + u < splits) s += v[u];
+  }
   return s;
 }
 
 // ---------------------------------------------------------------------------
 // out[m][c] = bf16(base[m][c] + s[a] sum_j P[m][j] L[a][j][c]) (JMAJOR: L2 [n][r][N])
-// or with L[a][c][j] (L1 [n][N][r]).  A workgroup has 16 NM rows and 256 columns, 64 a
-// wave.  P (its splits joined) is split into hi and lo in LDS, 16 of the rank a step: the
-// MFMA's 32 products are hi's 16 and lo's, against the same 16 of L.  L is the first
-// operand with its columns so dealt that a lane ends with 16 neighbouring ones of a row.
+// or with L[a][c][j] (L1 [n][N][r]).  A workgroup has 16 RW rows and goes over `blocks`
+// blocks of 128 columns, the next block's base and L under way; RW = 1: each wave has a
+// block of its own.  P (its splits joined) is split into hi and lo in LDS, 16 of the rank
+// a step: the MFMA's 32 products are hi's 16 and lo's, against the same 16 of L.  P is the
+// first operand and column i of L's fragment f is 8 i + f, so a lane ends with 8
+// neighbouring columns of 4 rows, and 16 lanes read and write 256 bytes of a row.  For that
+// a panel of L stands in LDS with column 8 i + f at place 16 f + i.  A rank above 16 NJ is
+// taken in runs of 64.
 // ---------------------------------------------------------------------------
-template <bool JMAJOR, int NM, int RMAX>
+template <bool JMAJOR, int NJ, int RW, int RMAX>
 __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
-  constexpr int BM = 16 * NM;
-  constexpr int LROW = 64 * 2 + 16;  // LDS bytes of a rank row of L2: 64 columns
-  __shared__ __align__(16) uint8_t smem[BM * (RMAX * 4 + 16) + (JMAJOR ? 4 * 16 * LROW : 0)];
+  constexpr int BM = 16 * RW, RC = 16 * NJ;
+  constexpr int NB = RW == 4 ? 2 : 1, G = 4 / RW, TG = 64 * RW;  // panel buffers; groups of waves, their threads
+  constexpr int LROW = JMAJOR ? 128 * 2 + 32 : RC * 2 + 16;      // LDS bytes of a row of the panel
+  constexpr int PB = JMAJOR ? RC * LROW : 128 * LROW;
+  constexpr int PL = 128 * RC / 8 / TG;                          // 16-byte pieces of a panel a thread
+  constexpr int PROW = RMAX * 4 + 16;                            // of a row of P: for each 16 of the rank hi, then lo
+  __shared__ __align__(16) uint8_t ps[BM * PROW];
+  __shared__ __align__(16) uint8_t panel[G][NB][PB];
   Tile tile;
   if (!find_tile(p.rows, BM, blockIdx.x, tile)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, g = lane >> 4;
+  const int grp = wave / RW, tg = tid % TG;
   const int r = p.r, r16 = (r + 15) / 16 * 16;
   const int64_t N = p.N;
-  const int prow = r16 * 4 + 16;  // LDS bytes of a row of P: for each 16 of the rank hi, then lo
-  for (int e = threadIdx.x; e < BM * r16 / 4; e += 256) {
+  const int nblocks = (int)((N + 127) / 128);
+  const int cb0 = RW == 4 ? blockIdx.y * p.blocks : blockIdx.y * 4 + grp;
+  const int cb1 = RW == 4 ? min(cb0 + p.blocks, nblocks) : min(cb0 + 1, nblocks);
+  const int runs = (r16 + RC - 1) / RC;
+  const uint16_t* L = p.L + (int64_t)tile.a * N * r;
+  int64_t at[4];  // this lane's 4 rows, or -1
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int64_t row = row_at(p.rows, tile, tile.p0 + (RW == 4 ? 16 * wave : 0) + 4 * g + v);
+    at[v] = row < 0 ? -1 : row * N;
+  }
+  // base: of rows that are not there a valid one's
+  auto load_base = [&](int cb, u32x4 (&b)[4]) {
+    const int64_t c = min((int64_t)cb * 128 + 8 * li, N - 8);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) b[v] = *(const u32x4*)(p.base + max(at[v], (int64_t)0) + c);
+  };
+  // pieces of the panel: JMAJOR 16 a row of the rank, else RC / 8 a column
+  auto load_panel = [&](int cb, int run, u32x4 (&l)[PL]) {
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+      const int e = TG * i + tg;
+      const int j = run * RC + (JMAJOR ? e / 16 : 8 * (e % (RC / 8)));
+      const int64_t c = (int64_t)cb * 128 + (JMAJOR ? 8 * (e % 16) : e / (RC / 8));
+      const int64_t o = JMAJOR ? (int64_t)min(j, r - 1) * N + min(c, N - 8) : min(c, N - 1) * r + min(j, r - 8);
+      l[i] = *(const u32x4*)(L + o);
+      if (j >= r) l[i] = u32x4{0u, 0u, 0u, 0u};  // P's zeros there are multiplied by it
+    }
+  };
+  auto store_panel = [&](uint8_t* to, const u32x4 (&l)[PL]) {
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+      const int e = TG * i + tg;
+      if constexpr (JMAJOR) {
+        uint8_t* const at = to + e / 16 * LROW + 2 * (e % 16);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          *(uint16_t*)(at + 64 * k) = (uint16_t)l[i][k];
+          *(uint16_t*)(at + 64 * k + 32) = (uint16_t)(l[i][k] >> 16);
+        }
+      } else {
+        const int c = e / (RC / 8);
+        *(u32x4*)(to + ((c & 7) * 16 + (c >> 3)) * LROW + 16 * (e % (RC / 8))) = l[i];
+      }
+    }
+  };
+  u32x4 b[4], l[PL];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) b[v] = u32x4{0u, 0u, 0u, 0u};
+  if (cb0 < cb1) {
+    load_panel(cb0, 0, l);
+    if (p.base) load_base(cb0, b);
+  }
+  for (int e = tid; e < BM * r16 / 4; e += 256) {
     const int m = e / (r16 / 4), j = 4 * (e % (r16 / 4));
     const int64_t row = row_at(p.rows, tile, tile.p0 + m);
     floatx4 v = {0.f, 0.f, 0.f, 0.f};
@@ -231,143 +434,151 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
     }
     uint2 part[2];
     split4(v, part);
-    uint8_t* to = smem + m * prow + (j / 16) * 64 + (j % 16) * 2;
+    uint8_t* to = ps + m * PROW + (j / 16) * 64 + (j % 16) * 2;
     *(uint2*)to = part[0];
     *(uint2*)(to + 32) = part[1];
   }
+  if (cb0 < cb1) store_panel(panel[grp][0], l);
   __syncthreads();
-  const int64_t c0 = (int64_t)blockIdx.y * 256 + 64 * wave;
-  if (c0 >= N) return;
-  uint8_t* stage = smem + BM * prow + wave * 16 * LROW;
-  const int64_t c = c0 + 16 * g;  // this lane's 16 columns of the result
-  int64_t at[NM];
-  u32x4 b[NM][2];
-#pragma unroll
-  for (int i = 0; i < NM; ++i) {
-    const int64_t row = row_at(p.rows, tile, tile.p0 + 16 * i + li);
-    at[i] = row < 0 || c >= N ? -1 : row * N + c;
-    b[i][0] = b[i][1] = u32x4{0u, 0u, 0u, 0u};
-    if (p.base && at[i] >= 0) {
-      b[i][0] = *(const u32x4*)(p.base + at[i]);
-      b[i][1] = *(const u32x4*)(p.base + at[i] + 8);
-    }
-  }
-  const uint16_t* L = p.L + (int64_t)tile.a * N * r;
-  floatx4 acc[4][NM];
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-#pragma unroll
-    for (int i = 0; i < NM; ++i) acc[q][i] = floatx4{0.f, 0.f, 0.f, 0.f};
-  for (int j0 = 0; j0 < r16; j0 += 16) {
-    bf16x8 f[4];
-    if constexpr (JMAJOR) {
-      u32x4 v[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int j = j0 + 8 * i + lane / 8;
-        const int64_t cc = c0 + 8 * (lane % 8);
-        v[i] = j < r && cc < N ? *(const u32x4*)(L + j * N + cc) : u32x4{0u, 0u, 0u, 0u};
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) *(u32x4*)(stage + (8 * i + lane / 8) * LROW + 16 * (lane % 8)) = v[i];
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        f[q] = lds_tr8(stage + (8 * (g & 1) + (li >> 2)) * LROW + 2 * (16 * (li & 3) + 4 * q), LROW);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t cc = min(c0 + 16 * (li >> 2) + 4 * q + (li & 3), N - 1);
-        const int j = j0 + 8 * (g & 1);
-        f[q] = __builtin_bit_cast(bf16x8, j < r ? *(const u32x4*)(L + cc * r + j) : u32x4{0u, 0u, 0u, 0u});
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NM; ++i) {
-      const bf16x8 t = *(const bf16x8*)(smem + (16 * i + li) * prow + (j0 / 16) * 64 + (g >> 1) * 32 + (g & 1) * 16);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) acc[q][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[q], t, acc[q][i], 0, 0, 0);
-    }
-  }
   const float s = p.s[tile.a];
+  const uint8_t* pa = ps + (RW == 4 ? 16 * wave + li : li) * PROW + (g >> 1) * 32 + (g & 1) * 16;
+  floatx4 acc[8];
 #pragma unroll
-  for (int i = 0; i < NM; ++i) {
-    if (at[i] < 0) continue;
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      u32x4 o;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {  // columns 8 hf + 2 w and the next, from acc[2 hf + w / 2]
-        const floatx4 v = acc[2 * hf + w / 2][i];
-        const float lo = __builtin_fmaf(s, v[2 * (w & 1)], __builtin_bit_cast(float, b[i][hf][w] << 16));
-        const float up = __builtin_fmaf(s, v[2 * (w & 1) + 1], __builtin_bit_cast(float, b[i][hf][w] & 0xFFFF0000u));
-        o[w] = pack_bf16x2(lo, up);
-      }
-      *(u32x4*)(p.out + at[i] + 8 * hf) = o;
+  for (int f = 0; f < 8; ++f) acc[f] = floatx4{0.f, 0.f, 0.f, 0.f};
+  // RW = 1: every wave goes through the same barriers, one past the columns' end idly
+  const int total = RW == 4 ? (cb1 - cb0) * runs : runs;
+  int cb = cb0, run = 0;
+  for (int t = 0; t < total; ++t) {
+    int ncb = cb, nrun = run + 1;
+    if (nrun == runs) {
+      nrun = 0;
+      ++ncb;
     }
+    const bool more = t + 1 < total && ncb < cb1, last = nrun == 0;
+    u32x4 nb[4];
+    if (more) {
+      load_panel(ncb, nrun, l);
+      if (last && p.base) load_base(ncb, nb);
+    }
+    uint8_t* const lp = panel[grp][NB == 2 ? t & 1 : 0];
+#pragma unroll
+    for (int st = 0; st < NJ; ++st) {
+      const bf16x8 a = *(const bf16x8*)(pa + (run * NJ + st) * 64);
+      const bool some = run * RC + 16 * st < r16;  // the same for all; P's places past r16 hold nothing
+      if (some) {
+#pragma unroll
+        for (int f = 0; f < 8; ++f) {
+          bf16x8 w;
+          if constexpr (JMAJOR)
+            w = lds_tr8(lp + (16 * st + 8 * (g & 1) + (li >> 2)) * LROW + 2 * (16 * f + 4 * (li & 3)), LROW);
+          else w = *(const bf16x8*)(lp + (16 * f + li) * LROW + 2 * (16 * st + 8 * (g & 1)));
+          acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w, acc[f], 0, 0, 0);
+        }
+      }
+    }
+    if (last) {
+      const int64_t c = (int64_t)cb * 128 + 8 * li;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        u32x4 o;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          o[k] = pack_bf16x2(__builtin_fmaf(s, acc[2 * k][v], __builtin_bit_cast(float, b[v][k] << 16)),
+                             __builtin_fmaf(s, acc[2 * k + 1][v], __builtin_bit_cast(float, b[v][k] & 0xFFFF0000u)));
+        if (at[v] >= 0 && c < N && cb < cb1) *(u32x4*)(p.out + at[v] + c) = o;
+      }
+#pragma unroll
+      for (int f = 0; f < 8; ++f) acc[f] = floatx4{0.f, 0.f, 0.f, 0.f};
+      if (more && p.base) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) b[v] = nb[v];
+      }
+    }
+    if (NB == 1 && t + 1 < total) __syncthreads();  // the panel's reads are done
+    if (more) store_panel(panel[grp][NB == 2 ? (t + 1) & 1 : 0], l);
+    if (t + 1 < total) __syncthreads();
+    cb = ncb;
+    run = nrun;
   }
 }
 
 // ---------------------------------------------------------------------------
 // dL[a][j][c] (or [c][j]) = s[a] sum over a's rows of P[m][j] Q[m][c]: a workgroup has
 // 128 columns of Q, 16 NJ of the rank (blockIdx.z: which 64) and up to p.item rows of an
-// adapter, 64 at a time through LDS, the next 64 under way in registers.  Rows past the
+// adapter, 64 at a time through LDS, two such steps under way in registers.  Rows past the
 // tile are zero in both.  An adapter whose rows are all here is written out, otherwise the
 // item's sums go to a part of their own, which k_adapters_join adds in order.  Q in 8 bits
 // (X8 1: e4m3, 2: e5m2) becomes bf16 on its way into LDS, and P is multiplied by the scale
 // of its row and this block of 128 columns.
 // ---------------------------------------------------------------------------
 template <int X8, int NJ>
-__device__ __forceinline__ void grad_tile(const AdapterRows& rows, const AdapterGrad& p, uint8_t* smem) {
+__device__ __forceinline__ void grad_tile(const AdapterRows& rows, const AdapterGrad& p, int cb, uint8_t* smem) {
   constexpr int KR = 64, RP = 16 * NJ;
-  constexpr int QROW = 128 * 2 + 16, PROW = RP * 2 + 16;
+  // 8 banks between neighbouring rows: the 4 rows of a transposing read fall on different ones
+  constexpr int QROW = 128 * 2 + 32, PROW = RP * 2 + 16;
   constexpr int JW = NJ == 4 ? 2 : 1, CW = 4 / JW;      // waves over the rank and over the columns
   constexpr int FJ = NJ / JW, FC = 8 / CW;              // a wave's fragments
   constexpr int QL = X8 ? 2 : 4;                        // 16-byte loads of Q a thread
-  constexpr int PL = (KR * RP / 4 + 255) / 256;         // 4-value pieces of P a thread
+  constexpr int PL = KR * RP / 4 / 256;                 // 4-value pieces of P a thread
+  constexpr int CP = X8 ? 8 : 16;                       // pieces of a row of Q
   uint8_t* qs = smem;
   uint8_t* ps = smem + KR * QROW;  // [3][KR] rows
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, g = lane >> 4;
   Tile tile;
   if (!find_tile(rows, p.item, blockIdx.x, tile)) return;
-  const int64_t N = p.N, c0 = (int64_t)blockIdx.y * 128;
+  const int64_t N = p.N, c0 = (int64_t)cb * 128;
   const int r = p.r, j0 = blockIdx.z * 64;
   const int64_t kb = (N + 127) / 128;
-  u32x4 q[QL];
-  floatx4 v[PL];
-  constexpr int CP = X8 ? 8 : 16;  // pieces of a row
-  auto load = [&](int p0) {
+  struct Stage {
+    u32x4 q[QL];
+    floatx4 v[PL];
+    float scale[PL];
+    uint32_t ok;  // which of the rows are there
+  };
+  // the rows of a step, one a lane; loaded a step before they are used
+  auto load_order = [&](int p0) -> int { return rows.order[min(p0 + lane, tile.p1 - 1)]; };
+  auto row_of = [&](int ord, int p0, int m, bool& ok) -> int64_t {
+    int row = p0 + m;
+    if (rows.order) row = __shfl(ord, m);
+    ok = p0 + m < tile.p1 && (uint64_t)(int64_t)row < (uint64_t)rows.M;
+    return ok ? row : 0;
+  };
+  auto load = [&](int p0, int ord, Stage& s) {
+    s.ok = 0;
 #pragma unroll
     for (int i = 0; i < QL; ++i) {
       const int e = 256 * i + tid;
-      const int64_t row = row_at(rows, tile, p0 + e / CP);
+      bool ok;
+      const int64_t row = row_of(ord, p0, e / CP, ok);
       const int64_t c = c0 + (e % CP) * (128 / CP);
-      q[i] = u32x4{0u, 0u, 0u, 0u};
-      if (row >= 0 && c < N) q[i] = *(const u32x4*)((const uint8_t*)p.Q + (row * N + c) * (X8 ? 1 : 2));
+      s.q[i] = *(const u32x4*)((const uint8_t*)p.Q + (row * N + (c < N ? c : 0)) * (X8 ? 1 : 2));
+      s.ok |= ok ? 1u << i : 0;
     }
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-      const int e = 256 * i + tid, m = e / (RP / 4), j = j0 + 4 * (e % (RP / 4));
-      v[i] = floatx4{0.f, 0.f, 0.f, 0.f};
-      if (m >= KR) continue;
-      const int64_t row = row_at(rows, tile, p0 + m);
-      if (row < 0 || j >= r) continue;
-      v[i] = join4(p.P + row * r + j, rows.M * r, p.splits);
-      if (X8) v[i] *= p.q_scales[row * kb + blockIdx.y];
+      const int e = 256 * i + tid, j = j0 + 4 * (e % (RP / 4));
+      bool ok;
+      const int64_t row = row_of(ord, p0, e / (RP / 4), ok);
+      s.v[i] = *(const floatx4*)(p.P + row * r + (j < r ? j : 0));
+      if constexpr (X8 != 0) s.scale[i] = p.q_scales[row * kb + cb];
+      s.ok |= ok && j < r ? 256u << i : 0;
     }
   };
-  auto store = [&]() {
+  auto store = [&](Stage& s) {
 #pragma unroll
     for (int i = 0; i < QL; ++i) {
       const int e = 256 * i + tid;
       uint8_t* to = qs + (e / CP) * QROW + (e % CP) * (256 / CP);
+      u32x4 v = s.q[i];
+      if (!(s.ok >> i & 1)) v = u32x4{0u, 0u, 0u, 0u};
       if constexpr (X8 == 0) {
-        *(u32x4*)to = q[i];
+        *(u32x4*)to = v;
       } else {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           float a[4], b[4];
-          unpack_fp8x4<X8 == 2>(q[i][2 * hf], a);
-          unpack_fp8x4<X8 == 2>(q[i][2 * hf + 1], b);
+          unpack_fp8x4<X8 == 2>(v[2 * hf], a);
+          unpack_fp8x4<X8 == 2>(v[2 * hf + 1], b);
           *(u32x4*)(to + 16 * hf) = u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]),
                                           pack_bf16x2(b[2], b[3])};
         }
@@ -376,9 +587,11 @@ __device__ __forceinline__ void grad_tile(const AdapterRows& rows, const Adapter
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
       const int e = 256 * i + tid, m = e / (RP / 4), j = 4 * (e % (RP / 4));
-      if (m >= KR) continue;
+      floatx4 v = s.v[i];
+      if constexpr (X8 != 0) v *= s.scale[i];
+      if (!(s.ok >> (8 + i) & 1)) v = floatx4{0.f, 0.f, 0.f, 0.f};
       uint2 part[3];
-      split4(v[i], part);
+      split4(v, part);
 #pragma unroll
       for (int w = 0; w < 3; ++w) *(uint2*)(ps + (w * KR + m) * PROW + 2 * j) = part[w];
     }
@@ -389,12 +602,7 @@ __device__ __forceinline__ void grad_tile(const AdapterRows& rows, const Adapter
   for (int j = 0; j < FJ; ++j)
 #pragma unroll
     for (int c = 0; c < FC; ++c) acc[j][c] = floatx4{0.f, 0.f, 0.f, 0.f};
-  load(tile.p0);
-  for (int p0 = tile.p0; p0 < tile.p1; p0 += KR) {
-    __syncthreads();
-    store();
-    if (p0 + KR < tile.p1) load(p0 + KR);
-    __syncthreads();
+  auto compute = [&]() {
 #pragma unroll
     for (int k = 0; k < KR; k += 32) {
       const int tr = k + 8 * g + (li >> 2), tc = 4 * (li & 3);
@@ -414,6 +622,30 @@ __device__ __forceinline__ void grad_tile(const AdapterRows& rows, const Adapter
             acc[j][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp[j][w], fq, acc[j][c], 0, 0, 0);
       }
     }
+  };
+  Stage sa, sb;
+  int oa = 0, ob = 0;
+  if (rows.order) {
+    oa = load_order(tile.p0);
+    ob = load_order(tile.p0 + KR);
+  }
+  load(tile.p0, oa, sa);
+  load(tile.p0 + KR, ob, sb);
+  if (rows.order) {
+    oa = load_order(tile.p0 + 2 * KR);
+    ob = load_order(tile.p0 + 3 * KR);
+  }
+  auto step = [&](int p0, Stage& s, int& ord) {
+    __syncthreads();  // the reads of the step before are done
+    store(s);
+    load(p0 + 2 * KR, ord, s);
+    if (rows.order) ord = load_order(p0 + 4 * KR);
+    __syncthreads();
+    compute();
+  };
+  for (int p0 = tile.p0; p0 < tile.p1; p0 += 2 * KR) {
+    step(p0, sa, oa);
+    if (p0 + KR < tile.p1) step(p0 + KR, sb, ob);
   }
   const float s = tile.whole ? p.s[tile.a] : 1.f;
   float* out = tile.whole ? p.out + (int64_t)tile.a * r * N : p.part + (int64_t)blockIdx.x * r * N;
@@ -434,11 +666,14 @@ __device__ __forceinline__ void grad_tile(const AdapterRows& rows, const Adapter
     }
 }
 
+// Both gradients in one launch: dL1's blocks of columns, then dL2's.
 template <int X8, int NJ>
-__global__ __launch_bounds__(256) void k_adapters_grad(AdapterRows rows, AdapterGrad p) {
-  constexpr int SMEM = 64 * (128 * 2 + 16) + 3 * 64 * (16 * NJ * 2 + 16);
+__global__ __launch_bounds__(256) void k_adapters_grad(AdapterRows rows, AdapterGrad p1, AdapterGrad p2) {
+  constexpr int SMEM = 64 * (128 * 2 + 32) + 3 * 64 * (16 * NJ * 2 + 16);
   __shared__ __align__(16) uint8_t smem[SMEM];
-  grad_tile<X8, NJ>(rows, p, smem);
+  const int n1 = (int)((p1.N + 127) / 128), cb = blockIdx.y;
+  if (cb < n1) grad_tile<X8, NJ>(rows, p1, cb, smem);
+  else grad_tile<0, NJ>(rows, p2, cb - n1, smem);
 }
 
 // Outputs of adapters with several items: their parts' sums in order; with none: zeros.
@@ -475,11 +710,11 @@ __global__ __launch_bounds__(256) void k_adapters_join(AdapterRows rows, Adapter
   }
 }
 
-template <bool KMAJOR, int NM>
-hipError_t narrow_of(const AdapterNarrow& p, dim3 gr, hipStream_t st) {
-  if (p.r <= 16) hipLaunchKernelGGL((k_adapters_narrow<KMAJOR, 1, NM>), gr, dim3(256), 0, st, p);
-  else if (p.r <= 32) hipLaunchKernelGGL((k_adapters_narrow<KMAJOR, 2, NM>), gr, dim3(256), 0, st, p);
-  else hipLaunchKernelGGL((k_adapters_narrow<KMAJOR, 4, NM>), gr, dim3(256), 0, st, p);
+template <bool KMAJOR, int NJ>
+hipError_t narrow_of(const AdapterNarrow& p, int bm, dim3 gr, hipStream_t st) {
+  if (bm == 16) hipLaunchKernelGGL((k_adapters_narrow_few<KMAJOR, NJ>), gr, dim3(256), 0, st, p);
+  else if (bm == 64) hipLaunchKernelGGL((k_adapters_narrow<KMAJOR, NJ, 1>), gr, dim3(256), 0, st, p);
+  else hipLaunchKernelGGL((k_adapters_narrow<KMAJOR, NJ, 2>), gr, dim3(256), 0, st, p);
   return hipGetLastError();
 }
 
@@ -487,31 +722,49 @@ hipError_t narrow(const AdapterCall& c, const AdapterPlan& pl, const uint16_t* A
                   bool kmajor, float* part, hipStream_t st) {
   AdapterNarrow p{c.rows, A, L, K, c.r, pl.krange, part};
   const dim3 gr((unsigned)pl.tiles, (unsigned)pl.splits, (unsigned)((c.r + 63) / 64));
-  if (pl.bm == 16) return kmajor ? narrow_of<true, 1>(p, gr, st) : narrow_of<false, 1>(p, gr, st);
-  return kmajor ? narrow_of<true, 4>(p, gr, st) : narrow_of<false, 4>(p, gr, st);
+  if (kmajor)
+    return c.r <= 16   ? narrow_of<true, 1>(p, pl.bm, gr, st)
+           : c.r <= 32 ? narrow_of<true, 2>(p, pl.bm, gr, st)
+                       : narrow_of<true, 4>(p, pl.bm, gr, st);
+  return c.r <= 16   ? narrow_of<false, 1>(p, pl.bm, gr, st)
+         : c.r <= 32 ? narrow_of<false, 2>(p, pl.bm, gr, st)
+                     : narrow_of<false, 4>(p, pl.bm, gr, st);
 }
 
-template <bool JMAJOR, int NM>
+template <bool JMAJOR, int RW>
 hipError_t wide_of(const AdapterWide& p, dim3 gr, hipStream_t st) {
-  if (p.r <= 64) hipLaunchKernelGGL((k_adapters_wide<JMAJOR, NM, 64>), gr, dim3(256), 0, st, p);
-  else hipLaunchKernelGGL((k_adapters_wide<JMAJOR, NM, 256>), gr, dim3(256), 0, st, p);
+  if (p.r <= 16) hipLaunchKernelGGL((k_adapters_wide<JMAJOR, 1, RW, 16>), gr, dim3(256), 0, st, p);
+  else if (p.r <= 32) hipLaunchKernelGGL((k_adapters_wide<JMAJOR, 2, RW, 32>), gr, dim3(256), 0, st, p);
+  else if (p.r <= 64) hipLaunchKernelGGL((k_adapters_wide<JMAJOR, 4, RW, 64>), gr, dim3(256), 0, st, p);
+  else hipLaunchKernelGGL((k_adapters_wide<JMAJOR, 4, RW, 256>), gr, dim3(256), 0, st, p);
   return hipGetLastError();
 }
 
 hipError_t wide(const AdapterCall& c, const AdapterPlan& pl, const float* part, const uint16_t* L, bool jmajor,
                 int64_t N, const uint16_t* base, uint16_t* out, float* T_out, hipStream_t st) {
-  AdapterWide p{c.rows, part, pl.splits, L, N, c.r, c.s, base, out, T_out};
-  const dim3 gr((unsigned)pl.tiles, (unsigned)((N + 255) / 256));
-  if (pl.bm == 16) return jmajor ? wide_of<true, 1>(p, gr, st) : wide_of<false, 1>(p, gr, st);
+  const bool few = pl.bm == 16;
+  int64_t tiles;
+  const int blocks = plan_adapters_wide(c.rows.M, c.rows.n, few, N, &tiles);
+  AdapterWide p{c.rows, part, pl.splits, L, N, c.r, c.s, base, out, T_out, blocks};
+  const int64_t nb = (N + 127) / 128;
+  const dim3 gr((unsigned)tiles, (unsigned)(few ? (nb + 3) / 4 : (nb + blocks - 1) / blocks));
+  if (few) return jmajor ? wide_of<true, 1>(p, gr, st) : wide_of<false, 1>(p, gr, st);
   return jmajor ? wide_of<true, 4>(p, gr, st) : wide_of<false, 4>(p, gr, st);
 }
 
+// out [M][r] of the listed rows = the splits' sum
+__global__ __launch_bounds__(256) void k_adapters_sum(const float* __restrict__ part, int64_t size, int splits,
+                                                      float* __restrict__ out) {
+  const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (e < size) *(floatx4*)(out + e) = join4(part + e, size, splits);
+}
+
 template <int X8>
-hipError_t grad_of(const AdapterRows& rows, const AdapterGrad& p, hipStream_t st) {
-  const dim3 gr((unsigned)p.items, (unsigned)((p.N + 127) / 128), (unsigned)((p.r + 63) / 64));
-  if (p.r <= 16) hipLaunchKernelGGL((k_adapters_grad<X8, 1>), gr, dim3(256), 0, st, rows, p);
-  else if (p.r <= 32) hipLaunchKernelGGL((k_adapters_grad<X8, 2>), gr, dim3(256), 0, st, rows, p);
-  else hipLaunchKernelGGL((k_adapters_grad<X8, 4>), gr, dim3(256), 0, st, rows, p);
+hipError_t grad_of(const AdapterRows& rows, const AdapterGrad& p1, const AdapterGrad& p2, hipStream_t st) {
+  const dim3 gr((unsigned)p1.items, (unsigned)((p1.N + 127) / 128 + (p2.N + 127) / 128), (unsigned)((p1.r + 63) / 64));
+  if (p1.r <= 16) hipLaunchKernelGGL((k_adapters_grad<X8, 1>), gr, dim3(256), 0, st, rows, p1, p2);
+  else if (p1.r <= 32) hipLaunchKernelGGL((k_adapters_grad<X8, 2>), gr, dim3(256), 0, st, rows, p1, p2);
+  else hipLaunchKernelGGL((k_adapters_grad<X8, 4>), gr, dim3(256), 0, st, rows, p1, p2);
   return hipGetLastError();
 }
 
@@ -530,22 +783,31 @@ hipError_t launch_adapters_bwd(const AdapterCall& c, const void* X, int x8, cons
                                hipStream_t st) {
   const AdapterPlan pl = plan_adapters_rows(c.rows.M, c.rows.n, c.o);
   const AdapterItems it = plan_adapters_items(c.rows.M, c.rows.n, c.h, c.o, c.r);
-  float* G = (float*)ws;
-  float* parts = G + pl.splits * c.rows.M * c.r;
-  hipError_t e = narrow(c, pl, dY, c.o, c.L2, false, G, st);
+  const int64_t size = c.rows.M * c.r;
+  float* gparts = (float*)ws;
+  float* G = pl.splits > 1 ? gparts + pl.splits * size : gparts;
+  float* parts = G + size;
+  hipError_t e = narrow(c, pl, dY, c.o, c.L2, false, gparts, st);
   if (e != hipSuccess) return e;
-  const AdapterGrad g1{X, x_scales, c.h, G, pl.splits, c.r, c.s, it.item, it.items, 1, parts, dL1};
-  const AdapterGrad g2{dY, nullptr, c.o, T, 1, c.r, c.s, it.item, it.items, 0, parts + it.items * c.r * c.h, dL2};
-  e = x8 == 0 ? grad_of<0>(c.rows, g1, st) : x8 == 1 ? grad_of<1>(c.rows, g1, st) : grad_of<2>(c.rows, g1, st);
+  // dX's kernel joins G's splits and leaves their sum
+  if (dX) {
+    e = wide(c, pl, gparts, c.L1, false, c.h, base, dX, pl.splits > 1 ? G : nullptr, st);
+  } else if (pl.splits > 1) {
+    hipLaunchKernelGGL(k_adapters_sum, dim3((unsigned)((size + 1023) / 1024)), dim3(256), 0, st, gparts, size,
+                       pl.splits, G);
+    e = hipGetLastError();
+  }
   if (e != hipSuccess) return e;
-  e = grad_of<0>(c.rows, g2, st);
+  const AdapterGrad g1{X, x_scales, c.h, G, c.r, c.s, it.item, it.items, 1, parts, dL1};
+  const AdapterGrad g2{dY, nullptr, c.o, T, c.r, c.s, it.item, it.items, 0, parts + it.items * c.r * c.h, dL2};
+  e = x8 == 0   ? grad_of<0>(c.rows, g1, g2, st)
+      : x8 == 1 ? grad_of<1>(c.rows, g1, g2, st)
+                : grad_of<2>(c.rows, g1, g2, st);
   if (e != hipSuccess) return e;
   const int64_t most = std::max(c.h, c.o) * c.r;
   const dim3 gr((unsigned)std::min<int64_t>((most + 1023) / 1024, 1024), (unsigned)c.rows.n, 2);
   hipLaunchKernelGGL(k_adapters_join, gr, dim3(256), 0, st, c.rows, g1, g2);
-  e = hipGetLastError();
-  if (e != hipSuccess || !dX) return e;
-  return wide(c, pl, G, c.L1, false, c.h, base, dX, nullptr, st);
+  return hipGetLastError();
 }
 
 }  // namespace nf4k

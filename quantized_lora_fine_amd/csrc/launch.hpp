@@ -233,13 +233,14 @@ struct AdapterWide {
   const uint16_t* base;  // or NULL
   uint16_t* out;
   float* T_out;  // the joined parts, or NULL
+  int blocks;    // blocks of 128 columns a workgroup goes over
 };
 struct AdapterGrad {
   const void* Q;          // [M][N], bf16 or codes
   const float* q_scales;  // of codes
   int64_t N;
-  const float* P;  // [splits][M][r]
-  int splits, r;
+  const float* P;  // [M][r]
+  int r;
   const float* s;
   int item;       // rows an item, a multiple of 64
   int64_t items;  // at most
@@ -250,12 +251,14 @@ struct AdapterGrad {
 constexpr int64_t kMaxAdapterRows = (int64_t)1 << 26;  // tiles of 16 rows stay one launch
 // Tiles of rows of the products of one row, and the splits of a contraction over K.
 struct AdapterPlan {
-  int bm;         // rows a tile: 16 or 64
+  int bm;         // rows a tile: 16, 64 or 128
   int64_t tiles;  // at most
   int splits;
   int64_t krange;
 };
 AdapterPlan plan_adapters_rows(int64_t M, int n, int64_t K);
+// Blocks of 128 columns a workgroup of the products over the rank, and its tiles of 64 rows (few: 16).
+int plan_adapters_wide(int64_t M, int n, bool few, int64_t N, int64_t* tiles);
 // Rows of an item of the adapters' gradients, and the items there are at most.
 struct AdapterItems {
   int item;

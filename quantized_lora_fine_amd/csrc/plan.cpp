@@ -115,25 +115,39 @@ int64_t route_counts(int64_t M, int n) {
   return plan_route(M, n, &runs, &run) ? 0 : ((int64_t)n + 1) * (runs + 1);
 }
 
-// Tiles of 16 rows where an adapter has few in the mean, else of 64.  About 1024
-// workgroups, each with 256 of the contraction or more: 4 waves with 2 steps of 32.
+// Tiles of `bm` rows there are at most: adapters' last tiles may be partly filled.
+static int64_t adapter_tiles(int64_t M, int n, int bm) {
+  return std::min<int64_t>(M, M / bm + std::min<int64_t>(M, n));
+}
+
+// Tiles of 16 rows where an adapter has few in the mean, else of 64, or of 128 where there
+// are enough of them.  About 512 workgroups, each with 256 of the contraction or more.
 AdapterPlan plan_adapters_rows(int64_t M, int n, int64_t K) {
   AdapterPlan p;
   const int64_t used = std::min<int64_t>(M, n);
-  p.bm = M <= 16 * used ? 16 : 64;
-  p.tiles = std::min<int64_t>(M, M / p.bm + used);
+  p.bm = M <= 16 * used ? 16 : M <= 256 * used ? 64 : 128;
+  p.tiles = adapter_tiles(M, n, p.bm);
   const int64_t most = std::max<int64_t>(1, (K + 255) / 256);
-  const int64_t want = std::min(most, (1024 + p.tiles - 1) / std::max<int64_t>(p.tiles, 1));
+  const int64_t want = std::min(most, (512 + p.tiles - 1) / std::max<int64_t>(p.tiles, 1));
   p.krange = ((K + want - 1) / want + 255) / 256 * 256;
   p.splits = (int)((K + p.krange - 1) / p.krange);
   return p;
+}
+
+int plan_adapters_wide(int64_t M, int n, bool few, int64_t N, int64_t* tiles) {
+  *tiles = adapter_tiles(M, n, few ? 16 : 64);
+  const int64_t blocks = (N + 127) / 128;
+  if (few) return 1;
+  // about 1024 workgroups
+  const int64_t each = *tiles * blocks / 1024;
+  return (int)std::max<int64_t>(1, std::min(each, blocks));
 }
 
 AdapterItems plan_adapters_items(int64_t M, int n, int64_t h, int64_t o, int r) {
   AdapterItems p;
   const int64_t tiles = ((h + 127) / 128 + (o + 127) / 128) * ((r + 63) / 64);
   const int64_t used = std::min<int64_t>(M, n);
-  const int64_t rows = std::max<int64_t>(128, M * tiles / 1024);
+  const int64_t rows = std::max<int64_t>(128, M * tiles / 640);
   p.item = (int)((std::min<int64_t>(rows, std::max<int64_t>(M, 64)) + 63) / 64 * 64);
   p.items = std::min<int64_t>(M, M / p.item + used);
   return p;
