@@ -97,6 +97,26 @@ __device__ __forceinline__ void split4(floatx4 x, uint2 (&part)[W]) {
   }
 }
 
+// A row of P as the products over rows take it: [nz][3][rp] bf16, the three parts of 64
+// columns of the rank (rp of them where there are fewer) after one another.
+__device__ __forceinline__ void store3(const Split3& o, int64_t row, int j, const uint2 (&part)[3]) {
+  uint16_t* const to = o.to + ((row * o.nz + j / 64) * 3) * o.rp + j % 64;
+#pragma unroll
+  for (int w = 0; w < 3; ++w) *(uint2*)(to + w * o.rp) = part[w];
+}
+
+// Rows 64 `block` and on of T in that form, and (block 0) zeros for rows that are not there.
+__device__ __forceinline__ void split_rows(const Split3& o, int64_t block, int64_t M, int r) {
+  if (block == 0 && threadIdx.x < kZeroBytes / 16) ((u32x4*)o.zero)[threadIdx.x] = u32x4{0u, 0u, 0u, 0u};
+  const int64_t e1 = min(64 * (block + 1), M) * r / 4;
+  for (int64_t e = 16 * block * r + threadIdx.x; e < e1; e += 256) {
+    const int64_t row = e / (r / 4);
+    uint2 part[3];
+    split4(*(const floatx4*)(o.from + 4 * e), part);
+    store3(o, row, (int)(4 * (e - row * (r / 4))), part);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // part[split][m][j] = sum over the split's k of A[m][k] L[a][k][j] (KMAJOR: L1
 // [n][K][r]) or A[m][k] L[a][j][k] (L2 [n][r][K]), for tiles of 16 rows.  A workgroup has
@@ -105,6 +125,7 @@ __device__ __forceinline__ void split4(floatx4 x, uint2 (&part)[W]) {
 // added in LDS in wave order.  A's rows are the MFMA's second operand, so a lane ends with
 // 4 neighbouring columns of one row; a row or column past the end repeats a valid one and
 // is not written.  L1 goes through LDS for transposing reads, each wave's own part.
+// Workgroups past the tiles split T for the products over rows (in a backward pass).
 // ---------------------------------------------------------------------------
 template <bool KMAJOR, int NJ>
 __global__ __launch_bounds__(256) void k_adapters_narrow_few(AdapterNarrow p) {
@@ -114,6 +135,10 @@ __global__ __launch_bounds__(256) void k_adapters_narrow_few(AdapterNarrow p) {
   constexpr int STAGE = KMAJOR ? 32 * ROW * kAhead : 0;                 // a wave's
   constexpr int SMEM = 4 * STAGE > 4 * BM * RP * 4 ? 4 * STAGE : 4 * BM * RP * 4;
   __shared__ __align__(16) uint8_t smem[SMEM];
+  if (blockIdx.x >= p.tiles) {
+    if (blockIdx.y == 0 && blockIdx.z == 0) split_rows(p.split, blockIdx.x - p.tiles, p.rows.M, p.r);
+    return;
+  }
   Tile tile;
   if (!find_tile(p.rows, BM, blockIdx.x, tile)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, g = lane >> 4;
@@ -210,6 +235,157 @@ constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (0x7 << 4) |
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 typedef __attribute__((address_space(1))) const void* global_ptr_t;
 
+// Reads of a buffer of LDS while copies are on their way into others: the compiler cannot
+// tell a transposing read from the copies' destinations and would wait for all copies
+// before each.  The reads and their wait are one block of assembly.  Transposing reads make
+// fragments of 8 rows (k) of a column, as lds_tr8: `at` is the byte address of the lane's 4
+// columns in row 8 g + e, ROW the bytes of a row.
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t lds_at(const uint8_t* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)p;
+}
+__device__ __forceinline__ bf16x8 halves(u32x2 a, u32x2 b) {
+  return __builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]});
+}
+template <int ROW>
+__device__ __forceinline__ void tr_read2(const uint32_t (&at)[2], bf16x8 (&f)[2]) {
+  u32x2 v[4];
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %4\n"
+      "ds_read_b64_tr_b16 %1, %4 offset:%6\n"
+      "ds_read_b64_tr_b16 %2, %5\n"
+      "ds_read_b64_tr_b16 %3, %5 offset:%6\n"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+      : "v"(at[0]), "v"(at[1]), "n"(4 * ROW));
+  f[0] = halves(v[0], v[1]);
+  f[1] = halves(v[2], v[3]);
+}
+template <int ROW>
+__device__ __forceinline__ void tr_read4(const uint32_t (&at)[4], bf16x8 (&f)[4]) {
+  u32x2 v[8];
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %8\n"
+      "ds_read_b64_tr_b16 %1, %8 offset:%12\n"
+      "ds_read_b64_tr_b16 %2, %9\n"
+      "ds_read_b64_tr_b16 %3, %9 offset:%12\n"
+      "ds_read_b64_tr_b16 %4, %10\n"
+      "ds_read_b64_tr_b16 %5, %10 offset:%12\n"
+      "ds_read_b64_tr_b16 %6, %11\n"
+      "ds_read_b64_tr_b16 %7, %11 offset:%12\n"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7])
+      : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(4 * ROW));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = halves(v[2 * i], v[2 * i + 1]);
+}
+// fragments that lie as they are read, 2048 bytes (16 rows of 128) apart
+template <int N>
+__device__ __forceinline__ void b128_read(uint32_t at, bf16x8 (&f)[N]) {
+  u32x4 v[N];
+  if constexpr (N == 1) {
+    asm volatile("ds_read_b128 %0, %1\n"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(v[0])
+                 : "v"(at));
+  } else if constexpr (N == 2) {
+    asm volatile("ds_read_b128 %0, %2\n"
+                 "ds_read_b128 %1, %2 offset:2048\n"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(v[0]), "=&v"(v[1])
+                 : "v"(at));
+  } else {
+    static_assert(N == 4, "1, 2 or 4 fragments");
+    asm volatile("ds_read_b128 %0, %4\n"
+                 "ds_read_b128 %1, %4 offset:2048\n"
+                 "ds_read_b128 %2, %4 offset:4096\n"
+                 "ds_read_b128 %3, %4 offset:6144\n"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+                 : "v"(at));
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = __builtin_bit_cast(bf16x8, v[i]);
+}
+// the same by transposing reads, with an address for each half
+template <int N>
+__device__ __forceinline__ void tr_read_rows(const uint32_t (&at)[2 * N], bf16x8 (&f)[N]) {
+  u32x2 v[2 * N];
+  if constexpr (N == 1) {
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %2\n"
+        "ds_read_b64_tr_b16 %1, %3\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1])
+        : "v"(at[0]), "v"(at[1]));
+  } else if constexpr (N == 2) {
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %4\n"
+        "ds_read_b64_tr_b16 %1, %5\n"
+        "ds_read_b64_tr_b16 %2, %6\n"
+        "ds_read_b64_tr_b16 %3, %7\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+        : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]));
+  } else {
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %8\n"
+        "ds_read_b64_tr_b16 %1, %9\n"
+        "ds_read_b64_tr_b16 %2, %10\n"
+        "ds_read_b64_tr_b16 %3, %11\n"
+        "ds_read_b64_tr_b16 %4, %12\n"
+        "ds_read_b64_tr_b16 %5, %13\n"
+        "ds_read_b64_tr_b16 %6, %14\n"
+        "ds_read_b64_tr_b16 %7, %15\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7])
+        : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]), "v"(at[6]), "v"(at[7]));
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = halves(v[2 * i], v[2 * i + 1]);
+}
+// the three parts of a fragment, PART bytes apart
+template <int ROW, int PART>
+__device__ __forceinline__ void tr_read3(uint32_t at, bf16x8 (&f)[3]) {
+  u32x2 v[6];
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %6\n"
+      "ds_read_b64_tr_b16 %1, %6 offset:%7\n"
+      "ds_read_b64_tr_b16 %2, %6 offset:%8\n"
+      "ds_read_b64_tr_b16 %3, %6 offset:%9\n"
+      "ds_read_b64_tr_b16 %4, %6 offset:%10\n"
+      "ds_read_b64_tr_b16 %5, %6 offset:%11\n"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5])
+      : "v"(at), "n"(4 * ROW), "n"(PART), "n"(PART + 4 * ROW), "n"(2 * PART), "n"(2 * PART + 4 * ROW));
+#pragma unroll
+  for (int i = 0; i < 3; ++i) f[i] = halves(v[2 * i], v[2 * i + 1]);
+}
+// two such fragments
+template <int ROW, int PART>
+__device__ __forceinline__ void tr_read6(const uint32_t (&at)[2], bf16x8 (&f)[2][3]) {
+  u32x2 v[12];
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %12\n"
+      "ds_read_b64_tr_b16 %1, %12 offset:%14\n"
+      "ds_read_b64_tr_b16 %2, %12 offset:%15\n"
+      "ds_read_b64_tr_b16 %3, %12 offset:%16\n"
+      "ds_read_b64_tr_b16 %4, %12 offset:%17\n"
+      "ds_read_b64_tr_b16 %5, %12 offset:%18\n"
+      "ds_read_b64_tr_b16 %6, %13\n"
+      "ds_read_b64_tr_b16 %7, %13 offset:%14\n"
+      "ds_read_b64_tr_b16 %8, %13 offset:%15\n"
+      "ds_read_b64_tr_b16 %9, %13 offset:%16\n"
+      "ds_read_b64_tr_b16 %10, %13 offset:%17\n"
+      "ds_read_b64_tr_b16 %11, %13 offset:%18\n"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7]),
+        "=&v"(v[8]), "=&v"(v[9]), "=&v"(v[10]), "=&v"(v[11])
+      : "v"(at[0]), "v"(at[1]), "n"(4 * ROW), "n"(PART), "n"(PART + 4 * ROW), "n"(2 * PART), "n"(2 * PART + 4 * ROW));
+#pragma unroll
+  for (int i = 0; i < 6; ++i) f[i / 3][i % 3] = halves(v[2 * i], v[2 * i + 1]);
+}
+
 template <bool KMAJOR, int NJ, int MW>
 __global__ __launch_bounds__(256) void k_adapters_narrow(AdapterNarrow p) {
   constexpr int RP = 16 * NJ, BM = 64 * MW;
@@ -219,6 +395,10 @@ __global__ __launch_bounds__(256) void k_adapters_narrow(AdapterNarrow p) {
   __shared__ __attribute__((aligned(1024))) uint8_t S1[SB];
   __shared__ __attribute__((aligned(1024))) uint8_t S2[SB];
   auto buf = [&](int b) -> uint8_t* { return b == 0 ? S0 : b == 1 ? S1 : S2; };
+  if (blockIdx.x >= p.tiles) {
+    if (blockIdx.y == 0 && blockIdx.z == 0) split_rows(p.split, blockIdx.x - p.tiles, p.rows.M, p.r);
+    return;
+  }
   Tile tile;
   if (!find_tile(p.rows, BM, blockIdx.x, tile)) return;
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4;
@@ -280,19 +460,27 @@ __global__ __launch_bounds__(256) void k_adapters_narrow(AdapterNarrow p) {
       const bool in = 32 * ks + 8 * g < left;
       const int piece = ((4 * ks + g) ^ (li & 7)) << 4;
       bf16x8 fx[MW];
+      b128_read<MW>(lds_at(at) + (wave * 16 * MW + li) * 128 + piece, fx);
+      if (!in) {
 #pragma unroll
-      for (int i = 0; i < MW; ++i) {
-        u32x4 v = *(const u32x4*)(at + (wave * 16 * MW + 16 * i + li) * 128 + piece);
-        if (!in) v = u32x4{0u, 0u, 0u, 0u};
-        fx[i] = __builtin_bit_cast(bf16x8, v);
+        for (int i = 0; i < MW; ++i) fx[i] = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
+      }
+      bf16x8 fl[NJ];
+      if constexpr (KMAJOR) {
+        // rows of the rank's own length: the second half of a fragment has its own address
+        uint32_t at2[2 * NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          at2[2 * j] = lds_at(at + XB) + (32 * ks + 8 * g + e) * rb + (((2 * j + (q >> 1)) ^ swz) << 4) + ((q & 1) << 3);
+          at2[2 * j + 1] = at2[2 * j] + 4 * rb;
+        }
+        tr_read_rows<NJ>(at2, fl);
+      } else {
+        b128_read<NJ>(lds_at(at + XB) + li * 128 + piece, fl);
       }
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        u32x4 v;
-        if constexpr (KMAJOR)
-          v = __builtin_bit_cast(u32x4, lds_tr8(at + XB + (32 * ks + 8 * g + e) * rb +
-                                                    (((2 * j + (q >> 1)) ^ swz) << 4) + ((q & 1) << 3), rb));
-        else v = *(const u32x4*)(at + XB + (16 * j + li) * 128 + piece);
+        u32x4 v = __builtin_bit_cast(u32x4, fl[j]);
         if (!in) v = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
         for (int i = 0; i < MW; ++i)
@@ -432,8 +620,9 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
       v = join4(p.part + row * r + j, p.rows.M * r, p.splits);
       if (p.T_out && blockIdx.y == 0) *(floatx4*)(p.T_out + row * r + j) = v;
     }
-    uint2 part[2];
+    uint2 part[3];
     split4(v, part);
+    if (p.split.to && blockIdx.y == 0 && row >= 0 && j < r) store3(p.split, row, j, part);
     uint8_t* to = ps + m * PROW + (j / 16) * 64 + (j % 16) * 2;
     *(uint2*)to = part[0];
     *(uint2*)(to + 32) = part[1];
@@ -504,28 +693,177 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
 
 // ---------------------------------------------------------------------------
 // dL[a][j][c] (or [c][j]) = s[a] sum over a's rows of P[m][j] Q[m][c]: a workgroup has
-// 128 columns of Q, 16 NJ of the rank (blockIdx.z: which 64) and up to p.item rows of an
-// adapter, 64 at a time through LDS, two such steps under way in registers.  Rows past the
-// tile are zero in both.  An adapter whose rows are all here is written out, otherwise the
-// item's sums go to a part of their own, which k_adapters_join adds in order.  Q in 8 bits
-// (X8 1: e4m3, 2: e5m2) becomes bf16 on its way into LDS, and P is multiplied by the scale
-// of its row and this block of 128 columns.
+// 256 columns of Q, 16 NJ of the rank (blockIdx.z: which 64) and up to p.item rows of an
+// adapter (blockIdx.y).  P is given as three bf16 parts.  Both are copied straight into LDS,
+// 32 rows a step through a ring of buffers, ST - 1 steps under way, and read with
+// transposing reads: the products contract the rows.  Rows past the tile come from zeros.
+// 16-byte pieces stand XORed by the row, so that the 4 rows of a transposing read fall on
+// different banks.  An adapter whose rows are all here is written out, otherwise the item's
+// sums go to a part of their own, which k_adapters_join adds in order.  One launch has
+// dL1's columns and then dL2's.
 // ---------------------------------------------------------------------------
-template <int X8, int NJ>
-__device__ __forceinline__ void grad_tile(const AdapterRows& rows, const AdapterGrad& p, int cb, uint8_t* smem) {
+template <int NJ>
+__global__ __launch_bounds__(512) void k_adapters_grad(AdapterRows rows, AdapterGrad p1, AdapterGrad p2) {
+  constexpr int KR = 32, RP = 16 * NJ, ST = 4;
+  constexpr int JW = NJ == 4 ? 2 : 1, CW = 8 / JW;      // waves over the rank and over the columns
+  constexpr int FJ = NJ / JW, FC = 16 / CW;             // a wave's fragments
+  constexpr int QB = KR * 512, PROW = 3 * RP * 2, CPR = PROW / 16;
+  constexpr int SB = QB + KR * PROW;
+  constexpr int NP = KR * CPR / 64, PI = NJ == 4 ? 2 : 1;  // 1 KB copies of P a step, and of a wave
+  constexpr int C = 2 + PI;                                // copies of a wave and step
+  __shared__ __attribute__((aligned(1024))) uint8_t S0[SB];
+  __shared__ __attribute__((aligned(1024))) uint8_t S1[SB];
+  __shared__ __attribute__((aligned(1024))) uint8_t S2[SB];
+  __shared__ __attribute__((aligned(1024))) uint8_t S3[SB];
+  __shared__ int list[kMaxAdapterItem];  // the tile's part of the order
+  auto buf = [&](int b) -> uint8_t* { return b == 0 ? S0 : b == 1 ? S1 : b == 2 ? S2 : S3; };
+  const int n1 = (int)((p1.N + 255) / 256);
+  const bool second = (int)blockIdx.x >= n1;
+  const AdapterGrad& p = second ? p2 : p1;
+  const int64_t N = p.N, c0 = (int64_t)(second ? blockIdx.x - n1 : blockIdx.x) * 256;
+  Tile tile;
+  if (!find_tile(rows, p.item, blockIdx.y, tile)) return;
+  const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = p.r, j0 = blockIdx.z * 64;
+  const int steps = (tile.p1 - tile.p0 + KR - 1) / KR;
+  const bool ordered = rows.order != nullptr;
+  if (ordered) {
+    for (int i = tid; i < tile.p1 - tile.p0; i += 512) list[i] = rows.order[tile.p0 + i];
+    __syncthreads();
+  }
+  // a step's row m, -1 where there is none
+  const int count = tile.p1 - tile.p0;
+  auto row_of = [&](int t, int m) -> int64_t {
+    const int i = KR * t + m;
+    int row = tile.p0 + i;
+    if (ordered) row = list[min(i, count - 1)];
+    return i < count && (uint64_t)(int64_t)row < (uint64_t)rows.M ? row : -1;
+  };
+  // Q: copy i has rows 2 (8 i + wave) and the next; P: pieces 64 k and on
+  int64_t qc = c0 + 8 * ((lane & 31) ^ (((2 * wave + (lane >> 5)) & 3) << 1));
+  qc = qc < N ? qc : 0;
+  int pm[PI], pc[PI];
+#pragma unroll
+  for (int i = 0; i < PI; ++i) {
+    const int e = 64 * ((8 * i + wave) % NP) + lane;
+    pm[i] = e / CPR;
+    pc[i] = e % CPR;
+    if (NJ == 4) pc[i] ^= ((pm[i] >> 1) & 1) << 1;
+  }
+  auto copy = [&](int t, int b) {
+    uint8_t* const to = buf(b);  // (steps past the last are all zeros, and not used)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t row = row_of(t, 2 * (8 * i + wave) + (lane >> 5));
+      const void* there = (const uint16_t*)p.Q + row * N + qc;
+      const void* from = row < 0 ? p.zero : there;
+      __builtin_amdgcn_global_load_lds((global_ptr_t)from, (lds_ptr_t)(to + (8 * i + wave) * 1024), 16, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < PI; ++i) {
+      const int64_t row = row_of(t, pm[i]);
+      const void* there = p.P3 + ((row * gridDim.z + blockIdx.z) * CPR + pc[i]) * 8;
+      const void* from = row < 0 ? p.zero : there;
+      __builtin_amdgcn_global_load_lds((global_ptr_t)from, (lds_ptr_t)(to + QB + (8 * i + wave) % NP * 1024), 16, 0, 0);
+    }
+  };
+  const int wj = wave / CW, wc = wave % CW;
+  const int e = li >> 2, q = li & 3;
+  floatx4 acc[FJ][FC];
+#pragma unroll
+  for (int j = 0; j < FJ; ++j)
+#pragma unroll
+    for (int c = 0; c < FC; ++c) acc[j][c] = floatx4{0.f, 0.f, 0.f, 0.f};
+  // a lane's addresses within a buffer
+  uint32_t pa[FJ], qa[FC];
+#pragma unroll
+  for (int j = 0; j < FJ; ++j)
+    pa[j] = QB + (8 * g + e) * PROW + (((2 * (wj * FJ + j) + (q >> 1)) ^ (NJ == 4 ? e & 2 : 0)) << 4) + ((q & 1) << 3);
+#pragma unroll
+  for (int c = 0; c < FC; ++c)
+    qa[c] = (8 * g + e) * 512 + (((2 * (wc * FC + c) + (q >> 1)) ^ (e << 1)) << 4) + ((q & 1) << 3);
+  auto compute = [&](int b) {
+    const uint32_t at = lds_at(buf(b));
+    uint32_t pt[FJ], qt[FC];
+#pragma unroll
+    for (int j = 0; j < FJ; ++j) pt[j] = at + pa[j];
+#pragma unroll
+    for (int c = 0; c < FC; ++c) qt[c] = at + qa[c];
+    bf16x8 fp[FJ][3], fq[FC];
+    if constexpr (FC == 4) tr_read4<512>(qt, fq);
+    else tr_read2<512>(qt, fq);
+    if constexpr (FJ == 2) tr_read6<PROW, 2 * RP>(pt, fp);
+    else tr_read3<PROW, 2 * RP>(pt[0], fp[0]);
+#pragma unroll
+    for (int w = 2; w >= 0; --w)
+#pragma unroll
+      for (int c = 0; c < FC; ++c)
+#pragma unroll
+        for (int j = 0; j < FJ; ++j)
+          acc[j][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp[j][w], fq[c], acc[j][c], 0, 0, 0);
+  };
+  auto step = [&](int t, int b) {
+    // this step's copies are there, everybody's, and the reads of the step before are done
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(wait_vm((ST - 2) * C) & kWaitLds);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    copy(t + ST - 1, (b + ST - 1) % ST);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(b);
+  };
+#pragma unroll
+  for (int b = 0; b < ST - 1; ++b) copy(b, b);
+  for (int t = 0; t < steps; t += ST) {
+    step(t, 0);
+#pragma unroll
+    for (int b = 1; b < ST; ++b)
+      if (t + b < steps) step(t + b, b);
+  }
+  const float s = tile.whole ? p.s[tile.a] : 1.f;
+  float* out = tile.whole ? p.out + (int64_t)tile.a * r * N : p.part + (int64_t)blockIdx.y * r * N;
+#pragma unroll
+  for (int j = 0; j < FJ; ++j)
+#pragma unroll
+    for (int c = 0; c < FC; ++c) {
+      const int jj = j0 + 16 * (wj * FJ + j) + 4 * g;
+      const int64_t cc = c0 + 16 * (wc * FC + c) + li;
+      if (jj >= r || cc >= N) continue;  // r % 4 == 0
+      const floatx4 o = acc[j][c] * s;
+      if (p.trans) {
+        *(floatx4*)(out + cc * r + jj) = o;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[(jj + i) * N + cc] = o[i];
+      }
+    }
+  __builtin_amdgcn_s_waitcnt(0);  // no copy is on its way into LDS that is no longer this workgroup's
+}
+
+// ---------------------------------------------------------------------------
+// The same for Q in 8 bits (E5M2 or e4m3): 128 columns a workgroup, which share a row's
+// scale.  Codes become bf16 and P, fp32, is multiplied by the scale of its row and this
+// block of columns and split on their way from registers into LDS, 64 rows at a time, two
+// such steps under way.
+// ---------------------------------------------------------------------------
+template <bool E5M2, int NJ>
+__global__ __launch_bounds__(256) void k_adapters_grad8(AdapterRows rows, AdapterGrad p) {
   constexpr int KR = 64, RP = 16 * NJ;
   // 8 banks between neighbouring rows: the 4 rows of a transposing read fall on different ones
   constexpr int QROW = 128 * 2 + 32, PROW = RP * 2 + 16;
   constexpr int JW = NJ == 4 ? 2 : 1, CW = 4 / JW;      // waves over the rank and over the columns
   constexpr int FJ = NJ / JW, FC = 8 / CW;              // a wave's fragments
-  constexpr int QL = X8 ? 2 : 4;                        // 16-byte loads of Q a thread
+  constexpr int QL = 2;                                 // 16-byte loads of Q a thread
   constexpr int PL = KR * RP / 4 / 256;                 // 4-value pieces of P a thread
-  constexpr int CP = X8 ? 8 : 16;                       // pieces of a row of Q
-  uint8_t* qs = smem;
-  uint8_t* ps = smem + KR * QROW;  // [3][KR] rows
+  constexpr int CP = 8;                                 // pieces of a row of Q
+  __shared__ __align__(16) uint8_t qs[KR * QROW];
+  __shared__ __align__(16) uint8_t ps[3 * KR * PROW];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, g = lane >> 4;
   Tile tile;
-  if (!find_tile(rows, p.item, blockIdx.x, tile)) return;
+  if (!find_tile(rows, p.item, blockIdx.y, tile)) return;
+  const int cb = blockIdx.x;
   const int64_t N = p.N, c0 = (int64_t)cb * 128;
   const int r = p.r, j0 = blockIdx.z * 64;
   const int64_t kb = (N + 127) / 128;
@@ -550,8 +888,8 @@ __device__ __forceinline__ void grad_tile(const AdapterRows& rows, const Adapter
       const int e = 256 * i + tid;
       bool ok;
       const int64_t row = row_of(ord, p0, e / CP, ok);
-      const int64_t c = c0 + (e % CP) * (128 / CP);
-      s.q[i] = *(const u32x4*)((const uint8_t*)p.Q + (row * N + (c < N ? c : 0)) * (X8 ? 1 : 2));
+      const int64_t c = c0 + 16 * (e % CP);
+      s.q[i] = *(const u32x4*)((const uint8_t*)p.Q + row * N + (c < N ? c : 0));
       s.ok |= ok ? 1u << i : 0;
     }
 #pragma unroll
@@ -560,7 +898,7 @@ __device__ __forceinline__ void grad_tile(const AdapterRows& rows, const Adapter
       bool ok;
       const int64_t row = row_of(ord, p0, e / (RP / 4), ok);
       s.v[i] = *(const floatx4*)(p.P + row * r + (j < r ? j : 0));
-      if constexpr (X8 != 0) s.scale[i] = p.q_scales[row * kb + cb];
+      s.scale[i] = p.q_scales[row * kb + cb];
       s.ok |= ok && j < r ? 256u << i : 0;
     }
   };
@@ -571,24 +909,19 @@ __device__ __forceinline__ void grad_tile(const AdapterRows& rows, const Adapter
       uint8_t* to = qs + (e / CP) * QROW + (e % CP) * (256 / CP);
       u32x4 v = s.q[i];
       if (!(s.ok >> i & 1)) v = u32x4{0u, 0u, 0u, 0u};
-      if constexpr (X8 == 0) {
-        *(u32x4*)to = v;
-      } else {
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float a[4], b[4];
-          unpack_fp8x4<X8 == 2>(v[2 * hf], a);
-          unpack_fp8x4<X8 == 2>(v[2 * hf + 1], b);
-          *(u32x4*)(to + 16 * hf) = u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]),
-                                          pack_bf16x2(b[2], b[3])};
-        }
+      for (int hf = 0; hf < 2; ++hf) {
+        float a[4], b[4];
+        unpack_fp8x4<E5M2>(v[2 * hf], a);
+        unpack_fp8x4<E5M2>(v[2 * hf + 1], b);
+        *(u32x4*)(to + 16 * hf) = u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]),
+                                        pack_bf16x2(b[2], b[3])};
       }
     }
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
       const int e = 256 * i + tid, m = e / (RP / 4), j = 4 * (e % (RP / 4));
-      floatx4 v = s.v[i];
-      if constexpr (X8 != 0) v *= s.scale[i];
+      floatx4 v = s.v[i] * s.scale[i];
       if (!(s.ok >> (8 + i) & 1)) v = floatx4{0.f, 0.f, 0.f, 0.f};
       uint2 part[3];
       split4(v, part);
@@ -648,7 +981,7 @@ __device__ __forceinline__ void grad_tile(const AdapterRows& rows, const Adapter
     if (p0 + KR < tile.p1) step(p0 + KR, sb, ob);
   }
   const float s = tile.whole ? p.s[tile.a] : 1.f;
-  float* out = tile.whole ? p.out + (int64_t)tile.a * r * N : p.part + (int64_t)blockIdx.x * r * N;
+  float* out = tile.whole ? p.out + (int64_t)tile.a * r * N : p.part + (int64_t)blockIdx.y * r * N;
 #pragma unroll
   for (int j = 0; j < FJ; ++j)
 #pragma unroll
@@ -664,16 +997,6 @@ __device__ __forceinline__ void grad_tile(const AdapterRows& rows, const Adapter
         for (int i = 0; i < 4; ++i) out[(jj + i) * N + cc] = o[i];
       }
     }
-}
-
-// Both gradients in one launch: dL1's blocks of columns, then dL2's.
-template <int X8, int NJ>
-__global__ __launch_bounds__(256) void k_adapters_grad(AdapterRows rows, AdapterGrad p1, AdapterGrad p2) {
-  constexpr int SMEM = 64 * (128 * 2 + 32) + 3 * 64 * (16 * NJ * 2 + 16);
-  __shared__ __align__(16) uint8_t smem[SMEM];
-  const int n1 = (int)((p1.N + 127) / 128), cb = blockIdx.y;
-  if (cb < n1) grad_tile<X8, NJ>(rows, p1, cb, smem);
-  else grad_tile<0, NJ>(rows, p2, cb - n1, smem);
 }
 
 // Outputs of adapters with several items: their parts' sums in order; with none: zeros.
@@ -719,9 +1042,10 @@ hipError_t narrow_of(const AdapterNarrow& p, int bm, dim3 gr, hipStream_t st) {
 }
 
 hipError_t narrow(const AdapterCall& c, const AdapterPlan& pl, const uint16_t* A, int64_t K, const uint16_t* L,
-                  bool kmajor, float* part, hipStream_t st) {
-  AdapterNarrow p{c.rows, A, L, K, c.r, pl.krange, part};
-  const dim3 gr((unsigned)pl.tiles, (unsigned)pl.splits, (unsigned)((c.r + 63) / 64));
+                  bool kmajor, float* part, const Split3& split, hipStream_t st) {
+  AdapterNarrow p{c.rows, A, L, K, c.r, pl.krange, part, (unsigned)pl.tiles, split};
+  const int64_t more = split.to ? (c.rows.M + 63) / 64 : 0;
+  const dim3 gr((unsigned)(pl.tiles + more), (unsigned)pl.splits, (unsigned)((c.r + 63) / 64));
   if (kmajor)
     return c.r <= 16   ? narrow_of<true, 1>(p, pl.bm, gr, st)
            : c.r <= 32 ? narrow_of<true, 2>(p, pl.bm, gr, st)
@@ -741,30 +1065,45 @@ hipError_t wide_of(const AdapterWide& p, dim3 gr, hipStream_t st) {
 }
 
 hipError_t wide(const AdapterCall& c, const AdapterPlan& pl, const float* part, const uint16_t* L, bool jmajor,
-                int64_t N, const uint16_t* base, uint16_t* out, float* T_out, hipStream_t st) {
+                int64_t N, const uint16_t* base, uint16_t* out, float* T_out, const Split3& split, hipStream_t st) {
   const bool few = pl.bm == 16;
   int64_t tiles;
   const int blocks = plan_adapters_wide(c.rows.M, c.rows.n, few, N, &tiles);
-  AdapterWide p{c.rows, part, pl.splits, L, N, c.r, c.s, base, out, T_out, blocks};
+  AdapterWide p{c.rows, part, pl.splits, L, N, c.r, c.s, base, out, T_out, blocks, split};
   const int64_t nb = (N + 127) / 128;
   const dim3 gr((unsigned)tiles, (unsigned)(few ? (nb + 3) / 4 : (nb + blocks - 1) / blocks));
   if (few) return jmajor ? wide_of<true, 1>(p, gr, st) : wide_of<false, 1>(p, gr, st);
   return jmajor ? wide_of<true, 4>(p, gr, st) : wide_of<false, 4>(p, gr, st);
 }
 
-// out [M][r] of the listed rows = the splits' sum
-__global__ __launch_bounds__(256) void k_adapters_sum(const float* __restrict__ part, int64_t size, int splits,
-                                                      float* __restrict__ out) {
+// The splits' sum, as it is or in three parts (where no input gradient's kernel leaves it).
+__global__ __launch_bounds__(256) void k_adapters_sum(const float* __restrict__ part, int64_t size, int splits, int r,
+                                                      float* __restrict__ out, Split3 split) {
   const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (e < size) *(floatx4*)(out + e) = join4(part + e, size, splits);
+  if (e >= size) return;
+  const floatx4 v = join4(part + e, size, splits);
+  if (out) *(floatx4*)(out + e) = v;
+  if (!split.to) return;
+  uint2 three[3];
+  split4(v, three);
+  store3(split, e / r, (int)(e % r), three);
 }
 
-template <int X8>
-hipError_t grad_of(const AdapterRows& rows, const AdapterGrad& p1, const AdapterGrad& p2, hipStream_t st) {
-  const dim3 gr((unsigned)p1.items, (unsigned)((p1.N + 127) / 128 + (p2.N + 127) / 128), (unsigned)((p1.r + 63) / 64));
-  if (p1.r <= 16) hipLaunchKernelGGL((k_adapters_grad<X8, 1>), gr, dim3(256), 0, st, rows, p1, p2);
-  else if (p1.r <= 32) hipLaunchKernelGGL((k_adapters_grad<X8, 2>), gr, dim3(256), 0, st, rows, p1, p2);
-  else hipLaunchKernelGGL((k_adapters_grad<X8, 4>), gr, dim3(256), 0, st, rows, p1, p2);
+template <bool E5M2>
+hipError_t grad8_of(const AdapterRows& rows, const AdapterGrad& p, hipStream_t st) {
+  const dim3 gr((unsigned)((p.N + 127) / 128), (unsigned)p.items, (unsigned)((p.r + 63) / 64));
+  if (p.r <= 16) hipLaunchKernelGGL((k_adapters_grad8<E5M2, 1>), gr, dim3(256), 0, st, rows, p);
+  else if (p.r <= 32) hipLaunchKernelGGL((k_adapters_grad8<E5M2, 2>), gr, dim3(256), 0, st, rows, p);
+  else hipLaunchKernelGGL((k_adapters_grad8<E5M2, 4>), gr, dim3(256), 0, st, rows, p);
+  return hipGetLastError();
+}
+
+// dL1 and dL2, or (p1.N = 0) dL2 alone
+hipError_t grad(const AdapterRows& rows, const AdapterGrad& p1, const AdapterGrad& p2, hipStream_t st) {
+  const dim3 gr((unsigned)((p1.N + 255) / 256 + (p2.N + 255) / 256), (unsigned)p2.items, (unsigned)((p2.r + 63) / 64));
+  if (p2.r <= 16) hipLaunchKernelGGL((k_adapters_grad<1>), gr, dim3(512), 0, st, rows, p1, p2);
+  else if (p2.r <= 32) hipLaunchKernelGGL((k_adapters_grad<2>), gr, dim3(512), 0, st, rows, p1, p2);
+  else hipLaunchKernelGGL((k_adapters_grad<4>), gr, dim3(512), 0, st, rows, p1, p2);
   return hipGetLastError();
 }
 
@@ -773,9 +1112,9 @@ hipError_t grad_of(const AdapterRows& rows, const AdapterGrad& p1, const Adapter
 hipError_t launch_adapters_fwd(const AdapterCall& c, const uint16_t* X, const uint16_t* base, uint16_t* Y, float* T_out,
                                void* ws, hipStream_t st) {
   const AdapterPlan pl = plan_adapters_rows(c.rows.M, c.rows.n, c.h);
-  hipError_t e = narrow(c, pl, X, c.h, c.L1, true, (float*)ws, st);
+  hipError_t e = narrow(c, pl, X, c.h, c.L1, true, (float*)ws, Split3{}, st);
   if (e != hipSuccess) return e;
-  return wide(c, pl, (const float*)ws, c.L2, true, c.o, base, Y, T_out, st);
+  return wide(c, pl, (const float*)ws, c.L2, true, c.o, base, Y, T_out, Split3{}, st);
 }
 
 hipError_t launch_adapters_bwd(const AdapterCall& c, const void* X, int x8, const float* x_scales, const uint16_t* dY,
@@ -783,26 +1122,38 @@ hipError_t launch_adapters_bwd(const AdapterCall& c, const void* X, int x8, cons
                                hipStream_t st) {
   const AdapterPlan pl = plan_adapters_rows(c.rows.M, c.rows.n, c.o);
   const AdapterItems it = plan_adapters_items(c.rows.M, c.rows.n, c.h, c.o, c.r);
-  const int64_t size = c.rows.M * c.r;
-  float* gparts = (float*)ws;
-  float* G = pl.splits > 1 ? gparts + pl.splits * size : gparts;
-  float* parts = G + size;
-  hipError_t e = narrow(c, pl, dY, c.o, c.L2, false, gparts, st);
+  const AdapterGradSpace sp = plan_adapters_space(c.rows.M, c.rows.n, c.h, c.o, c.r);
+  uint8_t* const w = (uint8_t*)ws;
+  float* const gparts = (float*)(w + sp.gparts);
+  float* const parts = (float*)(w + sp.parts);
+  const int nz = (c.r + 63) / 64, rp = c.r <= 16 ? 16 : c.r <= 32 ? 32 : 64;
+  const Split3 t3{T, (uint16_t*)(w + sp.t3), w, nz, rp};
+  // G for the products over rows: three parts, or fp32 beside 8-bit codes
+  const Split3 g3{nullptr, x8 ? nullptr : (uint16_t*)(w + sp.g), nullptr, nz, rp};
+  float* const G = !x8 ? nullptr : pl.splits > 1 ? (float*)(w + sp.g) : gparts;
+  float* const G_out = G == gparts ? nullptr : G;
+  hipError_t e = narrow(c, pl, dY, c.o, c.L2, false, gparts, t3, st);
   if (e != hipSuccess) return e;
   // dX's kernel joins G's splits and leaves their sum
   if (dX) {
-    e = wide(c, pl, gparts, c.L1, false, c.h, base, dX, pl.splits > 1 ? G : nullptr, st);
-  } else if (pl.splits > 1) {
+    e = wide(c, pl, gparts, c.L1, false, c.h, base, dX, G_out, g3, st);
+  } else if (G_out || g3.to) {
+    const int64_t size = c.rows.M * c.r;
     hipLaunchKernelGGL(k_adapters_sum, dim3((unsigned)((size + 1023) / 1024)), dim3(256), 0, st, gparts, size,
-                       pl.splits, G);
+                       pl.splits, c.r, G_out, g3);
     e = hipGetLastError();
   }
   if (e != hipSuccess) return e;
-  const AdapterGrad g1{X, x_scales, c.h, G, c.r, c.s, it.item, it.items, 1, parts, dL1};
-  const AdapterGrad g2{dY, nullptr, c.o, T, c.r, c.s, it.item, it.items, 0, parts + it.items * c.r * c.h, dL2};
-  e = x8 == 0   ? grad_of<0>(c.rows, g1, g2, st)
-      : x8 == 1 ? grad_of<1>(c.rows, g1, g2, st)
-                : grad_of<2>(c.rows, g1, g2, st);
+  const AdapterGrad g1{X, x_scales, c.h, G, g3.to, c.r, c.s, it.item, it.items, 1, parts, dL1, w};
+  const AdapterGrad g2{dY, nullptr, c.o, nullptr, t3.to, c.r, c.s, it.item, it.items, 0,
+                       parts + it.items * c.r * c.h, dL2, w};
+  if (x8) {
+    e = x8 == 1 ? grad8_of<false>(c.rows, g1, st) : grad8_of<true>(c.rows, g1, st);
+    if (e != hipSuccess) return e;
+  }
+  AdapterGrad first = g1;
+  if (x8) first.N = 0;
+  e = grad(c.rows, first, g2, st);
   if (e != hipSuccess) return e;
   const int64_t most = std::max(c.h, c.o) * c.r;
   const dim3 gr((unsigned)std::min<int64_t>((most + 1023) / 1024, 1024), (unsigned)c.rows.n, 2);

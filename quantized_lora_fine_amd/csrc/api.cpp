@@ -574,9 +574,7 @@ nf4_status check_adapters(int64_t M, int64_t rows, int64_t cols, int32_t n, int3
 size_t adapters_ws(int32_t op, int64_t M, int64_t rows, int64_t cols, int32_t n, int32_t r) {
   if (M == 0) return 0;
   if (op == NF4_OP_FWD) return (size_t)plan_adapters_rows(M, n, cols).splits * M * r * 4;
-  const size_t splits = (size_t)plan_adapters_rows(M, n, rows).splits;
-  return (splits + (splits > 1)) * M * r * 4 +
-         (size_t)plan_adapters_items(M, n, cols, rows, r).items * r * (rows + cols) * 4;
+  return plan_adapters_space(M, n, cols, rows, r).total;
 }
 
 size_t norm_ws(int64_t M, int64_t H) { return align256((size_t)std::max(rmsnorm_parts(M, (int)H), 1) * H * 4); }

@@ -213,6 +213,14 @@ struct AdapterCall {
   int64_t o, h;
   int r;
 };
+// T or G as three bf16 parts, for the products over rows
+constexpr int kZeroBytes = 512;
+struct Split3 {
+  const float* from;  // [M][r]
+  uint16_t* to;       // [M][nz][3][rp], or NULL
+  void* zero;         // kZeroBytes to be cleared
+  int nz, rp;
+};
 struct AdapterNarrow {
   AdapterRows rows;
   const uint16_t* A;  // [M][K]
@@ -221,6 +229,8 @@ struct AdapterNarrow {
   int r;
   int64_t krange;
   float* part;  // [splits][M][r]
+  unsigned tiles;  // workgroups past them split T
+  Split3 split;
 };
 struct AdapterWide {
   AdapterRows rows;
@@ -234,12 +244,14 @@ struct AdapterWide {
   uint16_t* out;
   float* T_out;  // the joined parts, or NULL
   int blocks;    // blocks of 128 columns a workgroup goes over
+  Split3 split;  // the joined parts in this form too, where `to` is set
 };
 struct AdapterGrad {
   const void* Q;          // [M][N], bf16 or codes
   const float* q_scales;  // of codes
   int64_t N;
-  const float* P;  // [M][r]
+  const float* P;      // [M][r], beside codes
+  const uint16_t* P3;  // in three parts, beside bf16
   int r;
   const float* s;
   int item;       // rows an item, a multiple of 64
@@ -247,7 +259,9 @@ struct AdapterGrad {
   int trans;      // out [n][N][r], else [n][r][N]
   float* part;    // [items][r * N]
   float* out;
+  const void* zero;  // kZeroBytes of zeros
 };
+constexpr int kMaxAdapterItem = 4096;
 constexpr int64_t kMaxAdapterRows = (int64_t)1 << 26;  // tiles of 16 rows stay one launch
 // Tiles of rows of the products of one row, and the splits of a contraction over K.
 struct AdapterPlan {
@@ -265,6 +279,11 @@ struct AdapterItems {
   int64_t items;
 };
 AdapterItems plan_adapters_items(int64_t M, int n, int64_t h, int64_t o, int r);
+// Byte offsets of the parts of the backward pass's workspace; the zeros come first.
+struct AdapterGradSpace {
+  size_t gparts, g, t3, parts, total;
+};
+AdapterGradSpace plan_adapters_space(int64_t M, int n, int64_t h, int64_t o, int r);
 NF4K_WEAK hipError_t launch_adapters_fwd(const AdapterCall& c, const uint16_t* X, const uint16_t* base, uint16_t* Y,
                                          float* T_out, void* ws, hipStream_t st);
 // x8: 0 X is bf16, 1 e4m3, 2 e5m2

@@ -143,14 +143,38 @@ int plan_adapters_wide(int64_t M, int n, bool few, int64_t N, int64_t* tiles) {
   return (int)std::max<int64_t>(1, std::min(each, blocks));
 }
 
+// The rows of an item: as many sets of 256 workgroups (one a compute unit) as take the
+// least time, by 25 ns a row and 4 us around a workgroup's loop, with the items' sums
+// written and read once more (5 TB/s).
 AdapterItems plan_adapters_items(int64_t M, int n, int64_t h, int64_t o, int r) {
-  AdapterItems p;
-  const int64_t tiles = ((h + 127) / 128 + (o + 127) / 128) * ((r + 63) / 64);
+  AdapterItems p{64, 1};
+  const int64_t cols = ((h + 255) / 256 + (o + 255) / 256) * ((r + 63) / 64);
   const int64_t used = std::min<int64_t>(M, n);
-  const int64_t rows = std::max<int64_t>(128, M * tiles / 640);
-  p.item = (int)((std::min<int64_t>(rows, std::max<int64_t>(M, 64)) + 63) / 64 * 64);
+  double least = 0;
+  for (int64_t k = 1; k <= 256; k = k < 8 ? k + 1 : k * 5 / 4) {
+    const int64_t item = std::min<int64_t>((((M + k - 1) / k) + 63) / 64 * 64, kMaxAdapterItem);
+    const int64_t items = (M + item - 1) / item + used / 2;
+    const int64_t sets = (items * cols + 255) / 256;
+    const double time = sets * (0.025 * item + 4) + (items > used ? 1.6e-6 * items * r * (h + o) : 0);
+    if (k == 1 || time < least) {
+      least = time;
+      p.item = (int)item;
+    }
+    if (item == 64) break;
+  }
   p.items = std::min<int64_t>(M, M / p.item + used);
   return p;
+}
+
+AdapterGradSpace plan_adapters_space(int64_t M, int n, int64_t h, int64_t o, int r) {
+  AdapterGradSpace s;
+  const int64_t rp = r <= 16 ? 16 : r <= 32 ? 32 : 64, three = M * ((r + 63) / 64) * 3 * rp * 2;
+  s.gparts = kZeroBytes;
+  s.g = s.gparts + (size_t)plan_adapters_rows(M, n, o).splits * M * r * 4;
+  s.t3 = s.g + (size_t)three;
+  s.parts = s.t3 + (size_t)three;
+  s.total = s.parts + (size_t)plan_adapters_items(M, n, h, o, r).items * r * (h + o) * 4;
+  return s;
 }
 
 // Tiles of the block-scaled product, with what one takes on an MI355X: `start`
