@@ -21,6 +21,7 @@
 // for the host.  Whatever the offsets and the order hold, no row outside the buffers is
 // touched.
 #include <algorithm>
+#include <type_traits>
 
 #include "fp8.hpp"
 #include "launch.hpp"
@@ -560,9 +561,10 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
   const int r = p.r, r16 = (r + 15) / 16 * 16;
   const int64_t N = p.N;
   const int nblocks = (int)((N + 127) / 128);
+  // RW = 1: a block past the columns' end goes through the same barriers and writes nothing
   const int cb0 = RW == 4 ? blockIdx.y * p.blocks : blockIdx.y * 4 + grp;
-  const int cb1 = RW == 4 ? min(cb0 + p.blocks, nblocks) : min(cb0 + 1, nblocks);
-  const int runs = (r16 + RC - 1) / RC;
+  const int cb1 = RW == 4 ? min(cb0 + p.blocks, nblocks) : cb0 + 1;
+  const int runs = RMAX == RC ? 1 : (r16 + RC - 1) / RC;
   const uint16_t* L = p.L + (int64_t)tile.a * N * r;
   int64_t at[4];  // this lane's 4 rows, or -1
 #pragma unroll
@@ -570,11 +572,14 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
     const int64_t row = row_at(p.rows, tile, tile.p0 + (RW == 4 ? 16 * wave : 0) + 4 * g + v);
     at[v] = row < 0 ? -1 : row * N;
   }
-  // base: of rows that are not there a valid one's
+  // base: of rows that are not there a valid one's; without a base one piece for all, not used
+  const uint16_t* const from = p.base ? p.base : p.L;
+  const int64_t some = p.base ? -1 : 0;
+  const uint32_t keep = p.base ? 0xFFFFFFFFu : 0u;
   auto load_base = [&](int cb, u32x4 (&b)[4]) {
     const int64_t c = min((int64_t)cb * 128 + 8 * li, N - 8);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) b[v] = *(const u32x4*)(p.base + max(at[v], (int64_t)0) + c);
+    for (int v = 0; v < 4; ++v) b[v] = *(const u32x4*)(from + ((max(at[v], (int64_t)0) + c) & some));
   };
   // pieces of the panel: JMAJOR 16 a row of the rank, else RC / 8 a column
   auto load_panel = [&](int cb, int run, u32x4 (&l)[PL]) {
@@ -605,89 +610,152 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
       }
     }
   };
-  u32x4 b[4], l[PL];
+  // The panels are numbered through the blocks and their runs of the rank; the one after the
+  // next is loaded while one is multiplied.
+  const int panels = (cb1 - cb0) * runs;
+  auto load_panel_no = [&](int i, u32x4 (&l)[PL]) {
+    i = min(i, panels - 1);
+    load_panel(runs == 1 ? cb0 + i : cb0 + i / runs, runs == 1 ? 0 : i % runs, l);
+  };
+  u32x4 b0[4], b1[4], l0[PL], l1[PL];
+  load_panel_no(0, l0);
+  load_base(cb0, b0);
+  if constexpr (NB == 2) load_panel_no(1, l1);
+  constexpr int PT = (BM * RMAX / 4 + 255) / 256;  // 4-value pieces of P a thread, up to 4 of them at once
+#pragma unroll 1
+  for (int i0 = 0; i0 < PT; i0 += 4) {
+    floatx4 v[PT < 4 ? PT : 4];
+    int64_t o[PT < 4 ? PT : 4];
 #pragma unroll
-  for (int v = 0; v < 4; ++v) b[v] = u32x4{0u, 0u, 0u, 0u};
-  if (cb0 < cb1) {
-    load_panel(cb0, 0, l);
-    if (p.base) load_base(cb0, b);
-  }
-  for (int e = tid; e < BM * r16 / 4; e += 256) {
-    const int m = e / (r16 / 4), j = 4 * (e % (r16 / 4));
-    const int64_t row = row_at(p.rows, tile, tile.p0 + m);
-    floatx4 v = {0.f, 0.f, 0.f, 0.f};
-    if (row >= 0 && j < r) {
-      v = join4(p.part + row * r + j, p.rows.M * r, p.splits);
-      if (p.T_out && blockIdx.y == 0) *(floatx4*)(p.T_out + row * r + j) = v;
+    for (int i = 0; i < (PT < 4 ? PT : 4); ++i) {
+      const int e = 256 * (i0 + i) + tid, m = e / (r16 / 4), j = 4 * (e % (r16 / 4));
+      const int64_t row = m < BM && j < r ? row_at(p.rows, tile, tile.p0 + m) : -1;
+      o[i] = row < 0 ? -1 : row * r + j;
+      v[i] = floatx4{0.f, 0.f, 0.f, 0.f};
     }
-    uint2 part[3];
-    split4(v, part);
-    if (p.split.to && blockIdx.y == 0 && row >= 0 && j < r) store3(p.split, row, j, part);
-    uint8_t* to = ps + m * PROW + (j / 16) * 64 + (j % 16) * 2;
-    *(uint2*)to = part[0];
-    *(uint2*)(to + 32) = part[1];
+    for (int q0 = 0; q0 < p.splits; q0 += 4) {
+      floatx4 x[PT < 4 ? PT : 4][4];
+#pragma unroll
+      for (int i = 0; i < (PT < 4 ? PT : 4); ++i)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          x[i][u] = *(const floatx4*)(p.part + min(q0 + u, p.splits - 1) * (p.rows.M * r) + max(o[i], (int64_t)0));
+#pragma unroll
+      for (int i = 0; i < (PT < 4 ? PT : 4); ++i)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (q0 + u < p.splits) v[i] += x[i][u];
+    }
+#pragma unroll
+    for (int i = 0; i < (PT < 4 ? PT : 4); ++i) {
+      const int e = 256 * (i0 + i) + tid, m = e / (r16 / 4), j = 4 * (e % (r16 / 4));
+      if (m >= BM) continue;
+      if (o[i] < 0) v[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+      else if (p.T_out && blockIdx.y == 0) *(floatx4*)(p.T_out + o[i]) = v[i];
+      uint2 part[2];
+      split4(v[i], part);
+      uint8_t* to = ps + m * PROW + (j / 16) * 64 + (j % 16) * 2;
+      *(uint2*)to = part[0];
+      *(uint2*)(to + 32) = part[1];
+    }
   }
-  if (cb0 < cb1) store_panel(panel[grp][0], l);
+  store_panel(panel[grp][0], l0);
   __syncthreads();
   const float s = p.s[tile.a];
   const uint8_t* pa = ps + (RW == 4 ? 16 * wave + li : li) * PROW + (g >> 1) * 32 + (g & 1) * 16;
   floatx4 acc[8];
-#pragma unroll
-  for (int f = 0; f < 8; ++f) acc[f] = floatx4{0.f, 0.f, 0.f, 0.f};
-  // RW = 1: every wave goes through the same barriers, one past the columns' end idly
-  const int total = RW == 4 ? (cb1 - cb0) * runs : runs;
-  int cb = cb0, run = 0;
-  for (int t = 0; t < total; ++t) {
-    int ncb = cb, nrun = run + 1;
-    if (nrun == runs) {
-      nrun = 0;
-      ++ncb;
-    }
-    const bool more = t + 1 < total && ncb < cb1, last = nrun == 0;
-    u32x4 nb[4];
-    if (more) {
-      load_panel(ncb, nrun, l);
-      if (last && p.base) load_base(ncb, nb);
-    }
-    uint8_t* const lp = panel[grp][NB == 2 ? t & 1 : 0];
+  auto multiply = [&](const uint8_t* lp, int run) {
 #pragma unroll
     for (int st = 0; st < NJ; ++st) {
+      if (NJ > 1 && run * RC + 16 * st >= r16) break;  // the same for all; P's places past r16 hold nothing
       const bf16x8 a = *(const bf16x8*)(pa + (run * NJ + st) * 64);
-      const bool some = run * RC + 16 * st < r16;  // the same for all; P's places past r16 hold nothing
-      if (some) {
 #pragma unroll
-        for (int f = 0; f < 8; ++f) {
-          bf16x8 w;
-          if constexpr (JMAJOR)
-            w = lds_tr8(lp + (16 * st + 8 * (g & 1) + (li >> 2)) * LROW + 2 * (16 * f + 4 * (li & 3)), LROW);
-          else w = *(const bf16x8*)(lp + (16 * f + li) * LROW + 2 * (16 * st + 8 * (g & 1)));
-          acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w, acc[f], 0, 0, 0);
+      for (int f = 0; f < 8; ++f) {
+        bf16x8 w;
+        if constexpr (JMAJOR)
+          w = lds_tr8(const_cast<uint8_t*>(lp) + (16 * st + 8 * (g & 1) + (li >> 2)) * LROW + 2 * (16 * f + 4 * (li & 3)),
+                      LROW);
+        else w = *(const bf16x8*)(lp + (16 * f + li) * LROW + 2 * (16 * st + 8 * (g & 1)));
+        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w, acc[f], 0, 0, 0);
+      }
+    }
+  };
+  auto clear = [&]() {
+#pragma unroll
+    for (int f = 0; f < 8; ++f) acc[f] = floatx4{0.f, 0.f, 0.f, 0.f};
+  };
+  auto write = [&](int cb, const u32x4 (&b)[4], auto all) {
+    const int64_t c = (int64_t)cb * 128 + 8 * li;
+    u32x4 o[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t w = b[v][k] & keep;
+        o[v][k] = pack_bf16x2(__builtin_fmaf(s, acc[2 * k][v], __builtin_bit_cast(float, w << 16)),
+                              __builtin_fmaf(s, acc[2 * k + 1][v], __builtin_bit_cast(float, w & 0xFFFF0000u)));
+      }
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (decltype(all)::value || (at[v] >= 0 && c < N)) *(u32x4*)(p.out + at[v] + c) = o[v];
+  };
+  if constexpr (NB == 1) {
+    // one block a wave
+    clear();
+    for (int run = 0; run < runs; ++run) {
+      if (run + 1 < runs) load_panel_no(run + 1, l0);
+      multiply(panel[grp][0], run);
+      if (run + 1 < runs) {
+        __syncthreads();  // the panel's reads are done
+        store_panel(panel[grp][0], l0);
+        __syncthreads();
+      }
+    }
+    write(cb0, b0, std::false_type{});
+  } else {
+    // Block cb, from panel i on, of which the next one's pieces are in `l` (the other set
+    // takes the one after that).  Whole tiles have a loop of their own, whose writes stand
+    // under no condition: the compiler then knows how many are on their way, and waits for
+    // no more of them than it has to.
+    auto one = [&](int i, int run, const u32x4 (&l)[PL], u32x4 (&after)[PL]) {
+      load_panel_no(i + 2, after);
+      multiply(panel[0][i & 1], run);
+      store_panel(panel[0][(i + 1) & 1], l);
+    };
+    auto go = [&](auto all) {
+      if constexpr (RMAX == RC) {
+        auto block = [&](int cb, const u32x4 (&b)[4], u32x4 (&nb)[4], const u32x4 (&l)[PL], u32x4 (&after)[PL]) {
+          load_base(min(cb + 1, cb1 - 1), nb);
+          clear();
+          one(cb - cb0, 0, l, after);
+          write(cb, b, all);
+          __syncthreads();
+        };
+        int cb = cb0;
+        for (; cb + 1 < cb1; cb += 2) {
+          block(cb, b0, b1, l1, l0);
+          block(cb + 1, b1, b0, l0, l1);
+        }
+        if (cb < cb1) block(cb, b0, b1, l1, l0);
+      } else {
+        for (int cb = cb0, i = 0; cb < cb1; ++cb) {
+          load_base(cb, b0);
+          clear();
+          for (int run = 0; run < runs; ++run, ++i) {
+            one(i, run, l1, l0);
+#pragma unroll
+            for (int k = 0; k < PL; ++k) l1[k] = l0[k];
+            __syncthreads();
+          }
+          write(cb, b0, all);
         }
       }
-    }
-    if (last) {
-      const int64_t c = (int64_t)cb * 128 + 8 * li;
+    };
+    bool all = (int64_t)cb1 * 128 <= N;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        u32x4 o;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          o[k] = pack_bf16x2(__builtin_fmaf(s, acc[2 * k][v], __builtin_bit_cast(float, b[v][k] << 16)),
-                             __builtin_fmaf(s, acc[2 * k + 1][v], __builtin_bit_cast(float, b[v][k] & 0xFFFF0000u)));
-        if (at[v] >= 0 && c < N && cb < cb1) *(u32x4*)(p.out + at[v] + c) = o;
-      }
-#pragma unroll
-      for (int f = 0; f < 8; ++f) acc[f] = floatx4{0.f, 0.f, 0.f, 0.f};
-      if (more && p.base) {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) b[v] = nb[v];
-      }
-    }
-    if (NB == 1 && t + 1 < total) __syncthreads();  // the panel's reads are done
-    if (more) store_panel(panel[grp][NB == 2 ? (t + 1) & 1 : 0], l);
-    if (t + 1 < total) __syncthreads();
-    cb = ncb;
-    run = nrun;
+    for (int v = 0; v < 4; ++v) all = all && at[v] >= 0;
+    if (__all(all)) go(std::true_type{});
+    else go(std::false_type{});
   }
 }
 
@@ -715,7 +783,7 @@ __global__ __launch_bounds__(512) void k_adapters_grad(AdapterRows rows, Adapter
   __shared__ __attribute__((aligned(1024))) uint8_t S1[SB];
   __shared__ __attribute__((aligned(1024))) uint8_t S2[SB];
   __shared__ __attribute__((aligned(1024))) uint8_t S3[SB];
-  __shared__ int list[kMaxAdapterItem];  // the tile's part of the order
+  __shared__ int list[kMaxAdapterItem + (ST + 1) * KR];
   auto buf = [&](int b) -> uint8_t* { return b == 0 ? S0 : b == 1 ? S1 : b == 2 ? S2 : S3; };
   const int n1 = (int)((p1.N + 255) / 256);
   const bool second = (int)blockIdx.x >= n1;
@@ -727,45 +795,50 @@ __global__ __launch_bounds__(512) void k_adapters_grad(AdapterRows rows, Adapter
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = p.r, j0 = blockIdx.z * 64;
   const int steps = (tile.p1 - tile.p0 + KR - 1) / KR;
-  const bool ordered = rows.order != nullptr;
-  if (ordered) {
-    for (int i = tid; i < tile.p1 - tile.p0; i += 512) list[i] = rows.order[tile.p0 + i];
-    __syncthreads();
-  }
-  // a step's row m, -1 where there is none
+  // the rows of every step, -1 where there is none
   const int count = tile.p1 - tile.p0;
-  auto row_of = [&](int t, int m) -> int64_t {
-    const int i = KR * t + m;
+  for (int i = tid; i < (steps + ST) * KR; i += 512) {
     int row = tile.p0 + i;
-    if (ordered) row = list[min(i, count - 1)];
-    return i < count && (uint64_t)(int64_t)row < (uint64_t)rows.M ? row : -1;
-  };
+    if (rows.order) row = rows.order[min(row, tile.p1 - 1)];
+    list[i] = i < count && (uint32_t)row < (uint32_t)rows.M ? row : -1;
+  }
+  __syncthreads();
   // Q: copy i has rows 2 (8 i + wave) and the next; P: pieces 64 k and on
-  int64_t qc = c0 + 8 * ((lane & 31) ^ (((2 * wave + (lane >> 5)) & 3) << 1));
+  const int qm = 2 * wave + (lane >> 5);
+  int64_t qc = c0 + 8 * ((lane & 31) ^ ((qm & 3) << 1 | (qm & 8)));
   qc = qc < N ? qc : 0;
-  int pm[PI], pc[PI];
+  const uint8_t* const qbase = (const uint8_t*)p.Q + 2 * qc;
+  const uint8_t* pbase[PI];
+  int pm[PI];
 #pragma unroll
   for (int i = 0; i < PI; ++i) {
     const int e = 64 * ((8 * i + wave) % NP) + lane;
     pm[i] = e / CPR;
-    pc[i] = e % CPR;
-    if (NJ == 4) pc[i] ^= ((pm[i] >> 1) & 1) << 1;
+    int c = e % CPR;
+    if (NJ == 4) c ^= (pm[i] & 2) | (pm[i] & 8) >> 1;
+    pbase[i] = (const uint8_t*)p.P3 + (blockIdx.z * CPR + c) * 16;
   }
-  auto copy = [&](int t, int b) {
-    uint8_t* const to = buf(b);  // (steps past the last are all zeros, and not used)
+  const uint32_t qstride = (uint32_t)N * 2, pstride = gridDim.z * PROW;
+  int rq[2], rp[PI];  // rows of the next copies
+  auto next_rows = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) rq[i] = list[KR * t + 16 * i + qm];
+#pragma unroll
+    for (int i = 0; i < PI; ++i) rp[i] = list[KR * t + pm[i]];
+  };
+  auto copy = [&](int b) {
+    uint8_t* const to = buf(b);  // (a step past the last is all zeros, and not used)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int64_t row = row_of(t, 2 * (8 * i + wave) + (lane >> 5));
-      const void* there = (const uint16_t*)p.Q + row * N + qc;
-      const void* from = row < 0 ? p.zero : there;
-      __builtin_amdgcn_global_load_lds((global_ptr_t)from, (lds_ptr_t)(to + (8 * i + wave) * 1024), 16, 0, 0);
+      const void* there = qbase + (uint64_t)(uint32_t)rq[i] * qstride;
+      __builtin_amdgcn_global_load_lds((global_ptr_t)(rq[i] < 0 ? p.zero : there),
+                                       (lds_ptr_t)(to + (8 * i + wave) * 1024), 16, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < PI; ++i) {
-      const int64_t row = row_of(t, pm[i]);
-      const void* there = p.P3 + ((row * gridDim.z + blockIdx.z) * CPR + pc[i]) * 8;
-      const void* from = row < 0 ? p.zero : there;
-      __builtin_amdgcn_global_load_lds((global_ptr_t)from, (lds_ptr_t)(to + QB + (8 * i + wave) % NP * 1024), 16, 0, 0);
+      const void* there = pbase[i] + (uint64_t)(uint32_t)rp[i] * pstride;
+      __builtin_amdgcn_global_load_lds((global_ptr_t)(rp[i] < 0 ? p.zero : there),
+                                       (lds_ptr_t)(to + QB + (8 * i + wave) % NP * 1024), 16, 0, 0);
     }
   };
   const int wj = wave / CW, wc = wave % CW;
@@ -779,22 +852,25 @@ __global__ __launch_bounds__(512) void k_adapters_grad(AdapterRows rows, Adapter
   uint32_t pa[FJ], qa[FC];
 #pragma unroll
   for (int j = 0; j < FJ; ++j)
-    pa[j] = QB + (8 * g + e) * PROW + (((2 * (wj * FJ + j) + (q >> 1)) ^ (NJ == 4 ? e & 2 : 0)) << 4) + ((q & 1) << 3);
+    pa[j] = QB + (8 * g + e) * PROW +
+            (((2 * (wj * FJ + j) + (q >> 1)) ^ (NJ == 4 ? (e & 2) | (g & 1) << 2 : 0)) << 4) + ((q & 1) << 3);
 #pragma unroll
   for (int c = 0; c < FC; ++c)
-    qa[c] = (8 * g + e) * 512 + (((2 * (wc * FC + c) + (q >> 1)) ^ (e << 1)) << 4) + ((q & 1) << 3);
-  auto compute = [&](int b) {
+    qa[c] = (8 * g + e) * 512 + (((2 * (wc * FC + c) + (q >> 1)) ^ (e << 1 | (g & 1) << 3)) << 4) + ((q & 1) << 3);
+  bf16x8 fp[FJ][3], fq[FC];
+  auto read = [&](int b) {
     const uint32_t at = lds_at(buf(b));
     uint32_t pt[FJ], qt[FC];
 #pragma unroll
     for (int j = 0; j < FJ; ++j) pt[j] = at + pa[j];
 #pragma unroll
     for (int c = 0; c < FC; ++c) qt[c] = at + qa[c];
-    bf16x8 fp[FJ][3], fq[FC];
     if constexpr (FC == 4) tr_read4<512>(qt, fq);
     else tr_read2<512>(qt, fq);
     if constexpr (FJ == 2) tr_read6<PROW, 2 * RP>(pt, fp);
     else tr_read3<PROW, 2 * RP>(pt[0], fp[0]);
+  };
+  auto multiply = [&]() {
 #pragma unroll
     for (int w = 2; w >= 0; --w)
 #pragma unroll
@@ -803,6 +879,9 @@ __global__ __launch_bounds__(512) void k_adapters_grad(AdapterRows rows, Adapter
         for (int j = 0; j < FJ; ++j)
           acc[j][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp[j][w], fq[c], acc[j][c], 0, 0, 0);
   };
+  // The two waves of a SIMD take turns with LDS and the matrix cores: the lower four read
+  // a step and multiply it, the upper four multiply the step before and read.
+  const bool early = wave < 4;
   auto step = [&](int t, int b) {
     // this step's copies are there, everybody's, and the reads of the step before are done
     __builtin_amdgcn_sched_barrier(0);
@@ -810,18 +889,30 @@ __global__ __launch_bounds__(512) void k_adapters_grad(AdapterRows rows, Adapter
     __builtin_amdgcn_s_waitcnt(wait_vm((ST - 2) * C) & kWaitLds);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    copy(t + ST - 1, (b + ST - 1) % ST);
+    copy((b + ST - 1) % ST);
+    next_rows(t + ST);
     __builtin_amdgcn_sched_barrier(0);
-    compute(b);
+    if (early) {
+      read(b);
+      multiply();
+    } else {
+      if (t > 0) multiply();
+      read(b);
+    }
   };
 #pragma unroll
-  for (int b = 0; b < ST - 1; ++b) copy(b, b);
+  for (int b = 0; b < ST - 1; ++b) {
+    next_rows(b);
+    copy(b);
+  }
+  next_rows(ST - 1);
   for (int t = 0; t < steps; t += ST) {
     step(t, 0);
 #pragma unroll
     for (int b = 1; b < ST; ++b)
       if (t + b < steps) step(t + b, b);
   }
+  if (!early) multiply();
   const float s = tile.whole ? p.s[tile.a] : 1.f;
   float* out = tile.whole ? p.out + (int64_t)tile.a * r * N : p.part + (int64_t)blockIdx.y * r * N;
 #pragma unroll
@@ -1064,19 +1155,19 @@ hipError_t wide_of(const AdapterWide& p, dim3 gr, hipStream_t st) {
   return hipGetLastError();
 }
 
-hipError_t wide(const AdapterCall& c, const AdapterPlan& pl, const float* part, const uint16_t* L, bool jmajor,
-                int64_t N, const uint16_t* base, uint16_t* out, float* T_out, const Split3& split, hipStream_t st) {
+hipError_t wide(const AdapterCall& c, const AdapterPlan& pl, const float* part, int splits, const uint16_t* L,
+                bool jmajor, int64_t N, const uint16_t* base, uint16_t* out, float* T_out, hipStream_t st) {
   const bool few = pl.bm == 16;
   int64_t tiles;
   const int blocks = plan_adapters_wide(c.rows.M, c.rows.n, few, N, &tiles);
-  AdapterWide p{c.rows, part, pl.splits, L, N, c.r, c.s, base, out, T_out, blocks, split};
+  AdapterWide p{c.rows, part, splits, L, N, c.r, c.s, base, out, T_out, blocks};
   const int64_t nb = (N + 127) / 128;
   const dim3 gr((unsigned)tiles, (unsigned)(few ? (nb + 3) / 4 : (nb + blocks - 1) / blocks));
   if (few) return jmajor ? wide_of<true, 1>(p, gr, st) : wide_of<false, 1>(p, gr, st);
   return jmajor ? wide_of<true, 4>(p, gr, st) : wide_of<false, 4>(p, gr, st);
 }
 
-// The splits' sum, as it is or in three parts (where no input gradient's kernel leaves it).
+// The splits' sum, as it is, in three parts, or both.
 __global__ __launch_bounds__(256) void k_adapters_sum(const float* __restrict__ part, int64_t size, int splits, int r,
                                                       float* __restrict__ out, Split3 split) {
   const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
@@ -1114,7 +1205,7 @@ hipError_t launch_adapters_fwd(const AdapterCall& c, const uint16_t* X, const ui
   const AdapterPlan pl = plan_adapters_rows(c.rows.M, c.rows.n, c.h);
   hipError_t e = narrow(c, pl, X, c.h, c.L1, true, (float*)ws, Split3{}, st);
   if (e != hipSuccess) return e;
-  return wide(c, pl, (const float*)ws, c.L2, true, c.o, base, Y, T_out, Split3{}, st);
+  return wide(c, pl, (const float*)ws, pl.splits, c.L2, true, c.o, base, Y, T_out, st);
 }
 
 hipError_t launch_adapters_bwd(const AdapterCall& c, const void* X, int x8, const float* x_scales, const uint16_t* dY,
@@ -1129,21 +1220,22 @@ hipError_t launch_adapters_bwd(const AdapterCall& c, const void* X, int x8, cons
   const int nz = (c.r + 63) / 64, rp = c.r <= 16 ? 16 : c.r <= 32 ? 32 : 64;
   const Split3 t3{T, (uint16_t*)(w + sp.t3), w, nz, rp};
   // G for the products over rows: three parts, or fp32 beside 8-bit codes
-  const Split3 g3{nullptr, x8 ? nullptr : (uint16_t*)(w + sp.g), nullptr, nz, rp};
-  float* const G = !x8 ? nullptr : pl.splits > 1 ? (float*)(w + sp.g) : gparts;
-  float* const G_out = G == gparts ? nullptr : G;
+  const Split3 g3{nullptr, x8 ? nullptr : (uint16_t*)(w + sp.g3), nullptr, nz, rp};
+  float* const G = pl.splits > 1 ? (float*)(w + sp.g) : gparts;
+  float* const G_out = pl.splits > 1 ? G : nullptr;
   hipError_t e = narrow(c, pl, dY, c.o, c.L2, false, gparts, t3, st);
   if (e != hipSuccess) return e;
-  // dX's kernel joins G's splits and leaves their sum
-  if (dX) {
-    e = wide(c, pl, gparts, c.L1, false, c.h, base, dX, G_out, g3, st);
-  } else if (G_out || g3.to) {
+  if (G_out || g3.to) {
     const int64_t size = c.rows.M * c.r;
     hipLaunchKernelGGL(k_adapters_sum, dim3((unsigned)((size + 1023) / 1024)), dim3(256), 0, st, gparts, size,
                        pl.splits, c.r, G_out, g3);
     e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  if (e != hipSuccess) return e;
+  if (dX) {
+    e = wide(c, pl, G_out ? G_out : gparts, G_out ? 1 : pl.splits, c.L1, false, c.h, base, dX, nullptr, st);
+    if (e != hipSuccess) return e;
+  }
   const AdapterGrad g1{X, x_scales, c.h, G, g3.to, c.r, c.s, it.item, it.items, 1, parts, dL1, w};
   const AdapterGrad g2{dY, nullptr, c.o, nullptr, t3.to, c.r, c.s, it.item, it.items, 0,
                        parts + it.items * c.r * c.h, dL2, w};

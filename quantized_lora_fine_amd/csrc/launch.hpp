@@ -244,7 +244,6 @@ struct AdapterWide {
   uint16_t* out;
   float* T_out;  // the joined parts, or NULL
   int blocks;    // blocks of 128 columns a workgroup goes over
-  Split3 split;  // the joined parts in this form too, where `to` is set
 };
 struct AdapterGrad {
   const void* Q;          // [M][N], bf16 or codes
@@ -281,7 +280,7 @@ struct AdapterItems {
 AdapterItems plan_adapters_items(int64_t M, int n, int64_t h, int64_t o, int r);
 // Byte offsets of the parts of the backward pass's workspace; the zeros come first.
 struct AdapterGradSpace {
-  size_t gparts, g, t3, parts, total;
+  size_t gparts, g, g3, t3, parts, total;
 };
 AdapterGradSpace plan_adapters_space(int64_t M, int n, int64_t h, int64_t o, int r);
 NF4K_WEAK hipError_t launch_adapters_fwd(const AdapterCall& c, const uint16_t* X, const uint16_t* base, uint16_t* Y,

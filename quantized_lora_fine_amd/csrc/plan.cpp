@@ -138,8 +138,8 @@ int plan_adapters_wide(int64_t M, int n, bool few, int64_t N, int64_t* tiles) {
   *tiles = adapter_tiles(M, n, few ? 16 : 64);
   const int64_t blocks = (N + 127) / 128;
   if (few) return 1;
-  // about 1024 workgroups
-  const int64_t each = *tiles * blocks / 1024;
+  // about 3072 workgroups
+  const int64_t each = *tiles * blocks / 3072;
   return (int)std::max<int64_t>(1, std::min(each, blocks));
 }
 
@@ -171,7 +171,8 @@ AdapterGradSpace plan_adapters_space(int64_t M, int n, int64_t h, int64_t o, int
   const int64_t rp = r <= 16 ? 16 : r <= 32 ? 32 : 64, three = M * ((r + 63) / 64) * 3 * rp * 2;
   s.gparts = kZeroBytes;
   s.g = s.gparts + (size_t)plan_adapters_rows(M, n, o).splits * M * r * 4;
-  s.t3 = s.g + (size_t)three;
+  s.g3 = s.g + (size_t)M * r * 4;
+  s.t3 = s.g3 + (size_t)three;
   s.parts = s.t3 + (size_t)three;
   s.total = s.parts + (size_t)plan_adapters_items(M, n, h, o, r).items * r * (h + o) * 4;
   return s;
