@@ -345,6 +345,44 @@ __device__ __forceinline__ void tr_read_rows(const uint32_t (&at)[2 * N], bf16x8
 #pragma unroll
   for (int i = 0; i < N; ++i) f[i] = halves(v[2 * i], v[2 * i + 1]);
 }
+// 8 rows of a column of codes, as bf16; `at`: the lane's 8 columns in row 8 g + (lane & 15) / 2
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+template <bool E5M2>
+__device__ __forceinline__ bf16x8 codes8(u32x2 v) {
+  u32x4 o;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float x[4];
+    unpack_fp8x4<E5M2>(v[i], x);
+    o[2 * i] = pack_bf16x2(x[0], x[1]);
+    o[2 * i + 1] = pack_bf16x2(x[2], x[3]);
+  }
+  return __builtin_bit_cast(bf16x8, o);
+}
+template <bool E5M2, int N>
+__device__ __forceinline__ void tr_read8(const uint32_t (&at)[N], bf16x8 (&f)[N]) {
+  u32x2 v[N];
+  if constexpr (N == 2) {
+    asm volatile(
+        "ds_read_b64_tr_b8 %0, %2\n"
+        "ds_read_b64_tr_b8 %1, %3\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1])
+        : "v"(at[0]), "v"(at[1]));
+  } else {
+    static_assert(N == 4, "2 or 4 fragments");
+    asm volatile(
+        "ds_read_b64_tr_b8 %0, %4\n"
+        "ds_read_b64_tr_b8 %1, %5\n"
+        "ds_read_b64_tr_b8 %2, %6\n"
+        "ds_read_b64_tr_b8 %3, %7\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+        : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]));
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = codes8<E5M2>(v[i]);
+}
 // the three parts of a fragment, PART bytes apart
 template <int ROW, int PART>
 __device__ __forceinline__ void tr_read3(uint32_t at, bf16x8 (&f)[3]) {
@@ -548,7 +586,7 @@ template <bool JMAJOR, int NJ, int RW, int RMAX>
 __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
   constexpr int BM = 16 * RW, RC = 16 * NJ;
   constexpr int NB = RW == 4 ? 2 : 1, G = 4 / RW, TG = 64 * RW;  // panel buffers; groups of waves, their threads
-  constexpr int LROW = JMAJOR ? 128 * 2 + 32 : RC * 2 + 16;      // LDS bytes of a row of the panel
+  constexpr int LROW = JMAJOR ? 128 * 2 + 32 : RC * 2;           // LDS bytes of a row of the panel
   constexpr int PB = JMAJOR ? RC * LROW : 128 * LROW;
   constexpr int PL = 128 * RC / 8 / TG;                          // 16-byte pieces of a panel a thread
   constexpr int PROW = RMAX * 4 + 16;                            // of a row of P: for each 16 of the rank hi, then lo
@@ -593,6 +631,12 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
       if (j >= r) l[i] = u32x4{0u, 0u, 0u, 0u};  // P's zeros there are multiplied by it
     }
   };
+  // Pieces of 16 bytes of a row of L1's panel stand XORed by this, so that the 16 lanes that
+  // LDS serves at once (0-3, 12-15 and 20-27, and so on) read from different banks.
+  auto place = [](int row) -> int {
+    const int k = row >> 2 & 3;
+    return NJ == 4 ? row & 7 : NJ == 2 ? (k & 1) << 1 ^ (k >> 1) * 3 : 0;
+  };
   auto store_panel = [&](uint8_t* to, const u32x4 (&l)[PL]) {
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
@@ -605,8 +649,8 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
           *(uint16_t*)(at + 64 * k + 32) = (uint16_t)(l[i][k] >> 16);
         }
       } else {
-        const int c = e / (RC / 8);
-        *(u32x4*)(to + ((c & 7) * 16 + (c >> 3)) * LROW + 16 * (e % (RC / 8))) = l[i];
+        const int c = e / (RC / 8), row = (c & 7) * 16 + (c >> 3);
+        *(u32x4*)(to + row * LROW + ((e % (RC / 8) ^ place(row)) << 4)) = l[i];
       }
     }
   };
@@ -675,7 +719,7 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
         if constexpr (JMAJOR)
           w = lds_tr8(const_cast<uint8_t*>(lp) + (16 * st + 8 * (g & 1) + (li >> 2)) * LROW + 2 * (16 * f + 4 * (li & 3)),
                       LROW);
-        else w = *(const bf16x8*)(lp + (16 * f + li) * LROW + 2 * (16 * st + 8 * (g & 1)));
+        else w = *(const bf16x8*)(lp + (16 * f + li) * LROW + (((2 * st + (g & 1)) ^ place(li)) << 4));
         acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w, acc[f], 0, 0, 0);
       }
     }
@@ -762,33 +806,46 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
 // ---------------------------------------------------------------------------
 // dL[a][j][c] (or [c][j]) = s[a] sum over a's rows of P[m][j] Q[m][c]: a workgroup has
 // 256 columns of Q, 16 NJ of the rank (blockIdx.z: which 64) and up to p.item rows of an
-// adapter (blockIdx.y).  P is given as three bf16 parts.  Both are copied straight into LDS,
-// 32 rows a step through a ring of buffers, ST - 1 steps under way, and read with
-// transposing reads: the products contract the rows.  Rows past the tile come from zeros.
-// 16-byte pieces stand XORed by the row, so that the 4 rows of a transposing read fall on
-// different banks.  An adapter whose rows are all here is written out, otherwise the item's
-// sums go to a part of their own, which k_adapters_join adds in order.  One launch has
-// dL1's columns and then dL2's.
+// adapter (blockIdx.y).  Both operands are copied straight into LDS, 32 rows a step through
+// a ring of ST buffers, and read with transposing reads: the products contract the rows.
+// Rows past the tile come from zeros.  16-byte pieces stand XORed by the row, so that the
+// lanes that LDS serves at once fall on different banks.  An adapter whose rows are all here
+// is written out, otherwise the item's sums go to a part of their own, which
+// k_adapters_join adds in order.
+//
+// bf16 (X8 0): P comes as three bf16 parts, made once for all columns.
+// 8 bits (X8 1: e4m3, 2: e5m2): the codes are read transposed and become bf16 in registers;
+// P comes in fp32 and is multiplied by the scales of its row, one for each 128 columns, and
+// split a step ahead into tiles beside the ring.
+//
+// The two waves of a SIMD take turns: the lower four read a step and multiply it (and split
+// before), the upper four multiply the step before and read (and split last).
 // ---------------------------------------------------------------------------
-template <int NJ>
-__global__ __launch_bounds__(512) void k_adapters_grad(AdapterRows rows, AdapterGrad p1, AdapterGrad p2) {
-  constexpr int KR = 32, RP = 16 * NJ, ST = 4;
+template <int X8, int NJ>
+struct GradTile {
+  static constexpr int KR = 32, RP = 16 * NJ, ST = X8 ? 5 : 4;
+  static constexpr int PROW = 3 * RP * 2;                         // LDS bytes of a row of P's parts
+  static constexpr int QROW = X8 ? 256 : 512, QB = KR * QROW;     // of Q
+  static constexpr int PB = X8 ? KR * RP * 4 : KR * PROW;         // of P as it is copied
+  static constexpr int SB = QB + PB + (X8 ? 256 : 0);             // a buffer, with the scales
+  // behind the ring P's parts for two blocks of columns, of two steps
+  static constexpr int SMEM = ST * SB + (X8 ? 4 * KR * PROW : 0);
+  static constexpr int LIST = kMaxAdapterItem + (ST + 1) * KR;
+};
+
+template <int X8, int NJ>
+__device__ __forceinline__ void grad_tile(const AdapterRows& rows, const AdapterGrad& p, int cblock, uint8_t* ring,
+                                          int* list) {
+  using G = GradTile<X8, NJ>;
+  constexpr int KR = G::KR, RP = G::RP, ST = G::ST, PROW = G::PROW, QB = G::QB, SB = G::SB;
   constexpr int JW = NJ == 4 ? 2 : 1, CW = 8 / JW;      // waves over the rank and over the columns
   constexpr int FJ = NJ / JW, FC = 16 / CW;             // a wave's fragments
-  constexpr int QB = KR * 512, PROW = 3 * RP * 2, CPR = PROW / 16;
-  constexpr int SB = QB + KR * PROW;
-  constexpr int NP = KR * CPR / 64, PI = NJ == 4 ? 2 : 1;  // 1 KB copies of P a step, and of a wave
-  constexpr int C = 2 + PI;                                // copies of a wave and step
-  __shared__ __attribute__((aligned(1024))) uint8_t S0[SB];
-  __shared__ __attribute__((aligned(1024))) uint8_t S1[SB];
-  __shared__ __attribute__((aligned(1024))) uint8_t S2[SB];
-  __shared__ __attribute__((aligned(1024))) uint8_t S3[SB];
-  __shared__ int list[kMaxAdapterItem + (ST + 1) * KR];
-  auto buf = [&](int b) -> uint8_t* { return b == 0 ? S0 : b == 1 ? S1 : b == 2 ? S2 : S3; };
-  const int n1 = (int)((p1.N + 255) / 256);
-  const bool second = (int)blockIdx.x >= n1;
-  const AdapterGrad& p = second ? p2 : p1;
-  const int64_t N = p.N, c0 = (int64_t)(second ? blockIdx.x - n1 : blockIdx.x) * 256;
+  constexpr int QI = X8 ? 1 : 2;                        // 1 KB copies of Q a wave and step
+  constexpr int NP = G::PB / 1024;                      // of P a step
+  constexpr int PI = NP > 8 ? 2 : 1;                    // and a wave
+  constexpr int C = QI + PI + (X8 ? 1 : 0);             // copies of a wave and step
+  const uint32_t split = lds_at(ring) + ST * SB;
+  const int64_t N = p.N, c0 = (int64_t)cblock * 256;
   Tile tile;
   if (!find_tile(rows, p.item, blockIdx.y, tile)) return;
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4;
@@ -803,11 +860,14 @@ __global__ __launch_bounds__(512) void k_adapters_grad(AdapterRows rows, Adapter
     list[i] = i < count && (uint32_t)row < (uint32_t)rows.M ? row : -1;
   }
   __syncthreads();
-  // Q: copy i has rows 2 (8 i + wave) and the next; P: pieces 64 k and on
-  const int qm = 2 * wave + (lane >> 5);
-  int64_t qc = c0 + 8 * ((lane & 31) ^ ((qm & 3) << 1 | (qm & 8)));
+
+  // where this lane's pieces come from; Q: rows 2 (8 i + wave) and the next (X8: 4 wave to + 3)
+  const int qm = X8 ? 4 * wave + (lane >> 4) : 2 * wave + (lane >> 5);
+  int64_t qc = X8 ? c0 + 16 * ((lane & 15) ^ (qm & 15)) : c0 + 8 * ((lane & 31) ^ ((qm & 3) << 1 | (qm & 8)));
   qc = qc < N ? qc : 0;
-  const uint8_t* const qbase = (const uint8_t*)p.Q + 2 * qc;
+  const uint8_t* const qbase = (const uint8_t*)p.Q + (X8 ? 1 : 2) * qc;
+  const uint32_t qstride = (uint32_t)N * (X8 ? 1 : 2);
+  constexpr int CPR = X8 ? RP / 4 : PROW / 16;  // pieces of a row of P
   const uint8_t* pbase[PI];
   int pm[PI];
 #pragma unroll
@@ -815,21 +875,28 @@ __global__ __launch_bounds__(512) void k_adapters_grad(AdapterRows rows, Adapter
     const int e = 64 * ((8 * i + wave) % NP) + lane;
     pm[i] = e / CPR;
     int c = e % CPR;
-    if (NJ == 4) c ^= (pm[i] & 2) | (pm[i] & 8) >> 1;
-    pbase[i] = (const uint8_t*)p.P3 + (blockIdx.z * CPR + c) * 16;
+    if constexpr (X8 != 0) {
+      pbase[i] = j0 + 4 * c < r ? (const uint8_t*)(p.P + j0 + 4 * c) : nullptr;
+    } else {
+      if (NJ == 4) c ^= (pm[i] & 2) | (pm[i] & 8) >> 1;
+      pbase[i] = (const uint8_t*)p.P3 + (blockIdx.z * CPR + c) * 16;
+    }
   }
-  const uint32_t qstride = (uint32_t)N * 2, pstride = gridDim.z * PROW;
-  int rq[2], rp[PI];  // rows of the next copies
+  const uint32_t pstride = X8 ? (uint32_t)r * 4 : gridDim.z * PROW;
+  const int kb = (int)((N + 127) / 128);
+  const float* const sbase = X8 ? p.q_scales + min(2 * cblock + (lane & 1), kb - 1) : nullptr;
+  int rq[QI], rp[PI], rs = 0;  // rows of the next copies
   auto next_rows = [&](int t) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) rq[i] = list[KR * t + 16 * i + qm];
+    for (int i = 0; i < QI; ++i) rq[i] = list[KR * t + 16 * i + qm];
 #pragma unroll
     for (int i = 0; i < PI; ++i) rp[i] = list[KR * t + pm[i]];
+    if constexpr (X8 != 0) rs = list[KR * t + (lane >> 1)];
   };
   auto copy = [&](int b) {
-    uint8_t* const to = buf(b);  // (a step past the last is all zeros, and not used)
+    uint8_t* const to = ring + b * SB;  // (a step past the last is all zeros, and not used)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < QI; ++i) {
       const void* there = qbase + (uint64_t)(uint32_t)rq[i] * qstride;
       __builtin_amdgcn_global_load_lds((global_ptr_t)(rq[i] < 0 ? p.zero : there),
                                        (lds_ptr_t)(to + (8 * i + wave) * 1024), 16, 0, 0);
@@ -837,10 +904,15 @@ __global__ __launch_bounds__(512) void k_adapters_grad(AdapterRows rows, Adapter
 #pragma unroll
     for (int i = 0; i < PI; ++i) {
       const void* there = pbase[i] + (uint64_t)(uint32_t)rp[i] * pstride;
-      __builtin_amdgcn_global_load_lds((global_ptr_t)(rp[i] < 0 ? p.zero : there),
+      __builtin_amdgcn_global_load_lds((global_ptr_t)(rp[i] < 0 || (X8 && !pbase[i]) ? p.zero : there),
                                        (lds_ptr_t)(to + QB + (8 * i + wave) % NP * 1024), 16, 0, 0);
     }
+    if constexpr (X8 != 0) {  // every wave copies the same scales
+      const void* there = sbase + (uint64_t)(uint32_t)rs * (uint32_t)kb;
+      __builtin_amdgcn_global_load_lds((global_ptr_t)(rs < 0 ? p.zero : there), (lds_ptr_t)(to + QB + G::PB), 4, 0, 0);
+    }
   };
+
   const int wj = wave / CW, wc = wave % CW;
   const int e = li >> 2, q = li & 3;
   floatx4 acc[FJ][FC];
@@ -848,24 +920,30 @@ __global__ __launch_bounds__(512) void k_adapters_grad(AdapterRows rows, Adapter
   for (int j = 0; j < FJ; ++j)
 #pragma unroll
     for (int c = 0; c < FC; ++c) acc[j][c] = floatx4{0.f, 0.f, 0.f, 0.f};
-  // a lane's addresses within a buffer
+  // a lane's addresses within a buffer, and within a tile of P's parts
   uint32_t pa[FJ], qa[FC];
 #pragma unroll
   for (int j = 0; j < FJ; ++j)
-    pa[j] = QB + (8 * g + e) * PROW +
+    pa[j] = (8 * g + e) * PROW +
             (((2 * (wj * FJ + j) + (q >> 1)) ^ (NJ == 4 ? (e & 2) | (g & 1) << 2 : 0)) << 4) + ((q & 1) << 3);
 #pragma unroll
-  for (int c = 0; c < FC; ++c)
-    qa[c] = (8 * g + e) * 512 + (((2 * (wc * FC + c) + (q >> 1)) ^ (e << 1 | (g & 1) << 3)) << 4) + ((q & 1) << 3);
+  for (int c = 0; c < FC; ++c) {
+    const int f = wc * FC + c;
+    if constexpr (X8 != 0) qa[c] = (8 * g + (li >> 1)) * 256 + ((f ^ ((g & 1) << 3 | li >> 1)) << 4) + ((li & 1) << 3);
+    else qa[c] = (8 * g + e) * 512 + (((2 * f + (q >> 1)) ^ (e << 1 | (g & 1) << 3)) << 4) + ((q & 1) << 3);
+  }
   bf16x8 fp[FJ][3], fq[FC];
-  auto read = [&](int b) {
-    const uint32_t at = lds_at(buf(b));
+  auto read = [&](int t, int b) {
+    const uint32_t at = lds_at(ring) + b * SB;
+    const uint32_t parts =
+        X8 ? split + ((t & 1) * 2 + (wc * FC >> 3)) * (KR * PROW) : at + QB;
     uint32_t pt[FJ], qt[FC];
 #pragma unroll
-    for (int j = 0; j < FJ; ++j) pt[j] = at + pa[j];
+    for (int j = 0; j < FJ; ++j) pt[j] = parts + pa[j];
 #pragma unroll
     for (int c = 0; c < FC; ++c) qt[c] = at + qa[c];
-    if constexpr (FC == 4) tr_read4<512>(qt, fq);
+    if constexpr (X8 != 0) tr_read8<X8 == 2, FC>(qt, fq);
+    else if constexpr (FC == 4) tr_read4<512>(qt, fq);
     else tr_read2<512>(qt, fq);
     if constexpr (FJ == 2) tr_read6<PROW, 2 * RP>(pt, fp);
     else tr_read3<PROW, 2 * RP>(pt[0], fp[0]);
@@ -879,25 +957,57 @@ __global__ __launch_bounds__(512) void k_adapters_grad(AdapterRows rows, Adapter
         for (int j = 0; j < FJ; ++j)
           acc[j][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp[j][w], fq[c], acc[j][c], 0, 0, 0);
   };
-  // The two waves of a SIMD take turns with LDS and the matrix cores: the lower four read
-  // a step and multiply it, the upper four multiply the step before and read.
+  // P's parts of step t, from buffer b, for both blocks of columns: a thread has 4 values
+  auto make_parts = [&](int t, int b) {
+    if (tid >= KR * RP / 4) return;
+    const int m = tid / (RP / 4), j = 4 * (tid % (RP / 4));
+    const uint32_t at = lds_at(ring) + b * SB + QB;
+    floatx4 v;
+    floatx2 sc;
+    asm volatile("ds_read_b128 %0, %2\n"
+                 "ds_read_b64 %1, %3\n"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(v), "=&v"(sc)
+                 : "v"(at + 16 * tid), "v"(at + G::PB + 8 * m));
+    const int piece = (j >> 3) ^ (NJ == 4 ? (m & 2) | (m & 8) >> 1 : 0);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint2 part[3];
+      split4(v * sc[k], part);
+      // (in assembly for the same reason as the reads; the barrier's wait counts them)
+      asm volatile("ds_write_b64 %0, %1\n"
+                   "ds_write_b64 %0, %2 offset:%4\n"
+                   "ds_write_b64 %0, %3 offset:%5"
+                   :
+                   : "v"(split + ((t & 1) * 2 + k) * (KR * PROW) + m * PROW + (piece << 4) + (j & 4) * 2),
+                     "v"(u32x2{part[0].x, part[0].y}), "v"(u32x2{part[1].x, part[1].y}),
+                     "v"(u32x2{part[2].x, part[2].y}), "n"(2 * RP), "n"(4 * RP)
+                   : "memory");
+    }
+  };
   const bool early = wave < 4;
-  auto step = [&](int t, int b) {
-    // this step's copies are there, everybody's, and the reads of the step before are done
+  // X8: the parts of the next step are made in this one, so its copies have to be there
+  constexpr int kFly = X8 ? ST - 3 : ST - 2;
+  auto arrive = [&]() {
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(wait_vm((ST - 2) * C) & kWaitLds);
+    __builtin_amdgcn_s_waitcnt(wait_vm(kFly * C) & kWaitLds);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+  };
+  auto step = [&](int t, int b) {
+    arrive();  // the copies are there, everybody's, and the reads of the step before are done
     copy((b + ST - 1) % ST);
     next_rows(t + ST);
     __builtin_amdgcn_sched_barrier(0);
     if (early) {
-      read(b);
+      if constexpr (X8 != 0) make_parts(t + 1, (b + 1) % ST);
+      read(t, b);
       multiply();
     } else {
       if (t > 0) multiply();
-      read(b);
+      read(t, b);
+      if constexpr (X8 != 0) make_parts(t + 1, (b + 1) % ST);
     }
   };
 #pragma unroll
@@ -906,6 +1016,10 @@ __global__ __launch_bounds__(512) void k_adapters_grad(AdapterRows rows, Adapter
     copy(b);
   }
   next_rows(ST - 1);
+  if constexpr (X8 != 0) {
+    arrive();
+    make_parts(0, 0);
+  }
   for (int t = 0; t < steps; t += ST) {
     step(t, 0);
 #pragma unroll
@@ -933,161 +1047,16 @@ __global__ __launch_bounds__(512) void k_adapters_grad(AdapterRows rows, Adapter
   __builtin_amdgcn_s_waitcnt(0);  // no copy is on its way into LDS that is no longer this workgroup's
 }
 
-// ---------------------------------------------------------------------------
-// The same for Q in 8 bits (E5M2 or e4m3): 128 columns a workgroup, which share a row's
-// scale.  Codes become bf16 and P, fp32, is multiplied by the scale of its row and this
-// block of columns and split on their way from registers into LDS, 64 rows at a time, two
-// such steps under way.
-// ---------------------------------------------------------------------------
-template <bool E5M2, int NJ>
-__global__ __launch_bounds__(256) void k_adapters_grad8(AdapterRows rows, AdapterGrad p) {
-  constexpr int KR = 64, RP = 16 * NJ;
-  // 8 banks between neighbouring rows: the 4 rows of a transposing read fall on different ones
-  constexpr int QROW = 128 * 2 + 32, PROW = RP * 2 + 16;
-  constexpr int JW = NJ == 4 ? 2 : 1, CW = 4 / JW;      // waves over the rank and over the columns
-  constexpr int FJ = NJ / JW, FC = 8 / CW;              // a wave's fragments
-  constexpr int QL = 2;                                 // 16-byte loads of Q a thread
-  constexpr int PL = KR * RP / 4 / 256;                 // 4-value pieces of P a thread
-  constexpr int CP = 8;                                 // pieces of a row of Q
-  __shared__ __align__(16) uint8_t qs[KR * QROW];
-  __shared__ __align__(16) uint8_t ps[3 * KR * PROW];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, g = lane >> 4;
-  Tile tile;
-  if (!find_tile(rows, p.item, blockIdx.y, tile)) return;
-  const int cb = blockIdx.x;
-  const int64_t N = p.N, c0 = (int64_t)cb * 128;
-  const int r = p.r, j0 = blockIdx.z * 64;
-  const int64_t kb = (N + 127) / 128;
-  struct Stage {
-    u32x4 q[QL];
-    floatx4 v[PL];
-    float scale[PL];
-    uint32_t ok;  // which of the rows are there
-  };
-  // the rows of a step, one a lane; loaded a step before they are used
-  auto load_order = [&](int p0) -> int { return rows.order[min(p0 + lane, tile.p1 - 1)]; };
-  auto row_of = [&](int ord, int p0, int m, bool& ok) -> int64_t {
-    int row = p0 + m;
-    if (rows.order) row = __shfl(ord, m);
-    ok = p0 + m < tile.p1 && (uint64_t)(int64_t)row < (uint64_t)rows.M;
-    return ok ? row : 0;
-  };
-  auto load = [&](int p0, int ord, Stage& s) {
-    s.ok = 0;
-#pragma unroll
-    for (int i = 0; i < QL; ++i) {
-      const int e = 256 * i + tid;
-      bool ok;
-      const int64_t row = row_of(ord, p0, e / CP, ok);
-      const int64_t c = c0 + 16 * (e % CP);
-      s.q[i] = *(const u32x4*)((const uint8_t*)p.Q + row * N + (c < N ? c : 0));
-      s.ok |= ok ? 1u << i : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      const int e = 256 * i + tid, j = j0 + 4 * (e % (RP / 4));
-      bool ok;
-      const int64_t row = row_of(ord, p0, e / (RP / 4), ok);
-      s.v[i] = *(const floatx4*)(p.P + row * r + (j < r ? j : 0));
-      s.scale[i] = p.q_scales[row * kb + cb];
-      s.ok |= ok && j < r ? 256u << i : 0;
-    }
-  };
-  auto store = [&](Stage& s) {
-#pragma unroll
-    for (int i = 0; i < QL; ++i) {
-      const int e = 256 * i + tid;
-      uint8_t* to = qs + (e / CP) * QROW + (e % CP) * (256 / CP);
-      u32x4 v = s.q[i];
-      if (!(s.ok >> i & 1)) v = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        float a[4], b[4];
-        unpack_fp8x4<E5M2>(v[2 * hf], a);
-        unpack_fp8x4<E5M2>(v[2 * hf + 1], b);
-        *(u32x4*)(to + 16 * hf) = u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]),
-                                        pack_bf16x2(b[2], b[3])};
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      const int e = 256 * i + tid, m = e / (RP / 4), j = 4 * (e % (RP / 4));
-      floatx4 v = s.v[i] * s.scale[i];
-      if (!(s.ok >> (8 + i) & 1)) v = floatx4{0.f, 0.f, 0.f, 0.f};
-      uint2 part[3];
-      split4(v, part);
-#pragma unroll
-      for (int w = 0; w < 3; ++w) *(uint2*)(ps + (w * KR + m) * PROW + 2 * j) = part[w];
-    }
-  };
-  const int wj = wave / CW, wc = wave % CW;
-  floatx4 acc[FJ][FC];
-#pragma unroll
-  for (int j = 0; j < FJ; ++j)
-#pragma unroll
-    for (int c = 0; c < FC; ++c) acc[j][c] = floatx4{0.f, 0.f, 0.f, 0.f};
-  auto compute = [&]() {
-#pragma unroll
-    for (int k = 0; k < KR; k += 32) {
-      const int tr = k + 8 * g + (li >> 2), tc = 4 * (li & 3);
-      bf16x8 fp[FJ][3];
-#pragma unroll
-      for (int j = 0; j < FJ; ++j)
-#pragma unroll
-        for (int w = 0; w < 3; ++w)
-          fp[j][w] = lds_tr8(ps + (w * KR + tr) * PROW + 2 * (16 * (wj * FJ + j) + tc), PROW);
-#pragma unroll
-      for (int c = 0; c < FC; ++c) {
-        const bf16x8 fq = lds_tr8(qs + tr * QROW + 2 * (16 * (wc * FC + c) + tc), QROW);
-#pragma unroll
-        for (int w = 2; w >= 0; --w)
-#pragma unroll
-          for (int j = 0; j < FJ; ++j)
-            acc[j][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp[j][w], fq, acc[j][c], 0, 0, 0);
-      }
-    }
-  };
-  Stage sa, sb;
-  int oa = 0, ob = 0;
-  if (rows.order) {
-    oa = load_order(tile.p0);
-    ob = load_order(tile.p0 + KR);
-  }
-  load(tile.p0, oa, sa);
-  load(tile.p0 + KR, ob, sb);
-  if (rows.order) {
-    oa = load_order(tile.p0 + 2 * KR);
-    ob = load_order(tile.p0 + 3 * KR);
-  }
-  auto step = [&](int p0, Stage& s, int& ord) {
-    __syncthreads();  // the reads of the step before are done
-    store(s);
-    load(p0 + 2 * KR, ord, s);
-    if (rows.order) ord = load_order(p0 + 4 * KR);
-    __syncthreads();
-    compute();
-  };
-  for (int p0 = tile.p0; p0 < tile.p1; p0 += 2 * KR) {
-    step(p0, sa, oa);
-    if (p0 + KR < tile.p1) step(p0 + KR, sb, ob);
-  }
-  const float s = tile.whole ? p.s[tile.a] : 1.f;
-  float* out = tile.whole ? p.out + (int64_t)tile.a * r * N : p.part + (int64_t)blockIdx.y * r * N;
-#pragma unroll
-  for (int j = 0; j < FJ; ++j)
-#pragma unroll
-    for (int c = 0; c < FC; ++c) {
-      const int jj = j0 + 16 * (wj * FJ + j) + 4 * g;
-      const int64_t cc = c0 + 16 * (wc * FC + c) + li;
-      if (jj >= r || cc >= N) continue;  // r % 4 == 0
-      const floatx4 o = acc[j][c] * s;
-      if (p.trans) {
-        *(floatx4*)(out + cc * r + jj) = o;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) out[(jj + i) * N + cc] = o[i];
-      }
-    }
+// dL1's columns, then dL2's (p1.N = 0: dL2's alone).
+template <int X8, int NJ>
+__global__ __launch_bounds__(512) void k_adapters_grad(AdapterRows rows, AdapterGrad p1, AdapterGrad p2) {
+  using G = GradTile<X8, NJ>;
+  using G0 = GradTile<0, NJ>;
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[G::SMEM > G0::SMEM ? G::SMEM : G0::SMEM];
+  __shared__ int list[G::LIST];
+  const int n1 = (int)((p1.N + 255) / 256), cb = blockIdx.x;
+  if (cb < n1) grad_tile<X8, NJ>(rows, p1, cb, ring, list);
+  else grad_tile<0, NJ>(rows, p2, cb - n1, ring, list);
 }
 
 // Outputs of adapters with several items: their parts' sums in order; with none: zeros.
@@ -1180,21 +1149,12 @@ __global__ __launch_bounds__(256) void k_adapters_sum(const float* __restrict__ 
   store3(split, e / r, (int)(e % r), three);
 }
 
-template <bool E5M2>
-hipError_t grad8_of(const AdapterRows& rows, const AdapterGrad& p, hipStream_t st) {
-  const dim3 gr((unsigned)((p.N + 127) / 128), (unsigned)p.items, (unsigned)((p.r + 63) / 64));
-  if (p.r <= 16) hipLaunchKernelGGL((k_adapters_grad8<E5M2, 1>), gr, dim3(256), 0, st, rows, p);
-  else if (p.r <= 32) hipLaunchKernelGGL((k_adapters_grad8<E5M2, 2>), gr, dim3(256), 0, st, rows, p);
-  else hipLaunchKernelGGL((k_adapters_grad8<E5M2, 4>), gr, dim3(256), 0, st, rows, p);
-  return hipGetLastError();
-}
-
-// dL1 and dL2, or (p1.N = 0) dL2 alone
-hipError_t grad(const AdapterRows& rows, const AdapterGrad& p1, const AdapterGrad& p2, hipStream_t st) {
+template <int X8>
+hipError_t grad_of(const AdapterRows& rows, const AdapterGrad& p1, const AdapterGrad& p2, hipStream_t st) {
   const dim3 gr((unsigned)((p1.N + 255) / 256 + (p2.N + 255) / 256), (unsigned)p2.items, (unsigned)((p2.r + 63) / 64));
-  if (p2.r <= 16) hipLaunchKernelGGL((k_adapters_grad<1>), gr, dim3(512), 0, st, rows, p1, p2);
-  else if (p2.r <= 32) hipLaunchKernelGGL((k_adapters_grad<2>), gr, dim3(512), 0, st, rows, p1, p2);
-  else hipLaunchKernelGGL((k_adapters_grad<4>), gr, dim3(512), 0, st, rows, p1, p2);
+  if (p2.r <= 16) hipLaunchKernelGGL((k_adapters_grad<X8, 1>), gr, dim3(512), 0, st, rows, p1, p2);
+  else if (p2.r <= 32) hipLaunchKernelGGL((k_adapters_grad<X8, 2>), gr, dim3(512), 0, st, rows, p1, p2);
+  else hipLaunchKernelGGL((k_adapters_grad<X8, 4>), gr, dim3(512), 0, st, rows, p1, p2);
   return hipGetLastError();
 }
 
@@ -1239,13 +1199,9 @@ hipError_t launch_adapters_bwd(const AdapterCall& c, const void* X, int x8, cons
   const AdapterGrad g1{X, x_scales, c.h, G, g3.to, c.r, c.s, it.item, it.items, 1, parts, dL1, w};
   const AdapterGrad g2{dY, nullptr, c.o, nullptr, t3.to, c.r, c.s, it.item, it.items, 0,
                        parts + it.items * c.r * c.h, dL2, w};
-  if (x8) {
-    e = x8 == 1 ? grad8_of<false>(c.rows, g1, st) : grad8_of<true>(c.rows, g1, st);
-    if (e != hipSuccess) return e;
-  }
-  AdapterGrad first = g1;
-  if (x8) first.N = 0;
-  e = grad(c.rows, first, g2, st);
+  e = x8 == 0   ? grad_of<0>(c.rows, g1, g2, st)
+      : x8 == 1 ? grad_of<1>(c.rows, g1, g2, st)
+                : grad_of<2>(c.rows, g1, g2, st);
   if (e != hipSuccess) return e;
   const int64_t most = std::max(c.h, c.o) * c.r;
   const dim3 gr((unsigned)std::min<int64_t>((most + 1023) / 1024, 1024), (unsigned)c.rows.n, 2);

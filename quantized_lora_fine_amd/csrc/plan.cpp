@@ -138,8 +138,10 @@ int plan_adapters_wide(int64_t M, int n, bool few, int64_t N, int64_t* tiles) {
   *tiles = adapter_tiles(M, n, few ? 16 : 64);
   const int64_t blocks = (N + 127) / 128;
   if (few) return 1;
-  // about 3072 workgroups
-  const int64_t each = *tiles * blocks / 3072;
+  // About 1024 workgroups (three are on a compute unit, so a second set is partly filled):
+  // 7977 rows by 11008 of rank 16 78 us, 8192 rows by 11008 of rank 64 94, against 103 and
+  // 116 for 256, 83 and 97 for 1536, 93 and 111 for 3072, whose starts are more of them.
+  const int64_t each = *tiles * blocks / 1024;
   return (int)std::max<int64_t>(1, std::min(each, blocks));
 }
 
