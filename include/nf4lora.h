@@ -674,7 +674,8 @@ nf4_status nf4_route_workspace_bytes(int64_t M, int32_t n, size_t *bytes);
  * rows and cols are multiples of 16, at most 2^22; M <= 2^26.  Products are of bf16
  * operands with fp32 sums; T stays fp32 (as two bf16 values in the second product, which
  * leave 2^-17 of each).  Adapters hold finite values.  M == 0 does nothing.
- *   ws      : nf4_adapters_workspace_bytes(NF4_OP_FWD, ...) bytes; one each for calls
+ *   ws      : nf4_adapters_workspace_bytes(NF4_OP_FWD, ...) bytes (0 for a few rows of a
+ *             small rank, ws is not used then); one each for calls
  *             that may overlap.
  * s, order and offsets need 4-byte alignment, the other pointers 16.
  * Errors: NF4_ERR_NULL, _SHAPE, _ALIGN, _WORKSPACE, _ALIAS, _HIP.

@@ -873,9 +873,15 @@ def _adapters(L1, L2, s, offsets, order, M: int, dev: int):
 
 
 def _adapters_ws(ws, op: int, M: int, o: int, h: int, n: int, r: int, device):
-    if ws is not None:
-        return _need_ws(ws)
-    return torch.empty(adapters_workspace_bytes(op, M, o, h, n, r), dtype=torch.uint8, device=device)
+    """(tensor, address, bytes) of the workspace: the given one, or a new one where one is needed."""
+    if ws is None:
+        need = adapters_workspace_bytes(op, M, o, h, n, r)
+        if not need:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _need_ws(ws)
+    return ws, ws.data_ptr(), ws.numel()
 
 
 def adapters_fwd(X: torch.Tensor, L1: torch.Tensor, L2: torch.Tensor, s: torch.Tensor, offsets: torch.Tensor,
@@ -895,9 +901,9 @@ def adapters_fwd(X: torch.Tensor, L1: torch.Tensor, L2: torch.Tensor, s: torch.T
     if T_out is None and want_T:
         T_out = torch.empty(M, r, dtype=torch.float32, device=X.device)
     t = None if T_out is None else _held(T_out, torch.float32, (M, r), dev, "T_out")
-    ws = _adapters_ws(ws, NF4_OP_FWD, M, o, h, n, r, X.device)
+    ws, wp, wn = _adapters_ws(ws, NF4_OP_FWD, M, o, h, n, r, X.device)
     _check(_lib.nf4_adapters_fwd(x, M, l1, l2, sp, n, o, h, r, ordp, off, b, _held(out, torch.bfloat16, (M, o), dev, "out"),
-                                 t, ws.data_ptr(), ws.numel(), _raw_stream(dev)), "nf4_adapters_fwd")
+                                 t, wp, wn, _raw_stream(dev)), "nf4_adapters_fwd")
     return out, T_out
 
 
@@ -927,10 +933,10 @@ def adapters_bwd(dY: torch.Tensor, X: torch.Tensor, T: torch.Tensor, L1: torch.T
         dL1 = torch.empty(n, h, r, dtype=f32, device=dY.device)
     if dL2 is None:
         dL2 = torch.empty(n, r, o, dtype=f32, device=dY.device)
-    ws = _adapters_ws(ws, NF4_OP_BWD, M, o, h, n, r, dY.device)
+    ws, wp, wn = _adapters_ws(ws, NF4_OP_BWD, M, o, h, n, r, dY.device)
     _check(_lib.nf4_adapters_bwd(x, sx, f, g, t, M, l1, l2, sp, n, o, h, r, ordp, off, b, dx,
                                  _held(dL1, f32, (n, h, r), dev, "dL1"), _held(dL2, f32, (n, r, o), dev, "dL2"),
-                                 ws.data_ptr(), ws.numel(), _raw_stream(dev)), "nf4_adapters_bwd")
+                                 wp, wn, _raw_stream(dev)), "nf4_adapters_bwd")
     return dX, dL1, dL2
 
 

@@ -225,7 +225,7 @@ __global__ __launch_bounds__(256) void k_adapters_narrow_few(AdapterNarrow p) {
 
 // ---------------------------------------------------------------------------
 // The same for tiles of BM = 64 MW rows: both operands are copied straight into LDS, 64 of
-// k a step through a ring of three buffers, two steps under way.  A wave owns 16 MW rows,
+// k a step through a ring of ST buffers, ST - 1 steps under way.  A wave owns 16 MW rows,
 // so nothing is joined.  16-byte pieces of a row of 128 bytes stand XORed by the row, so
 // that fragments of 16 rows fall on different banks; rows of L1 are as long as the rank,
 // and only those of 128 bytes need that.  A step past K repeats valid memory, and its
@@ -430,10 +430,12 @@ __global__ __launch_bounds__(256) void k_adapters_narrow(AdapterNarrow p) {
   constexpr int RP = 16 * NJ, BM = 64 * MW;
   constexpr int XB = BM * 128, SB = XB + RP * 128 + 128;
   constexpr int XI = 2 * MW, LI = NJ == 1 ? 1 : NJ / 2;  // copies of a wave and step
+  constexpr int ST = NJ == 4 && MW == 2 ? 3 : 4;         // two workgroups a compute unit, or more
   __shared__ __attribute__((aligned(1024))) uint8_t S0[SB];
   __shared__ __attribute__((aligned(1024))) uint8_t S1[SB];
   __shared__ __attribute__((aligned(1024))) uint8_t S2[SB];
-  auto buf = [&](int b) -> uint8_t* { return b == 0 ? S0 : b == 1 ? S1 : S2; };
+  __shared__ __attribute__((aligned(1024))) uint8_t S3[ST > 3 ? SB : 16];
+  auto buf = [&](int b) -> uint8_t* { return b == 0 ? S0 : b == 1 ? S1 : b == 2 ? S2 : S3; };
   if (blockIdx.x >= p.tiles) {
     if (blockIdx.y == 0 && blockIdx.z == 0) split_rows(p.split, blockIdx.x - p.tiles, p.rows.M, p.r);
     return;
@@ -531,19 +533,20 @@ __global__ __launch_bounds__(256) void k_adapters_narrow(AdapterNarrow p) {
     // this step's copies are there, everybody's, and the reads of the step before are done
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(wait_vm(XI + LI) & kWaitLds);
+    __builtin_amdgcn_s_waitcnt(wait_vm((ST - 2) * (XI + LI)) & kWaitLds);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    copy(t + 2, (b + 2) % 3);
+    copy(t + ST - 1, (b + ST - 1) % ST);
     __builtin_amdgcn_sched_barrier(0);
     compute(t, b);
   };
-  copy(0, 0);
-  copy(1, 1);
-  for (int t = 0; t < steps; t += 3) {
+#pragma unroll
+  for (int b = 0; b < ST - 1; ++b) copy(b, b);
+  for (int t = 0; t < steps; t += ST) {
     step(t, 0);
-    if (t + 1 < steps) step(t + 1, 1);
-    if (t + 2 < steps) step(t + 2, 2);
+#pragma unroll
+    for (int b = 1; b < ST; ++b)
+      if (t + b < steps) step(t + b, b);
   }
 #pragma unroll
   for (int i = 0; i < MW; ++i) {
@@ -695,7 +698,14 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
       const int e = 256 * (i0 + i) + tid, m = e / (r16 / 4), j = 4 * (e % (r16 / 4));
       if (m >= BM) continue;
       if (o[i] < 0) v[i] = floatx4{0.f, 0.f, 0.f, 0.f};
-      else if (p.T_out && blockIdx.y == 0) *(floatx4*)(p.T_out + o[i]) = v[i];
+      else if (blockIdx.y == 0) {
+        if (p.T_out) *(floatx4*)(p.T_out + o[i]) = v[i];
+        if (p.split.to) {
+          uint2 three[3];
+          split4(v[i], three);
+          store3(p.split, (o[i] - j) / r, j, three);
+        }
+      }
       uint2 part[2];
       split4(v[i], part);
       uint8_t* to = ps + m * PROW + (j / 16) * 64 + (j % 16) * 2;
@@ -804,6 +814,170 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
 }
 
 // ---------------------------------------------------------------------------
+// The forward pass of a tile of 16 rows in one launch, for ranks up to 32: every workgroup
+// of a tile makes the whole T, its 16 waves taking every 16th step of 32 columns of X, and
+// then its part of the columns of Y, a block of 128 a wave at a time.  Making T again in
+// each of a tile's workgroups reads L1[a] from the caches.  A call of a few rows is bound by
+// the host, for which a launch is 3.7 us (one token, rank 16, 4096 x 4096: 9.5 us a call
+// against 13.0 with two launches; by replayed graphs 9.3 against 8.5).
+// The products are those of k_adapters_narrow_few and k_adapters_wide.
+// ---------------------------------------------------------------------------
+template <int NJ>
+__global__ __launch_bounds__(1024) void k_adapters_few(AdapterFew p) {
+  constexpr int WV = 16, RP = 16 * NJ;
+  constexpr int AHEAD = 4, U = 4 / NJ;                    // steps whose loads are under way, and that are staged at once
+  constexpr int ROW = RP * 2 + (NJ == 1 ? 0 : 16);        // LDS bytes of a k row of L1
+  constexpr int STAGE = 32 * ROW * U;                     // a wave's
+  constexpr int LROW = 128 * 2 + 32, PB = RP * LROW;      // a row of L2's panel, and a wave's panel
+  constexpr int PL = 128 * RP / 8 / 64, PROW = RP * 4 + 16;
+  constexpr int AREA = STAGE > PB ? STAGE : PB;
+  constexpr int RED = WV * 16 * RP * 4;
+  __shared__ __align__(16) uint8_t smem[WV * AREA > RED ? WV * AREA : RED];
+  __shared__ __align__(16) uint8_t ps[16 * PROW];
+  Tile tile;
+  if (!find_tile(p.rows, 16, blockIdx.x, tile)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, g = lane >> 4;
+  const int r = p.r;
+  const int64_t K = p.K, N = p.N;
+  const int nblocks = (int)((N + 127) / 128), stride = WV * (int)gridDim.y;
+  const uint16_t* L2 = p.L2 + (int64_t)tile.a * N * r;
+  int64_t at[4];  // this lane's 4 rows of Y, or -1
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int64_t row = row_at(p.rows, tile, tile.p0 + 4 * g + v);
+    at[v] = row < 0 ? -1 : row * N;
+  }
+  const uint16_t* const from = p.base ? p.base : p.L2;  // without a base one piece for all, not used
+  const int64_t some = p.base ? -1 : 0;
+  const uint32_t keep = p.base ? 0xFFFFFFFFu : 0u;
+  auto load_block = [&](int cb, u32x4 (&l)[PL], u32x4 (&b)[4]) {
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+      const int j = 4 * i + lane / 16;
+      const int64_t c = min((int64_t)cb * 128 + 8 * (lane % 16), N - 8);
+      l[i] = *(const u32x4*)(L2 + (int64_t)min(j, r - 1) * N + c);
+      if (j >= r) l[i] = u32x4{0u, 0u, 0u, 0u};
+    }
+    const int64_t c = min((int64_t)cb * 128 + 8 * li, N - 8);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) b[v] = *(const u32x4*)(from + ((max(at[v], (int64_t)0) + c) & some));
+  };
+  int cb = blockIdx.y * WV + wave;
+  u32x4 l[PL], b[4];
+  load_block(min(cb, nblocks - 1), l, b);  // ahead of T's
+
+  // T
+  const int64_t trow = row_at(p.rows, tile, tile.p0 + tid / (RP / 4));
+  const int tj = 4 * (tid % (RP / 4));
+  floatx4 t = {0.f, 0.f, 0.f, 0.f};
+  {
+    const uint16_t* const x = p.X + max(row_at(p.rows, tile, tile.p0 + li), (int64_t)0) * K + 8 * g;
+    const uint16_t* const L1 = p.L1 + (int64_t)tile.a * K * r;
+    constexpr int PPR = 2 * NJ, KPL = 64 / PPR, NL = 32 / KPL;  // L1's pieces of 8 columns
+    uint8_t* const stage = smem + wave * AREA;
+    floatx4 acc[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+    constexpr u32x4 kZero = {0u, 0u, 0u, 0u};
+    for (int64_t s0 = 32 * wave; s0 < K; s0 += 32 * WV * AHEAD) {
+      u32x4 fx[AHEAD], fl[AHEAD][NL];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int64_t k = s0 + 32 * WV * u;
+        fx[u] = k + 8 * g < K ? *(const u32x4*)(x + k) : kZero;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+          const int64_t kr = k + KPL * i + lane / PPR;
+          const int j = 8 * (lane % PPR);
+          fl[u][i] = kr < K && j < r ? *(const u32x4*)(L1 + kr * r + j) : kZero;
+        }
+      }
+#pragma unroll
+      for (int u0 = 0; u0 < AHEAD; u0 += U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < NL; ++i)
+            *(u32x4*)(stage + (32 * u + KPL * i + lane / PPR) * ROW + 16 * (lane % PPR)) = fl[u0 + u][i];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                lds_tr8(stage + (32 * u + 8 * g + (li >> 2)) * ROW + 2 * (16 * j + 4 * (li & 3)), ROW),
+                __builtin_bit_cast(bf16x8, fx[u0 + u]), acc[j], 0, 0, 0);
+      }
+    }
+    __syncthreads();
+    float* const red = (float*)smem;  // [WV][16][RP]
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) *(floatx4*)(red + (wave * 16 + li) * RP + 16 * j + 4 * g) = acc[j];
+    __syncthreads();
+    if (tid < 16 * RP / 4) {
+      const float* const from = red + tid / (RP / 4) * RP + tj;
+      t = *(const floatx4*)from;
+#pragma unroll
+      for (int w = 1; w < WV; ++w) t += *(const floatx4*)(from + w * 16 * RP);
+    }
+  }
+  if (tid < 16 * RP / 4) {
+    // a row past the tile has another row's sums, or nothing of the rank's, and is not written
+    if (trow < 0 || tj >= r) t = floatx4{0.f, 0.f, 0.f, 0.f};
+    else if (p.T_out && blockIdx.y == 0) *(floatx4*)(p.T_out + trow * r + tj) = t;
+    uint2 part[2];
+    split4(t, part);
+    uint8_t* to = ps + tid / (RP / 4) * PROW + (tj / 16) * 64 + (tj % 16) * 2;
+    *(uint2*)to = part[0];
+    *(uint2*)(to + 32) = part[1];
+  }
+  __syncthreads();
+
+  // Y
+  const float s = p.s[tile.a];
+  const uint8_t* const pa = ps + li * PROW + (g >> 1) * 32 + (g & 1) * 16;
+  uint8_t* const panel = smem + wave * AREA;  // the wave's own: no barrier from here on
+  for (; cb < nblocks; cb += stride) {
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+      uint8_t* const to = panel + (4 * i + lane / 16) * LROW + 2 * (lane % 16);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        *(uint16_t*)(to + 64 * k) = (uint16_t)l[i][k];
+        *(uint16_t*)(to + 64 * k + 32) = (uint16_t)(l[i][k] >> 16);
+      }
+    }
+    u32x4 base[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) base[v] = b[v];
+    load_block(min(cb + stride, nblocks - 1), l, b);
+    floatx4 acc[8];
+#pragma unroll
+    for (int f = 0; f < 8; ++f) acc[f] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int st = 0; st < NJ; ++st) {
+      const bf16x8 a = *(const bf16x8*)(pa + st * 64);
+#pragma unroll
+      for (int f = 0; f < 8; ++f)
+        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            a, lds_tr8(panel + (16 * st + 8 * (g & 1) + (li >> 2)) * LROW + 2 * (16 * f + 4 * (li & 3)), LROW), acc[f],
+            0, 0, 0);
+    }
+    const int64_t c = (int64_t)cb * 128 + 8 * li;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      u32x4 o;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t w = base[v][k] & keep;
+        o[k] = pack_bf16x2(__builtin_fmaf(s, acc[2 * k][v], __builtin_bit_cast(float, w << 16)),
+                           __builtin_fmaf(s, acc[2 * k + 1][v], __builtin_bit_cast(float, w & 0xFFFF0000u)));
+      }
+      if (at[v] >= 0 && c < N) *(u32x4*)(p.out + at[v] + c) = o;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 // dL[a][j][c] (or [c][j]) = s[a] sum over a's rows of P[m][j] Q[m][c]: a workgroup has
 // 256 columns of Q, 16 NJ of the rank (blockIdx.z: which 64) and up to p.item rows of an
 // adapter (blockIdx.y).  Both operands are copied straight into LDS, 32 rows a step through
@@ -833,6 +1007,21 @@ struct GradTile {
   static constexpr int LIST = kMaxAdapterItem + (ST + 1) * KR;
 };
 
+// Zeros for an adapter without rows, where no other kernel writes them: its columns c0 to
+// c0 + 255 and the workgroup's 64 of the rank.
+__device__ __forceinline__ void clear_empty(const AdapterRows& rows, const AdapterGrad& p, int a, int64_t c0) {
+  const int M = (int)rows.M;
+  if (min(max(rows.offsets[a + 1], 0), M) > min(max(rows.offsets[a], 0), M)) return;
+  const int j0 = blockIdx.z * 64, rw = min(p.r - j0, 64);
+  const int64_t cols = min(p.N - c0, (int64_t)256);
+  float* const out = p.out + (int64_t)a * p.r * p.N;
+  constexpr floatx4 kZero = {0.f, 0.f, 0.f, 0.f};
+  for (int e = 4 * threadIdx.x; e < cols * rw; e += 4 * blockDim.x) {
+    if (p.trans) *(floatx4*)(out + (c0 + e / rw) * p.r + j0 + e % rw) = kZero;
+    else *(floatx4*)(out + (j0 + e / cols) * p.N + c0 + e % cols) = kZero;
+  }
+}
+
 template <int X8, int NJ>
 __device__ __forceinline__ void grad_tile(const AdapterRows& rows, const AdapterGrad& p, int cblock, uint8_t* ring,
                                           int* list) {
@@ -846,6 +1035,10 @@ __device__ __forceinline__ void grad_tile(const AdapterRows& rows, const Adapter
   constexpr int C = QI + PI + (X8 ? 1 : 0);             // copies of a wave and step
   const uint32_t split = lds_at(ring) + ST * SB;
   const int64_t N = p.N, c0 = (int64_t)cblock * 256;
+  if (blockIdx.y >= p.items) {
+    clear_empty(rows, p, blockIdx.y - (int)p.items, c0);
+    return;
+  }
   Tile tile;
   if (!find_tile(rows, p.item, blockIdx.y, tile)) return;
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4;
@@ -1125,11 +1318,12 @@ hipError_t wide_of(const AdapterWide& p, dim3 gr, hipStream_t st) {
 }
 
 hipError_t wide(const AdapterCall& c, const AdapterPlan& pl, const float* part, int splits, const uint16_t* L,
-                bool jmajor, int64_t N, const uint16_t* base, uint16_t* out, float* T_out, hipStream_t st) {
+                bool jmajor, int64_t N, const uint16_t* base, uint16_t* out, float* T_out, const Split3& split,
+                hipStream_t st) {
   const bool few = pl.bm == 16;
   int64_t tiles;
   const int blocks = plan_adapters_wide(c.rows.M, c.rows.n, few, N, &tiles);
-  AdapterWide p{c.rows, part, splits, L, N, c.r, c.s, base, out, T_out, blocks};
+  AdapterWide p{c.rows, part, splits, L, N, c.r, c.s, base, out, T_out, blocks, split};
   const int64_t nb = (N + 127) / 128;
   const dim3 gr((unsigned)tiles, (unsigned)(few ? (nb + 3) / 4 : (nb + blocks - 1) / blocks));
   if (few) return jmajor ? wide_of<true, 1>(p, gr, st) : wide_of<false, 1>(p, gr, st);
@@ -1151,7 +1345,8 @@ __global__ __launch_bounds__(256) void k_adapters_sum(const float* __restrict__ 
 
 template <int X8>
 hipError_t grad_of(const AdapterRows& rows, const AdapterGrad& p1, const AdapterGrad& p2, hipStream_t st) {
-  const dim3 gr((unsigned)((p1.N + 255) / 256 + (p2.N + 255) / 256), (unsigned)p2.items, (unsigned)((p2.r + 63) / 64));
+  const dim3 gr((unsigned)((p1.N + 255) / 256 + (p2.N + 255) / 256), (unsigned)(p2.items + (p2.single ? rows.n : 0)),
+                (unsigned)((p2.r + 63) / 64));
   if (p2.r <= 16) hipLaunchKernelGGL((k_adapters_grad<X8, 1>), gr, dim3(512), 0, st, rows, p1, p2);
   else if (p2.r <= 32) hipLaunchKernelGGL((k_adapters_grad<X8, 2>), gr, dim3(512), 0, st, rows, p1, p2);
   else hipLaunchKernelGGL((k_adapters_grad<X8, 4>), gr, dim3(512), 0, st, rows, p1, p2);
@@ -1163,9 +1358,16 @@ hipError_t grad_of(const AdapterRows& rows, const AdapterGrad& p1, const Adapter
 hipError_t launch_adapters_fwd(const AdapterCall& c, const uint16_t* X, const uint16_t* base, uint16_t* Y, float* T_out,
                                void* ws, hipStream_t st) {
   const AdapterPlan pl = plan_adapters_rows(c.rows.M, c.rows.n, c.h);
+  if (const int groups = plan_adapters_few(c.rows.M, c.rows.n, c.h, c.o, c.r)) {
+    const AdapterFew p{c.rows, X, c.L1, c.h, c.L2, c.o, c.r, c.s, base, Y, T_out};
+    const dim3 gr((unsigned)pl.tiles, (unsigned)groups);
+    if (c.r <= 16) hipLaunchKernelGGL(k_adapters_few<1>, gr, dim3(1024), 0, st, p);
+    else hipLaunchKernelGGL(k_adapters_few<2>, gr, dim3(1024), 0, st, p);
+    return hipGetLastError();
+  }
   hipError_t e = narrow(c, pl, X, c.h, c.L1, true, (float*)ws, Split3{}, st);
   if (e != hipSuccess) return e;
-  return wide(c, pl, (const float*)ws, pl.splits, c.L2, true, c.o, base, Y, T_out, st);
+  return wide(c, pl, (const float*)ws, pl.splits, c.L2, true, c.o, base, Y, T_out, Split3{}, st);
 }
 
 hipError_t launch_adapters_bwd(const AdapterCall& c, const void* X, int x8, const float* x_scales, const uint16_t* dY,
@@ -1185,24 +1387,29 @@ hipError_t launch_adapters_bwd(const AdapterCall& c, const void* X, int x8, cons
   float* const G_out = pl.splits > 1 ? G : nullptr;
   hipError_t e = narrow(c, pl, dY, c.o, c.L2, false, gparts, t3, st);
   if (e != hipSuccess) return e;
-  if (G_out || g3.to) {
-    const int64_t size = c.rows.M * c.r;
-    hipLaunchKernelGGL(k_adapters_sum, dim3((unsigned)((size + 1023) / 1024)), dim3(256), 0, st, gparts, size,
-                       pl.splits, c.r, G_out, g3);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
+  // G's splits are joined by a kernel of their own, or, few as they are, by dX's (every
+  // workgroup of which does it again; one leaves the sum)
+  const int64_t size = c.rows.M * c.r;
+  const bool fold = dX && pl.splits * size <= kAdapterFold;
+  if (fold) {
+    e = wide(c, pl, gparts, pl.splits, c.L1, false, c.h, base, dX, x8 ? G_out : nullptr, g3, st);
+  } else {
+    if (G_out || g3.to) {
+      hipLaunchKernelGGL(k_adapters_sum, dim3((unsigned)((size + 1023) / 1024)), dim3(256), 0, st, gparts, size,
+                         pl.splits, c.r, G_out, g3);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    if (dX) e = wide(c, pl, G, 1, c.L1, false, c.h, base, dX, nullptr, Split3{}, st);
   }
-  if (dX) {
-    e = wide(c, pl, G_out ? G_out : gparts, G_out ? 1 : pl.splits, c.L1, false, c.h, base, dX, nullptr, st);
-    if (e != hipSuccess) return e;
-  }
-  const AdapterGrad g1{X, x_scales, c.h, G, g3.to, c.r, c.s, it.item, it.items, 1, parts, dL1, w};
-  const AdapterGrad g2{dY, nullptr, c.o, nullptr, t3.to, c.r, c.s, it.item, it.items, 0,
+  if (e != hipSuccess) return e;
+  const AdapterGrad g1{X, x_scales, c.h, G, g3.to, c.r, c.s, it.item, it.items, it.single, 1, parts, dL1, w};
+  const AdapterGrad g2{dY, nullptr, c.o, nullptr, t3.to, c.r, c.s, it.item, it.items, it.single, 0,
                        parts + it.items * c.r * c.h, dL2, w};
   e = x8 == 0   ? grad_of<0>(c.rows, g1, g2, st)
       : x8 == 1 ? grad_of<1>(c.rows, g1, g2, st)
                 : grad_of<2>(c.rows, g1, g2, st);
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || it.single) return e;
   const int64_t most = std::max(c.h, c.o) * c.r;
   const dim3 gr((unsigned)std::min<int64_t>((most + 1023) / 1024, 1024), (unsigned)c.rows.n, 2);
   hipLaunchKernelGGL(k_adapters_join, gr, dim3(256), 0, st, c.rows, g1, g2);

@@ -573,7 +573,8 @@ nf4_status check_adapters(int64_t M, int64_t rows, int64_t cols, int32_t n, int3
 
 size_t adapters_ws(int32_t op, int64_t M, int64_t rows, int64_t cols, int32_t n, int32_t r) {
   if (M == 0) return 0;
-  if (op == NF4_OP_FWD) return (size_t)plan_adapters_rows(M, n, cols).splits * M * r * 4;
+  if (op == NF4_OP_FWD)
+    return plan_adapters_few(M, n, cols, rows, r) ? 0 : (size_t)plan_adapters_rows(M, n, cols).splits * M * r * 4;
   return plan_adapters_space(M, n, cols, rows, r).total;
 }
 
@@ -1195,9 +1196,9 @@ nf4_status nf4_adapters_fwd(const uint16_t* X, int64_t M, const uint16_t* L1, co
   if (M == 0) return NF4_OK;
   if (!X || !L1 || !L2 || !s || !offsets || !Y) return NF4_ERR_NULL;
   const size_t need = adapters_ws(NF4_OP_FWD, M, rows, cols, n, r);
-  if (!ws || ws_bytes < need) return NF4_ERR_WORKSPACE;
+  if (need && (!ws || ws_bytes < need)) return NF4_ERR_WORKSPACE;
   if (!aligned16(X) || !aligned16(L1) || !aligned16(L2) || !aligned4(s) || !aligned4(order) || !aligned4(offsets) ||
-      !aligned16(base) || !aligned16(Y) || !aligned16(T_out) || !aligned16(ws))
+      !aligned16(base) || !aligned16(Y) || !aligned16(T_out) || (need && !aligned16(ws)))
     return NF4_ERR_ALIGN;
   const size_t y = (size_t)(M * rows * 2);
   const Range ins[] = {rng(X, (size_t)(M * cols * 2)), rng(L1, (size_t)n * cols * r * 2),

@@ -244,6 +244,20 @@ struct AdapterWide {
   uint16_t* out;
   float* T_out;  // the joined parts, or NULL
   int blocks;    // blocks of 128 columns a workgroup goes over
+  Split3 split;  // the joined parts in this form too, where `to` is set
+};
+struct AdapterFew {
+  AdapterRows rows;
+  const uint16_t* X;
+  const uint16_t* L1;
+  int64_t K;
+  const uint16_t* L2;
+  int64_t N;
+  int r;
+  const float* s;
+  const uint16_t* base;  // or NULL
+  uint16_t* out;
+  float* T_out;  // or NULL
 };
 struct AdapterGrad {
   const void* Q;          // [M][N], bf16 or codes
@@ -255,6 +269,7 @@ struct AdapterGrad {
   const float* s;
   int item;       // rows an item, a multiple of 64
   int64_t items;  // at most
+  int single;     // every adapter's rows are one item, and the products clear what has none
   int trans;      // out [n][N][r], else [n][r][N]
   float* part;    // [items][r * N]
   float* out;
@@ -270,13 +285,17 @@ struct AdapterPlan {
   int64_t krange;
 };
 AdapterPlan plan_adapters_rows(int64_t M, int n, int64_t K);
+// Workgroups of a tile of 16 rows where one launch makes T and Y (0: two launches).
+int plan_adapters_few(int64_t M, int n, int64_t h, int64_t o, int r);
 // Blocks of 128 columns a workgroup of the products over the rank, and its tiles of 64 rows (few: 16).
 int plan_adapters_wide(int64_t M, int n, bool few, int64_t N, int64_t* tiles);
 // Rows of an item of the adapters' gradients, and the items there are at most.
 struct AdapterItems {
   int item;
   int64_t items;
+  int single;  // no adapter has two
 };
+constexpr int64_t kAdapterFold = 1 << 18;  // values of G's splits that dX's kernel joins
 AdapterItems plan_adapters_items(int64_t M, int n, int64_t h, int64_t o, int r);
 // Byte offsets of the parts of the backward pass's workspace; the zeros come first.
 struct AdapterGradSpace {

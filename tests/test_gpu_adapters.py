@@ -320,7 +320,13 @@ def test_adapters_refuse():
         with pytest.raises(ValueError):
             bad()
     small = torch.empty(16, dtype=torch.uint8, device=DEV)
-    for bad, status in ((lambda: nf4.adapters_fwd(X, L1, L2, s, off, ws=small), nf4.NF4_ERR_WORKSPACE),
+    # these few rows need no workspace, and take any; 40 rows of two adapters need one
+    assert nf4.adapters_workspace_bytes(nf4.NF4_OP_FWD, 8, 400, 272, 2, 16) == 0
+    some = nf4.adapters_fwd(X, L1, L2, s, off, order, base, ws=small)
+    assert torch.equal(some[0], nf4.adapters_fwd(X, L1, L2, s, off, order, base)[0])
+    d = Case(21, [20, 20], 0, 272, 400, 16, True)
+    XX, offd = on(d.X), d.lists()[0]
+    for bad, status in ((lambda: nf4.adapters_fwd(XX, L1, L2, s, offd, ws=small), nf4.NF4_ERR_WORKSPACE),
                         (lambda: nf4.adapters_bwd(dY, X, T, L1, L2, s, off, ws=small), nf4.NF4_ERR_WORKSPACE),
                         (lambda: nf4.adapters_fwd(X, L1[:, :, :12].contiguous(), L2[:, :12].contiguous(), s, off),
                          nf4.NF4_ERR_SHAPE),
