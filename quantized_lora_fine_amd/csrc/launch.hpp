@@ -190,7 +190,7 @@ NF4K_WEAK hipError_t launch_layernorm_bwd(const uint16_t* dY, const uint16_t* Hs
 // ---- rows sorted by id, and the adapters of many requests ----
 constexpr int kMaxIds = 4096;
 constexpr int64_t kMaxRoutedRows = (int64_t)1 << 30;
-// How the rows are split into runs, one a wave: true where one workgroup takes them all.
+// The rows of a wave's run, and the runs of one workgroup that takes them all (true), or the workgroups of 4.
 bool plan_route(int64_t M, int n, int* runs, int64_t* run);
 // ints of the counts that several workgroups share (0: one workgroup takes all rows)
 int64_t route_counts(int64_t M, int n);

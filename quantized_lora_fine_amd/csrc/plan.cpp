@@ -98,21 +98,26 @@ int rmsnorm_parts(int64_t M, int H) {
   return (int)(groups < most ? groups : most);
 }
 
-// Runs are of 512 rows, 8 loads of a lane under way, while they are 2048 at most.  One
-// workgroup takes up to 16 of them where their counts fit in 64 KB of LDS.
+// A wave's run is of 512 rows, 8 loads of a lane under way.  One workgroup takes up to 16 of
+// them where their counts fit in 64 KB of LDS.  Else `runs` counts workgroups of 4 runs, 256 of
+// them at most: each reads the counts of all.
 bool plan_route(int64_t M, int n, int* runs, int64_t* run) {
   const int64_t fit = std::min<int64_t>(16, 16384 / ((int64_t)n + 1));
   const bool one = M <= 512 * fit;
-  *run = one ? 64 * ((M + 64 * fit - 1) / (64 * fit)) : 512 * ((M + 512 * 2048 - 1) / (512 * 2048));
-  if (*run < 64) *run = 64;
-  *runs = (int)std::max<int64_t>(1, (M + *run - 1) / *run);
+  if (one) {
+    *run = std::max<int64_t>(64, 64 * ((M + 64 * fit - 1) / (64 * fit)));
+    *runs = (int)std::max<int64_t>(1, (M + *run - 1) / *run);
+  } else {
+    *run = 512 * ((M + 512 * 1024 - 1) / (512 * 1024));
+    *runs = (int)((M + 4 * *run - 1) / (4 * *run));
+  }
   return one;
 }
 
 int64_t route_counts(int64_t M, int n) {
   int runs;
   int64_t run;
-  return plan_route(M, n, &runs, &run) ? 0 : ((int64_t)n + 1) * (runs + 1);
+  return plan_route(M, n, &runs, &run) ? 0 : ((int64_t)n + 1) * runs;
 }
 
 // Tiles of `bm` rows there are at most: adapters' last tiles may be partly filled.

@@ -30,9 +30,13 @@ __device__ __forceinline__ void load_keys(const int32_t* ids, int64_t m, int64_t
   }
 }
 
-// counts[key] += 1 for the wave's rows [m0, m1)
-__device__ __forceinline__ void count_run(const int32_t* ids, int64_t m0, int64_t m1, int n, int* counts) {
-  for (int64_t m = m0 + (threadIdx.x & 63); m < m1; m += 64 * kAhead) {
+// counts[key] += 1 for the wave's rows [m0, m1), of which the first are in `keys`
+__device__ __forceinline__ void count_run(const int32_t* ids, int64_t m0, int64_t m1, int n, int* counts,
+                                          const int (&keys)[kAhead]) {
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (keys[u] >= 0) atomicAdd(counts + keys[u], 1);
+  for (int64_t m = m0 + (threadIdx.x & 63) + 64 * kAhead; m < m1; m += 64 * kAhead) {
     int key[kAhead];
     load_keys(ids, m, m1, n, key);
 #pragma unroll
@@ -43,27 +47,33 @@ __device__ __forceinline__ void count_run(const int32_t* ids, int64_t m0, int64_
 
 // order[next[key]++] = m for the wave's rows [m0, m1), in their order.  `next` is the
 // wave's own; the LDS operations of one wave stay in order, and the fences keep the
-// compiler from moving them.
+// compiler from moving them.  `keys` are the first ones, loaded already.
 __device__ __forceinline__ void place_run(const int32_t* ids, int64_t m0, int64_t m1, int n, int bits, int* next,
-                                          int32_t* order, int64_t rows) {
+                                          int32_t* order, int64_t rows, int (&keys)[kAhead]) {
   const int lane = threadIdx.x & 63;
   for (int64_t b = m0; b < m1; b += 64 * kAhead) {  // the same for every lane: ballots see the whole wave
-    int keys[kAhead];
-    load_keys(ids, b + lane, m1, n, keys);
+    if (b > m0) load_keys(ids, b + lane, m1, n, keys);
+    // the lanes of the same key, for all the rows at once: a ballot waits for the vector unit
+    uint64_t same[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) same[u] = __ballot(keys[u] >= 0);
+    for (int i = 0; i < bits; ++i) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const bool bit = (keys[u] >> i) & 1;
+        const uint64_t one = __ballot(bit);
+        same[u] &= bit ? one : ~one;
+      }
+    }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int key = keys[u];
       const bool in = key >= 0;
-      uint64_t same = __ballot(in);
-      for (int i = 0; i < bits; ++i) {
-        const uint64_t one = __ballot((key >> i) & 1);
-        same &= (key >> i) & 1 ? one : ~one;
-      }
-      const int rank = __popcll(same & (((uint64_t)1 << lane) - 1));
+      const int rank = __popcll(same[u] & (((uint64_t)1 << lane) - 1));
       const int at = in ? next[key] : 0;
       __atomic_signal_fence(__ATOMIC_SEQ_CST);
       __builtin_amdgcn_wave_barrier();
-      if (in && rank == 0) next[key] = at + __popcll(same);
+      if (in && rank == 0) next[key] = at + __popcll(same[u]);
       __atomic_signal_fence(__ATOMIC_SEQ_CST);
       __builtin_amdgcn_wave_barrier();
       // ids that change while this runs could move a place past the end
@@ -89,10 +99,12 @@ __global__ __launch_bounds__(1024) void k_route_one(const int32_t* __restrict__ 
   extern __shared__ int counts[];  // [runs][n + 1]
   __shared__ int red[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, runs = blockDim.x >> 6;
+  const int64_t m0 = min(wave * run, M), m1 = min(m0 + run, M);
+  int keys[kAhead];
+  load_keys(ids, m0 + lane, m1, n, keys);
   for (int i = threadIdx.x; i < runs * (n + 1); i += blockDim.x) counts[i] = 0;
   __syncthreads();
-  const int64_t m0 = min(wave * run, M), m1 = min(m0 + run, M);
-  count_run(ids, m0, m1, n, counts + wave * (n + 1));
+  count_run(ids, m0, m1, n, counts + wave * (n + 1), keys);
   __syncthreads();
   int base = 0;
   for (int k0 = 0; k0 <= n; k0 += blockDim.x) {
@@ -119,60 +131,92 @@ __global__ __launch_bounds__(1024) void k_route_one(const int32_t* __restrict__ 
     }
   }
   __syncthreads();
-  place_run(ids, m0, m1, n, bits, counts + wave * (n + 1), order, M);
+  place_run(ids, m0, m1, n, bits, counts + wave * (n + 1), order, M, keys);
 }
 
-// The same in three launches, a workgroup of one wave a run; counts [n + 1][runs].
-__global__ __launch_bounds__(64) void k_route_count(const int32_t* __restrict__ ids, int64_t M, int n, int64_t run,
-                                                    int* __restrict__ counts) {
+// The same in two launches, for many rows: a workgroup of 4 waves has a run for each; the
+// first launch counts the workgroups' ids, counts [workgroups][n + 1].
+__global__ __launch_bounds__(256) void k_route_count(const int32_t* __restrict__ ids, int64_t M, int n, int64_t run,
+                                                     int* __restrict__ counts) {
   extern __shared__ int mine[];
-  for (int i = threadIdx.x; i <= n; i += 64) mine[i] = 0;
+  const int64_t m0 = min((blockIdx.x * 4 + (threadIdx.x >> 6)) * run, M), m1 = min(m0 + run, M);
+  int keys[kAhead];
+  load_keys(ids, m0 + (threadIdx.x & 63), m1, n, keys);
+  for (int i = threadIdx.x; i <= n; i += 256) mine[i] = 0;
   __syncthreads();
-  const int64_t m0 = blockIdx.x * run;
-  count_run(ids, m0, min(m0 + run, M), n, mine);
+  count_run(ids, m0, m1, n, mine, keys);
   __syncthreads();
-  for (int i = threadIdx.x; i <= n; i += 64) counts[(int64_t)i * gridDim.x + blockIdx.x] = mine[i];
+  for (int i = threadIdx.x; i <= n; i += 256) counts[(int64_t)blockIdx.x * (n + 1) + i] = mine[i];
 }
-// A wave turns one key's counts into the places before each run, and totals[key] into their sum.
-__global__ __launch_bounds__(256) void k_route_scan(int* __restrict__ counts, int runs, int n,
-                                                    int* __restrict__ totals) {
-  const int key = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (key > n) return;
-  int* c = counts + (int64_t)key * runs;
+// The second adds up, key by key, the counts of the workgroups before and of all; its waves
+// count their own runs once more.
+__global__ __launch_bounds__(256) void k_route_place(const int32_t* __restrict__ ids, int64_t M, int n, int bits,
+                                                     int64_t run, const int* __restrict__ counts,
+                                                     int32_t* __restrict__ order, int32_t* __restrict__ offsets) {
+  extern __shared__ int next[];  // [4][n + 1]
+  __shared__ int red[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, groups = gridDim.x;
+  const int64_t m0 = min((blockIdx.x * 4 + wave) * run, M), m1 = min(m0 + run, M);
+  int keys[kAhead];
+  load_keys(ids, m0 + lane, m1, n, keys);
+  // the counts of 64 workgroups for the thread's two keys; the first are on their way while
+  // the ids are counted
+  int v[2][64];
+  auto load_counts = [&](int key, int g0) {
+    const int last = key < n;  // the second key is there
+#pragma unroll
+    for (int u = 0; u < 64; ++u) {
+      const int* const c = counts + (int64_t)min(g0 + u, groups - 1) * (n + 1) + min(key, n);
+      v[0][u] = c[0];
+      v[1][u] = c[last];
+    }
+  };
+  load_counts(2 * tid, 0);
+  for (int i = tid; i < 4 * (n + 1); i += 256) next[i] = 0;
+  __syncthreads();
+  count_run(ids, m0, m1, n, next + wave * (n + 1), keys);
+  __syncthreads();
   int base = 0;
-  for (int r0 = 0; r0 < runs; r0 += 256) {
-    int v[4];
+  for (int k0 = 0; k0 <= n; k0 += 512) {  // two neighbouring keys a thread
+    const int key = k0 + 2 * tid;
+    int before[2] = {0, 0}, all[2] = {0, 0};
+    for (int g0 = 0; g0 < groups; g0 += 64) {
+      if (k0 + g0 > 0) load_counts(key, g0);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = r0 + 64 * u + lane < runs ? c[r0 + 64 * u + lane] : 0;
+      for (int u = 0; u < 64; ++u)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int incl = wave_incl(v[u]);
-      if (r0 + 64 * u + lane < runs) c[r0 + 64 * u + lane] = base + incl - v[u];
-      base += __shfl(incl, 63);
+        for (int i = 0; i < 2; ++i) {
+          if (g0 + u < (int)blockIdx.x) before[i] += v[i][u];
+          if (g0 + u < groups) all[i] += v[i][u];
+        }
+    }
+    if (key > n) all[0] = 0;
+    if (key >= n) all[1] = 0;
+    const int incl = wave_incl(all[0] + all[1]);
+    if (lane == 63) red[wave] = incl;
+    __syncthreads();
+    int at = base + incl - all[0] - all[1];
+    for (int w = 0; w < 4; ++w) {
+      if (w < wave) at += red[w];
+      base += red[w];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (key + i <= n) {
+        if (blockIdx.x == 0) offsets[key + i] = at;
+        int to = at + before[i];
+        for (int w = 0; w < 4; ++w) {
+          const int c = next[w * (n + 1) + key + i];
+          next[w * (n + 1) + key + i] = to;
+          to += c;
+        }
+      }
+      at += all[i];
     }
   }
-  if (lane == 0) totals[key] = base;
-}
-__global__ __launch_bounds__(64) void k_route_place(const int32_t* __restrict__ ids, int64_t M, int n, int bits,
-                                                    int64_t run, const int* __restrict__ counts,
-                                                    const int* __restrict__ totals, int32_t* __restrict__ order,
-                                                    int32_t* __restrict__ offsets) {
-  extern __shared__ int next[];
-  const int lane = threadIdx.x;
-  int base = 0;
-  for (int k0 = 0; k0 <= n; k0 += 64) {
-    const int key = k0 + lane;
-    const int v = key <= n ? totals[key] : 0;
-    const int incl = wave_incl(v);
-    if (key <= n) {
-      next[key] = base + incl - v + counts[(int64_t)key * gridDim.x + blockIdx.x];
-      if (blockIdx.x == 0) offsets[key] = base + incl - v;
-    }
-    base += __shfl(incl, 63);
-  }
   __syncthreads();
-  const int64_t m0 = blockIdx.x * run;
-  place_run(ids, m0, min(m0 + run, M), n, bits, next, order, M);
+  place_run(ids, m0, m1, n, bits, next + wave * (n + 1), order, M, keys);
 }
 
 }  // namespace
@@ -189,15 +233,10 @@ hipError_t launch_route(const int32_t* ids, int64_t M, int n, int32_t* order, in
     hipLaunchKernelGGL(k_route_one, dim3(1), dim3(64 * runs), lds * runs, st, ids, M, n, bits, run, order, offsets);
     return hipGetLastError();
   }
-  int* totals = counts + (int64_t)(n + 1) * runs;
-  hipLaunchKernelGGL(k_route_count, dim3(runs), dim3(64), lds, st, ids, M, n, run, counts);
+  hipLaunchKernelGGL(k_route_count, dim3(runs), dim3(256), lds, st, ids, M, n, run, counts);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_route_scan, dim3(n / 4 + 1), dim3(256), 0, st, counts, runs, n, totals);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_route_place, dim3(runs), dim3(64), lds, st, ids, M, n, bits, run, counts, totals, order,
-                     offsets);
+  hipLaunchKernelGGL(k_route_place, dim3(runs), dim3(256), 4 * lds, st, ids, M, n, bits, run, counts, order, offsets);
   return hipGetLastError();
 }
 
