@@ -30,7 +30,6 @@ namespace nf4k {
 
 namespace {
 
-constexpr int kAhead = 2;  // steps of 32 columns whose loads are under way in k_adapters_narrow_few
 
 // Tile t of `bm` rows: its adapter, positions [p0, p1), and whether they are all of the
 // adapter's.  Every wave scans the tile counts of 64 adapters at a time.
@@ -130,7 +129,7 @@ __device__ __forceinline__ void split_rows(const Split3& o, int64_t block, int64
 // ---------------------------------------------------------------------------
 template <bool KMAJOR, int NJ>
 __global__ __launch_bounds__(256) void k_adapters_narrow_few(AdapterNarrow p) {
-  constexpr int NM = 1;
+  constexpr int NM = 1, kAhead = NJ == 4 ? 2 : 4;
   constexpr int RP = 16 * NJ, BM = 16 * NM;
   constexpr int ROW = RP * 2 + (NJ == 1 ? 0 : 16);                      // LDS bytes of a k row of L1
   constexpr int STAGE = KMAJOR ? 32 * ROW * kAhead : 0;                 // a wave's
@@ -471,10 +470,11 @@ __global__ __launch_bounds__(256) void k_adapters_narrow(AdapterNarrow p) {
       lp[i] = L + (int64_t)(j0 + min(e >> 3, rw - 1)) * K + k0;
     }
   }
-  // Tiles begin at different steps: rows whose width is a power of two would otherwise have
-  // all workgroups read from the same few memory channels at a time (16000 rows of 8192:
-  // 80 us against 90).
-  const int first = (int)(blockIdx.x * 5u % (unsigned)steps);
+  // Where the width is a power of two, tiles begin at different steps: all workgroups would
+  // otherwise read from the same few memory channels at a time (16000 rows of 8192: 80 us
+  // against 90).  Elsewhere the tiles' common steps share L (16384 rows of 28672 at rank 64:
+  // 178 us, and 196 with steps of their own).
+  const int first = (K & (K - 1)) == 0 ? (int)(blockIdx.x * 5u % (unsigned)steps) : 0;
   auto place = [&](int t) -> int { return t + first < steps ? t + first : t + first - steps; };
   auto copy = [&](int t, int b) {
     t = place(min(t, steps - 1));  // a step behind the last copies it once more, and is not used
@@ -591,7 +591,7 @@ __device__ __forceinline__ floatx4 join4(const float* part, int64_t stride, int 
 // taken in runs of 64.
 // ---------------------------------------------------------------------------
 template <bool JMAJOR, int NJ, int RW, int RMAX>
-__global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
+__global__ __launch_bounds__(256, RW == 1 && NJ < 4 ? 4 : 1) void k_adapters_wide(AdapterWide p) {
   constexpr int BM = 16 * RW, RC = 16 * NJ;
   constexpr int NB = RW == 4 ? 2 : 1, G = 4 / RW, TG = 64 * RW;  // panel buffers; groups of waves, their threads
   constexpr int LROW = JMAJOR ? 128 * 2 + 32 : RC * 2;           // LDS bytes of a row of the panel
@@ -622,13 +622,13 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
   const uint16_t* const from = p.base ? p.base : p.L;
   const int64_t some = p.base ? -1 : 0;
   const uint32_t keep = p.base ? 0xFFFFFFFFu : 0u;
-  auto load_base = [&](int cb, u32x4 (&b)[4]) {
+  auto load_base = [&](int cb, u32x4 (&b)[4]) __attribute__((always_inline)) {
     const int64_t c = min((int64_t)cb * 128 + 8 * li, N - 8);
 #pragma unroll
     for (int v = 0; v < 4; ++v) b[v] = *(const u32x4*)(from + ((max(at[v], (int64_t)0) + c) & some));
   };
   // pieces of the panel: JMAJOR 16 a row of the rank, else RC / 8 a column
-  auto load_panel = [&](int cb, int run, u32x4 (&l)[PL]) {
+  auto load_panel = [&](int cb, int run, u32x4 (&l)[PL]) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
       const int e = TG * i + tg;
@@ -645,7 +645,7 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
     const int k = row >> 2 & 3;
     return NJ == 4 ? row & 7 : NJ == 2 ? (k & 1) << 1 ^ (k >> 1) * 3 : 0;
   };
-  auto store_panel = [&](uint8_t* to, const u32x4 (&l)[PL]) {
+  auto store_panel = [&](uint8_t* to, const u32x4 (&l)[PL]) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
       const int e = TG * i + tg;
@@ -665,7 +665,7 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
   // The panels are numbered through the blocks and their runs of the rank; the one after the
   // next is loaded while one is multiplied.
   const int panels = (cb1 - cb0) * runs;
-  auto load_panel_no = [&](int i, u32x4 (&l)[PL]) {
+  auto load_panel_no = [&](int i, u32x4 (&l)[PL]) __attribute__((always_inline)) {
     i = min(i, panels - 1);
     load_panel(runs == 1 ? cb0 + i : cb0 + i / runs, runs == 1 ? 0 : i % runs, l);
   };
@@ -685,17 +685,18 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
       o[i] = row < 0 ? -1 : row * r + j;
       v[i] = floatx4{0.f, 0.f, 0.f, 0.f};
     }
-    for (int q0 = 0; q0 < p.splits; q0 += 4) {
-      floatx4 x[PT < 4 ? PT : 4][4];
+    constexpr int QU = RW == 1 && NJ < 4 ? 8 : 4;  // splits at once
+    for (int q0 = 0; q0 < p.splits; q0 += QU) {
+      floatx4 x[PT < 4 ? PT : 4][QU];
 #pragma unroll
       for (int i = 0; i < (PT < 4 ? PT : 4); ++i)
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < QU; ++u)
           x[i][u] = *(const floatx4*)(p.part + min(q0 + u, p.splits - 1) * (p.rows.M * r) + max(o[i], (int64_t)0));
 #pragma unroll
       for (int i = 0; i < (PT < 4 ? PT : 4); ++i)
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < QU; ++u)
           if (q0 + u < p.splits) v[i] += x[i][u];
     }
 #pragma unroll
@@ -723,7 +724,7 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
   const float s = p.s[tile.a];
   const uint8_t* pa = ps + (RW == 4 ? 16 * wave + li : li) * PROW + (g >> 1) * 32 + (g & 1) * 16;
   floatx4 acc[8];
-  auto multiply = [&](const uint8_t* lp, int run) {
+  auto multiply = [&](const uint8_t* lp, int run) __attribute__((always_inline)) {
 #pragma unroll
     for (int st = 0; st < NJ; ++st) {
       if (NJ > 1 && run * RC + 16 * st >= r16) break;  // the same for all; P's places past r16 hold nothing
@@ -739,11 +740,11 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
       }
     }
   };
-  auto clear = [&]() {
+  auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int f = 0; f < 8; ++f) acc[f] = floatx4{0.f, 0.f, 0.f, 0.f};
   };
-  auto write = [&](int cb, const u32x4 (&b)[4], auto all) {
+  auto write = [&](int cb, const u32x4 (&b)[4], auto all) __attribute__((always_inline)) {
     const int64_t c = (int64_t)cb * 128 + 8 * li;
     u32x4 o[4];
 #pragma unroll
@@ -776,14 +777,14 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
     // takes the one after that).  Whole tiles have a loop of their own, whose writes stand
     // under no condition: the compiler then knows how many are on their way, and waits for
     // no more of them than it has to.
-    auto one = [&](int i, int run, const u32x4 (&l)[PL], u32x4 (&after)[PL]) {
+    auto one = [&](int i, int run, const u32x4 (&l)[PL], u32x4 (&after)[PL]) __attribute__((always_inline)) {
       load_panel_no(i + 2, after);
       multiply(panel[0][i & 1], run);
       store_panel(panel[0][(i + 1) & 1], l);
     };
-    auto go = [&](auto all) {
+    auto go = [&](auto all) __attribute__((always_inline)) {
       if constexpr (RMAX == RC) {
-        auto block = [&](int cb, const u32x4 (&b)[4], u32x4 (&nb)[4], const u32x4 (&l)[PL], u32x4 (&after)[PL]) {
+        auto block = [&](int cb, const u32x4 (&b)[4], u32x4 (&nb)[4], const u32x4 (&l)[PL], u32x4 (&after)[PL]) __attribute__((always_inline)) {
           load_base(min(cb + 1, cb1 - 1), nb);
           clear();
           one(cb - cb0, 0, l, after);
@@ -819,7 +820,7 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
 }
 
 // ---------------------------------------------------------------------------
-// The forward pass of a tile of 16 rows in one launch, for ranks up to 32: every workgroup
+// The forward pass of a tile of 16 rows in one launch, for ranks up to 16: every workgroup
 // of a tile makes the whole T, its 16 waves taking every 16th step of 32 columns of X, and
 // then its part of the columns of Y, a block of 128 a wave at a time.  Making T again in
 // each of a tile's workgroups reads L1[a] from the caches.  A call of a few rows is bound by
@@ -827,12 +828,11 @@ __global__ __launch_bounds__(256) void k_adapters_wide(AdapterWide p) {
 // against 13.0 with two launches; by replayed graphs 9.3 against 8.5).
 // The products are those of k_adapters_narrow_few and k_adapters_wide.
 // ---------------------------------------------------------------------------
-template <int NJ>
 __global__ __launch_bounds__(1024) void k_adapters_few(AdapterFew p) {
-  constexpr int WV = 16, RP = 16 * NJ;
-  constexpr int AHEAD = 4, U = 4 / NJ;                    // steps whose loads are under way, and that are staged at once
-  constexpr int ROW = RP * 2 + (NJ == 1 ? 0 : 16);        // LDS bytes of a k row of L1
-  constexpr int STAGE = 32 * ROW * U;                     // a wave's
+  constexpr int WV = 16, RP = 16;
+  constexpr int AHEAD = 4;                                // steps whose loads are under way
+  constexpr int ROW = RP * 2;                             // LDS bytes of a k row of L1
+  constexpr int STAGE = 32 * ROW * AHEAD;                 // a wave's
   constexpr int LROW = 128 * 2 + 32, PB = RP * LROW;      // a row of L2's panel, and a wave's panel
   constexpr int PL = 128 * RP / 8 / 64, PROW = RP * 4 + 16;
   constexpr int AREA = STAGE > PB ? STAGE : PB;
@@ -878,45 +878,29 @@ __global__ __launch_bounds__(1024) void k_adapters_few(AdapterFew p) {
   {
     const uint16_t* const x = p.X + max(row_at(p.rows, tile, tile.p0 + li), (int64_t)0) * K + 8 * g;
     const uint16_t* const L1 = p.L1 + (int64_t)tile.a * K * r;
-    constexpr int PPR = 2 * NJ, KPL = 64 / PPR, NL = 32 / KPL;  // L1's pieces of 8 columns
     uint8_t* const stage = smem + wave * AREA;
-    floatx4 acc[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+    floatx4 acc = {0.f, 0.f, 0.f, 0.f};
     constexpr u32x4 kZero = {0u, 0u, 0u, 0u};
     for (int64_t s0 = 32 * wave; s0 < K; s0 += 32 * WV * AHEAD) {
-      u32x4 fx[AHEAD], fl[AHEAD][NL];
+      u32x4 fx[AHEAD], fl[AHEAD];
 #pragma unroll
       for (int u = 0; u < AHEAD; ++u) {
-        const int64_t k = s0 + 32 * WV * u;
+        const int64_t k = s0 + 32 * WV * u, kr = k + lane / 2;
+        const int j = 8 * (lane & 1);
         fx[u] = k + 8 * g < K ? *(const u32x4*)(x + k) : kZero;
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-          const int64_t kr = k + KPL * i + lane / PPR;
-          const int j = 8 * (lane % PPR);
-          fl[u][i] = kr < K && j < r ? *(const u32x4*)(L1 + kr * r + j) : kZero;
-        }
+        fl[u] = kr < K && j < r ? *(const u32x4*)(L1 + kr * r + j) : kZero;
       }
 #pragma unroll
-      for (int u0 = 0; u0 < AHEAD; u0 += U) {
+      for (int u = 0; u < AHEAD; ++u) *(u32x4*)(stage + u * 32 * ROW + lane * 16) = fl[u];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int i = 0; i < NL; ++i)
-            *(u32x4*)(stage + (32 * u + KPL * i + lane / PPR) * ROW + 16 * (lane % PPR)) = fl[u0 + u][i];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int j = 0; j < NJ; ++j)
-            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                lds_tr8(stage + (32 * u + 8 * g + (li >> 2)) * ROW + 2 * (16 * j + 4 * (li & 3)), ROW),
-                __builtin_bit_cast(bf16x8, fx[u0 + u]), acc[j], 0, 0, 0);
-      }
+      for (int u = 0; u < AHEAD; ++u)
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            lds_tr8(stage + (32 * u + 8 * g + (li >> 2)) * ROW + 8 * (li & 3), ROW),
+            __builtin_bit_cast(bf16x8, fx[u]), acc, 0, 0, 0);
     }
     __syncthreads();
     float* const red = (float*)smem;  // [WV][16][RP]
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) *(floatx4*)(red + (wave * 16 + li) * RP + 16 * j + 4 * g) = acc[j];
+    *(floatx4*)(red + (wave * 16 + li) * RP + 4 * g) = acc;
     __syncthreads();
     if (tid < 16 * RP / 4) {
       const float* const from = red + tid / (RP / 4) * RP + tj;
@@ -958,15 +942,11 @@ __global__ __launch_bounds__(1024) void k_adapters_few(AdapterFew p) {
     floatx4 acc[8];
 #pragma unroll
     for (int f = 0; f < 8; ++f) acc[f] = floatx4{0.f, 0.f, 0.f, 0.f};
+    const bf16x8 a = *(const bf16x8*)pa;
 #pragma unroll
-    for (int st = 0; st < NJ; ++st) {
-      const bf16x8 a = *(const bf16x8*)(pa + st * 64);
-#pragma unroll
-      for (int f = 0; f < 8; ++f)
-        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            a, lds_tr8(panel + (16 * st + 8 * (g & 1) + (li >> 2)) * LROW + 2 * (16 * f + 4 * (li & 3)), LROW), acc[f],
-            0, 0, 0);
-    }
+    for (int f = 0; f < 8; ++f)
+      acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+          a, lds_tr8(panel + (8 * (g & 1) + (li >> 2)) * LROW + 2 * (16 * f + 4 * (li & 3)), LROW), acc[f], 0, 0, 0);
     const int64_t c = (int64_t)cb * 128 + 8 * li;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
@@ -1366,8 +1346,7 @@ hipError_t launch_adapters_fwd(const AdapterCall& c, const uint16_t* X, const ui
   if (const int groups = plan_adapters_few(c.rows.M, c.rows.n, c.h, c.o, c.r)) {
     const AdapterFew p{c.rows, X, c.L1, c.h, c.L2, c.o, c.r, c.s, base, Y, T_out};
     const dim3 gr((unsigned)pl.tiles, (unsigned)groups);
-    if (c.r <= 16) hipLaunchKernelGGL(k_adapters_few<1>, gr, dim3(1024), 0, st, p);
-    else hipLaunchKernelGGL(k_adapters_few<2>, gr, dim3(1024), 0, st, p);
+    hipLaunchKernelGGL(k_adapters_few, gr, dim3(1024), 0, st, p);
     return hipGetLastError();
   }
   hipError_t e = narrow(c, pl, X, c.h, c.L1, true, (float*)ws, Split3{}, st);

@@ -285,7 +285,7 @@ struct AdapterPlan {
   int64_t krange;
 };
 AdapterPlan plan_adapters_rows(int64_t M, int n, int64_t K);
-// Workgroups of a tile of 16 rows where one launch makes T and Y (0: two launches).
+// Workgroups of a tile of 16 rows where one launch makes T and Y (rank up to 16; 0: two launches).
 int plan_adapters_few(int64_t M, int n, int64_t h, int64_t o, int r);
 // Blocks of 128 columns a workgroup of the products over the rank, and its tiles of 64 rows (few: 16).
 int plan_adapters_wide(int64_t M, int n, bool few, int64_t N, int64_t* tiles);

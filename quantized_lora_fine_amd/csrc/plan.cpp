@@ -142,11 +142,11 @@ AdapterPlan plan_adapters_rows(int64_t M, int n, int64_t K) {
 // One launch for a few tiles of 16 rows and a small L1[a], which every workgroup of a tile
 // reads: by replayed graphs 9.3 us against 8.5 for one token at rank 16 and 4096 x 4096,
 // 10.6 against 9.4 for 16 tokens of 8 adapters, but a launch (3.7 us) less on the host, which
-// bounds such calls.  At rank 64 it would be 14.3 against 10.9, for 52 tiles of rank 32 28
-// against 17.
+// bounds such calls.  At rank 32 it would be 14.1 and its registers too few, at rank 64 14.3
+// against 10.9, for 52 tiles of rank 32 28 against 17.
 int plan_adapters_few(int64_t M, int n, int64_t h, int64_t o, int r) {
   const AdapterPlan p = plan_adapters_rows(M, n, h);
-  if (p.bm != 16 || p.tiles > 16 || r > 32 || h * r > 1 << 17) return 0;
+  if (p.bm != 16 || p.tiles > 16 || r > 16 || h > 8192) return 0;
   return (int)(((o + 127) / 128 + 15) / 16);  // a block of 128 columns for every wave
 }
 
