@@ -80,20 +80,34 @@ __device__ __forceinline__ int64_t row_at(const AdapterRows& R, const Tile& t, i
   return (uint64_t)row < (uint64_t)R.M ? row : -1;
 }
 
-// Four neighbouring fp32 values as W bf16 ones each, from the largest on; one that is no
-// number stands in the first alone.
-template <int W>
-__device__ __forceinline__ void split4(floatx4 x, uint2 (&part)[W]) {
+// Four neighbouring fp32 values as two bf16 ones each; one that is no number stands in the
+// first alone.
+__device__ __forceinline__ void split4(floatx4 x, uint2 (&part)[2]) {
+  part[0] = uint2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
 #pragma unroll
-  for (int w = 0; w < W; ++w) {
-    part[w] = uint2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
-    if (w + 1 == W) break;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t word = i < 2 ? part[0].x : part[0].y;
+    const float h = __builtin_bit_cast(float, i & 1 ? word & 0xFFFF0000u : word << 16);
+    x[i] = fabsf(h) < INFINITY ? x[i] - h : 0.f;
+  }
+  part[1] = uint2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+}
+
+// As three bf16 ones each, whose sum they are: 8 bits at a time are cut off the top, and what
+// is left has 16 and then 8.  (An infinity leaves a NaN.)
+__device__ __forceinline__ void split4(floatx4 x, uint2 (&part)[3]) {
+#pragma unroll
+  for (int w = 0; w < 3; ++w) {
+    uint32_t b[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t word = i < 2 ? part[w].x : part[w].y;
-      const float h = __builtin_bit_cast(float, i & 1 ? word & 0xFFFF0000u : word << 16);
-      x[i] = fabsf(h) < INFINITY ? x[i] - h : 0.f;
+      const float v = x[i];
+      b[i] = __builtin_bit_cast(uint32_t, v);
     }
+    // the upper halves of two words
+    part[w] = uint2{__builtin_amdgcn_perm(b[1], b[0], 0x07060302u), __builtin_amdgcn_perm(b[3], b[2], 0x07060302u)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] -= __builtin_bit_cast(float, b[i] & 0xFFFF0000u);
   }
 }
 
@@ -351,10 +365,13 @@ __device__ __forceinline__ bf16x8 codes8(u32x2 v) {
   u32x4 o;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    float x[4];
-    unpack_fp8x4<E5M2>(v[i], x);
-    o[2 * i] = pack_bf16x2(x[0], x[1]);
-    o[2 * i + 1] = pack_bf16x2(x[2], x[3]);
+    if constexpr (E5M2) {
+      o[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(v[i], 1.f, false));
+      o[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(v[i], 1.f, true));
+    } else {
+      o[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[i], 1.f, false));
+      o[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[i], 1.f, true));
+    }
   }
   return __builtin_bit_cast(bf16x8, o);
 }
