@@ -1335,14 +1335,14 @@ hipError_t wide(const AdapterCall& c, const AdapterPlan& pl, const float* part, 
 // The splits' sum, as it is, in three parts, or both.
 __global__ __launch_bounds__(256) void k_adapters_sum(const float* __restrict__ part, int64_t size, int splits, int r,
                                                       float* __restrict__ out, Split3 split) {
-  const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (e >= size) return;
-  const floatx4 v = join4(part + e, size, splits);
-  if (out) *(floatx4*)(out + e) = v;
-  if (!split.to) return;
-  uint2 three[3];
-  split4(v, three);
-  store3(split, e / r, (int)(e % r), three);
+  for (int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; e < size; e += (int64_t)gridDim.x * 1024) {
+    const floatx4 v = join4(part + e, size, splits);
+    if (out) *(floatx4*)(out + e) = v;
+    if (!split.to) continue;
+    uint2 three[3];
+    split4(v, three);
+    store3(split, e / r, (int)(e % r), three);
+  }
 }
 
 template <int X8>
@@ -1396,8 +1396,10 @@ hipError_t launch_adapters_bwd(const AdapterCall& c, const void* X, int x8, cons
     e = wide(c, pl, gparts, pl.splits, c.L1, false, c.h, base, dX, x8 ? G_out : nullptr, g3, st);
   } else {
     if (G_out || g3.to) {
-      hipLaunchKernelGGL(k_adapters_sum, dim3((unsigned)((size + 1023) / 1024)), dim3(256), 0, st, gparts, size,
-                         pl.splits, c.r, G_out, g3);
+      // (2^20 workgroups at most: a launch's work-items stay below 2^32)
+      const int64_t groups = std::min<int64_t>((size + 1023) / 1024, 1 << 20);
+      hipLaunchKernelGGL(k_adapters_sum, dim3((unsigned)groups), dim3(256), 0, st, gparts, size, pl.splits, c.r, G_out,
+                         g3);
       e = hipGetLastError();
       if (e != hipSuccess) return e;
     }

@@ -199,7 +199,8 @@ AdapterGradSpace plan_adapters_space(int64_t M, int n, int64_t h, int64_t o, int
   s.g3 = s.g + (size_t)M * r * 4;
   s.t3 = s.g3 + (size_t)three;
   s.parts = s.t3 + (size_t)three;
-  s.total = s.parts + (size_t)plan_adapters_items(M, n, h, o, r).items * r * (h + o) * 4;
+  const AdapterItems it = plan_adapters_items(M, n, h, o, r);
+  s.total = s.parts + (it.single ? 0 : (size_t)it.items * r * (h + o) * 4);
   return s;
 }
 
