@@ -673,10 +673,10 @@ nf4_status nf4_route_workspace_bytes(int64_t M, int32_t n, size_t *bytes);
  *   Y       : bf16 [M][rows];  T_out : fp32 [M][r] for nf4_adapters_bwd, or NULL.
  * rows and cols are multiples of 16, at most 2^22; M <= 2^26.  Products are of bf16
  * operands with fp32 sums; T stays fp32 (as two bf16 values in the second product, which
- * leave 2^-17 of each).  Adapters hold finite values.  M == 0 does nothing.
+ * leave 2^-17 of each).  Adapters hold finite values; what a row holds that is not finite
+ * stays in that row.  M == 0 does nothing.
  *   ws      : nf4_adapters_workspace_bytes(NF4_OP_FWD, ...) bytes (0 for a few rows of a
- *             small rank, ws is not used then); one each for calls
- *             that may overlap.
+ *             small rank, ws is not used then); one each for calls that may overlap.
  * s, order and offsets need 4-byte alignment, the other pointers 16.
  * Errors: NF4_ERR_NULL, _SHAPE, _ALIGN, _WORKSPACE, _ALIAS, _HIP.
  */
@@ -703,7 +703,8 @@ nf4_status nf4_adapters_workspace_bytes(int32_t op, int64_t M, int64_t rows, int
  *   base    : bf16 [M][cols], the gradient through the shared projection (dY W), dX itself
  *             (in place), or NULL for 0.  dX NULL: no input gradient.
  * An adapter without rows gets zeros.  Sums are fp32 in a fixed order; G and T enter the
- * products for dL1 and dL2 with all their bits (as three bf16 values).  M == 0 writes zeros to dL1 and dL2.
+ * products for dL1 and dL2 with all their bits (as three bf16 values; an infinity in a row
+ * makes a NaN, of its own adapter's sums alone).  M == 0 writes zeros to dL1 and dL2.
  * Everything else, and errors (_ARG: x_format), as nf4_adapters_fwd.
  */
 nf4_status nf4_adapters_bwd(const void *X, const float *x_scales, int32_t x_format, const uint16_t *dY, const float *T,

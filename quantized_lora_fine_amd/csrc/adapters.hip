@@ -11,9 +11,14 @@
 // adapter (dL1, dL2).  All run on v_mfma_f32_16x16x32_bf16.  X, dY, L1 and L2 are bf16 as
 // they are; T and G are fp32 and enter a product as a sum of bf16 values: two where the
 // result is bf16 (they leave 2^-17 of a value), three where it is fp32 (which leave nothing
-// of its 24 bits; two would leave 2e-6 of a sum, ten times an fp32 sum's own error).  That
-// is MFMAs in products that are bound by memory.  8-bit codes are bf16 values exactly, and
-// their scale, one for a row and 128 columns, goes to that row of G.
+// of its 24 bits; two would leave 2e-6 of a sum, ten times an fp32 sum's own error).  The
+// matrix cores have room for it: three parts at rank 64 are their highest load, 32 % of the
+// cycles.  8-bit codes are bf16 values exactly, and their scale, one for a row and 128
+// columns, goes to that row of G.
+//
+// All of it is bound by memory where there are many rows (X and dY are read, base and Y or dX
+// read and written), by launches and latencies that follow one another where there are few.
+// Times below are of one MI355X by kernel trace; a large copy there reaches 5.4 TB/s.
 //
 // Rows are named by (order, offsets): adapter a's are order[offsets[a]] to
 // order[offsets[a + 1] - 1] (without an order: the rows of these numbers).  A workgroup takes
@@ -29,7 +34,6 @@
 namespace nf4k {
 
 namespace {
-
 
 // Tile t of `bm` rows: its adapter, positions [p0, p1), and whether they are all of the
 // adapter's.  Every wave scans the tile counts of 64 adapters at a time.
@@ -138,7 +142,9 @@ __device__ __forceinline__ void split_rows(const Split3& o, int64_t block, int64
 // waves take every fourth step of 32 k, kAhead steps' loads under way, and their sums are
 // added in LDS in wave order.  A's rows are the MFMA's second operand, so a lane ends with
 // 4 neighbouring columns of one row; a row or column past the end repeats a valid one and
-// is not written.  L1 goes through LDS for transposing reads, each wave's own part.
+// and is not written.  L1 goes through LDS for transposing reads, each wave's own part.
+// For tiles most of whose rows are not there: no barrier in the loop, whose few steps are
+// latencies one behind the other.  64 rows of 4096 by 48 adapters of rank 32 (12 MB) 6.0 us.
 // Workgroups past the tiles split T for the products over rows (in a backward pass).
 // ---------------------------------------------------------------------------
 template <bool KMAJOR, int NJ>
@@ -242,7 +248,11 @@ __global__ __launch_bounds__(256) void k_adapters_narrow_few(AdapterNarrow p) {
 // so nothing is joined.  16-byte pieces of a row of 128 bytes stand XORed by the row, so
 // that fragments of 16 rows fall on different banks; rows of L1 are as long as the rank,
 // and only those of 128 bytes need that.  A step past K repeats valid memory, and its
-// fragments are zeroed.
+// fragments are zeroed.  Tiles of 128 rows read L half as often; 64 are taken where adapters
+// have up to 256 rows each in the mean, whose last tiles of 128 would be half empty.
+// 16384 rows of 28672 at rank 64: 179 us, 5.3 TB/s, the copy's rate.  8192 rows of 4096 at
+// rank 64: 29 us, 7977 at rank 16: 26, about twice their bytes' time, since 8 to 16 steps a
+// workgroup do not hide its start.
 // ---------------------------------------------------------------------------
 constexpr int kWaitLds = 15 | (3 << 14) | (0x7 << 4);  // lgkmcnt(0), vmcnt as it is
 constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8); }
@@ -606,6 +616,10 @@ __device__ __forceinline__ floatx4 join4(const float* part, int64_t stride, int 
 // neighbouring columns of 4 rows, and 16 lanes read and write 256 bytes of a row.  For that
 // a panel of L stands in LDS with column 8 i + f at place 16 f + i.  A rank above 16 NJ is
 // taken in runs of 64.
+// Bound by reading base and writing the output: 7977 rows by 11008 of rank 16 79 us (4.4 TB/s),
+// 8192 by 11008 of rank 64 92 (3.9), 16384 by 8192 of rank 64 119 (4.5), where a copy of such a
+// size reaches 5.4; the rest are the starts of 1024 workgroups, with the joining of P in each.
+// 64 rows by 11008 of rank 32: 9.9 us.
 // ---------------------------------------------------------------------------
 template <bool JMAJOR, int NJ, int RW, int RMAX>
 __global__ __launch_bounds__(256, RW == 1 && NJ < 4 ? 4 : 1) void k_adapters_wide(AdapterWide p) {
@@ -841,7 +855,7 @@ __global__ __launch_bounds__(256, RW == 1 && NJ < 4 ? 4 : 1) void k_adapters_wid
 // of a tile makes the whole T, its 16 waves taking every 16th step of 32 columns of X, and
 // then its part of the columns of Y, a block of 128 a wave at a time.  Making T again in
 // each of a tile's workgroups reads L1[a] from the caches.  A call of a few rows is bound by
-// the host, for which a launch is 3.7 us (one token, rank 16, 4096 x 4096: 9.5 us a call
+// the host, for which a launch is 3.7 us (one token, rank 16, 4096 x 4096: 8.5 us a call
 // against 13.0 with two launches; by replayed graphs 9.3 against 8.5).
 // The products are those of k_adapters_narrow_few and k_adapters_wide.
 // ---------------------------------------------------------------------------
@@ -996,6 +1010,14 @@ __global__ __launch_bounds__(1024) void k_adapters_few(AdapterFew p) {
 //
 // The two waves of a SIMD take turns: the lower four read a step and multiply it (and split
 // before), the upper four multiply the step before and read (and split last).
+//
+// A step takes 0.78 us at rank 16, the copy's rate, and 0.97 at rank 64, whose parts of P are
+// 12 KB beside Q's 16 and whose MFMAs are four times as many (busy 32 % of the cycles, LDS
+// 18 %, no conflicts); a workgroup's start and end are 7 us.  8192 rows by 11008 and 4096
+// columns, 8 adapters of rank 64: 85 us; 16384 rows by 8192 columns of codes and 28672 of dY at
+// rank 64: 341 (3.2 TB/s).  Measured beside it: tiles of 512 columns, 316 us for the latter but
+// 89 for the former; two workgroups a compute unit with rings of two steps, 8 % slower; rings of
+// 5 to 7 steps, level.
 // ---------------------------------------------------------------------------
 template <int X8, int NJ>
 struct GradTile {
@@ -1255,6 +1277,7 @@ __global__ __launch_bounds__(512) void k_adapters_grad(AdapterRows rows, Adapter
 }
 
 // Outputs of adapters with several items: their parts' sums in order; with none: zeros.
+// Bound by the parts' bytes: 7 of 64 x 36864 and their sum, 76 MB, 15 us.
 __global__ __launch_bounds__(256) void k_adapters_join(AdapterRows rows, AdapterGrad p0, AdapterGrad p1) {
   const AdapterGrad& p = blockIdx.z ? p1 : p0;
   const int a = blockIdx.y, lane = threadIdx.x & 63;
@@ -1332,7 +1355,9 @@ hipError_t wide(const AdapterCall& c, const AdapterPlan& pl, const float* part, 
   return jmajor ? wide_of<true, 4>(p, gr, st) : wide_of<false, 4>(p, gr, st);
 }
 
-// The splits' sum, as it is, in three parts, or both.
+// The splits' sum, as it is, in three parts, or both: 4 splits of 16384 rows of rank 64 5.4 us.
+// Where there are few values every workgroup of dX's product adds the splits up by itself
+// instead, which saves a launch.
 __global__ __launch_bounds__(256) void k_adapters_sum(const float* __restrict__ part, int64_t size, int splits, int r,
                                                       float* __restrict__ out, Split3 split) {
   for (int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; e < size; e += (int64_t)gridDim.x * 1024) {

@@ -8,6 +8,11 @@
 // and the lowest of them moves that place on.  No order depends on timing: the counts
 // are integers, and every place has one writer.
 // Rows whose id is outside [0, n) count as id n and come last.
+//
+// Bound by latencies that follow one another, not by bytes (131072 rows: 1 MB).  Up to some
+// 8192 rows one workgroup does everything: 64 rows of 48 ids 3.5 us, a launch with its two
+// trips to memory.  131072 rows of 256 ids take 3.4 and 10.6 us in two launches; with a third
+// between them for the counts' sums it was 17.6 a call, and is 13.2.
 #include <algorithm>
 
 #include "common.hpp"
