@@ -248,8 +248,7 @@ __global__ __launch_bounds__(256) void k_adapters_narrow_few(AdapterNarrow p) {
 // so nothing is joined.  16-byte pieces of a row of 128 bytes stand XORed by the row, so
 // that fragments of 16 rows fall on different banks; rows of L1 are as long as the rank,
 // and only those of 128 bytes need that.  A step past K repeats valid memory, and its
-// fragments are zeroed.  Tiles of 128 rows read L half as often; 64 are taken where adapters
-// have up to 256 rows each in the mean, whose last tiles of 128 would be half empty.
+// fragments are zeroed.
 // 16384 rows of 28672 at rank 64: 179 us, 5.3 TB/s, the copy's rate.  8192 rows of 4096 at
 // rank 64: 29 us, 7977 at rank 16: 26, about twice their bytes' time, since 8 to 16 steps a
 // workgroup do not hide its start.
@@ -855,8 +854,8 @@ __global__ __launch_bounds__(256, RW == 1 && NJ < 4 ? 4 : 1) void k_adapters_wid
 // of a tile makes the whole T, its 16 waves taking every 16th step of 32 columns of X, and
 // then its part of the columns of Y, a block of 128 a wave at a time.  Making T again in
 // each of a tile's workgroups reads L1[a] from the caches.  A call of a few rows is bound by
-// the host, for which a launch is 3.7 us (one token, rank 16, 4096 x 4096: 8.5 us a call
-// against 13.0 with two launches; by replayed graphs 9.3 against 8.5).
+// the host, for which a launch is 3.7 us (one token, rank 16, 4096 x 4096: 8.5 to
+// 9.2 us a call against 13.0 with two launches; by replayed graphs 8.3 against 8.1).
 // The products are those of k_adapters_narrow_few and k_adapters_wide.
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(1024) void k_adapters_few(AdapterFew p) {
@@ -1342,16 +1341,14 @@ hipError_t wide_of(const AdapterWide& p, dim3 gr, hipStream_t st) {
   return hipGetLastError();
 }
 
-hipError_t wide(const AdapterCall& c, const AdapterPlan& pl, const float* part, int splits, const uint16_t* L,
+hipError_t wide(const AdapterCall& c, const float* part, int splits, const uint16_t* L,
                 bool jmajor, int64_t N, const uint16_t* base, uint16_t* out, float* T_out, const Split3& split,
                 hipStream_t st) {
-  const bool few = pl.bm == 16;
-  int64_t tiles;
-  const int blocks = plan_adapters_wide(c.rows.M, c.rows.n, few, N, &tiles);
-  AdapterWide p{c.rows, part, splits, L, N, c.r, c.s, base, out, T_out, blocks, split};
+  const AdapterWidePlan pl = plan_adapters_wide(c.rows.M, c.rows.n, N, c.r);
+  AdapterWide p{c.rows, part, splits, L, N, c.r, c.s, base, out, T_out, pl.blocks, split};
   const int64_t nb = (N + 127) / 128;
-  const dim3 gr((unsigned)tiles, (unsigned)(few ? (nb + 3) / 4 : (nb + blocks - 1) / blocks));
-  if (few) return jmajor ? wide_of<true, 1>(p, gr, st) : wide_of<false, 1>(p, gr, st);
+  const dim3 gr((unsigned)pl.tiles, (unsigned)(pl.bm == 16 ? (nb + 3) / 4 : (nb + pl.blocks - 1) / pl.blocks));
+  if (pl.bm == 16) return jmajor ? wide_of<true, 1>(p, gr, st) : wide_of<false, 1>(p, gr, st);
   return jmajor ? wide_of<true, 4>(p, gr, st) : wide_of<false, 4>(p, gr, st);
 }
 
@@ -1384,22 +1381,22 @@ hipError_t grad_of(const AdapterRows& rows, const AdapterGrad& p1, const Adapter
 
 hipError_t launch_adapters_fwd(const AdapterCall& c, const uint16_t* X, const uint16_t* base, uint16_t* Y, float* T_out,
                                void* ws, hipStream_t st) {
-  const AdapterPlan pl = plan_adapters_rows(c.rows.M, c.rows.n, c.h);
+  const AdapterPlan pl = plan_adapters_rows(c.rows.M, c.rows.n, c.h, false);
   if (const int groups = plan_adapters_few(c.rows.M, c.rows.n, c.h, c.o, c.r)) {
     const AdapterFew p{c.rows, X, c.L1, c.h, c.L2, c.o, c.r, c.s, base, Y, T_out};
-    const dim3 gr((unsigned)pl.tiles, (unsigned)groups);
+    const dim3 gr((unsigned)pl.tiles, (unsigned)groups);  // (these tiles are of 16 rows: M <= 16 n)
     hipLaunchKernelGGL(k_adapters_few, gr, dim3(1024), 0, st, p);
     return hipGetLastError();
   }
   hipError_t e = narrow(c, pl, X, c.h, c.L1, true, (float*)ws, Split3{}, st);
   if (e != hipSuccess) return e;
-  return wide(c, pl, (const float*)ws, pl.splits, c.L2, true, c.o, base, Y, T_out, Split3{}, st);
+  return wide(c, (const float*)ws, pl.splits, c.L2, true, c.o, base, Y, T_out, Split3{}, st);
 }
 
 hipError_t launch_adapters_bwd(const AdapterCall& c, const void* X, int x8, const float* x_scales, const uint16_t* dY,
                                const float* T, const uint16_t* base, uint16_t* dX, float* dL1, float* dL2, void* ws,
                                hipStream_t st) {
-  const AdapterPlan pl = plan_adapters_rows(c.rows.M, c.rows.n, c.o);
+  const AdapterPlan pl = plan_adapters_rows(c.rows.M, c.rows.n, c.o, true);
   const AdapterItems it = plan_adapters_items(c.rows.M, c.rows.n, c.h, c.o, c.r);
   const AdapterGradSpace sp = plan_adapters_space(c.rows.M, c.rows.n, c.h, c.o, c.r);
   uint8_t* const w = (uint8_t*)ws;
@@ -1418,7 +1415,7 @@ hipError_t launch_adapters_bwd(const AdapterCall& c, const void* X, int x8, cons
   const int64_t size = c.rows.M * c.r;
   const bool fold = dX && pl.splits * size <= kAdapterFold;
   if (fold) {
-    e = wide(c, pl, gparts, pl.splits, c.L1, false, c.h, base, dX, x8 ? G_out : nullptr, g3, st);
+    e = wide(c, gparts, pl.splits, c.L1, false, c.h, base, dX, x8 ? G_out : nullptr, g3, st);
   } else {
     if (G_out || g3.to) {
       // (2^20 workgroups at most: a launch's work-items stay below 2^32)
@@ -1428,7 +1425,7 @@ hipError_t launch_adapters_bwd(const AdapterCall& c, const void* X, int x8, cons
       e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
-    if (dX) e = wide(c, pl, G, 1, c.L1, false, c.h, base, dX, nullptr, Split3{}, st);
+    if (dX) e = wide(c, G, 1, c.L1, false, c.h, base, dX, nullptr, Split3{}, st);
   }
   if (e != hipSuccess) return e;
   const AdapterGrad g1{X, x_scales, c.h, G, g3.to, c.r, c.s, it.item, it.items, it.single, 1, parts, dL1, w};

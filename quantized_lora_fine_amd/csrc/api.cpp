@@ -574,7 +574,7 @@ nf4_status check_adapters(int64_t M, int64_t rows, int64_t cols, int32_t n, int3
 size_t adapters_ws(int32_t op, int64_t M, int64_t rows, int64_t cols, int32_t n, int32_t r) {
   if (M == 0) return 0;
   if (op == NF4_OP_FWD)
-    return plan_adapters_few(M, n, cols, rows, r) ? 0 : (size_t)plan_adapters_rows(M, n, cols).splits * M * r * 4;
+    return plan_adapters_few(M, n, cols, rows, r) ? 0 : (size_t)plan_adapters_rows(M, n, cols, false).splits * M * r * 4;
   return plan_adapters_space(M, n, cols, rows, r).total;
 }
 

@@ -277,18 +277,24 @@ struct AdapterGrad {
 };
 constexpr int kMaxAdapterItem = 4096;
 constexpr int64_t kMaxAdapterRows = (int64_t)1 << 26;  // tiles of 16 rows stay one launch
-// Tiles of rows of the products of one row, and the splits of a contraction over K.
+// Tiles of rows of the products of one row, and the splits of a contraction over K
+// (`lines`: by L2's rows, for G; else by L1's columns, for T).
 struct AdapterPlan {
   int bm;         // rows a tile: 16, 64 or 128
   int64_t tiles;  // at most
   int splits;
   int64_t krange;
 };
-AdapterPlan plan_adapters_rows(int64_t M, int n, int64_t K);
+AdapterPlan plan_adapters_rows(int64_t M, int n, int64_t K, bool lines);
 // Workgroups of a tile of 16 rows where one launch makes T and Y (rank up to 16; 0: two launches).
 int plan_adapters_few(int64_t M, int n, int64_t h, int64_t o, int r);
-// Blocks of 128 columns a workgroup of the products over the rank, and its tiles of 64 rows (few: 16).
-int plan_adapters_wide(int64_t M, int n, bool few, int64_t N, int64_t* tiles);
+// Tiles of rows of the products over the rank.
+struct AdapterWidePlan {
+  int bm;         // rows a tile: 16 (4 blocks of 128 columns a workgroup, one a wave) or 64
+  int64_t tiles;  // at most
+  int blocks;     // blocks of 128 columns that a workgroup of 64 rows goes over
+};
+AdapterWidePlan plan_adapters_wide(int64_t M, int n, int64_t N, int r);
 // Rows of an item of the adapters' gradients, and the items there are at most.
 struct AdapterItems {
   int item;

@@ -125,12 +125,19 @@ static int64_t adapter_tiles(int64_t M, int n, int bm) {
   return std::min<int64_t>(M, M / bm + std::min<int64_t>(M, n));
 }
 
-// Tiles of 16 rows where an adapter has few in the mean, else of 64, or of 128 where there
-// are enough of them.  About 512 workgroups, each with 256 of the contraction or more.
-AdapterPlan plan_adapters_rows(int64_t M, int n, int64_t K) {
+// Tiles of 16 rows where an adapter has few in the mean or the product is small, else of 64, or
+// of 128 where there are enough of them.  About 512 workgroups, each with 256 of the contraction
+// or more.  Measured (us, tiles of 16 / of 64): T of 256 rows by 4096 of rank 16 4.4 / 5.7, of 1024
+// rows 6.6 / 7.3, by 11008 8.6 / 11.7, but of 4096 rows by 11008 of rank 64 39 / 31.  G (`lines`:
+// L2's rows lie as the contraction does, so that its panel costs the larger tiles less) of 256
+// rows by 4096 4.4 / 5.0 and of 1024 of rank 64 11.6 / 8.7; of 256 rows of 32 adapters by 28672 of
+// rank 16 13 / 23, of 512 rows of rank 32 39 / 26.  Tiles of 128 against 64, both passes' calls: 32
+// rows of each of 16 adapters 35.5 / 34.5, 512 rows of each 127 / 129.
+AdapterPlan plan_adapters_rows(int64_t M, int n, int64_t K, bool lines) {
   AdapterPlan p;
   const int64_t used = std::min<int64_t>(M, n);
-  p.bm = M <= 16 * used ? 16 : M <= 256 * used ? 64 : 128;
+  const bool few = M <= (lines ? 8 : 16) * used || M * K <= (lines ? (int64_t)1 << 20 : (int64_t)10 << 20);
+  p.bm = few ? 16 : M <= 256 * used ? 64 : 128;
   p.tiles = adapter_tiles(M, n, p.bm);
   const int64_t most = std::max<int64_t>(1, (K + 255) / 256);
   const int64_t want = std::min(most, (512 + p.tiles - 1) / std::max<int64_t>(p.tiles, 1));
@@ -140,25 +147,34 @@ AdapterPlan plan_adapters_rows(int64_t M, int n, int64_t K) {
 }
 
 // One launch for a few tiles of 16 rows and a small L1[a], which every workgroup of a tile
-// reads: by replayed graphs 9.3 us against 8.5 for one token at rank 16 and 4096 x 4096,
-// 10.6 against 9.4 for 16 tokens of 8 adapters, but a launch (3.7 us) less on the host, which
-// bounds such calls.  At rank 32 it would be 14.1 and its registers too few, at rank 64 14.3
-// against 10.9, for 52 tiles of rank 32 28 against 17.
+// reads.  It saves a launch (3.7 us) on the host, which bounds such calls, and costs time on the
+// device: a call / by replayed graphs, against two launches, one token at rank 16 and 4096 x
+// 4096 9.2 / 8.3 against 13.0 / 8.1 us, at 8192 x 8192 10.3 / 10.3 against 13.0 / 9.3, 16 tokens
+// of one adapter 11.2 / 11.1 against 13.3 / 8.7 and 15.5 / 15.4 against 13.1 / 9.9, 200 tokens 11.6 /
+// 11.5 against 13.0 / 9.5.  At rank 32 it would be 14.1 and its registers too few, at rank 64
+// 14.3 against 10.9, for 52 tiles of rank 32 28 against 17.
 int plan_adapters_few(int64_t M, int n, int64_t h, int64_t o, int r) {
-  const AdapterPlan p = plan_adapters_rows(M, n, h);
-  if (p.bm != 16 || p.tiles > 16 || r > 16 || h > 8192) return 0;
+  const int64_t used = std::min<int64_t>(M, n);
+  if (M > 16 * used || adapter_tiles(M, n, 16) > 16 || r > 16 || h > (M <= 2 * used ? 8192 : 4096)) return 0;
   return (int)(((o + 127) / 128 + 15) / 16);  // a block of 128 columns for every wave
 }
 
-int plan_adapters_wide(int64_t M, int n, bool few, int64_t N, int64_t* tiles) {
-  *tiles = adapter_tiles(M, n, few ? 16 : 64);
+// Tiles of 16 rows, whose waves have a block each, up to so many workgroups: they start sooner,
+// but read L for every 16 rows.  Measured (us, tiles of 16 / of 64): Y of 64 rows of 16 adapters by
+// 11008 of rank 16 7 / 13, of 1024 rows by 4096 of rank 64 13 / 22, of 2048 by 4096 of rank 128 48 /
+// 123, of 1024 by 28672 of rank 16 29 / 33 (3640 workgroups) and of 2048 61 / 54; at rank 64 of 512
+// rows 37 / 64 (1848) and of 1024 63 / 52.
+AdapterWidePlan plan_adapters_wide(int64_t M, int n, int64_t N, int r) {
   const int64_t blocks = (N + 127) / 128;
-  if (few) return 1;
+  AdapterWidePlan p{16, adapter_tiles(M, n, 16), 1};
+  if (p.tiles * ((blocks + 3) / 4) <= (r <= 32 ? 3500 : 1800)) return p;
+  p.bm = 64;
+  p.tiles = adapter_tiles(M, n, 64);
   // About 1024 workgroups (three are on a compute unit, so a second set is partly filled):
   // 7977 rows by 11008 of rank 16 78 us, 8192 rows by 11008 of rank 64 94, against 103 and
   // 116 for 256, 83 and 97 for 1536, 93 and 111 for 3072, whose starts are more of them.
-  const int64_t each = *tiles * blocks / 1024;
-  return (int)std::max<int64_t>(1, std::min(each, blocks));
+  p.blocks = (int)std::max<int64_t>(1, std::min(p.tiles * blocks / 1024, blocks));
+  return p;
 }
 
 // The rows of an item: as many sets of 256 workgroups (one a compute unit) as take the
@@ -195,7 +211,7 @@ AdapterGradSpace plan_adapters_space(int64_t M, int n, int64_t h, int64_t o, int
   AdapterGradSpace s;
   const int64_t rp = r <= 16 ? 16 : r <= 32 ? 32 : 64, three = M * ((r + 63) / 64) * 3 * rp * 2;
   s.gparts = kZeroBytes;
-  s.g = s.gparts + (size_t)plan_adapters_rows(M, n, o).splits * M * r * 4;
+  s.g = s.gparts + (size_t)plan_adapters_rows(M, n, o, true).splits * M * r * 4;
   s.g3 = s.g + (size_t)M * r * 4;
   s.t3 = s.g3 + (size_t)three;
   s.parts = s.t3 + (size_t)three;

@@ -56,12 +56,13 @@ int main() {
   for (int i = 0; i < 100000; ++i) route_plan(pick(0, 9) ? any(30) : 0, (int)any(12), ones);
   CHECK(ones[0] && ones[1]);
 
-  bool bm16 = false, bm64 = false, bm128 = false, few = false, fold = false, single = false, several = false;
+  bool bm16 = false, bm64 = false, bm128 = false, few = false, fold = false, single = false, wide16 = false, wide64 = false, several = false;
   for (int i = 0; i < 200000; ++i) {
     const int64_t M = any(26), h = 16 * any(18), o = 16 * any(18);
     const int n = (int)any(12), r = 8 * (int)pick(1, 32);
-    for (int64_t K : {h, o}) {
-      const AdapterPlan p = plan_adapters_rows(M, n, K);
+    for (bool lines : {false, true}) {
+      const int64_t K = lines ? o : h;
+      const AdapterPlan p = plan_adapters_rows(M, n, K, lines);
       CHECK(p.bm == 16 || p.bm == 64 || p.bm == 128);
       bm16 |= p.bm == 16, bm64 |= p.bm == 64, bm128 |= p.bm == 128;
       // the splits cover the contraction, and none is empty
@@ -70,14 +71,14 @@ int main() {
       // work-items of a launch, with those that split T
       CHECK((p.tiles + (M + 63) / 64) * 256 < (int64_t)1 << 32);
     }
-    const AdapterPlan p = plan_adapters_rows(M, n, h);
-    int64_t tiles = 0;
-    const int blocks = plan_adapters_wide(M, n, p.bm == 16, o, &tiles);
-    CHECK(blocks >= 1 && tiles * 256 < (int64_t)1 << 32);
-    CHECK(((o + 127) / 128 + blocks - 1) / blocks <= 65535);
+    const AdapterPlan p = plan_adapters_rows(M, n, h, false);
+    const AdapterWidePlan w = plan_adapters_wide(M, n, o, r);
+    CHECK((w.bm == 16 || w.bm == 64) && w.blocks >= 1 && w.tiles * 256 < (int64_t)1 << 32);
+    CHECK(((o + 127) / 128 + w.blocks - 1) / w.blocks <= 65535);
+    wide16 |= w.bm == 16, wide64 |= w.bm == 64;
     if (const int groups = plan_adapters_few(M, n, h, o, r)) {
       few = true;
-      CHECK(p.bm == 16 && r <= 16 && groups <= 65535 && p.tiles <= 16);
+      CHECK(p.bm == 16 && r <= 16 && groups <= 65535 && p.tiles <= 16);  // one launch of the tiles planned here
     }
     const AdapterItems it = plan_adapters_items(M, n, h, o, r);
     CHECK(it.item % 64 == 0 && it.item >= 64 && it.item <= kMaxAdapterItem && it.items >= 1);
@@ -86,7 +87,7 @@ int main() {
     single |= it.single != 0;
     several |= !it.single && it.item < M;
     const AdapterGradSpace s = plan_adapters_space(M, n, h, o, r);
-    const int64_t splits = plan_adapters_rows(M, n, o).splits;
+    const int64_t splits = plan_adapters_rows(M, n, o, true).splits;
     CHECK(s.gparts >= kZeroBytes && s.g - s.gparts >= (size_t)(splits * M * r * 4) && s.g3 - s.g >= (size_t)M * r * 4);
     CHECK(s.gparts % 16 == 0 && s.g % 16 == 0 && s.g3 % 16 == 0 && s.t3 % 16 == 0 && s.parts % 16 == 0);
     CHECK(s.t3 - s.g3 >= (size_t)M * r * 6 && s.parts - s.t3 >= (size_t)M * r * 6);
@@ -102,15 +103,15 @@ int main() {
         counts[(size_t)a] = a + 1 == n ? left : pick(0, most);
         left -= counts[(size_t)a];
       }
-      for (int64_t K : {h, o}) {
-        const AdapterPlan q = plan_adapters_rows(M, n, K);
+      for (bool lines : {false, true}) {
+        const AdapterPlan q = plan_adapters_rows(M, n, lines ? o : h, lines);
         CHECK(tiles_of(counts, q.bm) <= q.tiles);
       }
-      CHECK(tiles_of(counts, p.bm == 16 ? 16 : 64) <= tiles);
+      CHECK(tiles_of(counts, w.bm) <= w.tiles);
       CHECK(tiles_of(counts, it.item) <= it.items);
     }
   }
-  CHECK(bm16 && bm64 && bm128 && few && fold && single && several);
+  CHECK(bm16 && bm64 && bm128 && few && wide16 && wide64 && fold && single && several);
   if (failures) {
     std::printf("%d failures\n", failures);
     return 1;

@@ -40,8 +40,13 @@ WIDTHS = [(272, 144, 16), (1040, 528, 32), (528, 272, 64), (144, 400, 136), (272
           (2048, 1024, 48), (8208, 144, 16)]
 
 
-@pytest.mark.parametrize("h,o,r", WIDTHS)
-@pytest.mark.parametrize("counts", COUNTS, ids=str)
+# enough rows and columns for the larger tiles of every product, whole ones and not
+LARGE = [([3000, 0, 1500, 700], 8208, 8208, 16), ([170] * 30, 8208, 8208, 32), ([2600, 2624], 8192, 8192, 64),
+         ([170] * 30, 4112, 8208, 64), ([2000, 96], 8208, 8208, 136), ([4096], 4096, 8192, 8)]
+CASES = [(c, *w) for c in COUNTS for w in WIDTHS] + LARGE
+
+
+@pytest.mark.parametrize("counts,h,o,r", CASES, ids=str)
 def test_forward_in_whole_numbers(counts, h, o, r):
     rng = np.random.default_rng(sum(counts) + h + r)
     ids, order, offsets = lists(counts, 5, rng)
@@ -103,6 +108,27 @@ def test_gradients_in_whole_numbers(counts, h, o, r, fmt):
                              dev(offsets, torch.int32), dev(order, torch.int32), dev(sx, F32) if fmt else None,
                              want_dX=False)
     assert torch.equal(again[1], dL1) and torch.equal(again[2], dL2)
+
+
+@pytest.mark.parametrize("counts,h,o,r", CASES, ids=str)
+def test_dense_gradients_in_whole_numbers(counts, h, o, r):
+    # every row and column takes part; G is below 2^16, which two bf16 values hold
+    rng = np.random.default_rng(sum(counts) + 5 * h + r)
+    ids, order, offsets = lists(counts, 5, rng)
+    n, M = len(counts), len(ids)
+    dy, x, t = rng.integers(-1, 2, (M, o)), rng.integers(-2, 3, (M, h)), rng.integers(-8, 9, (M, r))
+    l1, l2 = rng.integers(-1, 2, (n, h, r)), rng.integers(-1, 2, (n, r, o))
+    s, base = rng.choice([0.5, 1.0, 2.0], n), rng.integers(-64, 65, (M, h))
+    (dx, _), (dl1, S1), (dl2, S2) = around.adapters_bwd(dy, x, t, l1, l2, s, order, offsets, base)
+    # dL1's terms are 2 |G|, of about 0.54 sqrt(o); its sums of magnitudes count G's own terms, which cancel
+    g = np.abs(np.stack([dy[m] @ l2[a].T if a >= 0 else np.zeros(r) for m, a in enumerate(ids)]))
+    assert np.max(g) < 2 ** 16 and 2 * np.max(np.sum(g, 0)) < 2 ** 23 and np.max(S2) < 2 ** 23 and r * np.max(g) < 2 ** 22
+    dX, dL1, dL2 = nf4.adapters_bwd(dev(dy, BF16), dev(x, BF16), dev(t, F32), dev(l1, BF16), dev(l2, BF16), dev(s, F32),
+                                    dev(offsets, torch.int32), dev(order, torch.int32), base=dev(base, BF16))
+    some = torch.from_numpy(ids >= 0)
+    assert torch.equal(dX.cpu()[some], torch.from_numpy(dx).to(BF16)[some])
+    assert torch.equal(dL1.cpu().double(), torch.from_numpy(dl1))
+    assert torch.equal(dL2.cpu().double(), torch.from_numpy(dl2))
 
 
 def small(M, cols, top, seed):
