@@ -1337,14 +1337,17 @@ hipError_t wide_of(const AdapterWide& p, dim3 gr, hipStream_t st) {
   if (p.r <= 16) hipLaunchKernelGGL((k_adapters_wide<JMAJOR, 1, RW, 16>), gr, dim3(256), 0, st, p);
   else if (p.r <= 32) hipLaunchKernelGGL((k_adapters_wide<JMAJOR, 2, RW, 32>), gr, dim3(256), 0, st, p);
   else if (p.r <= 64) hipLaunchKernelGGL((k_adapters_wide<JMAJOR, 4, RW, 64>), gr, dim3(256), 0, st, p);
+  // (with panels of 64 of L2's rows for each wave a compute unit would hold one workgroup: 1024
+  // rows by 4096 of rank 128 26 us against 20)
+  else if (p.r <= 128)
+    hipLaunchKernelGGL((k_adapters_wide<JMAJOR, RW == 1 && JMAJOR ? 2 : 4, RW, 128>), gr, dim3(256), 0, st, p);
   else hipLaunchKernelGGL((k_adapters_wide<JMAJOR, 4, RW, 256>), gr, dim3(256), 0, st, p);
   return hipGetLastError();
 }
 
-hipError_t wide(const AdapterCall& c, const float* part, int splits, const uint16_t* L,
+hipError_t wide(const AdapterCall& c, const AdapterWidePlan& pl, const float* part, int splits, const uint16_t* L,
                 bool jmajor, int64_t N, const uint16_t* base, uint16_t* out, float* T_out, const Split3& split,
                 hipStream_t st) {
-  const AdapterWidePlan pl = plan_adapters_wide(c.rows.M, c.rows.n, N, c.r);
   AdapterWide p{c.rows, part, splits, L, N, c.r, c.s, base, out, T_out, pl.blocks, split};
   const int64_t nb = (N + 127) / 128;
   const dim3 gr((unsigned)pl.tiles, (unsigned)(pl.bm == 16 ? (nb + 3) / 4 : (nb + pl.blocks - 1) / pl.blocks));
@@ -1353,10 +1356,10 @@ hipError_t wide(const AdapterCall& c, const float* part, int splits, const uint1
 }
 
 // The splits' sum, as it is, in three parts, or both: 4 splits of 16384 rows of rank 64 5.4 us.
-// Where there are few values every workgroup of dX's product adds the splits up by itself
-// instead, which saves a launch.
-__global__ __launch_bounds__(256) void k_adapters_sum(const float* __restrict__ part, int64_t size, int splits, int r,
-                                                      float* __restrict__ out, Split3 split) {
+// Where there are few values every workgroup of the next product adds the splits up by itself
+// instead, which saves a launch.  `out` may be `part`.
+__global__ __launch_bounds__(256) void k_adapters_sum(const float* part, int64_t size, int splits, int r, float* out,
+                                                      Split3 split) {
   for (int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; e < size; e += (int64_t)gridDim.x * 1024) {
     const floatx4 v = join4(part + e, size, splits);
     if (out) *(floatx4*)(out + e) = v;
@@ -1365,6 +1368,13 @@ __global__ __launch_bounds__(256) void k_adapters_sum(const float* __restrict__ 
     split4(v, three);
     store3(split, e / r, (int)(e % r), three);
   }
+}
+
+hipError_t sum(const float* part, int64_t size, int splits, int r, float* out, const Split3& split, hipStream_t st) {
+  // (2^20 workgroups at most: a launch's work-items stay below 2^32)
+  const int64_t groups = std::min<int64_t>((size + 1023) / 1024, 1 << 20);
+  hipLaunchKernelGGL(k_adapters_sum, dim3((unsigned)groups), dim3(256), 0, st, part, size, splits, r, out, split);
+  return hipGetLastError();
 }
 
 template <int X8>
@@ -1390,7 +1400,12 @@ hipError_t launch_adapters_fwd(const AdapterCall& c, const uint16_t* X, const ui
   }
   hipError_t e = narrow(c, pl, X, c.h, c.L1, true, (float*)ws, Split3{}, st);
   if (e != hipSuccess) return e;
-  return wide(c, (const float*)ws, pl.splits, c.L2, true, c.o, base, Y, T_out, Split3{}, st);
+  const AdapterWidePlan wp = plan_adapters_wide(c.rows.M, c.rows.n, c.o, c.r);
+  float* const T = (float*)ws;
+  const bool fold = plan_adapters_fold(c.rows.M, c.r, pl.splits, wp, c.o);
+  if (!fold) e = sum(T, c.rows.M * c.r, pl.splits, c.r, T, Split3{}, st);
+  if (e != hipSuccess) return e;
+  return wide(c, wp, T, fold ? pl.splits : 1, c.L2, true, c.o, base, Y, T_out, Split3{}, st);
 }
 
 hipError_t launch_adapters_bwd(const AdapterCall& c, const void* X, int x8, const float* x_scales, const uint16_t* dY,
@@ -1410,22 +1425,14 @@ hipError_t launch_adapters_bwd(const AdapterCall& c, const void* X, int x8, cons
   float* const G_out = pl.splits > 1 ? G : nullptr;
   hipError_t e = narrow(c, pl, dY, c.o, c.L2, false, gparts, t3, st);
   if (e != hipSuccess) return e;
-  // G's splits are joined by a kernel of their own, or, few as they are, by dX's (every
-  // workgroup of which does it again; one leaves the sum)
-  const int64_t size = c.rows.M * c.r;
-  const bool fold = dX && pl.splits * size <= kAdapterFold;
-  if (fold) {
-    e = wide(c, gparts, pl.splits, c.L1, false, c.h, base, dX, x8 ? G_out : nullptr, g3, st);
+  // G's splits are joined by a kernel of their own, or by dX's
+  const AdapterWidePlan wp = plan_adapters_wide(c.rows.M, c.rows.n, c.h, c.r);
+  if (dX && plan_adapters_fold(c.rows.M, c.r, pl.splits, wp, c.h)) {
+    e = wide(c, wp, gparts, pl.splits, c.L1, false, c.h, base, dX, x8 ? G_out : nullptr, g3, st);
   } else {
-    if (G_out || g3.to) {
-      // (2^20 workgroups at most: a launch's work-items stay below 2^32)
-      const int64_t groups = std::min<int64_t>((size + 1023) / 1024, 1 << 20);
-      hipLaunchKernelGGL(k_adapters_sum, dim3((unsigned)groups), dim3(256), 0, st, gparts, size, pl.splits, c.r, G_out,
-                         g3);
-      e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
-    if (dX) e = wide(c, G, 1, c.L1, false, c.h, base, dX, nullptr, Split3{}, st);
+    if (G_out || g3.to) e = sum(gparts, c.rows.M * c.r, pl.splits, c.r, G_out, g3, st);
+    if (e != hipSuccess) return e;
+    if (dX) e = wide(c, wp, G, 1, c.L1, false, c.h, base, dX, nullptr, Split3{}, st);
   }
   if (e != hipSuccess) return e;
   const AdapterGrad g1{X, x_scales, c.h, G, g3.to, c.r, c.s, it.item, it.items, it.single, 1, parts, dL1, w};

@@ -295,13 +295,14 @@ struct AdapterWidePlan {
   int blocks;     // blocks of 128 columns that a workgroup of 64 rows goes over
 };
 AdapterWidePlan plan_adapters_wide(int64_t M, int n, int64_t N, int r);
+// Whether their workgroups add up the splits by themselves, or a launch before them does.
+bool plan_adapters_fold(int64_t M, int r, int splits, const AdapterWidePlan& w, int64_t N);
 // Rows of an item of the adapters' gradients, and the items there are at most.
 struct AdapterItems {
   int item;
   int64_t items;
   int single;  // no adapter has two
 };
-constexpr int64_t kAdapterFold = 1 << 18;  // values of G's splits that dX's kernel joins
 AdapterItems plan_adapters_items(int64_t M, int n, int64_t h, int64_t o, int r);
 // Byte offsets of the parts of the backward pass's workspace; the zeros come first.
 struct AdapterGradSpace {

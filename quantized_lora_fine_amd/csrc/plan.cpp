@@ -177,6 +177,15 @@ AdapterWidePlan plan_adapters_wide(int64_t M, int n, int64_t N, int r) {
   return p;
 }
 
+// Every workgroup of a tile adds the splits up again: up to 48 MB of such reading in all.  Past
+// that a launch does it once.  By replayed graphs, with / without that launch: 256 rows by 4096 of
+// rank 16 12.8 / 10.2 us, 2048 rows of rank 64 (32 MB) 32.7 / 31.4, 4096 rows of rank 128 (512 MB)
+// 72 / 122.
+bool plan_adapters_fold(int64_t M, int r, int splits, const AdapterWidePlan& w, int64_t N) {
+  const int64_t blocks = (N + 127) / 128, groups = w.bm == 16 ? (blocks + 3) / 4 : (blocks + w.blocks - 1) / w.blocks;
+  return splits == 1 || splits * M * r * 4 * groups <= (int64_t)48 << 20;
+}
+
 // The rows of an item: as many sets of 256 workgroups (one a compute unit) as take the
 // least time, by 25 ns a row and 4 us around a workgroup's loop, with the items' sums
 // written and read once more (5 TB/s).

@@ -56,7 +56,7 @@ int main() {
   for (int i = 0; i < 100000; ++i) route_plan(pick(0, 9) ? any(30) : 0, (int)any(12), ones);
   CHECK(ones[0] && ones[1]);
 
-  bool bm16 = false, bm64 = false, bm128 = false, few = false, fold = false, single = false, wide16 = false, wide64 = false, several = false;
+  bool bm16 = false, bm64 = false, bm128 = false, few = false, fold = false, sum = false, single = false, wide16 = false, wide64 = false, several = false;
   for (int i = 0; i < 200000; ++i) {
     const int64_t M = any(26), h = 16 * any(18), o = 16 * any(18);
     const int n = (int)any(12), r = 8 * (int)pick(1, 32);
@@ -92,7 +92,8 @@ int main() {
     CHECK(s.gparts % 16 == 0 && s.g % 16 == 0 && s.g3 % 16 == 0 && s.t3 % 16 == 0 && s.parts % 16 == 0);
     CHECK(s.t3 - s.g3 >= (size_t)M * r * 6 && s.parts - s.t3 >= (size_t)M * r * 6);
     CHECK(s.total - s.parts >= (it.single ? 0 : (size_t)it.items * r * (h + o) * 4));
-    fold |= splits * M * r <= kAdapterFold;
+    (plan_adapters_fold(M, r, (int)splits, plan_adapters_wide(M, n, h, r), h) ? fold : sum) = true;
+    CHECK(plan_adapters_fold(M, r, 1, w, o));
     // whatever the rows' counts are, the launches hold their tiles and items
     if (M <= 1 << 16 && i % 8 == 0) {
       std::vector<int64_t> counts((size_t)n, 0);
@@ -111,7 +112,7 @@ int main() {
       CHECK(tiles_of(counts, it.item) <= it.items);
     }
   }
-  CHECK(bm16 && bm64 && bm128 && few && wide16 && wide64 && fold && single && several);
+  CHECK(bm16 && bm64 && bm128 && few && wide16 && wide64 && fold && sum && single && several);
   if (failures) {
     std::printf("%d failures\n", failures);
     return 1;

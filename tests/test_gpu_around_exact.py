@@ -42,7 +42,8 @@ WIDTHS = [(272, 144, 16), (1040, 528, 32), (528, 272, 64), (144, 400, 136), (272
 
 # enough rows and columns for the larger tiles of every product, whole ones and not
 LARGE = [([3000, 0, 1500, 700], 8208, 8208, 16), ([170] * 30, 8208, 8208, 32), ([2600, 2624], 8192, 8192, 64),
-         ([170] * 30, 4112, 8208, 64), ([2000, 96], 8208, 8208, 136), ([4096], 4096, 8192, 8)]
+         ([170] * 30, 4112, 8208, 64), ([2000, 96], 8208, 8208, 136), ([4096], 4096, 8192, 8),
+         ([2000, 96], 8208, 8208, 96), ([170] * 16, 8192, 8192, 128), ([100] * 12, 4096, 4096, 128)]
 CASES = [(c, *w) for c in COUNTS for w in WIDTHS] + LARGE
 
 
