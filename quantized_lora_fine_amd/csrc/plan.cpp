@@ -172,7 +172,7 @@ AdapterWidePlan plan_adapters_wide(int64_t M, int n, int64_t N, int r) {
   p.tiles = adapter_tiles(M, n, 64);
   // About 1024 workgroups (three are on a compute unit, so a second set is partly filled):
   // 7977 rows by 11008 of rank 16 78 us, 8192 rows by 11008 of rank 64 94, against 103 and
-  // 116 for 256, 83 and 97 for 1536, 93 and 111 for 3072, whose starts are more of them.
+  // 116 for 256, 83 and 97 for 1536, and more beyond, whose starts are more of them.
   p.blocks = (int)std::max<int64_t>(1, std::min(p.tiles * blocks / 1024, blocks));
   return p;
 }
