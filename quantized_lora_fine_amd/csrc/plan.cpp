@@ -191,15 +191,18 @@ bool plan_adapters_fold(int64_t M, int r, int splits, const AdapterWidePlan& w, 
 // written and read once more (5 TB/s).
 AdapterItems plan_adapters_items(int64_t M, int n, int64_t h, int64_t o, int r) {
   AdapterItems p{64, 1, 0};
-  // a launch for the join costs more than the rows that others could take
-  if (M <= 1024 && n <= 64) {
+  // Of few rows a launch for the join costs more than the rows that others could take.  A call in
+  // one item / in several: 16 adapters of 512 rows in all at 4096 x 4096 and rank 16 21 / 26 us, one
+  // of 512 rows 22 / 25 and of 1024 32 / 29; at rank 64, whose rows take longer, 33 / 42, of 256 27 /
+  // 29, of 512 36 / 33 and of 1024 52 / 40.
+  const int64_t used = std::min<int64_t>(M, n);
+  if (M <= 1024 && n <= 64 && M <= (r <= 32 ? 512 : 256) * used) {
     p.item = (int)((M + 63) / 64 * 64);
     p.items = std::min<int64_t>(M, n);
     p.single = 1;
     return p;
   }
   const int64_t cols = ((h + 255) / 256 + (o + 255) / 256) * ((r + 63) / 64);
-  const int64_t used = std::min<int64_t>(M, n);
   double least = 0;
   for (int64_t k = 1; k <= 256; k = k < 8 ? k + 1 : k * 5 / 4) {
     const int64_t item = std::min<int64_t>((((M + k - 1) / k) + 63) / 64 * 64, kMaxAdapterItem);
