@@ -614,7 +614,7 @@ __device__ __forceinline__ floatx4 join4(const float* part, int64_t stride, int 
 // first operand and column i of L's fragment f is 8 i + f, so a lane ends with 8
 // neighbouring columns of 4 rows, and 16 lanes read and write 256 bytes of a row.  For that
 // a panel of L stands in LDS with column 8 i + f at place 16 f + i.  A rank above 16 NJ is
-// taken in runs of 64.
+// taken in runs of 16 NJ.
 // Bound by reading base and writing the output: 7977 rows by 11008 of rank 16 79 us (4.4 TB/s),
 // 8192 by 11008 of rank 64 92 (3.9), 16384 by 8192 of rank 64 119 (4.5), where a copy of such a
 // size reaches 5.4; the rest are the starts of 1024 workgroups, with the joining of P in each.
