@@ -84,15 +84,19 @@ __device__ __forceinline__ int64_t row_at(const AdapterRows& R, const Tile& t, i
   return (uint64_t)row < (uint64_t)R.M ? row : -1;
 }
 
-// Four neighbouring fp32 values as two bf16 ones each; one that is no number stands in the
-// first alone.
+// Four neighbouring fp32 values as two bf16 ones each.  The first is at most the largest bf16
+// value, which fp32's last ones would round past to an infinity; what lies beyond stands in the
+// second, and so does an infinity or a NaN.
 __device__ __forceinline__ void split4(floatx4 x, uint2 (&part)[2]) {
-  part[0] = uint2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+  constexpr float kTop = 0x1.FEp127f;
+  float c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = __builtin_amdgcn_fmed3f(x[i], -kTop, kTop);
+  part[0] = uint2{pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3])};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t word = i < 2 ? part[0].x : part[0].y;
-    const float h = __builtin_bit_cast(float, i & 1 ? word & 0xFFFF0000u : word << 16);
-    x[i] = fabsf(h) < INFINITY ? x[i] - h : 0.f;
+    x[i] -= __builtin_bit_cast(float, i & 1 ? word & 0xFFFF0000u : word << 16);
   }
   part[1] = uint2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
 }
