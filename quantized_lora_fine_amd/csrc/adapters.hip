@@ -35,17 +35,20 @@ namespace nf4k {
 
 namespace {
 
-// Tile t of `bm` rows: its adapter, positions [p0, p1), and whether they are all of the
-// adapter's.  Every wave scans the tile counts of 64 adapters at a time.
+// Tile t of `bm` rows: its adapter, positions [p0, p1), whether they are all of the adapter's,
+// and, where they are not, its number among the tiles of adapters that have several.  Every wave
+// scans the tile counts of 64 adapters at a time.
 struct Tile {
   int a;
   int p0, p1;
   bool whole;
+  uint32_t part;
 };
 __device__ __forceinline__ bool find_tile(const AdapterRows& R, int bm, uint32_t t, Tile& tile) {
   const int lane = threadIdx.x & 63;
   const int M = (int)R.M;
   uint32_t base = 0;  // (counts may wrap where offsets do not ascend; the rows stay inside all the same)
+  uint32_t alone = 0;  // tiles that are all of their adapter's
   for (int a0 = 0; a0 < R.n; a0 += 64) {
     const int i = a0 + lane;
     int lo = 0, cnt = 0;
@@ -60,7 +63,7 @@ __device__ __forceinline__ bool find_tile(const AdapterRows& R, int bm, uint32_t
       const uint32_t v = __shfl_up(incl, o);
       if (lane >= o) incl += v;
     }
-    const uint64_t hit = __ballot(base + incl > t);
+    const uint64_t hit = __ballot(base + incl > t), single = __ballot(tiles == 1);
     if (hit) {
       const int l = __builtin_ctzll(hit);
       const uint32_t first = base + (uint32_t)__builtin_amdgcn_readlane((int)(incl - tiles), l);
@@ -70,9 +73,11 @@ __device__ __forceinline__ bool find_tile(const AdapterRows& R, int bm, uint32_t
       tile.p0 = (int)min(p0, (int64_t)l0 + ln);
       tile.p1 = (int)min(p0 + bm, (int64_t)l0 + ln);
       tile.whole = ln <= bm;
+      tile.part = t - alone - (uint32_t)__popcll(single & (((uint64_t)1 << l) - 1));
       return tile.p0 < tile.p1;
     }
     base += (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
+    alone += (uint32_t)__popcll(single);
   }
   return false;
 }
@@ -1068,6 +1073,7 @@ __device__ __forceinline__ void grad_tile(const AdapterRows& rows, const Adapter
   }
   Tile tile;
   if (!find_tile(rows, p.item, blockIdx.y, tile)) return;
+  if (!tile.whole && tile.part >= (uint32_t)p.parts) return;  // offsets that do not ascend
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = p.r, j0 = blockIdx.z * 64;
@@ -1248,7 +1254,7 @@ __device__ __forceinline__ void grad_tile(const AdapterRows& rows, const Adapter
   }
   if (!early) multiply();
   const float s = tile.whole ? p.s[tile.a] : 1.f;
-  float* out = tile.whole ? p.out + (int64_t)tile.a * r * N : p.part + (int64_t)blockIdx.y * r * N;
+  float* out = tile.whole ? p.out + (int64_t)tile.a * r * N : p.part + (int64_t)tile.part * r * N;
 #pragma unroll
   for (int j = 0; j < FJ; ++j)
 #pragma unroll
@@ -1285,7 +1291,7 @@ __global__ __launch_bounds__(256) void k_adapters_join(AdapterRows rows, Adapter
   const AdapterGrad& p = blockIdx.z ? p1 : p0;
   const int a = blockIdx.y, lane = threadIdx.x & 63;
   const int M = (int)rows.M;
-  // items before a's, and a's own
+  // the parts before a's (an adapter of one item has none), and a's own items
   uint32_t first = 0, own = 0;
   for (int a0 = 0; a0 <= a; a0 += 64) {
     const int i = a0 + lane;
@@ -1297,7 +1303,7 @@ __global__ __launch_bounds__(256) void k_adapters_join(AdapterRows rows, Adapter
     }
     const uint64_t me = __ballot(i == a);
     if (me) own = (uint32_t)__builtin_amdgcn_readlane((int)items, __builtin_ctzll(me));
-    uint32_t sum = i < a ? items : 0;
+    uint32_t sum = i < a && items > 1 ? items : 0;
 #pragma unroll
     for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
     first += sum;
@@ -1305,8 +1311,8 @@ __global__ __launch_bounds__(256) void k_adapters_join(AdapterRows rows, Adapter
   if (own == 1) return;
   const int64_t size = (int64_t)p.r * p.N;
   const float s = p.s[a];
-  // items past the launch (offsets that do not ascend) have no part
-  const uint32_t end = min(first + own, (uint32_t)p.items);
+  // (offsets that do not ascend: some items have no part)
+  const uint32_t end = min(first + own, (uint32_t)p.parts);
   for (int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; e < size; e += (int64_t)gridDim.x * 1024) {
     floatx4 v = {0.f, 0.f, 0.f, 0.f};
     for (uint32_t i = first; i < end; ++i) v += *(const floatx4*)(p.part + i * size + e);
@@ -1439,9 +1445,9 @@ hipError_t launch_adapters_bwd(const AdapterCall& c, const void* X, int x8, cons
     if (dX) e = wide(c, wp, G, 1, c.L1, false, c.h, base, dX, nullptr, Split3{}, st);
   }
   if (e != hipSuccess) return e;
-  const AdapterGrad g1{X, x_scales, c.h, G, g3.to, c.r, c.s, it.item, it.items, it.single, 1, parts, dL1, w};
-  const AdapterGrad g2{dY, nullptr, c.o, nullptr, t3.to, c.r, c.s, it.item, it.items, it.single, 0,
-                       parts + it.items * c.r * c.h, dL2, w};
+  const AdapterGrad g1{X, x_scales, c.h, G, g3.to, c.r, c.s, it.item, it.items, it.parts, it.single, 1, parts, dL1, w};
+  const AdapterGrad g2{dY, nullptr, c.o, nullptr, t3.to, c.r, c.s, it.item, it.items, it.parts, it.single, 0,
+                       parts + it.parts * c.r * c.h, dL2, w};
   e = x8 == 0   ? grad_of<0>(c.rows, g1, g2, st)
       : x8 == 1 ? grad_of<1>(c.rows, g1, g2, st)
                 : grad_of<2>(c.rows, g1, g2, st);

@@ -575,7 +575,7 @@ size_t adapters_ws(int32_t op, int64_t M, int64_t rows, int64_t cols, int32_t n,
   if (M == 0) return 0;
   if (op == NF4_OP_FWD)
     return plan_adapters_few(M, n, cols, rows, r) ? 0 : (size_t)plan_adapters_rows(M, n, cols, false).splits * M * r * 4;
-  return plan_adapters_space(M, n, cols, rows, r).total;
+  return plan_adapters_bwd_bytes(M, n, cols, rows, r);
 }
 
 size_t norm_ws(int64_t M, int64_t H) { return align256((size_t)std::max(rmsnorm_parts(M, (int)H), 1) * H * 4); }

@@ -269,9 +269,10 @@ struct AdapterGrad {
   const float* s;
   int item;       // rows an item, a multiple of 64
   int64_t items;  // at most
+  int64_t parts;  // items of adapters that have several, at most
   int single;     // every adapter's rows are one item, and the products clear what has none
   int trans;      // out [n][N][r], else [n][r][N]
-  float* part;    // [items][r * N]
+  float* part;    // [parts][r * N]
   float* out;
   const void* zero;  // kZeroBytes of zeros
 };
@@ -297,18 +298,23 @@ struct AdapterWidePlan {
 AdapterWidePlan plan_adapters_wide(int64_t M, int n, int64_t N, int r);
 // Whether their workgroups add up the splits by themselves, or a launch before them does.
 bool plan_adapters_fold(int64_t M, int r, int splits, const AdapterWidePlan& w, int64_t N);
-// Rows of an item of the adapters' gradients, and the items there are at most.
+// Rows of an item of the adapters' gradients, the items there are at most, and those of adapters
+// that have several, whose sums need a place of their own.
 struct AdapterItems {
   int item;
   int64_t items;
-  int single;  // no adapter has two
+  int single;  // no adapter has two, and no join is launched
+  int64_t parts;
 };
 AdapterItems plan_adapters_items(int64_t M, int n, int64_t h, int64_t o, int r);
-// Byte offsets of the parts of the backward pass's workspace; the zeros come first.
+// Byte offsets of the parts of the backward pass's workspace; the zeros come first.  `total` has
+// room for every item's sums.
 struct AdapterGradSpace {
   size_t gparts, g, g3, t3, parts, total;
 };
 AdapterGradSpace plan_adapters_space(int64_t M, int n, int64_t h, int64_t o, int r);
+// Its bytes: without the room of items that are all of their adapter's and go straight to the results.
+size_t plan_adapters_bwd_bytes(int64_t M, int n, int64_t h, int64_t o, int r);
 NF4K_WEAK hipError_t launch_adapters_fwd(const AdapterCall& c, const uint16_t* X, const uint16_t* base, uint16_t* Y,
                                          float* T_out, void* ws, hipStream_t st);
 // x8: 0 X is bf16, 1 e4m3, 2 e5m2

@@ -190,7 +190,7 @@ bool plan_adapters_fold(int64_t M, int r, int splits, const AdapterWidePlan& w, 
 // least time, by 25 ns a row and 4 us around a workgroup's loop, with the items' sums
 // written and read once more (5 TB/s).
 AdapterItems plan_adapters_items(int64_t M, int n, int64_t h, int64_t o, int r) {
-  AdapterItems p{64, 1, 0};
+  AdapterItems p{64, 1, 0, 0};
   // Of few rows a launch for the join costs more than the rows that others could take.  A call in
   // one item / in several: 16 adapters of 512 rows in all at 4096 x 4096 and rank 16 21 / 26 us, one
   // of 512 rows 22 / 25 and of 1024 32 / 29; at rank 64, whose rows take longer, 33 / 42, of 256 27 /
@@ -216,6 +216,8 @@ AdapterItems plan_adapters_items(int64_t M, int n, int64_t h, int64_t o, int r) 
     if (item == 64) break;
   }
   p.items = std::min<int64_t>(M, M / p.item + used);
+  // c > item rows are fewer than 2 c / item items
+  p.parts = p.item >= M ? 0 : std::min<int64_t>(p.items, 2 * M / p.item);
   return p;
 }
 
@@ -230,6 +232,11 @@ AdapterGradSpace plan_adapters_space(int64_t M, int n, int64_t h, int64_t o, int
   const AdapterItems it = plan_adapters_items(M, n, h, o, r);
   s.total = s.parts + (it.single ? 0 : (size_t)it.items * r * (h + o) * 4);
   return s;
+}
+
+size_t plan_adapters_bwd_bytes(int64_t M, int n, int64_t h, int64_t o, int r) {
+  const AdapterItems it = plan_adapters_items(M, n, h, o, r);
+  return plan_adapters_space(M, n, h, o, r).total - (it.single ? 0 : (size_t)(it.items - it.parts) * r * (h + o) * 4);
 }
 
 // Tiles of the block-scaled product, with what one takes on an MI355X: `start`
