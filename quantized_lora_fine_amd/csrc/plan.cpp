@@ -127,16 +127,20 @@ static int64_t adapter_tiles(int64_t M, int n, int bm) {
 
 // Tiles of 16 rows where an adapter has few in the mean or the product is small, else of 64, or
 // of 128 where there are enough of them.  About 512 workgroups, each with 256 of the contraction
-// or more.  Measured (us, tiles of 16 / of 64): T of 256 rows by 4096 of rank 16 4.4 / 5.7, of 1024
-// rows 6.6 / 7.3, by 11008 8.6 / 11.7, but of 4096 rows by 11008 of rank 64 39 / 31.  G (`lines`:
-// L2's rows lie as the contraction does, so that its panel costs the larger tiles less) of 256
-// rows by 4096 4.4 / 5.0 and of 1024 of rank 64 11.6 / 8.7; of 256 rows of 32 adapters by 28672 of
-// rank 16 13 / 23, of 512 rows of rank 32 39 / 26.  Tiles of 128 against 64, both passes' calls: 32
-// rows of each of 16 adapters 35.5 / 34.5, 512 rows of each 127 / 129.
+// or more.  Measured (us, whole calls by replayed graphs with 1024 columns on the other side, tiles
+// of 16 / larger ones).  T, one adapter: 256 rows by 4096 of rank 16 9.5 / 10.7, 1024 rows 11.2 / 13.2,
+// by 11008 13.6 / 19.3; of rank 64 20.4 / 26.5, 700 rows by 28672 26.1 / 32.1 (2^20 times 19.1), but
+// 1024 by 28672 37.0 / 34.5 (28) and 4096 by 11008 50.0 / 43.4.  Two adapters as one (21.0 / 26.6).
+// Where there are more, the tiles of 16 read more of the pool again: 8 of rank 64, 2048 rows by 4096
+// 24.4 / 25.1 (8.0), 1024 by 28672 61.8 / 40.7; 16, 1024 by 11008 30.7 / 27.5 (10.8).  G (`lines`: L2's
+// rows lie as the contraction does, so that its panel costs the larger tiles less): 256 rows by 4096
+// of rank 16 16.2 / 16.8, of rank 64 26.4 / 26.1; of 32 adapters by 28672 of rank 16 70 / 78, but 512
+// rows of rank 32 107 / 94.  Tiles of 128 against 64, both passes: 32 rows of each of 16 adapters at
+// 4096 x 4096 36.7 / 35.7, 8192 rows of one of rank 64 73 / 70, of 64 adapters 82 / 85.
 AdapterPlan plan_adapters_rows(int64_t M, int n, int64_t K, bool lines) {
   AdapterPlan p;
   const int64_t used = std::min<int64_t>(M, n);
-  const bool few = M <= (lines ? 8 : 16) * used || M * K <= (lines ? (int64_t)1 << 20 : (int64_t)10 << 20);
+  const bool few = M <= (lines ? 8 : 16) * used || M * K <= (int64_t)(lines ? 1 : used <= 2 ? 20 : 10) << 20;
   p.bm = few ? 16 : M <= 256 * used ? 64 : 128;
   p.tiles = adapter_tiles(M, n, p.bm);
   const int64_t most = std::max<int64_t>(1, (K + 255) / 256);
@@ -160,14 +164,16 @@ int plan_adapters_few(int64_t M, int n, int64_t h, int64_t o, int r) {
 }
 
 // Tiles of 16 rows, whose waves have a block each, up to so many workgroups: they start sooner,
-// but read L for every 16 rows.  Measured (us, tiles of 16 / of 64): Y of 64 rows of 16 adapters by
-// 11008 of rank 16 7 / 13, of 1024 rows by 4096 of rank 64 13 / 22, of 2048 by 4096 of rank 128 48 /
-// 123, of 1024 by 28672 of rank 16 29 / 33 (3640 workgroups) and of 2048 61 / 54; at rank 64 of 512
-// rows 37 / 64 (1848) and of 1024 63 / 52.
+// but read L for every 16 rows.  Measured (us, whole calls of 1024 columns of X by replayed graphs,
+// tiles of 16 / of 64): 64 rows of 16 adapters by 11008 of rank 16 9.1 / 15.9, one adapter's 640 rows by
+// 28672 22.0 / 22.8 (2296 workgroups), 1024 36.9 / 35.6 (3640), 2048 66 / 57; of rank 64 1024 rows by 4096
+// 18.0 / 21.4, 512 by 28672 33.6 / 39.2 (1848), 3800 by 4096 38.3 / 42.6 (1904), but 4096 41.6 / 34.0 (2056)
+// and 1024 by 28672 68 / 48; of rank 128 2048 by 4096 level.  (What is left on the wrong side are some
+// hundred rows of each of a few adapters by 28672: 448 of 4, 1792 workgroups, 40.9 / 32.0.)
 AdapterWidePlan plan_adapters_wide(int64_t M, int n, int64_t N, int r) {
   const int64_t blocks = (N + 127) / 128;
   AdapterWidePlan p{16, adapter_tiles(M, n, 16), 1};
-  if (p.tiles * ((blocks + 3) / 4) <= (r <= 32 ? 3500 : 1800)) return p;
+  if (p.tiles * ((blocks + 3) / 4) <= (r <= 32 ? 3500 : 2000)) return p;
   p.bm = 64;
   p.tiles = adapter_tiles(M, n, 64);
   // About 1024 workgroups (three are on a compute unit, so a second set is partly filled):
@@ -178,9 +184,9 @@ AdapterWidePlan plan_adapters_wide(int64_t M, int n, int64_t N, int r) {
 }
 
 // Every workgroup of a tile adds the splits up again: up to 48 MB of such reading in all.  Past
-// that a launch does it once.  By replayed graphs, with / without that launch: 256 rows by 4096 of
-// rank 16 12.8 / 10.2 us, 2048 rows of rank 64 (32 MB) 32.7 / 31.4, 4096 rows of rank 128 (512 MB)
-// 72 / 122.
+// that a launch does it once.  By replayed graphs at 4096 x 4096, with / without that launch: 256 rows
+// of rank 16 12.9 / 10.4 us, 2048 rows of rank 64 33.1 / 31.2 (16 MB), their gradients 58.7 / 61.1 (64 MB),
+// those of 4096 rows of rank 128 115 / 164 (512 MB).
 bool plan_adapters_fold(int64_t M, int r, int splits, const AdapterWidePlan& w, int64_t N) {
   const int64_t blocks = (N + 127) / 128, groups = w.bm == 16 ? (blocks + 3) / 4 : (blocks + w.blocks - 1) / w.blocks;
   return splits == 1 || splits * M * r * 4 * groups <= (int64_t)48 << 20;
