@@ -1073,7 +1073,6 @@ __device__ __forceinline__ void grad_tile(const AdapterRows& rows, const Adapter
   }
   Tile tile;
   if (!find_tile(rows, p.item, blockIdx.y, tile)) return;
-  if (!tile.whole && tile.part >= (uint32_t)p.parts) return;  // offsets that do not ascend
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = p.r, j0 = blockIdx.z * 64;
@@ -1254,6 +1253,7 @@ __device__ __forceinline__ void grad_tile(const AdapterRows& rows, const Adapter
   }
   if (!early) multiply();
   const float s = tile.whole ? p.s[tile.a] : 1.f;
+  const bool room = tile.whole || tile.part < (uint32_t)p.parts;  // else offsets that do not ascend
   float* out = tile.whole ? p.out + (int64_t)tile.a * r * N : p.part + (int64_t)tile.part * r * N;
 #pragma unroll
   for (int j = 0; j < FJ; ++j)
@@ -1261,7 +1261,7 @@ __device__ __forceinline__ void grad_tile(const AdapterRows& rows, const Adapter
     for (int c = 0; c < FC; ++c) {
       const int jj = j0 + 16 * (wj * FJ + j) + 4 * g;
       const int64_t cc = c0 + 16 * (wc * FC + c) + li;
-      if (jj >= r || cc >= N) continue;  // r % 4 == 0
+      if (jj >= r || cc >= N || !room) continue;  // r % 4 == 0
       const floatx4 o = acc[j][c] * s;
       if (p.trans) {
         *(floatx4*)(out + cc * r + jj) = o;
