@@ -664,8 +664,9 @@ nf4_status nf4_route_workspace_bytes(int64_t M, int32_t n, size_t *bytes);
  *   offsets, order : DEVICE int32, as nf4_route writes them: adapter a's rows are
  *             order[offsets[a]] to order[offsets[a + 1] - 1], in [0, M); order NULL: the
  *             rows offsets[a] to offsets[a + 1] - 1 themselves.  Read by the kernels, so
- *             nothing waits for the routing.  Rows that no adapter has are neither read nor
- *             written.  Offsets outside [0, M] are taken as the nearest of the two, and
+ *             nothing waits for the routing.  Rows that no adapter has are not written, and
+ *             no result depends on what they hold: Y keeps what it held there, which is
+ *             base's where it is base.  Offsets outside [0, M] are taken as the nearest of the two, and
  *             entries of order outside [0, M) name no row; where offsets do not ascend, or
  *             a row is listed twice, which rows are written, and with what, is unspecified
  *             (never any outside the buffers).
@@ -702,9 +703,11 @@ nf4_status nf4_adapters_workspace_bytes(int32_t op, int64_t M, int64_t rows, int
  *   dY      : bf16 [M][rows];  T : fp32 [M][r].
  *   base    : bf16 [M][cols], the gradient through the shared projection (dY W), dX itself
  *             (in place), or NULL for 0.  dX NULL: no input gradient.
- * An adapter without rows gets zeros.  Sums are fp32 in a fixed order; G and T enter the
- * products for dL1 and dL2 with all their bits (as three bf16 values; an infinity in a row
- * makes a NaN, of its own adapter's sums alone).  M == 0 writes zeros to dL1 and dL2.
+ * An adapter without rows gets zeros, and rows that no adapter has are not written in dX
+ * (in place they keep base's).  Sums are fp32 in a fixed order; G and T enter the products
+ * for dL1 and dL2 with all their bits (as three bf16 values; an infinity in a row makes a
+ * NaN, of its own adapter's sums alone).  Beside codes it is G times the scale of its row and
+ * 128 columns, rounded to fp32 once, that enters dL1's.  M == 0 writes zeros to dL1 and dL2.
  * Everything else, and errors (_ARG: x_format), as nf4_adapters_fwd.
  */
 nf4_status nf4_adapters_bwd(const void *X, const float *x_scales, int32_t x_format, const uint16_t *dY, const float *T,

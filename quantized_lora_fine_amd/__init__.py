@@ -890,7 +890,8 @@ def adapters_fwd(X: torch.Tensor, L1: torch.Tensor, L2: torch.Tensor, s: torch.T
     """nf4_adapters_fwd: (Y bf16 [M][o], T fp32 [M][r] or None), Y = base + s[a] (X L1[a]) L2[a] for the rows of each
     adapter a of the pool L1 [n][h][r], L2 [n][r][o], s fp32 [n].  offsets (and order) as route() gives them; base bf16
     [M][o] is the shared projection's result, or None for 0, and `out` may be base itself.  Rows that no adapter has
-    are not written (undefined in results that this call allocates)."""
+    are not written: they keep what `out` and T_out held (base's rows, in place), and hold nothing defined in results
+    that this call allocates."""
     M, h = _matrix(X, "X")
     dev = _device_for(X, "X")
     n, o, hl, r, l1, l2, sp, ordp, off = _adapters(L1, L2, s, offsets, order, M, dev)
@@ -913,7 +914,9 @@ def adapters_bwd(dY: torch.Tensor, X: torch.Tensor, T: torch.Tensor, L1: torch.T
                  dL1: torch.Tensor | None = None, dL2: torch.Tensor | None = None, ws: torch.Tensor | None = None):
     """nf4_adapters_bwd: (dX bf16 [M][h] or None, dL1 fp32 [n][h][r], dL2 fp32 [n][r][o]) from the forward's T and X, or
     from an 8-bit checkpoint of X: codes and x_scales as the norms and fp8_quantize give them.  base bf16 [M][h] is the
-    gradient through the shared projection, or None for 0, and `dX` may be base itself."""
+    gradient through the shared projection, or None for 0, and `dX` may be base itself.  Rows that no adapter has are
+    not written in dX: they keep what it held (base's rows, in place), and hold nothing defined where this call
+    allocates it.  Where rows without an adapter go on to other calls, give `dX` (base itself, or a tensor of zeros)."""
     M, o = _matrix(dY, "dY")
     dev = _device_for(dY, "dY")
     n, ol, h, r, l1, l2, sp, ordp, off = _adapters(L1, L2, s, offsets, order, M, dev)

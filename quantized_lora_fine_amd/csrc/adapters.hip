@@ -14,7 +14,7 @@
 // of its 24 bits; two would leave 2e-6 of a sum, ten times an fp32 sum's own error).  The
 // matrix cores have room for it: three parts at rank 64 are their highest load, 32 % of the
 // cycles.  8-bit codes are bf16 values exactly, and their scale, one for a row and 128
-// columns, goes to that row of G.
+// columns, goes to that row of G, whose product with it is rounded to fp32 once.
 //
 // All of it is bound by memory where there are many rows (X and dY are read, base and Y or dX
 // read and written), by launches and latencies that follow one another where there are few.
@@ -151,7 +151,7 @@ __device__ __forceinline__ void split_rows(const Split3& o, int64_t block, int64
 // waves take every fourth step of 32 k, kAhead steps' loads under way, and their sums are
 // added in LDS in wave order.  A's rows are the MFMA's second operand, so a lane ends with
 // 4 neighbouring columns of one row; a row or column past the end repeats a valid one and
-// and is not written.  L1 goes through LDS for transposing reads, each wave's own part.
+// is not written.  L1 goes through LDS for transposing reads, each wave's own part.
 // For tiles most of whose rows are not there: no barrier in the loop, whose few steps are
 // latencies one behind the other.  64 rows of 4096 by 48 adapters of rank 32 (12 MB) 6.0 us.
 // Workgroups past the tiles split T for the products over rows (in a backward pass).
@@ -507,8 +507,10 @@ __global__ __launch_bounds__(256) void k_adapters_narrow(AdapterNarrow p) {
   }
   // Where the width is a power of two, tiles begin at different steps: all workgroups would
   // otherwise read from the same few memory channels at a time (16000 rows of 8192: 80 us
-  // against 90).  Elsewhere the tiles' common steps share L (16384 rows of 28672 at rank 64:
-  // 178 us, and 196 with steps of their own).
+  // against 90; whole calls of 8192 rows of 16384 at rank 64 82 against 119, of 8192 level).
+  // Elsewhere the tiles' common steps share L (16384 rows of 28672 at rank 64: 178 us, and 196
+  // with steps of their own).  Multiples of 4096 that are no power of two need neither: calls of
+  // 8192 rows of 12288 and 24576 are level.  Of 11008, at rank 64, apart would be 69 against 72.
   const int first = (K & (K - 1)) == 0 ? (int)(blockIdx.x * 5u % (unsigned)steps) : 0;
   auto place = [&](int t) -> int { return t + first < steps ? t + first : t + first - steps; };
   auto copy = [&](int t, int b) {
@@ -862,9 +864,11 @@ __global__ __launch_bounds__(256, RW == 1 && NJ < 4 ? 4 : 1) void k_adapters_wid
 // The forward pass of a tile of 16 rows in one launch, for ranks up to 16: every workgroup
 // of a tile makes the whole T, its 16 waves taking every 16th step of 32 columns of X, and
 // then its part of the columns of Y, a block of 128 a wave at a time.  Making T again in
-// each of a tile's workgroups reads L1[a] from the caches.  A call of a few rows is bound by
-// the host, for which a launch is 3.7 us (one token, rank 16, 4096 x 4096: 8.5 to
-// 9.2 us a call against 13.0 with two launches; by replayed graphs 8.3 against 8.1).
+// each of a tile's workgroups reads L1[a] from the caches.  An eager call of a few rows in two
+// launches is bound by the host, for which each is 3.7 us; in one it is bound by this kernel's
+// chain of loads: offsets, order, two rounds of X and L1, the join, Y (one token, rank 16,
+// 4096 x 4096: 11.4 us a call that allocates its results and 8.5 one that is given them, against 15.2
+// and 13.0 with two launches; by replayed graphs 8.4 against 8.1).
 // The products are those of k_adapters_narrow_few and k_adapters_wide.
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(1024) void k_adapters_few(AdapterFew p) {
@@ -1013,8 +1017,8 @@ __global__ __launch_bounds__(1024) void k_adapters_few(AdapterFew p) {
 //
 // bf16 (X8 0): P comes as three bf16 parts, made once for all columns.
 // 8 bits (X8 1: e4m3, 2: e5m2): the codes are read transposed and become bf16 in registers;
-// P comes in fp32 and is multiplied by the scales of its row, one for each 128 columns, and
-// split a step ahead into tiles beside the ring.
+// P comes in fp32 and is multiplied by the scales of its row, one for each 128 columns (rounded
+// to fp32), and split a step ahead into tiles beside the ring.
 //
 // The two waves of a SIMD take turns: the lower four read a step and multiply it (and split
 // before), the upper four multiply the step before and read (and split last).
@@ -1273,7 +1277,7 @@ __device__ __forceinline__ void grad_tile(const AdapterRows& rows, const Adapter
   __builtin_amdgcn_s_waitcnt(0);  // no copy is on its way into LDS that is no longer this workgroup's
 }
 
-// dL1's columns, then dL2's (p1.N = 0: dL2's alone).
+// dL1's columns, then dL2's.
 template <int X8, int NJ>
 __global__ __launch_bounds__(512) void k_adapters_grad(AdapterRows rows, AdapterGrad p1, AdapterGrad p2) {
   using G = GradTile<X8, NJ>;

@@ -151,11 +151,13 @@ AdapterPlan plan_adapters_rows(int64_t M, int n, int64_t K, bool lines) {
 }
 
 // One launch for a few tiles of 16 rows and a small L1[a], which every workgroup of a tile
-// reads.  It saves a launch (3.7 us) on the host, which bounds such calls, and costs time on the
-// device: a call / by replayed graphs, against two launches, one token at rank 16 and 4096 x
-// 4096 9.2 / 8.3 against 13.0 / 8.1 us, at 8192 x 8192 10.3 / 10.3 against 13.0 / 9.3, 16 tokens
-// of one adapter 11.2 / 11.1 against 13.3 / 8.7 and 15.5 / 15.4 against 13.1 / 9.9, 200 tokens 11.6 /
-// 11.5 against 13.0 / 9.5.  At rank 32 it would be 14.1 and its registers too few, at rank 64
+// reads.  It saves a launch (3.7 us) on the host, which bounds such a call in two, and costs time on
+// the device, so that an eager call gains and a replayed one loses: a call with its results
+// allocated / by replayed graphs, against two launches, one token at rank 16 and 4096 x 4096 11.4 / 8.4
+// against 15.2 / 8.1 us, at 8192 x 8192 11.5 / 10.3 against 15.5 / 9.4, at 4096 x 4096 16 tokens of one
+// adapter 11.6 / 11.1 against 15.5 / 8.9, 64 of 8 at rank 8 11.6 / 10.5 against 15.6 / 9.4, 128 of 8
+// 11.5 / 11.6 against 15.7 / 9.4; 16 tokens of one adapter at 8192 x 8192, which take two launches,
+// would be 15.4 in one, against 10.  At rank 32 it would be 14.1 and its registers too few, at rank 64
 // 14.3 against 10.9, for 52 tiles of rank 32 28 against 17.
 int plan_adapters_few(int64_t M, int n, int64_t h, int64_t o, int r) {
   const int64_t used = std::min<int64_t>(M, n);
