@@ -625,8 +625,10 @@ nf4_status nf4_layernorm_workspace_bytes(int64_t M, int64_t H, size_t *bytes);
  *   dX = rstd * (u - mean(u) - xhat * mean(u * xhat)) + dH   -> bf16 [M][H]
  *   dw = sum over rows of dY * xhat,  db = sum over rows of dY  -> fp32 [H]
  * dX is the gradient of x and of res alike; dH (bf16 [M][H], or NULL) is the gradient
- * that reaches h along the residual stream.  db may be NULL.  dw and db are summed in a
- * fixed order.  M == 0 writes zeros to them.
+ * that reaches h along the residual stream.  db may be NULL.  mean and rstd are taken as
+ * the fp32 values that they are: in a row far from zero xhat is off by up to 2^-24 |mean| rstd
+ * from the forward's.  Sums are fp32, dw's and db's in a fixed order.  M == 0 writes zeros to
+ * them.
  *   ws : nf4_layernorm_workspace_bytes(M, H) bytes; one each for calls that may overlap.
  * Errors as nf4_rmsnorm_bwd.
  */
